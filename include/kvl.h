@@ -341,11 +341,215 @@ kvl_status kvl_read_status(const void *d_plan, int32_t *code, int64_t *detail, v
  * host can read and leaves the context usable. */
 kvl_status kvl_diag_wait_timeout(int32_t limit_us, int32_t *d_status, void *stream);
 
+/* ---------------------------------------------------------------------------
+ * The 8-bit paged cache: pages of codes of one byte with a float32 scale for each
+ * (page, head), who writes them (kvl_cache_append), who reads them (kvl_attend), the
+ * rotary positions of their keys (kvl_rotary) and who owns them (kvl_pages_*).
+ *
+ * Codes are laid out as a pool of the copy calls above with P = 2 and Rp = H*d bytes,
+ * scales as one with B = 1 and Rp = 4*H, both indexed by the same page ids, so slices,
+ * merge-scatters, gathers and scatter-backs persist and restore both parts of a page:
+ *   code of (layer l, plane p, page b, slot s, head h, element e):
+ *       codes  + ((((l*2 + p)*N + b)*B + s)*H + h)*d + e       (p: 0 = K, 1 = V)
+ *   scale of (l, p, b, h):  scales[((l*2 + p)*N + b)*H + h]
+ *   value = code * scale.
+ *
+ * Device-side problems are recorded in a report (KVL_REPORT_BYTES of device memory,
+ * 16-byte aligned, prepared by kvl_report_reset and read by kvl_read_status): the
+ * offending sequence (page, pair) is left out, everything else is done, nothing traps.
+ * Unlike a plan's status a report does not hold later calls back.  A NULL report
+ * records nothing.  detail = the batch entry (or pair) with the smallest number.
+ * ------------------------------------------------------------------------- */
+#define KVL_REPORT_BYTES 256
+#define KVL_CODE_FLOAT 0 /* 8-bit float: 4 exponent bits, 3 mantissa bits, +-448, NaN, no infinity */
+#define KVL_CODE_INT 1   /* signed 8-bit integer, -127 .. 127 */
+#define KVL_TYPE_BFLOAT 0
+#define KVL_TYPE_HALF 1
+#define KVL_TYPE_FLOAT 2
+
+typedef struct kvl_cache {
+    int32_t n_layers;     /* L */
+    int32_t n_kv_heads;   /* H */
+    int32_t head_dim;     /* d: a multiple of 16, at most 256 */
+    int32_t block_tokens; /* B: tokens per page, any */
+    int64_t pool_blocks;  /* N: pages */
+    int32_t code_type;    /* KVL_CODE_FLOAT or KVL_CODE_INT */
+    int32_t reserved;     /* 0 */
+    void *codes;          /* [L][2][N][B][H][d], 16-byte aligned */
+    float *scales;        /* [L][2][N][H] */
+} kvl_cache;
+
+/* A batch of sequences (host struct, device arrays).  Entry i of the batch is the
+ * sequence of slot slots[i] (or slot i): its pages are table entries
+ * tables[slot*table_stride ...] (or, with table_offsets, tables[table_offsets[slot]] up
+ * to table_offsets[slot + 1], e.g. a plan's blk_off and its packed tables), it holds
+ * lens[slot] tokens and its fresh tokens, the last of those it holds, are the rows
+ * starts[i] .. starts[i + 1] of the call's row arrays. */
+typedef struct kvl_sequences {
+    int32_t n_seq;   /* batch entries */
+    int32_t n_slots; /* rows of lens (and of tables) */
+    int64_t n_rows;  /* rows of the row arrays: starts[n_seq] is at most this */
+    int64_t table_stride;
+    const int32_t *tables;
+    const int64_t *table_offsets; /* NULL, or n_slots + 1 */
+    const int32_t *lens;          /* n_slots */
+    const int32_t *slots;         /* NULL, or n_seq */
+    const int32_t *starts;        /* n_seq + 1 */
+} kvl_sequences;
+
+/* Rows of heads: element e of head h of row t is at data + t*row_stride + h*head_stride
+ * + e*(element size); strides in bytes, everything a multiple of 16 bytes.  So q, k and v
+ * may be parts of one fused projection's rows. */
+typedef struct kvl_rows {
+    void *data;
+    int64_t row_stride;
+    int64_t head_stride;
+} kvl_rows;
+
+/* Prepare a report: no problem recorded. */
+kvl_status kvl_report_reset(void *d_report, void *stream);
+
+/* Rotary positions.  The first 2*n_freq elements of a head are n_freq pairs: (i, i + n_freq),
+ * or (2i, 2i + 1) when interleaved; pair i of a row at position p turns by the angle
+ * p * inv_freq[i]: a' = gain*(a cos - b sin), b' = gain*(b cos + a sin).  The elements
+ * after the pairs are copied.  Scaling for long contexts is in inv_freq and gain
+ * (kvl_rotary_frequencies).  The angle is reduced exactly, however long the context. */
+typedef struct kvl_rope {
+    const float *inv_freq; /* device, n_freq */
+    int32_t n_freq;        /* 2*n_freq <= head_dim */
+    int32_t interleaved;   /* 0 or 1 */
+    float gain;            /* 1, or the attention gain of a scaled context */
+    int32_t reserved;      /* 0 */
+} kvl_rope;
+
+/* kvl_rotary -- turn n_sets tensors (at most 4, e.g. q and k; src[i] -> dst[i], which may
+ * be the same memory with the same strides and must not otherwise overlap) of n_rows rows
+ * by their positions, in one launch.  inverse != 0 applies the transposed map: the
+ * gradient of the inputs from that of the outputs.  src, dst and n_heads are host arrays
+ * of n_sets; positions is a device array of n_rows int32.  head_dim: a multiple of 8
+ * (of 4 for KVL_TYPE_FLOAT) up to 512; n_freq a multiple of 4. */
+kvl_status kvl_rotary(const kvl_rope *rope, int64_t n_rows, int32_t head_dim, int32_t type,
+                      const int32_t *positions, int32_t n_sets, const kvl_rows *src,
+                      const kvl_rows *dst, const int32_t *n_heads, int32_t inverse, void *stream);
+
+/* Frequencies of n_freq pairs (host arrays, host work): inv_freq[i] = base^(-i/n_freq), then
+ *   KVL_ROPE_PLAIN       nothing more
+ *   KVL_ROPE_LINEAR      divided by factor (positions interpolated)
+ *   KVL_ROPE_BASE        base *= factor^(n_freq/(n_freq - 1)): the slowest pair slows by factor
+ *   KVL_ROPE_WAVELENGTH  pairs that turn fewer than `low` times over trained_context tokens
+ *                        slow by factor, those that turn more than `high` times stay, a
+ *                        linear join in the number of turns between them
+ * *gain receives 1, or with scale_gain != 0 the logarithmic gain 0.1*ln(factor) + 1. */
+#define KVL_ROPE_PLAIN 0
+#define KVL_ROPE_LINEAR 1
+#define KVL_ROPE_BASE 2
+#define KVL_ROPE_WAVELENGTH 3
+kvl_status kvl_rotary_frequencies(int32_t kind, double base, int32_t n_freq, double factor,
+                                  double low, double high, double trained_context,
+                                  int32_t scale_gain, float *inv_freq, float *gain);
+
+/* kvl_cache_append -- quantise the batch's fresh K and V rows into their pages of one layer.
+ * Fresh token t of entry i (row starts[i] + t) takes cache position lens - (fresh tokens) + t.
+ * For each page and head that receives rows x, with qmax 448 (float) or 127 (int):
+ *   scale' = max(scale, max|x| * (1/qmax), 1e-30) in 32 bits, where the old scale counts only if the page's
+ *            first fresh slot is not slot 0 (the page held tokens before);
+ *   codes of the slots before the fresh ones become round(code * (scale / scale'));
+ *   a fresh element's code is round(clamp(x * (1/scale'))), to nearest, ties to even.
+ * max|x| is over finite elements; an infinity takes the largest code of its sign, a NaN
+ * the NaN code (float) or 0 (int).  With a rope (NULL: none) K is turned by its cache
+ * position first, in 32 bits.  Pages of different entries that receive rows must differ
+ * (kvl_pages_extend sees to it).  type: of the rows, KVL_TYPE_*. */
+kvl_status kvl_cache_append(const kvl_cache *cache, int32_t layer, const kvl_sequences *seqs,
+                            int32_t type, const kvl_rows *k, const kvl_rows *v,
+                            const kvl_rope *rope, void *d_report, void *stream);
+
+/* kvl_attend -- attention of the batch's fresh rows over their sequences' cached tokens (the
+ * fresh ones among them).  Fresh row t of an entry stands at position p = lens - (fresh rows)
+ * + t; query head h reads KV head h / (n_heads / H).  With s_j = sm_scale * (q . K_j):
+ *   visible: 0 <= j < lens, j <= p if causal, j > p - window if window > 0;
+ *   out = sum_j softmax(s)_j V_j,  lse = log(sum_j exp(s_j)) (natural, optional).
+ * A row that sees nothing gets out = 0 and lse = -infinity.  Cached bytes that no row sees
+ * (slots past lens, pages past the sequence's end) are never part of a result, whatever they
+ * hold.  Statistics and sums are held in 32 bits, probabilities enter the products in 16.
+ *   max_new   0, or a bound on the fresh rows of any entry that the caller knows; it chooses
+ *             kernels, results do not depend on it */
+typedef struct kvl_attention {
+    kvl_rows q;       /* n_rows rows of n_heads heads */
+    kvl_rows out;     /* likewise; must not overlap q */
+    float *lse;       /* NULL, or [n_rows][n_heads] */
+    int32_t n_heads;  /* a multiple of n_kv_heads */
+    int32_t type;     /* KVL_TYPE_BFLOAT or KVL_TYPE_HALF, of q and out */
+    float sm_scale;
+    int32_t causal;   /* 0 or 1 */
+    int32_t window;   /* 0: none; > 0 needs causal */
+    int32_t max_new;
+} kvl_attention;
+
+/* Device memory kvl_attend needs for one call (0 for a bad cache); it holds partial results
+ * of a row split over several CTAs.  The first KVL_ATTEND_ZERO_BYTES have to be zero before
+ * the first call and are zero again after every call; calls that may run at the same time
+ * need a workspace each. */
+#define KVL_ATTEND_ZERO_BYTES 16384
+size_t kvl_attend_workspace_bytes(const kvl_cache *cache);
+kvl_status kvl_attend(const kvl_cache *cache, int32_t layer, const kvl_sequences *seqs,
+                      const kvl_attention *attn, void *d_workspace, size_t workspace_bytes,
+                      void *d_report, void *stream);
+
+/* Page bookkeeping, all of it in device memory, without a host in the loop.
+ * refs[b] counts the table entries of live sequences that name page b (0: free); slot s
+ * holds lens[s] tokens in the pages tables[s*table_stride ...], ceil(lens[s] / B) of them;
+ * entries past those mean nothing.  Which page is taken is a function of the state alone:
+ * always the free pages with the lowest numbers. */
+typedef struct kvl_pages {
+    int64_t pool_blocks;  /* N */
+    int32_t block_tokens; /* B */
+    int32_t n_slots;      /* at most 1048576 */
+    int64_t table_stride; /* entries per slot: a sequence holds at most this many pages */
+    int32_t *tables;
+    int32_t *lens;
+    int32_t *refs;        /* N */
+    int32_t *pairs;       /* [N][2] page copies to make: (from, to), 8-byte aligned */
+    int32_t *n_pairs;     /* their number */
+} kvl_pages;
+
+/* kvl_pages_extend -- slots[i] (n of them, distinct) will hold counts[i] more tokens.  Entry by
+ * entry, in order: if the sequence's last page is partly filled and was shared when the call
+ * began, it is replaced by a free page (pairs receives (old, new), to be copied by
+ * kvl_pages_copy before the tokens are appended); then the further pages it needs follow.
+ * Pages are handed out lowest number first; lens, tables and refs follow.  If the free pages
+ * (pages freed by this call do not count) or a table row's entries are not enough for the
+ * whole batch, nothing is changed, n_pairs is 0 and the report says KVL_ERANGE.  One call gives
+ * one sequence at most 1048576 pages. */
+kvl_status kvl_pages_extend(const kvl_pages *pages, int32_t n, const int32_t *slots,
+                            const int32_t *counts, void *d_report, void *stream);
+
+/* kvl_pages_fork -- children[i] becomes a copy of parents[i]: same length, same pages, each
+ * with one more reference.  A child must be empty (length 0), named once, and no parent. */
+kvl_status kvl_pages_fork(const kvl_pages *pages, int32_t n, const int32_t *parents,
+                          const int32_t *children, void *d_report, void *stream);
+
+/* kvl_pages_free -- the sequences of slots[0 .. n) end: length 0, one reference less on each of
+ * their pages.  An empty slot stays as it is. */
+kvl_status kvl_pages_free(const kvl_pages *pages, int32_t n, const int32_t *slots,
+                          void *d_report, void *stream);
+
+/* kvl_pages_compact -- move the live pages to the numbers below their count n_live: the k-th
+ * live page numbered n_live or more (in order) goes to the k-th free number below n_live.
+ * tables (of every slot) and refs are rewritten, pairs receives the copies to make. */
+kvl_status kvl_pages_compact(const kvl_pages *pages, void *d_report, void *stream);
+
+/* kvl_pages_copy -- copy the pages of pairs[0 .. *d_n_pairs) (device; at most max_pairs of
+ * them), codes and scales of every layer, from pair[0] to pair[1].  Sources and destinations
+ * must be disjoint and destinations distinct, as extend and compact leave them. */
+kvl_status kvl_pages_copy(const kvl_cache *cache, const int32_t *pairs, const int32_t *d_n_pairs,
+                          int64_t max_pairs, void *d_report, void *stream);
+
 /* Human-readable name of a status code (static string). */
 const char *kvl_status_string(kvl_status s);
 
 /* Kernel launches one call of each entry point makes (for launch accounting):
- * which = 0 plan, 1 slice, 2 merge-scatter, 3 gather / scatter-back. */
+ * which = 0 plan, 1 slice, 2 merge-scatter, 3 gather / scatter-back, 4 rotary, 5 append,
+ * 6 attend (at most), 7 pages extend, 8 fork, 9 free, 10 compact, 11 copy. */
 int32_t kvl_launches_per_call(int32_t which);
 
 #ifdef __cplusplus

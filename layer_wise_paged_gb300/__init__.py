@@ -38,11 +38,39 @@ class kvl_launch(ctypes.Structure):
 KVL_LAUNCH_HOST_SRC, KVL_LAUNCH_HOST_DST, KVL_LAUNCH_OVERLAP_PREVIOUS, KVL_LAUNCH_SHARE_SMS = 1, 2, 4, 8
 KVL_LAUNCH_PLAN_READY = 16
 
+KVL_REPORT_BYTES = 256
+KVL_CODE_FLOAT, KVL_CODE_INT = 0, 1
+KVL_TYPE_BFLOAT, KVL_TYPE_HALF, KVL_TYPE_FLOAT = 0, 1, 2
+KVL_ROPE_PLAIN, KVL_ROPE_LINEAR, KVL_ROPE_BASE, KVL_ROPE_WAVELENGTH = 0, 1, 2, 3
+KVL_ATTEND_ZERO_BYTES = 16384
+
 
 class kvl_geom(ctypes.Structure):
     _fields_ = [("n_layers", ctypes.c_int32), ("n_planes", ctypes.c_int32),
                 ("block_tokens", ctypes.c_int32), ("plane_row_bytes", ctypes.c_int32),
                 ("pool_blocks", ctypes.c_int64)]
+
+
+def _struct(name, fields):
+    return type(name, (ctypes.Structure,), {"_fields_": fields})
+
+
+_i32, _i64, _ptr, _f32 = ctypes.c_int32, ctypes.c_int64, ctypes.c_void_p, ctypes.c_float
+kvl_cache = _struct("kvl_cache", [
+    ("n_layers", _i32), ("n_kv_heads", _i32), ("head_dim", _i32), ("block_tokens", _i32),
+    ("pool_blocks", _i64), ("code_type", _i32), ("reserved", _i32), ("codes", _ptr), ("scales", _ptr)])
+kvl_sequences = _struct("kvl_sequences", [
+    ("n_seq", _i32), ("n_slots", _i32), ("n_rows", _i64), ("table_stride", _i64), ("tables", _ptr),
+    ("table_offsets", _ptr), ("lens", _ptr), ("slots", _ptr), ("starts", _ptr)])
+kvl_rows = _struct("kvl_rows", [("data", _ptr), ("row_stride", _i64), ("head_stride", _i64)])
+kvl_rope = _struct("kvl_rope", [("inv_freq", _ptr), ("n_freq", _i32), ("interleaved", _i32),
+                                ("gain", _f32), ("reserved", _i32)])
+kvl_attention = _struct("kvl_attention", [
+    ("q", kvl_rows), ("out", kvl_rows), ("lse", _ptr), ("n_heads", _i32), ("type", _i32),
+    ("sm_scale", _f32), ("causal", _i32), ("window", _i32), ("max_new", _i32)])
+kvl_pages = _struct("kvl_pages", [
+    ("pool_blocks", _i64), ("block_tokens", _i32), ("n_slots", _i32), ("table_stride", _i64),
+    ("tables", _ptr), ("lens", _ptr), ("refs", _ptr), ("pairs", _ptr), ("n_pairs", _ptr)])
 
 
 # struct kvl_request, 112 bytes, field for field
@@ -80,6 +108,23 @@ def lib():
         L.kvl_diag_wait_timeout.argtypes, L.kvl_diag_wait_timeout.restype = [i32, vp, vp], i32
         L.kvl_status_string.argtypes, L.kvl_status_string.restype = [i32], ctypes.c_char_p
         L.kvl_launches_per_call.argtypes, L.kvl_launches_per_call.restype = [i32], i32
+        P = ctypes.POINTER
+        cp, sp, rp, op, pg = (P(t) for t in (kvl_cache, kvl_sequences, kvl_rows, kvl_rope, kvl_pages))
+        L.kvl_report_reset.argtypes = [vp, vp]
+        L.kvl_rotary.argtypes = [op, i64, i32, i32, vp, i32, rp, rp, P(i32), i32, vp]
+        L.kvl_rotary_frequencies.argtypes = [i32, ctypes.c_double, i32, ctypes.c_double, ctypes.c_double,
+                                             ctypes.c_double, ctypes.c_double, i32, vp, P(ctypes.c_float)]
+        L.kvl_cache_append.argtypes = [cp, i32, sp, i32, rp, rp, op, vp, vp]
+        L.kvl_attend_workspace_bytes.argtypes, L.kvl_attend_workspace_bytes.restype = [cp], sz
+        L.kvl_attend.argtypes = [cp, i32, sp, P(kvl_attention), vp, sz, vp, vp]
+        L.kvl_pages_extend.argtypes = [pg, i32, vp, vp, vp, vp]
+        L.kvl_pages_fork.argtypes = [pg, i32, vp, vp, vp, vp]
+        L.kvl_pages_free.argtypes = [pg, i32, vp, vp, vp]
+        L.kvl_pages_compact.argtypes = [pg, vp, vp]
+        L.kvl_pages_copy.argtypes = [cp, vp, vp, i64, vp, vp]
+        for f in (L.kvl_report_reset, L.kvl_rotary, L.kvl_rotary_frequencies, L.kvl_cache_append, L.kvl_attend,
+                  L.kvl_pages_extend, L.kvl_pages_fork, L.kvl_pages_free, L.kvl_pages_compact, L.kvl_pages_copy):
+            f.restype = i32
         for f in (L.kvl_batch_plan, L.kvl_batch_plan_static_scratch, L.kvl_slice_layer, L.kvl_merge_scatter_paged,
                   L.kvl_gather_layer_objects, L.kvl_read_status):
             f.restype = i32
@@ -220,7 +265,7 @@ def pack_requests(requests, *, hit_base=0, miss_base=0, obj_base=0, src_table_ba
     return out[:len(requests)] if requests else out[:0]
 
 
-__all__ = ["build", "lib", "geom", "kvl_geom", "kvl_launch", "KVL_LAUNCH_HOST_SRC",
+__all__ = ["kvl_cache", "kvl_sequences", "kvl_rows", "kvl_rope", "kvl_attention", "kvl_pages", "build", "lib", "geom", "kvl_geom", "kvl_launch", "KVL_LAUNCH_HOST_SRC",
            "KVL_LAUNCH_HOST_DST", "REQUEST_DTYPE", "pack_requests", "check",
            "KvlError", "kvl_plan_bytes", "kvl_plan_layout", "kvl_batch_plan", "kvl_batch_plan_static_scratch",
            "kvl_slice_layer",

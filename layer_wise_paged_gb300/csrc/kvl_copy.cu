@@ -47,15 +47,12 @@
 #include <cstdint>
 
 #include "kvl_internal.cuh"
+#include "kvl_ptx.cuh"
 
 namespace kvl {
 namespace {
 
 enum Op { OP_SLICE = 0, OP_MERGE = 1, OP_GATHER = 2, OP_SCATTER = 3 };
-
-#ifndef KVL_PDL
-#define KVL_PDL 1
-#endif
 
 // Pipeline depth.  A launch that has its SMs to itself keeps kDeepStages stages (192
 // KiB): one CTA must keep enough bytes in flight to hold its SM's share of the HBM
@@ -66,7 +63,6 @@ enum Op { OP_SLICE = 0, OP_MERGE = 1, OP_GATHER = 2, OP_SCATTER = 3 };
 // bytes in flight as one deep CTA.
 constexpr int kDeepStages = 6;
 constexpr int kShallowStages = 3;
-constexpr unsigned long long kWaitLimitNs = 2000000000ull;  // 2 s per mbarrier wait
 static_assert(kStageBytes % 16 == 0 && kShallowStages >= 2 && kDeepStages >= kShallowStages,
               "stage geometry");
 
@@ -102,203 +98,6 @@ struct ItemMeta {
     int32_t blk_a, tok_a, tok_b;
     bool layer_first_a, layer_first_b;
 };
-
-// ---- PTX wrappers ----------------------------------------------------------
-
-__device__ __forceinline__ uint32_t smem_u32(const void *p)
-{
-    return static_cast<uint32_t>(__cvta_generic_to_shared(p));
-}
-
-__device__ __forceinline__ unsigned long long global_ns()
-{
-    unsigned long long t;
-    asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
-    return t;
-}
-
-__device__ __forceinline__ void mbar_init(uint32_t bar, uint32_t count)
-{
-    asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(count) : "memory");
-}
-
-__device__ __forceinline__ void mbar_inval(uint32_t bar)
-{
-    asm volatile("mbarrier.inval.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
-}
-
-__device__ __forceinline__ void fence_mbar_init()
-{
-    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-}
-
-__device__ __forceinline__ void fence_proxy_async_smem()
-{
-    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-}
-
-__device__ __forceinline__ void mbar_arrive_expect_tx(uint32_t bar, uint32_t bytes)
-{
-    asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes)
-                 : "memory");
-}
-
-__device__ __forceinline__ bool mbar_try_wait(uint32_t bar, uint32_t parity)
-{
-    uint32_t ok;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(ok)
-        : "r"(bar), "r"(parity)
-        : "memory");
-    return ok != 0;
-}
-
-// Bounded wait for a phase of a stage's mbarrier; false when the limit passed.
-__device__ __forceinline__ bool mbar_wait_bounded(uint32_t bar, uint32_t parity,
-                                                  unsigned long long limit_ns = kWaitLimitNs)
-{
-    if (mbar_try_wait(bar, parity)) return true;
-    const unsigned long long t0 = global_ns();
-    while (!mbar_try_wait(bar, parity)) {
-        if (global_ns() - t0 > limit_ns) return false;
-    }
-    return true;
-}
-
-// Complete `bytes` of an mbarrier's expected transaction count from this thread.
-__device__ __forceinline__ void mbar_complete_tx(uint32_t bar, uint32_t bytes)
-{
-    asm volatile("mbarrier.complete_tx.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
-}
-
-__device__ __forceinline__ void bulk_load(uint32_t dst_smem, const void *src, uint32_t bytes,
-                                          uint32_t bar)
-{
-    asm volatile(
-        "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
-            dst_smem),
-        "l"(src), "r"(bytes), "r"(bar)
-        : "memory");
-}
-
-// One box of a 5-D tensor map (coordinates innermost first) into shared memory,
-// completing on the stage's mbarrier like bulk_load.
-__device__ __forceinline__ void tensor_load_5d(uint32_t dst_smem, const void *map, int32_t c0,
-                                               int32_t c1, int32_t c2, int32_t c3, int32_t c4,
-                                               uint32_t bar)
-{
-    asm volatile(
-        "cp.async.bulk.tensor.5d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-        " [%0], [%1, {%2, %3, %4, %5, %6}], [%7];" ::"r"(dst_smem),
-        "l"(map), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(c4), "r"(bar)
-        : "memory");
-}
-
-// The plan wrote its tensor maps with generic stores and a release to the tensor-map
-// proxy; this is the matching acquire, before the first tensor load through `map`.
-__device__ __forceinline__ void acquire_tensor_map(const void *map)
-{
-    asm volatile("fence.proxy.tensormap::generic.acquire.gpu [%0], 128;" ::"l"(map) : "memory");
-}
-
-__device__ __forceinline__ void bulk_store(void *dst, uint32_t src_smem, uint32_t bytes)
-{
-    asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(dst),
-                 "r"(src_smem), "r"(bytes)
-                 : "memory");
-}
-
-__device__ __forceinline__ void bulk_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
-
-// All but the newest store group have finished reading shared memory.
-__device__ __forceinline__ void bulk_wait_read_all_but_one()
-{
-    asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
-}
-
-__device__ __forceinline__ void bulk_wait_all() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
-
-// Programmatic dependent launch: the next kernel on the stream may be scheduled
-// while this one runs; it waits for this grid's completion (and its memory) in
-// grid_dependency_wait() before touching any data.
-__device__ __forceinline__ void allow_dependents_launch()
-{
-#if KVL_PDL
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-#endif
-}
-
-__device__ __forceinline__ void grid_dependency_wait()
-{
-#if KVL_PDL
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-#endif
-}
-
-// Warm L2 with the line holding p.  A hint only: L2 is the device's point of
-// coherence, so a line fetched before a preceding kernel's writes land is updated by
-// them, and no later load can see it stale.
-__device__ __forceinline__ void prefetch_l2(const void *p)
-{
-    asm volatile("prefetch.global.L2 [%0];" ::"l"(p));
-}
-
-// Bulk prefetch of `bytes` (a multiple of 16, 16-byte aligned) into L2: a hint, with
-// the same coherence as prefetch_l2.
-__device__ __forceinline__ void bulk_prefetch_l2(const void *p, uint32_t bytes)
-{
-    asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(p), "r"(bytes) : "memory");
-}
-
-// 32-bit load through the read-only path; volatile so that it is issued where it
-// stands, ahead of the loads that follow it.
-__device__ __forceinline__ uint32_t ld_nc_u32(const void *p)
-{
-    uint32_t r;
-    asm volatile("ld.global.nc.u32 %0, [%1];" : "=r"(r) : "l"(p));
-    return r;
-}
-
-__device__ __forceinline__ void mbar_arrive(uint32_t bar)
-{
-    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
-}
-
-// Ordinary SM accesses, for the side of a copy that lives in pinned host memory.
-__device__ __forceinline__ uint4 ld_global_v4(const uint8_t *p)
-{
-    uint4 r;
-    asm volatile("ld.global.v4.u32 {%0, %1, %2, %3}, [%4];"
-                 : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w)
-                 : "l"(p));
-    return r;
-}
-
-__device__ __forceinline__ void st_global_v4(uint8_t *p, const uint4 &v)
-{
-    asm volatile("st.global.v4.u32 [%0], {%1, %2, %3, %4};" ::"l"(p), "r"(v.x), "r"(v.y), "r"(v.z),
-                 "r"(v.w)
-                 : "memory");
-}
-
-__device__ __forceinline__ uint4 ld_shared_v4(uint32_t a)
-{
-    uint4 r;
-    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
-                 : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w)
-                 : "r"(a));
-    return r;
-}
-
-__device__ __forceinline__ void st_shared_v4(uint32_t a, const uint4 &v)
-{
-    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(v.x), "r"(v.y), "r"(v.z),
-                 "r"(v.w)
-                 : "memory");
-}
 
 // Read `nrows` rows of `row_bytes` (row r at rowptr(r)) into shared memory at
 // sbase + r*row_bytes with 16-byte loads: four rows and four vectors per lane, 8 KiB a
