@@ -1,0 +1,68 @@
+// kvl_attend.cuh -- what the attention kernels share: arguments, the visible range of a row,
+// and how a call's work is cut into equal shares.
+//
+// Both kernels compute, for a row with scores s_j = sm_scale q.K_j over the visible tokens,
+//   x_j = s_j log2(e) + log2(vs_j),  m = max x_j,  w_j = 2^(x_j - m),
+//   O = sum w_j codeV_j,  l = sum w_j / vs_j,   out = O / l,   lse = ln(l) + m ln(2),
+// with vs_j the V scale of token j's page: w_j 2^m / vs_j is the probability's numerator.  The
+// V scale rides in the exponent, so the products take the codes as they are, and w_j lies in
+// [0, 1] with 1 at the token that counts most: as a 16-bit half it has 11 significant bits
+// wherever it matters (below 2^-14 of the largest weight an absolute error of 2^-25).  The
+// maximum, l, O and every score are 32-bit.
+//
+// Slots come in groups of 16, each within one page (a page whose size is no multiple of 16
+// ends in a part of a group), so a group has one K and one V scale and 16 consecutive rows.
+#pragma once
+
+#include "kvl_quant.cuh"
+
+namespace kvl {
+
+struct AttendArgs {
+    kvl_cache cache;
+    kvl_sequences seqs;
+    kvl_attention attn;
+    int32_t layer;
+    int32_t max_rows;  // entries with more (rows x heads of a group) belong to the other kernel
+    uint32_t *counters;
+    float *parts;      // partial results of rows split over CTAs
+    void *report;
+};
+
+namespace {
+
+constexpr int kGroup = 16;
+
+// What one batch entry costs: `tiles` row tiles for each KV head, each walking the groups
+// [g0, g0 + groups).
+struct Cost {
+    Entry e;
+    int32_t tiles, g0, groups;
+};
+
+__device__ __forceinline__ int32_t group_of(int32_t token, int32_t B, int32_t per_block)
+{
+    const int32_t b = token / B;
+    return b * per_block + (token - b * B) / kGroup;
+}
+
+__device__ __forceinline__ int64_t units_of(const Cost &c, int H) { return int64_t(H) * c.tiles * c.groups; }
+
+// 2^x; -infinity gives 0.
+__device__ __forceinline__ float exp2_of(float x)
+{
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+
+// The V scale of a page as the kernels use it: at least the smallest an append writes (a page
+// of zeros whose scale is 0 contributes nothing either way); a NaN stays.
+__device__ __forceinline__ float v_scale(float s) { return s < kTinyScale ? kTinyScale : s; }
+
+}  // namespace
+
+size_t attend_rows_part_bytes(int head_dim);  // for each SM
+kvl_status launch_attend_rows(const AttendArgs &a, int sms, void *stream);
+
+}  // namespace kvl

@@ -1,0 +1,600 @@
+// kvl_attend_rows.cu -- attention of few rows a sequence: decoded tokens, drafted tokens.
+//
+// Bound by HBM: each cached byte is read once, and 2 * 8 multiply-adds a byte are far below the
+// tensor rate, so what counts is bytes in flight and few instructions a byte.
+//
+// A warp takes 16 tokens of one KV head at a time from its own ring in shared memory (filled by
+// 16-byte asynchronous copies, kStages groups ahead, no barrier between warps) and computes the
+// transposed products with 16 x 8 x 16 tensor instructions:
+//   S^T [16 tokens x 8 rows] = K [16 x d] Q^T,   O^T [d x 8 rows] += V^T [d x 16] P^T.
+// Tokens (then elements of V) fill the 16-high operand and the rows, i.e. the query heads of
+// the KV head times the fresh tokens, the 8-wide one: a group of 4 or 8 heads wastes half or
+// nothing where rows in the high operand would waste three quarters.  The order of elements
+// in a product's inner dimension is free, so a lane reads its codes as 16-byte vectors, converts
+// them in registers and needs no transposition; P^T comes out of S^T by an 8 x 8 register
+// transpose.
+//
+// Work: every (entry, KV head, row tile) is a job of as many units as it has groups; the units
+// of all jobs in a row are cut into equal contiguous shares, one a CTA, so a long sequence is
+// split over many CTAs and short ones share one.  A job's groups are dealt to the CTA's warps,
+// whose results are joined in shared memory; a job that crosses shares leaves its parts in the
+// workspace and the CTA that finishes last joins them, in order of the shares.
+#include "kvl_attend.cuh"
+
+namespace kvl {
+namespace {
+
+constexpr int kWarps = 8;
+constexpr int kThreads = kWarps * 32;
+constexpr int kStages = 3;
+constexpr int kCtasPerSm = 2;
+constexpr int kUnitsPerCta = 16;  // a share is at least two groups a warp
+
+template <int D, int NT>
+struct Shape {
+    static constexpr int kRows = 8 * NT;
+    static constexpr int kGroupBytes = kGroup * D;            // K or V of a group
+    static constexpr int kRing = kStages * 2 * kGroupBytes;   // one warp's ring
+    static constexpr int kORow = D + 4;                       // floats; the pad spreads rows over banks
+    static constexpr int kOBytes = kRows * kORow * 4;         // one warp's O, over its ring
+    static constexpr int kWarpBytes = kRing > kOBytes ? kRing : kOBytes;
+    static constexpr int kQBytes = kRows * D * 2;
+    static constexpr int kSmem = kQBytes + kWarps * kWarpBytes;
+    static constexpr int kPartFloats = kRows * (D + 2);       // m, l, O of a part
+};
+
+__device__ __forceinline__ void copy_async16(uint32_t dst, const void *src, bool ok)
+{
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(ok ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void copy_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copy_async_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+
+__device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                         uint32_t b1)
+{
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+                 : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t x)
+{
+    uint32_t r;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
+    return r;
+}
+
+// Byte offset of 16-byte chunk c of row r in a group's K (V) tile.  A lane reads K by rows
+// lane/4 and chunks lane%4 + 4i, V by rows 2(lane%4) and chunk(s) lane/4; the chunk is XORed
+// so that the 8 lanes of a shared-memory phase hit 8 different 16-byte columns of 128.
+template <int D>
+__device__ __forceinline__ uint32_t k_at(int r, int c)
+{
+    if constexpr (D == 64) return r * 64 + c * 16;
+    else return r * D + ((c ^ ((r & 1) << 2)) << 4);
+}
+template <int D>
+__device__ __forceinline__ uint32_t v_at(int r, int c)
+{
+    if constexpr (D == 64)
+        return (r >> 1) * 128 + (((((r & 1) << 2) | c) ^ (r & 6)) << 4);
+    else if constexpr (D == 128)
+        return r * 128 + ((c ^ (r & 6)) << 4);
+    else
+        return r * 256 + ((c ^ (((r >> 1) & 1) | (r & 4))) << 4);
+}
+
+template <int NT>
+__device__ __forceinline__ Cost cost_of(const AttendArgs &a, int i, void *rep)
+{
+    const int B = a.cache.block_tokens, per_block = (B + kGroup - 1) / kGroup;
+    Cost c;
+    c.e = load_entry(a.seqs, B, i, rep);
+    const int64_t rows = int64_t(c.e.fresh) * (a.attn.n_heads / a.cache.n_kv_heads);
+    c.tiles = rows > a.max_rows ? 0 : int32_t((rows + 8 * NT - 1) / (8 * NT));
+    const int32_t lo = a.attn.window > 0 ? max(0, c.e.len - c.e.fresh - a.attn.window + 1) : 0;
+    c.g0 = group_of(lo, B, per_block);
+    // a sequence of no tokens is one group of none: its rows still get their zeros
+    c.groups = max(1, c.e.len > 0 ? group_of(c.e.len - 1, B, per_block) + 1 - c.g0 : 0);
+    return c;
+}
+
+template <int CODE, int TYPE, int D, int NT>
+__global__ void __launch_bounds__(kThreads, kCtasPerSm) attend_rows_kernel(const __grid_constant__ AttendArgs a)
+{
+    using S = Shape<D, NT>;
+    constexpr int kRows = S::kRows, kChunks = D / 16, kLaneBytes = D / 8;
+    extern __shared__ __align__(128) uint8_t smem[];
+    __shared__ int64_t s_scan[kWarps], s_off;
+    __shared__ int s_entry, s_last;
+    __shared__ float s_m[kWarps][kRows], s_l[kWarps][kRows], s_cq[kRows];
+
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, nn = lane >> 2, kk = lane & 3;
+    const int H = a.cache.n_kv_heads, d = a.cache.head_dim, B = a.cache.block_tokens;
+    const int G = a.attn.n_heads / H, per_block = (B + kGroup - 1) / kGroup;
+    const int64_t N = a.cache.pool_blocks;
+
+    // ---- this CTA's share of the units ----
+    const int n_seq = a.seqs.n_seq, per_thread = (n_seq + kThreads - 1) / kThreads;
+    const int i0 = min(n_seq, tid * per_thread), i1 = min(n_seq, i0 + per_thread);
+    int64_t mine = 0;
+    for (int i = i0; i < i1; ++i) mine += units_of(cost_of<NT>(a, i, blockIdx.x == 0 ? a.report : nullptr), H);
+    int64_t scan = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int64_t y = __shfl_up_sync(0xffffffffu, scan, o);
+        if (lane >= o) scan += y;
+    }
+    if (lane == 31) s_scan[warp] = scan;
+    __syncthreads();
+    int64_t before = scan - mine, total = 0;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+        if (w < warp) before += s_scan[w];
+        total += s_scan[w];
+    }
+    const int64_t shares = min(int64_t(gridDim.x), (total + kUnitsPerCta - 1) / kUnitsPerCta);
+    if (int64_t(blockIdx.x) >= shares) return;
+    int64_t u = total * blockIdx.x / shares;
+    const int64_t u_end = total * (blockIdx.x + 1) / shares;
+    if (u >= before && u < before + mine) {
+        int64_t at = before;
+        int i = i0;
+        for (; i < i1; ++i) {
+            const int64_t n = units_of(cost_of<NT>(a, i, nullptr), H);
+            if (u < at + n) break;
+            at += n;
+        }
+        s_entry = i;
+        s_off = u - at;
+    }
+    __syncthreads();
+    int entry = s_entry;
+    int64_t off = s_off;  // units of the entry before u
+    Cost c = cost_of<NT>(a, entry, nullptr);
+
+    const uint32_t ring = smem_u32(smem) + S::kQBytes + warp * S::kWarpBytes;
+    __half *sq = reinterpret_cast<__half *>(smem);
+    const uint8_t *codes = static_cast<const uint8_t *>(a.cache.codes);
+    const int64_t plane = int64_t(a.layer) * 2 * N, v_plane_bytes = N * B * H * d;
+
+    while (u < u_end) {
+        while (off >= units_of(c, H)) {  // on to the entry that holds unit u
+            off -= units_of(c, H);
+            c = cost_of<NT>(a, ++entry, nullptr);
+        }
+        const int job = int(off / c.groups);
+        const int ga = int(off - int64_t(job) * c.groups);
+        const int gb = int(min(int64_t(c.groups), ga + (u_end - u)));
+        const int64_t job_u0 = u - ga;
+        const int h = job / c.tiles, tile = job - h * c.tiles;
+        const int rows = min(kRows, c.e.fresh * G - tile * kRows);
+        const int pos0 = c.e.len - c.e.fresh;
+
+        // ---- groups of this warp: ga + warp + kWarps * k.  Lane k holds the k-th's page, scales
+        // and place; the next 32 are fetched while these are worked on.
+        const int count = (gb - ga - warp + kWarps - 1) / kWarps;  // may be <= 0
+        auto place_of = [&](int k, int &t0, int &nv) -> int32_t {  // page of the k-th group, -1: none
+            t0 = 0;
+            nv = 0;
+            if (k >= count) return -1;
+            const int g = c.g0 + ga + warp + kWarps * k;
+            const int blk = g / per_block, slot = (g - blk * per_block) * kGroup;
+            t0 = blk * B + slot;
+            nv = min(min(kGroup, B - slot), c.e.len - t0);
+            if (nv <= 0) return -1;
+            const int32_t page = c.e.table[blk];
+            if (page < 0 || page >= N) {
+                report(a.report, KVL_ERANGE, entry);
+                nv = 0;
+                return -1;
+            }
+            return page;
+        };
+        auto scales_of = [&](int32_t page, float &ks, float &vs) {
+            ks = 0.f;
+            vs = 1.f;
+            if (page >= 0) {
+                ks = __ldg(a.cache.scales + (plane + page) * H + h);
+                vs = v_scale(__ldg(a.cache.scales + (plane + N + page) * H + h));
+            }
+        };
+        int t0_l, nv_l, t0_n, nv_n;
+        int32_t page_l = place_of(lane, t0_l, nv_l), page_n = -1;
+        float ks_l, vs_l, ks_n = 0.f, vs_n = 1.f;
+
+        // ---- Q: each row scaled by a power of two into the range of a half (undone in s_cq)
+        for (int r = warp; r < kRows; r += kWarps) {
+            const int row = tile * kRows + r;
+            const bool ok = r < rows;
+            const uint8_t *src = static_cast<const uint8_t *>(a.attn.q.data) +
+                                 (int64_t(c.e.row0) + (ok ? row / G : 0)) * a.attn.q.row_stride +
+                                 int64_t(h * G + (ok ? row % G : 0)) * a.attn.q.head_stride;
+            float v[D / 32];
+            float amax = 0.f;
+#pragma unroll
+            for (int x = 0; x < D / 64; ++x) {
+                const int e = lane * 2 + 64 * x;
+                uint32_t w = 0;
+                if (ok && e < d) w = *reinterpret_cast<const uint32_t *>(src + 2 * e);
+                if constexpr (TYPE == KVL_TYPE_BFLOAT) {
+                    v[2 * x] = __uint_as_float(w << 16);
+                    v[2 * x + 1] = __uint_as_float(w & 0xffff0000u);
+                } else {
+                    const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&w));
+                    v[2 * x] = f.x;
+                    v[2 * x + 1] = f.y;
+                }
+                amax = fmaxf(amax, fmaxf(fabsf(v[2 * x]), fabsf(v[2 * x + 1])));
+            }
+#pragma unroll
+            for (int o = 16; o; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+            // amax * up in [1, 2) (exact powers of two; a row of zeros or infinities stays)
+            const uint32_t ex = (__float_as_uint(amax) >> 23) & 0xffu;
+            const bool plain = ex < 2 || ex > 252;
+            const float up = plain ? 1.f : __uint_as_float((254u - ex) << 23);
+            const float down = plain ? 1.f : __uint_as_float(ex << 23);
+#pragma unroll
+            for (int x = 0; x < D / 64; ++x)
+                *reinterpret_cast<__half2 *>(sq + r * D + lane * 2 + 64 * x) =
+                    __floats2half2_rn(v[2 * x] * up, v[2 * x + 1] * up);
+            if (lane == 0) s_cq[r] = a.attn.sm_scale * kLog2e * down;
+        }
+        scales_of(page_l, ks_l, vs_l);
+        page_n = place_of(32 + lane, t0_n, nv_n);
+        __syncthreads();
+
+        // visible tokens of this lane's columns (rows 2kk, 2kk + 1 of each tile of 8) and of all rows
+        int lo[NT][2], hi[NT][2];
+        float cq[NT][2];
+        const int first_pos = pos0 + (tile * kRows) / G, last_pos = pos0 + (tile * kRows + rows - 1) / G;
+        const int all_hi = a.attn.causal ? min(c.e.len, first_pos + 1) : c.e.len;
+        const int all_lo = a.attn.window > 0 ? max(0, last_pos - a.attn.window + 1) : 0;
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+                const int r = 8 * t + 2 * kk + x;
+                const int pos = pos0 + (tile * kRows + r) / G;
+                hi[t][x] = a.attn.causal ? min(c.e.len, pos + 1) : c.e.len;
+                lo[t][x] = a.attn.window > 0 ? max(0, pos - a.attn.window + 1) : 0;
+                if (r >= rows) { lo[t][x] = 0; hi[t][x] = c.e.len; }
+                cq[t][x] = s_cq[r];
+            }
+
+        float o[NT][kChunks][4], m[NT][2], l[NT][2];
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+            m[t][0] = m[t][1] = -INFINITY;
+            l[t][0] = l[t][1] = 0.f;
+#pragma unroll
+            for (int x = 0; x < kChunks; ++x) o[t][x][0] = o[t][x][1] = o[t][x][2] = o[t][x][3] = 0.f;
+        }
+
+        // start of the k-th group's copies: its page is lane k%32's, of these 32 or the next
+        int base_k = 0;
+        auto load_group = [&](int k) {
+            if (k < count) {
+                const bool ahead = k - base_k >= 32;
+                const int32_t page = __shfl_sync(0xffffffffu, ahead ? page_n : page_l, k & 31);
+                const int t0 = __shfl_sync(0xffffffffu, ahead ? t0_n : t0_l, k & 31);
+                const int nv = __shfl_sync(0xffffffffu, ahead ? nv_n : nv_l, k & 31);
+                const uint32_t dst = ring + (k % kStages) * (2 * S::kGroupBytes);
+                const uint8_t *src = codes + (((plane + max(page, 0)) * B + t0 % B) * H + h) * d;
+#pragma unroll
+                for (int x = 0; x < D / 32; ++x) {  // 512 bytes an instruction
+                    const int id = x * 32 + lane, r = id / kChunks, ch = id % kChunks;
+                    const bool ok = r < nv && ch * 16 < d;
+                    const uint8_t *p = src + (ok ? int64_t(r) * H * d + ch * 16 : 0);
+                    copy_async16(dst + k_at<D>(r, ch), p, ok);
+                    copy_async16(dst + S::kGroupBytes + v_at<D>(r, ch), p + v_plane_bytes, ok);
+                }
+            }
+            copy_async_commit();
+        };
+#pragma unroll
+        for (int k = 0; k < kStages - 1; ++k) load_group(k);
+
+        for (int k = 0; k < count; ++k) {
+            if (k - base_k == 32) {
+                base_k += 32;
+                page_l = page_n; t0_l = t0_n; nv_l = nv_n; ks_l = ks_n; vs_l = vs_n;
+                page_n = place_of(base_k + 32 + lane, t0_n, nv_n);
+            }
+            if (k - base_k == 8) scales_of(page_n, ks_n, vs_n);
+            copy_async_wait<kStages - 2>();
+            __syncwarp();
+            load_group(k + kStages - 1);
+            const int t0 = __shfl_sync(0xffffffffu, t0_l, k & 31), nv = __shfl_sync(0xffffffffu, nv_l, k & 31);
+            const float ks = __shfl_sync(0xffffffffu, ks_l, k & 31), vs = __shfl_sync(0xffffffffu, vs_l, k & 31);
+            const float ivs = __fdividef(1.f, vs), lvs = __log2f(vs);
+            const uint8_t *kt = smem + (ring - smem_u32(smem)) + (k % kStages) * (2 * S::kGroupBytes);
+            const uint8_t *vt = kt + S::kGroupBytes;
+
+            // ---- S^T = K Q^T
+            float s[NT][4];
+#pragma unroll
+            for (int t = 0; t < NT; ++t) s[t][0] = s[t][1] = s[t][2] = s[t][3] = 0.f;
+#pragma unroll
+            for (int i = 0; i < D / 64; ++i) {
+                const int ch = kk + 4 * i;
+                const uint4 ka = *reinterpret_cast<const uint4 *>(kt + k_at<D>(nn, ch));
+                const uint4 kb = *reinterpret_cast<const uint4 *>(kt + k_at<D>(nn + 8, ch));
+                const uint32_t wa[4] = {ka.x, ka.y, ka.z, ka.w}, wb[4] = {kb.x, kb.y, kb.z, kb.w};
+                uint32_t q[NT][8];
+#pragma unroll
+                for (int t = 0; t < NT; ++t) {
+                    const uint4 *p = reinterpret_cast<const uint4 *>(sq + (8 * t + nn) * D + ch * 16);
+                    const uint4 x = p[0], y = p[1];
+                    q[t][0] = x.x; q[t][1] = x.y; q[t][2] = x.z; q[t][3] = x.w;
+                    q[t][4] = y.x; q[t][5] = y.y; q[t][6] = y.z; q[t][7] = y.w;
+                }
+#pragma unroll
+                for (int w = 0; w < 4; ++w) {
+                    const uint32_t a0 = codes_lo<CODE>(wa[w]), a1 = codes_lo<CODE>(wb[w]);
+                    const uint32_t a2 = codes_hi<CODE>(wa[w]), a3 = codes_hi<CODE>(wb[w]);
+#pragma unroll
+                    for (int t = 0; t < NT; ++t) mma16816(s[t], a0, a1, a2, a3, q[t][2 * w], q[t][2 * w + 1]);
+                }
+            }
+
+            // ---- softmax over tokens nn, nn + 8 of columns 2kk, 2kk + 1
+            const bool whole = nv == kGroup && t0 >= all_lo && t0 + kGroup <= all_hi;
+            bool grew = false;
+            float mn[NT][2];
+#pragma unroll
+            for (int t = 0; t < NT; ++t) {
+#pragma unroll
+                for (int x = 0; x < 4; ++x) {
+                    s[t][x] = fmaf(s[t][x], ks * cq[t][x & 1], lvs);
+                    if (!whole) {
+                        const int r = nn + 8 * (x >> 1);
+                        if (r >= nv || t0 + r < lo[t][x & 1] || t0 + r >= hi[t][x & 1]) s[t][x] = -INFINITY;
+                    }
+                }
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                    float v = fmaxf(s[t][x], s[t][x + 2]);
+                    v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 4));
+                    v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 8));
+                    v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 16));
+                    mn[t][x] = fmaxf(m[t][x], v);
+                    grew |= mn[t][x] > m[t][x];
+                }
+            }
+            if (__any_sync(0xffffffffu, grew)) {
+#pragma unroll
+                for (int t = 0; t < NT; ++t)
+#pragma unroll
+                    for (int x = 0; x < 2; ++x) {
+                        const float f = mn[t][x] == -INFINITY ? 1.f : exp2_of(m[t][x] - mn[t][x]);
+                        m[t][x] = mn[t][x];
+                        l[t][x] *= f;
+#pragma unroll
+                        for (int j = 0; j < kChunks; ++j) {
+                            o[t][j][x] *= f;
+                            o[t][j][x + 2] *= f;
+                        }
+                    }
+            }
+            uint32_t p0[NT], p1[NT];
+#pragma unroll
+            for (int t = 0; t < NT; ++t) {
+                float w[4];
+#pragma unroll
+                for (int x = 0; x < 4; ++x) {
+                    const float ref = m[t][x & 1] == -INFINITY ? 0.f : m[t][x & 1];
+                    w[x] = exp2_of(s[t][x] - ref);
+                    if (whole) l[t][x & 1] = fmaf(w[x], ivs, l[t][x & 1]);
+                    else if (s[t][x] != -INFINITY) l[t][x & 1] = fmaf(w[x], ivs, l[t][x & 1]);
+                }
+                p0[t] = transpose8x8(pack2<KVL_TYPE_HALF>(w[0], w[1]));
+                p1[t] = transpose8x8(pack2<KVL_TYPE_HALF>(w[2], w[3]));
+            }
+
+            // ---- O^T += V^T P^T: tokens 2kk, 2kk + 1, 2kk + 8, 2kk + 9, elements from nn * D/8 on
+            uint32_t vw[4][kLaneBytes / 4];
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                const int row = 2 * kk + (r & 1) + 8 * (r >> 1);
+                if constexpr (D == 64) {
+                    const uint2 x = *reinterpret_cast<const uint2 *>(vt + v_at<D>(row, nn >> 1) + 8 * (nn & 1));
+                    vw[r][0] = x.x; vw[r][1] = x.y;
+                } else {
+#pragma unroll
+                    for (int y = 0; y < D / 128; ++y) {
+                        const uint4 x = *reinterpret_cast<const uint4 *>(vt + v_at<D>(row, nn * (D / 128) + y));
+                        vw[r][4 * y] = x.x; vw[r][4 * y + 1] = x.y; vw[r][4 * y + 2] = x.z; vw[r][4 * y + 3] = x.w;
+                    }
+                }
+            }
+            // a NaN in a token that some rows do not see must not reach them through 0 * NaN
+            uint32_t nan_words = 0;
+            if (CODE == KVL_CODE_FLOAT && !whole) {
+#pragma unroll
+                for (int r = 0; r < 4; ++r)
+#pragma unroll
+                    for (int x = 0; x < kLaneBytes / 4; ++x)
+                        nan_words |= __vcmpeq4(vw[r][x] & 0x7f7f7f7fu, 0x7f7f7f7fu);
+            }
+            const bool has_nan = CODE == KVL_CODE_FLOAT && !whole && __any_sync(0xffffffffu, nan_words != 0);
+#pragma unroll
+            for (int x = 0; x < kLaneBytes / 4; ++x) {
+#pragma unroll
+                for (int y = 0; y < 2; ++y) {  // elements 4x + 2y, 4x + 2y + 1 of the lane's run
+                    const uint32_t u0 = __byte_perm(vw[0][x], vw[1][x], y ? 0x7362 : 0x5140);
+                    const uint32_t u1 = __byte_perm(vw[2][x], vw[3][x], y ? 0x7362 : 0x5140);
+                    uint32_t a0 = codes_lo<CODE>(u0), a1 = codes_hi<CODE>(u0), a2 = codes_lo<CODE>(u1), a3 = codes_hi<CODE>(u1);
+                    if (has_nan) {
+                        // NaN codes leave the product; a second one of NaN marks with the rows' view of
+                        // the tokens tells which results they belong to
+                        auto split = [](uint32_t &v) {
+                            uint32_t mark = 0;  // a converted NaN code has every exponent bit set
+                            if ((v & 0x7c00u) == 0x7c00u) mark |= 0xffffu;
+                            if ((v & 0x7c000000u) == 0x7c000000u) mark |= 0xffff0000u;
+                            v &= ~mark;
+                            return mark & 0x3c003c00u;  // 1.0
+                        };
+                        const uint32_t n0 = split(a0), n1 = split(a1), n2 = split(a2), n3 = split(a3);
+#pragma unroll
+                        for (int t = 0; t < NT; ++t) {
+                            uint32_t see[2];
+#pragma unroll
+                            for (int z = 0; z < 2; ++z) {
+                                const uint32_t v0 = s[t][2 * z] != -INFINITY ? 0x3c00u : 0u;
+                                const uint32_t v1 = s[t][2 * z + 1] != -INFINITY ? 0x3c000000u : 0u;
+                                see[z] = transpose8x8(v0 | v1);
+                            }
+                            float z[4] = {0.f, 0.f, 0.f, 0.f};
+                            mma16816(z, n0, n1, n2, n3, see[0], see[1]);
+#pragma unroll
+                            for (int q = 0; q < 4; ++q)
+                                if (z[q] > 0.f) o[t][2 * x + y][q] = NAN;
+                        }
+                    }
+#pragma unroll
+                    for (int t = 0; t < NT; ++t) mma16816(o[t][2 * x + y], a0, a1, a2, a3, p0[t], p1[t]);
+                }
+            }
+        }
+        copy_async_wait<0>();
+        __syncwarp();
+
+        // ---- join the warps
+        float *so = reinterpret_cast<float *>(smem + S::kQBytes + warp * S::kWarpBytes);
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+                float v = l[t][x];
+                v += __shfl_xor_sync(0xffffffffu, v, 4);
+                v += __shfl_xor_sync(0xffffffffu, v, 8);
+                v += __shfl_xor_sync(0xffffffffu, v, 16);
+                const int r = 8 * t + 2 * kk + x;
+                if (nn == 0) {
+                    s_m[warp][r] = m[t][x];
+                    s_l[warp][r] = v;
+                }
+                if (r < rows) {
+#pragma unroll
+                    for (int y = 0; y < kLaneBytes / 4; ++y)
+                        *reinterpret_cast<float4 *>(so + r * S::kORow + nn * kLaneBytes + 4 * y) =
+                            make_float4(o[t][2 * y][x], o[t][2 * y][x + 2], o[t][2 * y + 1][x], o[t][2 * y + 1][x + 2]);
+                }
+            }
+        }
+        __syncthreads();
+        const bool complete = ga == 0 && gb == c.groups;
+        auto finish = [&](int r, int e, float4 v, float big, float sum) {  // 4 elements of a row's result
+            if (e >= d) return;
+            const int row = tile * kRows + r;
+            const int64_t t = int64_t(c.e.row0) + row / G;
+            const int head = h * G + row % G;
+            const float inv = sum == 0.f ? 0.f : 1.f / sum;  // 0: the row sees nothing
+            uint8_t *dst = static_cast<uint8_t *>(a.attn.out.data) + t * a.attn.out.row_stride +
+                           int64_t(head) * a.attn.out.head_stride + 2 * e;
+            *reinterpret_cast<uint2 *>(dst) = make_uint2(pack2<TYPE>(v.x * inv, v.y * inv), pack2<TYPE>(v.z * inv, v.w * inv));
+            if (e == 0 && a.attn.lse)
+                a.attn.lse[t * a.attn.n_heads + head] = sum == 0.f ? -INFINITY : (big + __log2f(sum)) * (1.f / kLog2e);
+        };
+        float *part = a.parts + (int64_t(blockIdx.x) * 2 + (ga == 0 ? 1 : 0)) * S::kPartFloats;
+        for (int x = tid; x < rows * (D / 4); x += kThreads) {
+            const int r = x / (D / 4), e = (x % (D / 4)) * 4;
+            float big = -INFINITY;
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w) big = fmaxf(big, s_m[w][r]);
+            float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+            float sum = 0.f;
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w) {
+                const float f = s_m[w][r] == -INFINITY ? 0.f : exp2_of(s_m[w][r] - big);
+                const float4 y = *reinterpret_cast<const float4 *>(
+                    reinterpret_cast<const float *>(smem + S::kQBytes + w * S::kWarpBytes) + r * S::kORow + e);
+                v.x += y.x * f; v.y += y.y * f; v.z += y.z * f; v.w += y.w * f;
+                sum += s_l[w][r] * f;
+            }
+            if (complete) {
+                finish(r, e, v, big, sum);
+            } else {
+                *reinterpret_cast<float4 *>(part + 2 * kRows + r * D + e) = v;
+                if (e == 0) {
+                    part[r] = big;
+                    part[kRows + r] = sum;
+                }
+            }
+        }
+        if (!complete) {
+            // parts of this job: shares first .. last; the one that arrives last joins them
+            const int first = int(((job_u0 + 1) * shares - 1) / total);
+            const int last = int(((job_u0 + c.groups) * shares - 1) / total);
+            __threadfence();
+            __syncthreads();
+            if (tid == 0) s_last = atomicAdd(&a.counters[first], 1u) == uint32_t(last - first);
+            __syncthreads();
+            if (s_last) {
+                __threadfence();
+                if (tid == 0) a.counters[first] = 0;
+                for (int x = tid; x < rows * (D / 4); x += kThreads) {
+                    const int r = x / (D / 4), e = (x % (D / 4)) * 4;
+                    float big = -INFINITY;
+                    for (int b = first; b <= last; ++b)
+                        big = fmaxf(big, __ldcg(a.parts + (int64_t(b) * 2 + (b == first)) * S::kPartFloats + r));
+                    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+                    float sum = 0.f;
+#pragma unroll 4
+                    for (int b = first; b <= last; ++b) {
+                        const float *p = a.parts + (int64_t(b) * 2 + (b == first)) * S::kPartFloats;
+                        const float mb = __ldcg(p + r), lb = __ldcg(p + kRows + r);
+                        const float4 y = __ldcg(reinterpret_cast<const float4 *>(p + 2 * kRows + r * D + e));
+                        const float f = mb == -INFINITY ? 0.f : exp2_of(mb - big);
+                        v.x += y.x * f; v.y += y.y * f; v.z += y.z * f; v.w += y.w * f;
+                        sum += lb * f;
+                    }
+                    finish(r, e, v, big, sum);
+                }
+            }
+        }
+        __syncthreads();  // Q, the rings and the joined results are free again
+        off += gb - ga;
+        u += gb - ga;
+    }
+}
+
+template <int CODE, int TYPE, int D, int NT>
+kvl_status launch_rows(const AttendArgs &a, int sms, void *stream)
+{
+    static std::atomic<unsigned long long> ready[kMaxDevices];
+    if (!allow_smem(attend_rows_kernel<CODE, TYPE, D, NT>, ready, Shape<D, NT>::kSmem)) return KVL_ECUDA;
+    attend_rows_kernel<CODE, TYPE, D, NT><<<sms * kCtasPerSm, kThreads, Shape<D, NT>::kSmem, static_cast<cudaStream_t>(stream)>>>(a);
+    return launch_status();
+}
+
+template <int CODE, int TYPE>
+kvl_status launch_rows_dim(const AttendArgs &a, int sms, void *stream)
+{
+    if (a.cache.head_dim <= 64) return launch_rows<CODE, TYPE, 64, 1>(a, sms, stream);
+    if (a.cache.head_dim <= 128) return launch_rows<CODE, TYPE, 128, 1>(a, sms, stream);
+    return launch_rows<CODE, TYPE, 256, 1>(a, sms, stream);
+}
+
+}  // namespace
+
+size_t attend_rows_part_bytes(int head_dim)
+{
+    const int D = head_dim <= 64 ? 64 : head_dim <= 128 ? 128 : 256;
+    return size_t(2) * kCtasPerSm * (8 * (D + 2)) * sizeof(float);
+}
+
+kvl_status launch_attend_rows(const AttendArgs &a, int sms, void *stream)
+{
+    const bool bf = a.attn.type == KVL_TYPE_BFLOAT;
+    if (a.cache.code_type == KVL_CODE_FLOAT)
+        return bf ? launch_rows_dim<KVL_CODE_FLOAT, KVL_TYPE_BFLOAT>(a, sms, stream)
+                  : launch_rows_dim<KVL_CODE_FLOAT, KVL_TYPE_HALF>(a, sms, stream);
+    return bf ? launch_rows_dim<KVL_CODE_INT, KVL_TYPE_BFLOAT>(a, sms, stream)
+              : launch_rows_dim<KVL_CODE_INT, KVL_TYPE_HALF>(a, sms, stream);
+}
+
+}  // namespace kvl
