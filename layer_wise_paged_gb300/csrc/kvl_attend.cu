@@ -7,6 +7,10 @@
 namespace kvl {
 namespace {
 
+// Entries with more rows than this (fresh tokens x query heads of a KV head) go to the tensor-memory
+// kernel.
+constexpr int kChunkRows = 64;
+
 // SMs the workspace is sized for (a host without a device sizes it for a GB300).
 int workspace_sms()
 {
@@ -22,7 +26,8 @@ using namespace kvl;
 extern "C" size_t kvl_attend_workspace_bytes(const kvl_cache *cache)
 {
     if (check_cache(cache) != KVL_OK) return 0;
-    return KVL_ATTEND_ZERO_BYTES + size_t(workspace_sms()) * attend_rows_part_bytes(cache->head_dim);
+    const size_t rows = attend_rows_part_bytes(cache->head_dim), chunk = attend_chunk_part_bytes(cache->head_dim);
+    return KVL_ATTEND_ZERO_BYTES + size_t(workspace_sms()) * (rows > chunk ? rows : chunk);
 }
 
 extern "C" kvl_status kvl_attend(const kvl_cache *cache, int32_t layer, const kvl_sequences *seqs,
@@ -53,5 +58,16 @@ extern "C" kvl_status kvl_attend(const kvl_cache *cache, int32_t layer, const kv
     a.counters = static_cast<uint32_t *>(d_workspace);
     a.parts = reinterpret_cast<float *>(static_cast<uint8_t *>(d_workspace) + KVL_ATTEND_ZERO_BYTES);
     a.report = d_report;
-    return launch_attend_rows(a, sms, stream);
+    // Which kernel an entry is worked by depends on its rows alone; the bound on them only tells
+    // which launches can be left out.
+    const int64_t bound = attn->max_new > 0 && attn->max_new < seqs->n_rows ? attn->max_new : seqs->n_rows;
+    const int64_t most = bound * (attn->n_heads / cache->n_kv_heads);
+    if (cache->head_dim > 128 || most <= kChunkRows) return launch_attend_rows(a, sms, stream);
+    if (seqs->n_seq == 1) {
+        a.max_rows = 0;
+        return launch_attend_chunk(a, sms, stream);
+    }
+    a.max_rows = kChunkRows;
+    s = launch_attend_chunk(a, sms, stream);
+    return s ? s : launch_attend_rows(a, sms, stream);
 }

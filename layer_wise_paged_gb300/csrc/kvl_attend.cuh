@@ -23,7 +23,8 @@ struct AttendArgs {
     kvl_sequences seqs;
     kvl_attention attn;
     int32_t layer;
-    int32_t max_rows;  // entries with more (rows x heads of a group) belong to the other kernel
+    int32_t max_rows;  // entries with at most so many rows (fresh tokens x query heads of a KV head) are
+                       // attend_rows', the others attend_chunk's
     uint32_t *counters;
     float *parts;      // partial results of rows split over CTAs
     void *report;
@@ -64,5 +65,7 @@ __device__ __forceinline__ float v_scale(float s) { return s < kTinyScale ? kTin
 
 size_t attend_rows_part_bytes(int head_dim);  // for each SM
 kvl_status launch_attend_rows(const AttendArgs &a, int sms, void *stream);
+size_t attend_chunk_part_bytes(int head_dim);
+kvl_status launch_attend_chunk(const AttendArgs &a, int sms, void *stream);
 
 }  // namespace kvl

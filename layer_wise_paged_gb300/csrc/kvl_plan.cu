@@ -629,7 +629,7 @@ extern "C" int32_t kvl_launches_per_call(int32_t which)
     case 0: return 2;  // plan: scan + fill
     case 1: case 2: case 3: return 1;
     case 4: case 5: return 1;           // rotary, append
-    case 6: return 1;                   // attend
+    case 6: return 2;                   // attend: chunks, rows
     case 7: case 8: case 9: return 1;   // pages extend, fork, free
     case 10: return 2;                  // compact: counts, then tables
     case 11: return 1;                  // copy
