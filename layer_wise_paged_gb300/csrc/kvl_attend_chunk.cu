@@ -32,10 +32,12 @@ constexpr int kPlaces = 4;                  // steps whose scales are kept (see 
 constexpr int kStepsPerCta = 2;             // a share is at least this many steps
 constexpr float kSlack = 8.f;               // log2 of the largest weight before O is rescaled
 
-// Scales and places of a step's groups.
+// Scales and places of a step's groups; partial[w]: some row sees only a part of the two groups that
+// converting warp w filled.
 struct Places {
     float ks[kGroups], lvs[kGroups], ivs[kGroups];
     int32_t t0[kGroups], nv[kGroups];
+    int32_t partial[4];
 };
 
 template <int D>
@@ -343,12 +345,14 @@ __global__ void __launch_bounds__(kThreads, 1) attend_chunk_kernel(const __grid_
             const int cw = warp - 8;
             constexpr int kLanes = D / 16, kPer = 32 / kLanes, kVecs = 32 / kPer;  // 32 slots a warp
             const int ch = lane % kLanes, rw = lane / kLanes;
-            // the warp's two groups of step s: this lane's is the one of its half of the lanes
+            // Lane l looks after group l % 2 of the warp's two in step l / 2 of a batch of 16 steps: its
+            // page, place and scales.  The next batch's are fetched while this one is worked on, so
+            // no step waits for a table entry or a scale.
             auto place = [&](int s, int &t0, int &nv) -> int32_t {
                 t0 = 0;
                 nv = 0;
-                const int g = t.g0 + s * kGroups + cw * 2 + (lane >> 4);
-                if (g >= t.g1 || s >= sb) return -1;
+                const int g = t.g0 + (sa + s) * kGroups + cw * 2 + (lane & 1);
+                if (g >= t.g1 || s >= n) return -1;
                 const int blk = g / per_block, slot = (g - blk * per_block) * kGroup;
                 t0 = blk * B + slot;
                 nv = min(min(kGroup, B - slot), sh.e.len - t0);
@@ -361,18 +365,37 @@ __global__ void __launch_bounds__(kThreads, 1) attend_chunk_kernel(const __grid_
                 }
                 return page;
             };
+            auto scales = [&](int32_t page, float &ks, float &vs) {
+                ks = 0.f;
+                vs = 1.f;
+                if (page >= 0) {
+                    ks = __ldg(a.cache.scales + (plane + page) * H + h);
+                    vs = v_scale(__ldg(a.cache.scales + (plane + N + page) * H + h));
+                }
+            };
+            int t0, nv, t0n, nvn;
+            int32_t page = place(lane >> 1, t0, nv), page_n = place(16 + (lane >> 1), t0n, nvn);
+            float ks, vs, ksn = 0.f, vsn = 1.f;
+            scales(page, ks, vs);
             uint4 kreg[kVecs], vreg[kVecs];
-            auto fetch = [&](uint4 (&reg)[kVecs], int32_t page, int t0, int nv, bool v) {
+            auto fetch = [&](uint4 (&reg)[kVecs], int s, int base, bool v) {  // step s's codes, of this batch or the next
+                const bool ahead = s - base >= 16;
+                const uint8_t *half[2];
+                int valid[2];
+#pragma unroll
+                for (int y = 0; y < 2; ++y) {
+                    const int from = ((s & 15) << 1) | y;
+                    const int32_t pg = __shfl_sync(0xffffffffu, ahead ? page_n : page, from);
+                    const int tt = __shfl_sync(0xffffffffu, ahead ? t0n : t0, from);
+                    valid[y] = __shfl_sync(0xffffffffu, ahead ? nvn : nv, from);
+                    if (ch * 16 >= d) valid[y] = 0;
+                    half[y] = codes + (v ? v_plane_bytes : 0) + (((plane + max(pg, 0)) * B + tt % B) * H + h) * d + ch * 16;
+                }
 #pragma unroll
                 for (int x = 0; x < kVecs; ++x) {
-                    const int r = x * kPer + rw;  // of the warp's 32 slots
-                    const int from = (r >> 4) << 4;
-                    const int32_t pg = __shfl_sync(0xffffffffu, page, from);
-                    const int tt = __shfl_sync(0xffffffffu, t0, from), nn = __shfl_sync(0xffffffffu, nv, from);
+                    const int r = (x % (kVecs / 2)) * kPer + rw, y = x / (kVecs / 2);  // slot r of the warp's group y
                     reg[x] = make_uint4(0, 0, 0, 0);
-                    if ((r & 15) < nn && ch * 16 < d)
-                        reg[x] = __ldg(reinterpret_cast<const uint4 *>(
-                            codes + (v ? v_plane_bytes : 0) + (((plane + pg) * B + tt % B + (r & 15)) * H + h) * d + ch * 16));
+                    if (r < valid[y]) reg[x] = __ldg(reinterpret_cast<const uint4 *>(half[y] + int64_t(r) * H * d));
                 }
             };
             auto convert = [&](const uint4 (&reg)[kVecs], uint8_t *dst) {
@@ -389,62 +412,59 @@ __global__ void __launch_bounds__(kThreads, 1) attend_chunk_kernel(const __grid_
                     *reinterpret_cast<uint4 *>(p + (((un + 1) ^ (r & 7)) << 4)) = hi;
                 }
             };
-            int t0, nv;
-            int32_t page = place(sa, t0, nv);
-            fetch(kreg, page, t0, nv, false);
-            bool ok = true;
-            for (int s = 0; s < n && ok; ++s) {
-                const uint32_t k = it + s, st = k % kStages, ph = (k / kStages) & 1;
-                // V of this step on its way while K is converted
-                fetch(vreg, page, t0, nv, true);
-                const bool whole_l = nv == kGroup && t0 >= t.all_lo && t0 + kGroup <= t.all_hi;
-                const bool whole = __all_sync(0xffffffffu, whole_l);
-                float ks = 0.f, vs = 1.f;
-                if (page >= 0 && (lane & 15) == 0) {
-                    ks = __ldg(a.cache.scales + (plane + page) * H + h);
-                    vs = v_scale(__ldg(a.cache.scales + (plane + N + page) * H + h));
+            fetch(kreg, 0, 0, false);
+            fetch(vreg, 0, 0, true);
+            int base = 0;
+            for (int s = 0; s < n; ++s) {
+                if (s - base == 16) {
+                    base += 16;
+                    page = page_n; t0 = t0n; nv = nvn; ks = ksn; vs = vsn;
+                    page_n = place(base + 16 + (lane >> 1), t0n, nvn);
                 }
-                int t0n, nvn;
-                const int32_t page_n = place(sa + s + 1, t0n, nvn);
-                if (!(ok = wait_bar(bar + 8 * (K_EMPTY + st), ph ^ 1, gone))) break;
-                if ((lane & 15) == 0) {
-                    Places &pl = places[k % kPlaces];
-                    const int g = cw * 2 + (lane >> 4);
+                if (s - base == 4) scales(page_n, ksn, vsn);
+                const uint32_t k = it + s, st = k % kStages, ph = (k / kStages) & 1;
+                const int two_lanes = (s & 15) << 1;
+                const bool here = (lane & ~1) == two_lanes;
+                const bool partial = __any_sync(0xffffffffu, here && !(nv == kGroup && t0 >= t.all_lo && t0 + kGroup <= t.all_hi));
+                if (!wait_bar(bar + 8 * (K_EMPTY + st), ph ^ 1, gone)) break;
+                Places &pl = places[k % kPlaces];
+                if (here) {
+                    const int g = cw * 2 + (lane & 1);
                     pl.ks[g] = ks;
                     pl.lvs[g] = __log2f(vs);
                     pl.ivs[g] = __fdividef(1.f, vs);
                     pl.t0[g] = t0;
                     pl.nv[g] = nv;
+                    pl.partial[cw] = partial;
                 }
                 convert(kreg, smem + C::kK + st * C::kTileBytes);
                 fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(bar + 8 * (K_FULL + st));
-                fetch(kreg, page_n, t0n, nvn, false);
-                if (CODE == KVL_CODE_FLOAT && !whole) {
+                if (s + 1 < n) fetch(kreg, s + 1, base, false);
+                if (CODE == KVL_CODE_FLOAT && partial) {
                     // NaN codes of a step that some rows see in part would reach the others as 0 * NaN:
                     // they leave the products here and come back where the rows are written
                     uint32_t any = 0;
 #pragma unroll
                     for (int x = 0; x < kVecs; ++x) {
-                        uint32_t *w = reinterpret_cast<uint32_t *>(&vreg[x]);
+                        uint32_t w[4] = {vreg[x].x, vreg[x].y, vreg[x].z, vreg[x].w};
 #pragma unroll
                         for (int y = 0; y < 4; ++y) {
                             const uint32_t bad = __vcmpeq4(w[y] & 0x7f7f7f7fu, 0x7f7f7f7fu);
                             any |= bad;
                             w[y] &= ~bad;
                         }
+                        vreg[x] = make_uint4(w[0], w[1], w[2], w[3]);
                     }
                     if (any) s_nan = 1;
                 }
-                if (!(ok = wait_bar(bar + 8 * (V_EMPTY + st), ph ^ 1, gone))) break;
+                if (!wait_bar(bar + 8 * (V_EMPTY + st), ph ^ 1, gone)) break;
                 convert(vreg, smem + C::kV + st * C::kTileBytes);
                 fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(bar + 8 * (V_FULL + st));
-                page = page_n;
-                t0 = t0n;
-                nv = nvn;
+                if (s + 1 < n) fetch(vreg, s + 1, base, true);
             }
         } else if (warp == 12) {
             // ---- issue the products
@@ -502,6 +522,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_chunk_kernel(const __grid_
             int lo = a.attn.window > 0 ? max(0, pos - a.attn.window + 1) : 0;
             if (r >= t.rows) { lo = t.all_lo; hi = t.all_hi; }
             const float cq = s_cq[r];
+            constexpr uint32_t kHidden = 0xff800000u;  // -infinity
             bool ok = true;
             for (int s = 0; s < n; ++s) {
                 const uint32_t ph = (it_g[g] + s) & 1;
@@ -509,29 +530,32 @@ __global__ void __launch_bounds__(kThreads, 1) attend_chunk_kernel(const __grid_
                 if (!ok) break;
                 tmem_fence_after();
                 const Places &pl = places[(it + s) % kPlaces];
-                // the step's largest x
-                float big = -INFINITY;
-                bool whole = true;
+                auto hide = [&](uint32_t (&x)[32], int gi) {  // scores of groups gi, gi + 1 that the row does not see
 #pragma unroll
+                    for (int y = 0; y < 2; ++y) {
+                        const int first = max(lo - pl.t0[gi + y], 0), past = min(hi - pl.t0[gi + y], pl.nv[gi + y]);
+#pragma unroll
+                        for (int e = 0; e < 16; ++e)
+                            if (e < first || e >= past) x[16 * y + e] = kHidden;
+                    }
+                };
+                const bool whole = !(pl.partial[0] | pl.partial[1] | pl.partial[2] | pl.partial[3]);
+                // the step's largest x: scales are not negative, so a group's largest comes from its
+                // largest score
+                float big = -INFINITY;
+#pragma unroll 1
                 for (int c = 0; c < 4; ++c) {
                     uint32_t x[32];
                     tmem_ld32(ts + 32 * c, x);
                     tmem_wait_ld();
+                    if (!whole) hide(x, 2 * c);
 #pragma unroll
                     for (int y = 0; y < 2; ++y) {
-                        const int gi = 2 * c + y, t0 = pl.t0[gi], nv = pl.nv[gi];
-                        const float f = pl.ks[gi] * cq, b = pl.lvs[gi];
-                        float top = -INFINITY;
-                        if (__all_sync(0xffffffffu, nv == kGroup && t0 >= lo && t0 + kGroup <= hi)) {
+                        float top = __uint_as_float(x[16 * y]);
 #pragma unroll
-                            for (int e = 0; e < 16; ++e) top = fmaxf(top, fmaf(__uint_as_float(x[16 * y + e]), f, b));
-                        } else {
-                            whole = false;
-#pragma unroll
-                            for (int e = 0; e < 16; ++e)
-                                if (e < nv && t0 + e >= lo && t0 + e < hi) top = fmaxf(top, fmaf(__uint_as_float(x[16 * y + e]), f, b));
-                        }
-                        big = fmaxf(big, top);
+                        for (int e = 1; e < 16; ++e) top = fmaxf(top, __uint_as_float(x[16 * y + e]));
+                        const float z = fmaf(top, pl.ks[2 * c + y] * cq, pl.lvs[2 * c + y]);
+                        if (top != -INFINITY) big = fmaxf(big, z);
                     }
                 }
                 const bool grow = big > row_m + kSlack || (row_m == -INFINITY && big > -INFINITY);
@@ -556,35 +580,29 @@ __global__ void __launch_bounds__(kThreads, 1) attend_chunk_kernel(const __grid_
                     }
                 }
                 const float ref = row_m == -INFINITY ? 0.f : row_m;
-#pragma unroll
+#pragma unroll 1
                 for (int c = 0; c < 4; ++c) {
                     uint32_t x[32], p[16];
                     tmem_ld32(ts + 32 * c, x);
                     tmem_wait_ld();
+                    if (!whole) hide(x, 2 * c);
 #pragma unroll
                     for (int y = 0; y < 2; ++y) {
-                        const int gi = 2 * c + y;
-                        const float f = pl.ks[gi] * cq, b = pl.lvs[gi] - ref, iv = pl.ivs[gi];
-                        float w[16];
-                        if (whole) {
+                        const float f = pl.ks[2 * c + y] * cq, b = pl.lvs[2 * c + y] - ref;
+                        float sum = 0.f;
 #pragma unroll
-                            for (int e = 0; e < 16; ++e) {
-                                w[e] = exp2_of(fmaf(__uint_as_float(x[16 * y + e]), f, b));
-                                row_l = fmaf(w[e], iv, row_l);
+                        for (int e = 0; e < 16; e += 2) {
+                            // a hidden score is -infinity: its weight has to be 0 whatever f and b are
+                            float w0 = exp2_of(fmaf(__uint_as_float(x[16 * y + e]), f, b));
+                            float w1 = exp2_of(fmaf(__uint_as_float(x[16 * y + e + 1]), f, b));
+                            if (!whole) {
+                                if (x[16 * y + e] == kHidden) w0 = 0.f;
+                                if (x[16 * y + e + 1] == kHidden) w1 = 0.f;
                             }
-                        } else {
-                            const int t0 = pl.t0[gi], nv = pl.nv[gi];
-#pragma unroll
-                            for (int e = 0; e < 16; ++e) {
-                                w[e] = 0.f;
-                                if (e < nv && t0 + e >= lo && t0 + e < hi) {
-                                    w[e] = exp2_of(fmaf(__uint_as_float(x[16 * y + e]), f, b));
-                                    row_l = fmaf(w[e], iv, row_l);
-                                }
-                            }
+                            sum += w0 + w1;
+                            p[8 * y + e / 2] = pack2<KVL_TYPE_HALF>(w0, w1);
                         }
-#pragma unroll
-                        for (int e = 0; e < 8; ++e) p[8 * y + e] = pack2<KVL_TYPE_HALF>(w[2 * e], w[2 * e + 1]);
+                        if (sum != 0.f) row_l = fmaf(sum, pl.ivs[2 * c + y], row_l);
                     }
                     tmem_st16(ts + 16 * c, p);
                 }
