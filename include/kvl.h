@@ -471,6 +471,7 @@ kvl_status kvl_cache_append(const kvl_cache *cache, int32_t layer, const kvl_seq
  * A row that sees nothing gets out = 0 and lse = -infinity.  Cached bytes that no row sees
  * (slots past lens, pages past the sequence's end) are never part of a result, whatever they
  * hold.  Statistics and sums are held in 32 bits, probabilities enter the products in 16.
+ * n_rows * (n_heads / H) is below 2^31 - 256.
  *   max_new   0, or a bound on the fresh rows of any entry that the caller knows; it chooses
  *             kernels, results do not depend on it */
 typedef struct kvl_attention {

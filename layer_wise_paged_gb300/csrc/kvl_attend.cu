@@ -42,6 +42,7 @@ extern "C" kvl_status kvl_attend(const kvl_cache *cache, int32_t layer, const kv
         (attn->type != KVL_TYPE_BFLOAT && attn->type != KVL_TYPE_HALF) || !(attn->sm_scale > 0.f && attn->sm_scale < INFINITY) ||
         (attn->causal & ~1) || attn->window < 0 || (attn->window > 0 && !attn->causal) || attn->max_new < 0)
         return KVL_EINVAL;
+    if (seqs->n_rows * (attn->n_heads / cache->n_kv_heads) > INT32_MAX - 256) return KVL_EINVAL;
     if (bad_report(d_report)) return KVL_EALIGN;
     if (seqs->n_seq == 0 || seqs->n_rows == 0) return KVL_OK;
     if ((s = check_rows(&attn->q)) || (s = check_rows(&attn->out))) return s;

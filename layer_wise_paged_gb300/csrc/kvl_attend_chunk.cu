@@ -22,15 +22,20 @@
 namespace kvl {
 namespace {
 
-constexpr int kThreads = 512;
+constexpr int kThreads = 384;  // 8 softmax warps, 4 converting: 168 registers a thread
 constexpr int kTileRows = 128;
 constexpr int kJobRows = 2 * kTileRows;
 constexpr int kSlots = 128;                 // slots of a step
 constexpr int kGroups = kSlots / kGroup;    // 8
 constexpr int kStages = 2;
 constexpr int kPlaces = 4;                  // steps whose scales are kept (see place_full)
+constexpr int kBatch = 512;                 // entries whose steps are held at a time
 constexpr int kStepsPerCta = 2;             // a share is at least this many steps
-constexpr float kSlack = 8.f;               // log2 of the largest weight before O is rescaled
+// A row's reference is set kHead above its largest x so far and moved only when an x passes it by
+// kSlack: weights up to 2^14 are halves still, and those below 2^-14 keep 2^-25 of the largest
+// weight's 2^-4 or more.  With the reference at the maximum and a slack of 8, one of a warpgroup's
+// 128 rows moved in most steps and held the others up for 1,000 cycles.
+constexpr float kSlack = 14.f, kHead = 4.f;
 
 // Scales and places of a step's groups; partial[w]: some row sees only a part of the two groups that
 // converting warp w filled.
@@ -51,7 +56,7 @@ struct Chunk {
 };
 
 // Barriers (each in its own 8 bytes).
-enum Bar { K_FULL = 0, K_EMPTY = 2, V_FULL = 4, V_EMPTY = 6, S_FULL = 8, P_FULL = 10, PV_DONE = 12, BARS = 14 };
+enum Bar { K_FULL = 0, K_EMPTY = 2, V_FULL = 4, V_EMPTY = 6, S_FULL = 8, P_FULL = 10, PV_DONE = 12, TURN = 14, LEAVE = 16, BARS = 17 };
 
 // ---- tensor-core wrappers -------------------------------------------------------------------
 
@@ -70,25 +75,42 @@ __host__ __device__ constexpr uint32_t instr_desc(int n, bool b_mn)
     return (1u << 4) | (uint32_t(b_mn) << 16) | (uint32_t(n >> 3) << 17) | (uint32_t(kTileRows >> 4) << 24);
 }
 
-__device__ __forceinline__ void mma_smem(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool add)
+// One lane of a converged warp, the same one every time.
+__device__ __forceinline__ uint32_t elect_one()
+{
+    uint32_t r;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+    return r;
+}
+
+// Products are issued by a whole warp of which one lane (`one`) is elected: addresses and descriptors
+// stay uniform, so that they are kept in uniform registers and an issue takes few instructions.
+// Computed by a lone lane, each product cost 100 to 160 cycles of issue where it runs for 64.
+__device__ __forceinline__ void mma_smem(uint32_t one, uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool add)
 {
     asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(uint32_t(add))
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d), "l"(a), "l"(b), "r"(idesc),
+        "r"(uint32_t(add)), "r"(one)
         : "memory");
 }
 
-__device__ __forceinline__ void mma_tmem(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool add)
+__device__ __forceinline__ void mma_tmem(uint32_t one, uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool add)
 {
     asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d), "r"(a), "l"(b), "r"(idesc), "r"(uint32_t(add))
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d), "r"(a), "l"(b), "r"(idesc),
+        "r"(uint32_t(add)), "r"(one)
         : "memory");
 }
 
-__device__ __forceinline__ void mma_commit(uint32_t bar)
+// Arrives on the barrier when the products that the elected lane has issued so far have ended.
+__device__ __forceinline__ void mma_commit(uint32_t one, uint32_t bar)
 {
-    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+    asm volatile(
+        "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %1, 0;\n\t"
+        "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(bar), "r"(one)
+        : "memory");
 }
 
 __device__ __forceinline__ void tmem_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
@@ -109,16 +131,18 @@ __device__ __forceinline__ void tmem_ld32(uint32_t at, uint32_t (&r)[32])
         : "r"(at));
 }
 
-__device__ __forceinline__ void tmem_st32(uint32_t at, const uint32_t (&r)[32])
+__device__ __forceinline__ void tmem_ld8(uint32_t at, uint32_t (&r)[8])
 {
-    asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
-        "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31};" ::"r"(r[0]),
-        "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]),
-        "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]),
-        "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]),
-        "r"(r[29]), "r"(r[30]), "r"(r[31]), "r"(at)
-        : "memory");
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+                 : "r"(at));
+}
+
+__device__ __forceinline__ void tmem_st8(uint32_t at, const uint32_t (&r)[8])
+{
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%8], {%0,%1,%2,%3,%4,%5,%6,%7};" ::"r"(r[0]), "r"(r[1]), "r"(r[2]),
+                 "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(at)
+                 : "memory");
 }
 
 __device__ __forceinline__ void tmem_st16(uint32_t at, const uint32_t (&r)[16])
@@ -130,14 +154,43 @@ __device__ __forceinline__ void tmem_st16(uint32_t at, const uint32_t (&r)[16])
         : "memory");
 }
 
-// Bounded wait that also leaves when another role has given up.
+// Two floats in one register pair, and arithmetic on both at once.
+__device__ __forceinline__ uint64_t pair_of(float x, float y)
+{
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(x), "f"(y));
+    return r;
+}
+__device__ __forceinline__ float2 split_pair(uint64_t x)
+{
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(x));
+    return r;
+}
+__device__ __forceinline__ uint64_t fma_pair(uint64_t a, uint64_t b, uint64_t c)
+{
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ uint64_t add_pair(uint64_t a, uint64_t b)
+{
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+
+// Bounded wait that also leaves when another role has given up.  The limit (kWaitLimitNs at the
+// highest clock) is looked at every 256 tries: reading the global timer on the way in cost up to a
+// thousand cycles after the barrier had completed.
 __device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, volatile int *gone)
 {
     if (mbar_try_wait(bar, parity)) return true;
-    const unsigned long long t0 = global_ns();
-    while (!mbar_try_wait(bar, parity)) {
+    const long long t0 = clock64();
+    for (uint32_t tries = 1; !mbar_try_wait(bar, parity); ++tries) {
+        if (tries & 255) continue;
         if (*gone) return false;
-        if (global_ns() - t0 > kWaitLimitNs) {
+        if (clock64() - t0 > 2 * static_cast<long long>(kWaitLimitNs)) {
             *gone = 1;
             return false;
         }
@@ -155,16 +208,17 @@ struct Tile {
     int32_t all_lo, all_hi;  // tokens every row sees
 };
 
-__device__ __forceinline__ Tile tile_of(const AttendArgs &a, const Entry &e, int tile)
+__device__ __forceinline__ Tile tile_of(const AttendArgs &a, int32_t len, int32_t fresh, int tile)
 {
     const int B = a.cache.block_tokens, per_block = (B + kGroup - 1) / kGroup, G = a.attn.n_heads / a.cache.n_kv_heads;
     Tile t;
-    t.rows = int32_t(min(int64_t(kJobRows), int64_t(e.fresh) * G - int64_t(tile) * kJobRows));
-    const int pos0 = e.len - e.fresh;
-    const int first = pos0 + int(int64_t(tile) * kJobRows / G), last = pos0 + int((int64_t(tile) * kJobRows + t.rows - 1) / G);
-    const int hi = a.attn.causal ? min(e.len, last + 1) : e.len;
+    const uint32_t row0 = uint32_t(tile) * kJobRows;
+    t.rows = min(kJobRows, int32_t(uint32_t(fresh) * G - row0));
+    const int pos0 = len - fresh;
+    const int first = pos0 + int(row0 / uint32_t(G)), last = pos0 + int((row0 + t.rows - 1) / uint32_t(G));
+    const int hi = a.attn.causal ? min(len, last + 1) : len;
     const int lo = a.attn.window > 0 ? max(0, first - a.attn.window + 1) : 0;
-    t.all_hi = a.attn.causal ? min(e.len, first + 1) : e.len;
+    t.all_hi = a.attn.causal ? min(len, first + 1) : len;
     t.all_lo = a.attn.window > 0 ? max(0, last - a.attn.window + 1) : 0;
     t.g0 = t.g1 = 0;
     if (hi > lo) {
@@ -175,21 +229,88 @@ __device__ __forceinline__ Tile tile_of(const AttendArgs &a, const Entry &e, int
     return t;
 }
 
-struct Share {
+__device__ __forceinline__ int32_t tiles_of(const AttendArgs &a, const Entry &e)
+{
+    const int32_t rows = e.fresh * (a.attn.n_heads / a.cache.n_kv_heads);  // the host has bounded n_rows
+    return rows > a.max_rows ? (rows + kJobRows - 1) / kJobRows : 0;
+}
+
+// Steps of one KV head of an entry, all tiles: a warp's lanes take a tile each.
+__device__ __forceinline__ int64_t warp_steps(const AttendArgs &a, int32_t len, int32_t fresh, int32_t tiles, int lane)
+{
+    int64_t n = 0;
+    for (int t = lane; t < tiles; t += 32) n += tile_of(a, len, fresh, t).steps;
+#pragma unroll
+    for (int o = 16; o; o >>= 1) n += __shfl_xor_sync(0xffffffffu, n, o);
+    return n;
+}
+
+// Where a CTA stands in its share, and the job it works on: in shared memory, so that the roles' loops
+// hold only what they use in registers.
+struct Job {
+    int64_t u, u_end, off;    // next unit, the share's end, units of the entry before u
+    int64_t total, shares;
+    int64_t row_base, u0;     // the tile's first row, the job's first unit
     Entry e;
-    int32_t tiles;
-    int64_t steps;  // of one KV head, all tiles
+    Tile t;
+    int32_t entry, h, sa, n;  // KV head; steps [sa, sa + n) of the tile
+    int32_t pos0;             // position of the entry's first fresh row
+    int32_t two;              // the second half tile has rows
+    uint32_t it, it_g[2];     // steps done by this CTA, and of each half tile: the barriers' phases
+    bool complete;            // the share holds the whole job
 };
 
-__device__ __forceinline__ Share share_of(const AttendArgs &a, int i, void *rep)
+// The job that holds unit job.u; called by one whole warp.
+__device__ __forceinline__ void next_job(const AttendArgs &a, Job &job, int lane)
 {
-    Share s;
-    s.e = load_entry(a.seqs, a.cache.block_tokens, i, rep);
-    const int64_t rows = int64_t(s.e.fresh) * (a.attn.n_heads / a.cache.n_kv_heads);
-    s.tiles = rows > a.max_rows ? int32_t((rows + kJobRows - 1) / kJobRows) : 0;
-    s.steps = 0;
-    for (int t = 0; t < s.tiles; ++t) s.steps += tile_of(a, s.e, t).steps;
-    return s;
+    const int H = a.cache.n_kv_heads, B = a.cache.block_tokens;
+    int64_t off = job.off;
+    int entry = job.entry;
+    Entry e = load_entry(a.seqs, B, entry, nullptr);
+    int32_t tiles = tiles_of(a, e);
+    int64_t steps = warp_steps(a, e.len, e.fresh, tiles, lane);
+    while (off >= H * steps) {
+        off -= H * steps;
+        e = load_entry(a.seqs, B, ++entry, nullptr);
+        tiles = tiles_of(a, e);
+        steps = warp_steps(a, e.len, e.fresh, tiles, lane);
+    }
+    const int h = int(off / steps);
+    int64_t rest = off - h * steps;
+    // the tile whose steps hold `rest`: 32 tiles at a time
+    int tile = 0;
+    for (int base = 0; base < tiles; base += 32) {
+        const int n = base + lane < tiles ? tile_of(a, e.len, e.fresh, base + lane).steps : 0;
+        int sum = n;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int y = __shfl_up_sync(0xffffffffu, sum, o);
+            if (lane >= o) sum += y;
+        }
+        const unsigned past = __ballot_sync(0xffffffffu, rest < sum);
+        if (past) {
+            const int l = __ffs(past) - 1;
+            tile = base + l;
+            rest -= __shfl_sync(0xffffffffu, sum - n, l);
+            break;
+        }
+        rest -= __shfl_sync(0xffffffffu, sum, 31);
+    }
+    if (lane == 0) {
+        const Tile t = tile_of(a, e.len, e.fresh, tile);
+        job.off = off;
+        job.entry = entry;
+        job.e = e;
+        job.t = t;
+        job.h = h;
+        job.sa = int(rest);
+        job.n = int(min(int64_t(t.steps) - rest, job.u_end - job.u));
+        job.u0 = job.u - rest;
+        job.row_base = int64_t(tile) * kJobRows;
+        job.pos0 = e.len - e.fresh;
+        job.two = t.rows > kTileRows;
+        job.complete = job.n == t.steps;
+    }
 }
 
 template <int CODE, int TYPE, int D>
@@ -200,48 +321,67 @@ __global__ void __launch_bounds__(kThreads, 1) attend_chunk_kernel(const __grid_
     __shared__ __align__(8) unsigned long long bars[BARS];
     __shared__ Places places[kPlaces];
     __shared__ float s_cq[kJobRows];
-    __shared__ int64_t s_scan[kThreads / 32], s_off;
-    __shared__ int s_entry, s_last, s_gone, s_nan;
+    __shared__ uint32_t s_steps[kBatch];
+    __shared__ Job job;
+    __shared__ int s_last, s_gone, s_nan;
     __shared__ uint32_t s_tmem;
 
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
     const int H = a.cache.n_kv_heads, d = a.cache.head_dim, B = a.cache.block_tokens;
     const int G = a.attn.n_heads / H, per_block = (B + kGroup - 1) / kGroup;
     const int64_t N = a.cache.pool_blocks;
 
-    // ---- this CTA's share of the steps
-    const int n_seq = a.seqs.n_seq, per_thread = (n_seq + kThreads - 1) / kThreads;
-    const int i0 = min(n_seq, tid * per_thread), i1 = min(n_seq, i0 + per_thread);
-    int64_t mine = 0;
-    for (int i = i0; i < i1; ++i) mine += H * share_of(a, i, blockIdx.x == 0 ? a.report : nullptr).steps;
-    int64_t scan = mine;
+    // ---- this CTA's share of the steps: the entries' steps a batch at a time (entry i of a batch by
+    // warp i % 12, its tiles by the lanes), their sum, then the entry that holds the share's first
+    int64_t total = 0, shares = 0, u = -1, before = 0;
+    for (int pass = 0; pass < 2; ++pass) {
+        for (int base = 0; base < a.seqs.n_seq; base += kBatch) {
+            const int n = min(kBatch, a.seqs.n_seq - base);
+            if (pass == 0 || a.seqs.n_seq > kBatch) {
+                __syncthreads();
+                for (int i = warp; i < n; i += kThreads / 32) {
+                    const Entry e = load_entry(a.seqs, B, base + i, pass == 0 && blockIdx.x == 0 && lane == 0 ? a.report : nullptr);
+                    const int64_t steps = warp_steps(a, e.len, e.fresh, tiles_of(a, e), lane);
+                    if (lane == 0) s_steps[i] = uint32_t(min(steps, int64_t(0xffffffffu)));
+                }
+                __syncthreads();
+            }
+            // 32 lanes scan the batch; every warp does, and finds the same
+            for (int i = 0; i < n; i += 32) {
+                int64_t x = i + lane < n ? int64_t(s_steps[i + lane]) * H : 0, sum = x;
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const int64_t y = __shfl_up_sync(0xffffffffu, scan, o);
-        if (lane >= o) scan += y;
-    }
-    if (lane == 31) s_scan[warp] = scan;
-    __syncthreads();
-    int64_t before = scan - mine, total = 0;
-#pragma unroll
-    for (int w = 0; w < kThreads / 32; ++w) {
-        if (w < warp) before += s_scan[w];
-        total += s_scan[w];
-    }
-    const int64_t shares = min(int64_t(gridDim.x), (total + kStepsPerCta - 1) / kStepsPerCta);
-    if (int64_t(blockIdx.x) >= shares) return;
-    int64_t u = total * blockIdx.x / shares;
-    const int64_t u_end = total * (blockIdx.x + 1) / shares;
-    if (u >= before && u < before + mine) {
-        int64_t at = before;
-        int i = i0;
-        for (; i < i1; ++i) {
-            const int64_t n = H * share_of(a, i, nullptr).steps;
-            if (u < at + n) break;
-            at += n;
+                for (int o = 1; o < 32; o <<= 1) {
+                    const int64_t y = __shfl_up_sync(0xffffffffu, sum, o);
+                    if (lane >= o) sum += y;
+                }
+                if (pass == 1) {
+                    const unsigned past = __ballot_sync(0xffffffffu, u < before + sum);
+                    if (past) {
+                        const int l = __ffs(past) - 1;
+                        const int64_t at = before + __shfl_sync(0xffffffffu, sum - x, l);
+                        if (tid == 0) {
+                            job.entry = base + i + l;
+                            job.off = u - at;
+                            job.u = u;
+                            job.u_end = total * (blockIdx.x + 1) / shares;
+                            job.total = total;
+                            job.shares = shares;
+                            job.it = job.it_g[0] = job.it_g[1] = 0;
+                        }
+                        base = a.seqs.n_seq;  // found: leave both loops
+                        break;
+                    }
+                }
+                before += __shfl_sync(0xffffffffu, sum, 31);
+            }
         }
-        s_entry = i;
-        s_off = u - at;
+        if (pass == 0) {
+            total = before;
+            shares = min(int64_t(gridDim.x), (total + kStepsPerCta - 1) / kStepsPerCta);
+            if (int64_t(blockIdx.x) >= shares) return;
+            u = total * blockIdx.x / shares;
+            before = 0;
+        }
     }
 
     const uint32_t bar = smem_u32(bars);
@@ -251,69 +391,53 @@ __global__ void __launch_bounds__(kThreads, 1) attend_chunk_kernel(const __grid_
         for (int s = 0; s < kStages; ++s) {
             mbar_init(bar + 8 * (K_FULL + s), 4);   // the converting warps
             mbar_init(bar + 8 * (V_FULL + s), 4);
-            mbar_init(bar + 8 * (K_EMPTY + s), 1);  // products done
-            mbar_init(bar + 8 * (V_EMPTY + s), 1);
+            mbar_init(bar + 8 * (K_EMPTY + s), 2);  // both tiles' products done
+            mbar_init(bar + 8 * (V_EMPTY + s), 2);
         }
         for (int g = 0; g < 2; ++g) {
             mbar_init(bar + 8 * (S_FULL + g), 2);   // product done, and the issuing thread (which has seen the
                                                     // step's places: K_FULL's release reaches the softmax by it)
             mbar_init(bar + 8 * (P_FULL + g), 4);   // the tile's softmax warps
             mbar_init(bar + 8 * (PV_DONE + g), 1);
+            mbar_init(bar + 8 * (TURN + g), 1);     // the other tile's products of the step before are issued
         }
+        mbar_init(bar + 8 * LEAVE, 1);
         fence_mbar_init();
         s_gone = 0;
     }
-    if (warp == 12) {
+    if (warp == 8) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(&s_tmem)) : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
     }
     tmem_fence_before();
     __syncthreads();
     tmem_fence_after();
-    const uint32_t tmem = s_tmem;  // columns: S0 0, S1 128, O0 256, O1 384
+    const uint32_t tmem = __shfl_sync(0xffffffffu, s_tmem, 0);  // columns: S0 0, S1 128, O0 256, O1 384
     volatile int *gone = &s_gone;
 
-    int entry = s_entry;
-    int64_t off = s_off;
-    Share sh = share_of(a, entry, nullptr);
     const uint8_t *codes = static_cast<const uint8_t *>(a.cache.codes);
     const int64_t plane = int64_t(a.layer) * 2 * N, v_plane_bytes = N * B * H * d;
-    uint32_t it = 0;        // steps done by this CTA (phases of the K and V barriers)
-    uint32_t it_g[2] = {0, 0};  // steps of each tile (phases of its barriers)
 
-    while (u < u_end) {
-        while (off >= H * sh.steps) {
-            off -= H * sh.steps;
-            sh = share_of(a, ++entry, nullptr);
-        }
-        // the job: KV head h, row tile `tile`, steps [sa, sb)
-        const int h = int(off / sh.steps);
-        int64_t rest = off - h * sh.steps;
-        int tile = 0;
-        Tile t = tile_of(a, sh.e, 0);
-        while (rest >= t.steps) {
-            rest -= t.steps;
-            t = tile_of(a, sh.e, ++tile);
-        }
-        const int sa = int(rest), sb = int(min(int64_t(t.steps), rest + (u_end - u))), n = sb - sa;
-        const int64_t job_u0 = u - sa;
-        const bool two = t.rows > kTileRows;
-        const int pos0 = sh.e.len - sh.e.fresh;
-        const int64_t row_base = int64_t(tile) * kJobRows;
+    while (true) {
+        if (warp == 0) next_job(a, job, lane);
+        if (tid == 0) s_nan = 0;
+        __syncthreads();
 
         // ---- Q: each row scaled by a power of two into the range of a half (undone in s_cq)
-        if (tid == 0) s_nan = 0;
         {
+            const int rows = job.t.rows, h = job.h, row0 = job.e.row0;
+            const int64_t row_base = job.row_base;
             constexpr int kLanes = D / 8, kPer = 32 / kLanes;  // lanes of a row, rows of a warp's vector
             const int at = (lane % kLanes) * 8;
 #pragma unroll 4
-            for (int r = warp * kPer + lane / kLanes; r < kJobRows; r += kThreads / 32 * kPer) {
+            for (int r0 = warp * kPer; r0 < kJobRows; r0 += kThreads / 32 * kPer) {
+                const int r = r0 + lane / kLanes;
                 float v[8];
 #pragma unroll
                 for (int x = 0; x < 8; ++x) v[x] = 0.f;
-                if (r < t.rows && at < d) {
+                if (r < rows && at < d) {
                     const int64_t row = row_base + r;
-                    load8<TYPE>(static_cast<const uint8_t *>(a.attn.q.data) + (sh.e.row0 + row / G) * a.attn.q.row_stride +
+                    load8<TYPE>(static_cast<const uint8_t *>(a.attn.q.data) + (row0 + row / G) * a.attn.q.row_stride +
                                     (h * G + row % G) * a.attn.q.head_stride + 2 * at, v);
                 }
                 float amax = 0.f;
@@ -339,27 +463,31 @@ __global__ void __launch_bounds__(kThreads, 1) attend_chunk_kernel(const __grid_
         fence_proxy_async_smem();
         __syncthreads();
 
-        float row_m = -INFINITY, row_l = 0.f;  // of this softmax thread's row
-        if (warp >= 8 && warp < 12) {
+        if (warp >= 8) {
             // ---- convert K and V
-            const int cw = warp - 8;
-            constexpr int kLanes = D / 16, kPer = 32 / kLanes, kVecs = 32 / kPer;  // 32 slots a warp
-            const int ch = lane % kLanes, rw = lane / kLanes;
+            const int cw = warp - 8, n = job.n, h = job.h, len = job.e.len;
+            const uint32_t it = job.it;
+            const int32_t *table = job.e.table;
+            const int g0 = job.t.g0 + job.sa * kGroups, g1 = job.t.g1, all_lo = job.t.all_lo, all_hi = job.t.all_hi;
+            constexpr int kPer = 512 / D, kVecs = 32 / kPer;  // rows of a warp's vector, vectors of its 32 slots
+            // 8 lanes of a shared-memory phase write 4 chunks of an even and of an odd row: with the
+            // swizzle, 8 different 16-byte columns
+            const int ch = (lane & 3) | (D == 128 ? (lane >> 4) << 2 : 0), rw = D == 128 ? (lane >> 2) & 3 : lane >> 2;
             // Lane l looks after group l % 2 of the warp's two in step l / 2 of a batch of 16 steps: its
             // page, place and scales.  The next batch's are fetched while this one is worked on, so
             // no step waits for a table entry or a scale.
             auto place = [&](int s, int &t0, int &nv) -> int32_t {
                 t0 = 0;
                 nv = 0;
-                const int g = t.g0 + (sa + s) * kGroups + cw * 2 + (lane & 1);
-                if (g >= t.g1 || s >= n) return -1;
+                const int g = g0 + s * kGroups + cw * 2 + (lane & 1);
+                if (g >= g1 || s >= n) return -1;
                 const int blk = g / per_block, slot = (g - blk * per_block) * kGroup;
                 t0 = blk * B + slot;
-                nv = min(min(kGroup, B - slot), sh.e.len - t0);
+                nv = min(min(kGroup, B - slot), len - t0);
                 if (nv <= 0) return -1;
-                const int32_t page = sh.e.table[blk];
+                const int32_t page = table[blk];
                 if (page < 0 || page >= N) {
-                    report(a.report, KVL_ERANGE, entry);
+                    report(a.report, KVL_ERANGE, job.entry);
                     nv = 0;
                     return -1;
                 }
@@ -425,7 +553,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_chunk_kernel(const __grid_
                 const uint32_t k = it + s, st = k % kStages, ph = (k / kStages) & 1;
                 const int two_lanes = (s & 15) << 1;
                 const bool here = (lane & ~1) == two_lanes;
-                const bool partial = __any_sync(0xffffffffu, here && !(nv == kGroup && t0 >= t.all_lo && t0 + kGroup <= t.all_hi));
+                const bool partial = __any_sync(0xffffffffu, here && !(nv == kGroup && t0 >= all_lo && t0 + kGroup <= all_hi));
                 if (!wait_bar(bar + 8 * (K_EMPTY + st), ph ^ 1, gone)) break;
                 Places &pl = places[k % kPlaces];
                 if (here) {
@@ -466,101 +594,123 @@ __global__ void __launch_bounds__(kThreads, 1) attend_chunk_kernel(const __grid_
                 if (lane == 0) mbar_arrive(bar + 8 * (V_FULL + st));
                 if (s + 1 < n) fetch(vreg, s + 1, base, true);
             }
-        } else if (warp == 12) {
-            // ---- issue the products
-            if (lane == 0) {
-                constexpr uint32_t kS = instr_desc(kSlots, false), kO = instr_desc(D, true);
-                const int tiles = two ? 2 : 1;
-                auto scores = [&](int g, uint32_t st) {
-                    const uint32_t q = sm + C::kQ + g * C::kTileBytes, k = sm + C::kK + st * C::kTileBytes;
-#pragma unroll
-                    for (int x = 0; x < D / 16; ++x) {
-                        const uint32_t o = (x >> 2) * (kTileRows * 128) + (x & 3) * 32;
-                        mma_smem(tmem + g * 128, matrix_desc(q + o, 16, 1024), matrix_desc(k + o, 16, 1024), kS, x > 0);
-                    }
-                    mma_commit(bar + 8 * (S_FULL + g));
-                    mbar_arrive(bar + 8 * (S_FULL + g));
-                };
-                auto values = [&](int g, uint32_t st, bool add) {
-                    const uint32_t v = sm + C::kV + st * C::kTileBytes;
-#pragma unroll
-                    for (int x = 0; x < kSlots / 16; ++x)
-                        mma_tmem(tmem + 256 + g * 128, tmem + g * 128 + x * 8,
-                                 matrix_desc(v + x * 2048, kTileRows * 128, 1024), kO, add || x > 0);
-                    mma_commit(bar + 8 * (PV_DONE + g));
-                };
-                bool ok = true;
-                for (int s = 0; s <= n && ok; ++s) {
-                    const uint32_t k = it + s, st = k % kStages;
-                    const uint32_t kp = k - 1, sp = kp % kStages;
-                    for (int g = 0; g < tiles && ok; ++g) {
-                        if (s > 0) {
-                            ok = wait_bar(bar + 8 * (P_FULL + g), (it_g[g] + s - 1) & 1, gone) &&
-                                 (g > 0 || wait_bar(bar + 8 * (V_FULL + sp), (kp / kStages) & 1, gone));
-                            if (!ok) break;
-                            tmem_fence_after();
-                            values(g, sp, s > 1);
-                            if (g == tiles - 1) mma_commit(bar + 8 * (V_EMPTY + sp));
-                        }
-                        if (s < n) {
-                            if (g == 0 && !(ok = wait_bar(bar + 8 * (K_FULL + st), (k / kStages) & 1, gone))) break;
-                            tmem_fence_after();
-                            scores(g, st);
-                            if (g == tiles - 1) mma_commit(bar + 8 * (K_EMPTY + st));
-                        }
-                    }
-                }
-            }
-            __syncwarp();
-        } else if (warp < 8 && (warp < 4 || two)) {
+        } else if (warp < 4 || job.two) {
             // ---- softmax: row r of the job, TMEM lane r % 128
-            const int g = warp >> 2, r = tid & 255;
+            const int g = warp >> 2, r = tid & 255;  // (uniform: warp is)
             const uint32_t lanes = uint32_t(warp & 3) << 21;  // lane 32 (warp % 4), in bits 16 and up
             const uint32_t ts = tmem + lanes + g * 128, to = tmem + lanes + 256 + g * 128;
-            const int pos = pos0 + int((row_base + r) / G);
-            int hi = a.attn.causal ? min(sh.e.len, pos + 1) : sh.e.len;
-            int lo = a.attn.window > 0 ? max(0, pos - a.attn.window + 1) : 0;
-            if (r >= t.rows) { lo = t.all_lo; hi = t.all_hi; }
+            const uint32_t it = job.it, it_g1 = job.it_g[1], it_g = g ? it_g1 : job.it_g[0];
+            const int n = job.n;
+            int lo, hi;
+            {
+                const int pos = job.pos0 + int((job.row_base + r) / G), len = job.e.len;
+                hi = a.attn.causal ? min(len, pos + 1) : len;
+                lo = a.attn.window > 0 ? max(0, pos - a.attn.window + 1) : 0;
+                if (r >= job.t.rows) { lo = job.t.all_lo; hi = job.t.all_hi; }
+            }
+            float row_m = -INFINITY, row_l = 0.f;
             const float cq = s_cq[r];
-            constexpr uint32_t kHidden = 0xff800000u;  // -infinity
+            // The warpgroup's first warp issues its tile's products.
+            const bool leads = (warp & 3) == 0;
+            const uint32_t it_u = __shfl_sync(0xffffffffu, it, 0);
+            auto done = [&](uint32_t one, int which) {
+                mma_commit(one, bar + 8 * which);
+                if (!job.two && one) mbar_arrive(bar + 8 * which);  // for the tile without rows
+            };
+            auto scores = [&](int s) {  // S = Q K^T of step s
+                const uint32_t k = it_u + s, st = k % kStages;
+                if (!__all_sync(0xffffffffu, wait_bar(bar + 8 * (K_FULL + st), (k / kStages) & 1, gone))) return;
+                tmem_fence_after();
+                const uint64_t qa = matrix_desc(sm + C::kQ + g * C::kTileBytes, 16, 1024);
+                const uint64_t ka = matrix_desc(sm + C::kK + st * C::kTileBytes, 16, 1024);
+                const uint32_t one = elect_one();
+#pragma unroll
+                for (int x = 0; x < D / 16; ++x) {
+                    const uint32_t o = ((x >> 2) * (kTileRows * 128) + (x & 3) * 32) >> 4;
+                    mma_smem(one, tmem + g * 128, qa + o, ka + o, instr_desc(kSlots, false), x > 0);
+                }
+                mma_commit(one, bar + 8 * (S_FULL + g));
+                if (one) mbar_arrive(bar + 8 * (S_FULL + g));
+                done(one, K_EMPTY + st);
+            };
+            auto values = [&](int s) {  // O += P V of step s
+                const uint32_t k = it_u + s, st = k % kStages;
+                if (!__all_sync(0xffffffffu, wait_bar(bar + 8 * (V_FULL + st), (k / kStages) & 1, gone))) return;
+                tmem_fence_after();
+                const uint64_t va = matrix_desc(sm + C::kV + st * C::kTileBytes, kTileRows * 128, 1024);
+                const uint32_t one = elect_one();
+#pragma unroll
+                for (int x = 0; x < kSlots / 16; ++x)
+                    mma_tmem(one, tmem + 256 + g * 128, tmem + g * 128 + x * 8, va + x * (2048 >> 4), instr_desc(D, true),
+                             s > 0 || x > 0);
+                mma_commit(one, bar + 8 * (PV_DONE + g));
+                done(one, V_EMPTY + st);
+            };
+            if (leads) scores(0);
             bool ok = true;
             for (int s = 0; s < n; ++s) {
-                const uint32_t ph = (it_g[g] + s) & 1;
+                const uint32_t ph = (it_g + s) & 1;
                 ok = __all_sync(0xffffffffu, wait_bar(bar + 8 * (S_FULL + g), ph, gone));
                 if (!ok) break;
                 tmem_fence_after();
                 const Places &pl = places[(it + s) % kPlaces];
+                const bool whole = !(pl.partial[0] | pl.partial[1] | pl.partial[2] | pl.partial[3]);
+                // The step's 128 scores of the row stay in registers.  x = score * f + b by groups; a group that the row does not see at all gets
+                // harmless ones (its page's scales may be anything).
+                uint32_t x0[32], x1[32], x2[32], x3[32];
+                auto seen = [&](int gi, int &first, int &past) {
+                    first = max(lo - pl.t0[gi], 0);
+                    past = min(hi - pl.t0[gi], pl.nv[gi]);
+                };
                 auto hide = [&](uint32_t (&x)[32], int gi) {  // scores of groups gi, gi + 1 that the row does not see
 #pragma unroll
                     for (int y = 0; y < 2; ++y) {
-                        const int first = max(lo - pl.t0[gi + y], 0), past = min(hi - pl.t0[gi + y], pl.nv[gi + y]);
+                        int first, past;
+                        seen(gi + y, first, past);
 #pragma unroll
                         for (int e = 0; e < 16; ++e)
-                            if (e < first || e >= past) x[16 * y + e] = kHidden;
+                            if (e < first || e >= past) x[16 * y + e] = 0xff800000u;  // -infinity
                     }
                 };
-                const bool whole = !(pl.partial[0] | pl.partial[1] | pl.partial[2] | pl.partial[3]);
-                // the step's largest x: scales are not negative, so a group's largest comes from its
-                // largest score
+                auto factors = [&](int gi, float &f, float &b, float &iv) {
+                    f = pl.ks[gi] * cq;
+                    f = f < 1e-37f ? 1e-37f : f;  // keeps -infinity * f from being a NaN
+                    b = pl.lvs[gi];
+                    iv = pl.ivs[gi];
+                    if (!whole) {
+                        int first, past;
+                        seen(gi, first, past);
+                        if (past <= first) { f = 1.f; b = 0.f; iv = 0.f; }
+                    }
+                };
                 float big = -INFINITY;
-#pragma unroll 1
-                for (int c = 0; c < 4; ++c) {
-                    uint32_t x[32];
-                    tmem_ld32(ts + 32 * c, x);
-                    tmem_wait_ld();
-                    if (!whole) hide(x, 2 * c);
+                auto largest = [&](const uint32_t (&x)[32], int gi) {
 #pragma unroll
                     for (int y = 0; y < 2; ++y) {
-                        float top = __uint_as_float(x[16 * y]);
+                        float top = fmaxf(__uint_as_float(x[16 * y]), __uint_as_float(x[16 * y + 1]));
 #pragma unroll
-                        for (int e = 1; e < 16; ++e) top = fmaxf(top, __uint_as_float(x[16 * y + e]));
-                        const float z = fmaf(top, pl.ks[2 * c + y] * cq, pl.lvs[2 * c + y]);
-                        if (top != -INFINITY) big = fmaxf(big, z);
+                        for (int e = 2; e < 16; e += 2)
+                            top = fmaxf(top, fmaxf(__uint_as_float(x[16 * y + e]), __uint_as_float(x[16 * y + e + 1])));
+                        float f, b, iv;
+                        factors(gi + y, f, b, iv);
+                        big = fmaxf(big, fmaf(top, f, b));  // scales are not negative: the group's largest x
                     }
-                }
+                };
+                tmem_ld32(ts, x0);
+                tmem_ld32(ts + 32, x1);
+                tmem_wait_ld();
+                tmem_ld32(ts + 64, x2);
+                tmem_ld32(ts + 96, x3);
+                if (!whole) { hide(x0, 0); hide(x1, 2); }
+                largest(x0, 0);
+                largest(x1, 2);
+                tmem_wait_ld();
+                if (!whole) { hide(x2, 4); hide(x3, 6); }
+                largest(x2, 4);
+                largest(x3, 6);
                 const bool grow = big > row_m + kSlack || (row_m == -INFINITY && big > -INFINITY);
                 if (__any_sync(0xffffffffu, grow)) {
-                    const float m = grow ? big : row_m;
+                    const float m = grow ? big + kHead : row_m;
                     const float f = grow ? exp2_of(row_m - m) : 1.f;  // 0 from a first maximum
                     row_l *= f;
                     row_m = m;
@@ -568,64 +718,78 @@ __global__ void __launch_bounds__(kThreads, 1) attend_chunk_kernel(const __grid_
                         ok = __all_sync(0xffffffffu, wait_bar(bar + 8 * (PV_DONE + g), ph ^ 1, gone));
                         if (!ok) break;
                         tmem_fence_after();
-#pragma unroll
-                        for (int c = 0; c < D / 32; ++c) {
-                            uint32_t x[32];
-                            tmem_ld32(to + 32 * c, x);
+#pragma unroll 1
+                        for (int c = 0; c < D / 8; ++c) {  // 8 at a time: the scores stay in their registers
+                            uint32_t x[8];
+                            tmem_ld8(to + 8 * c, x);
                             tmem_wait_ld();
 #pragma unroll
-                            for (int e = 0; e < 32; ++e) x[e] = __float_as_uint(__uint_as_float(x[e]) * f);
-                            tmem_st32(to + 32 * c, x);
+                            for (int e = 0; e < 8; ++e) x[e] = __float_as_uint(__uint_as_float(x[e]) * f);
+                            tmem_st8(to + 8 * c, x);
                         }
                     }
                 }
                 const float ref = row_m == -INFINITY ? 0.f : row_m;
-#pragma unroll 1
-                for (int c = 0; c < 4; ++c) {
-                    uint32_t x[32], p[16];
-                    tmem_ld32(ts + 32 * c, x);
-                    tmem_wait_ld();
-                    if (!whole) hide(x, 2 * c);
+                auto weigh = [&](const uint32_t (&x)[32], int c) {
+                    uint32_t p[16];
 #pragma unroll
                     for (int y = 0; y < 2; ++y) {
-                        const float f = pl.ks[2 * c + y] * cq, b = pl.lvs[2 * c + y] - ref;
-                        float sum = 0.f;
+                        float f, b, iv;
+                        factors(2 * c + y, f, b, iv);
+                        const uint64_t ff = pair_of(f, f), bb = pair_of(b - ref, b - ref);
+                        uint64_t s0 = 0, s1 = 0;  // two pairs of partial sums
 #pragma unroll
-                        for (int e = 0; e < 16; e += 2) {
-                            // a hidden score is -infinity: its weight has to be 0 whatever f and b are
-                            float w0 = exp2_of(fmaf(__uint_as_float(x[16 * y + e]), f, b));
-                            float w1 = exp2_of(fmaf(__uint_as_float(x[16 * y + e + 1]), f, b));
-                            if (!whole) {
-                                if (x[16 * y + e] == kHidden) w0 = 0.f;
-                                if (x[16 * y + e + 1] == kHidden) w1 = 0.f;
-                            }
-                            sum += w0 + w1;
-                            p[8 * y + e / 2] = pack2<KVL_TYPE_HALF>(w0, w1);
+                        for (int e = 0; e < 16; e += 4) {
+                            float2 u = split_pair(fma_pair(pair_of(__uint_as_float(x[16 * y + e]), __uint_as_float(x[16 * y + e + 1])), ff, bb));
+                            float2 v = split_pair(fma_pair(pair_of(__uint_as_float(x[16 * y + e + 2]), __uint_as_float(x[16 * y + e + 3])), ff, bb));
+                            u.x = exp2_of(u.x); u.y = exp2_of(u.y); v.x = exp2_of(v.x); v.y = exp2_of(v.y);
+                            s0 = add_pair(s0, pair_of(u.x, u.y));
+                            s1 = add_pair(s1, pair_of(v.x, v.y));
+                            p[8 * y + e / 2] = pack2<KVL_TYPE_HALF>(u.x, u.y);
+                            p[8 * y + e / 2 + 1] = pack2<KVL_TYPE_HALF>(v.x, v.y);
                         }
-                        if (sum != 0.f) row_l = fmaf(sum, pl.ivs[2 * c + y], row_l);
+                        const float2 sum = split_pair(add_pair(s0, s1));
+                        row_l = fmaf(sum.x + sum.y, iv, row_l);
                     }
                     tmem_st16(ts + 16 * c, p);
-                }
+                };
+                asm volatile("" ::: "memory");  // the groups' factors are read again rather than kept in registers
+                weigh(x0, 0);
+                weigh(x1, 1);
+                weigh(x2, 2);
+                weigh(x3, 3);
                 tmem_wait_st();
                 tmem_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(bar + 8 * (P_FULL + g));
+                if (leads && __all_sync(0xffffffffu, wait_bar(bar + 8 * (P_FULL + g), ph, gone))) {
+                    // The tiles take turns: a tile's two products run one after the other, not mixed with the
+                    // other tile's, so one tile is at its softmax while the other is at its products
+                    // (mixed, both wait for both: 341 us instead of 233 for 512 rows on 31,232).
+                    const uint32_t turn = it_g1 + s - (g == 0);
+                    if (job.two && (g == 1 || s > 0) && !__all_sync(0xffffffffu, wait_bar(bar + 8 * (TURN + g), turn & 1, gone))) break;
+                    values(s);
+                    if (s + 1 < n) scores(s + 1);
+                    if (job.two && lane == 0) mbar_arrive(bar + 8 * (TURN + 1 - g));
+                }
             }
             if (ok) {
-                ok = __all_sync(0xffffffffu, wait_bar(bar + 8 * (PV_DONE + g), (it_g[g] + n - 1) & 1, gone));
+                ok = __all_sync(0xffffffffu, wait_bar(bar + 8 * (PV_DONE + g), (it_g + n - 1) & 1, gone));
                 tmem_fence_after();
             }
             // ---- the row's result, or its part
-            const bool complete = sa == 0 && sb == t.steps;
+            const bool complete = job.complete;
+            const int rows = job.t.rows, h = job.h;
+            const Entry e_ = job.e;
             uint32_t nan_at[D / 32];
 #pragma unroll
             for (int c = 0; c < D / 32; ++c) nan_at[c] = 0;
-            if (ok && CODE == KVL_CODE_FLOAT && *const_cast<volatile int *>(&s_nan) && r < t.rows) {
+            if (ok && CODE == KVL_CODE_FLOAT && *const_cast<volatile int *>(&s_nan) && r < rows) {
                 // elements that a NaN code of a seen token reaches, from the steps that were cleared
-                for (int gi = t.g0 + sa * kGroups; gi < min(t.g1, t.g0 + sb * kGroups); ++gi) {
+                for (int gi = job.t.g0 + job.sa * kGroups; gi < min(job.t.g1, job.t.g0 + (job.sa + n) * kGroups); ++gi) {
                     const int blk = gi / per_block, slot = (gi - blk * per_block) * kGroup, t0 = blk * B + slot;
-                    const int nv = min(min(kGroup, B - slot), sh.e.len - t0);
-                    const int32_t page = sh.e.table[blk];
+                    const int nv = min(min(kGroup, B - slot), e_.len - t0);
+                    const int32_t page = e_.table[blk];
                     if (page < 0 || page >= N) continue;
                     for (int e = 0; e < nv; ++e) {
                         if (t0 + e < lo || t0 + e >= hi) continue;
@@ -639,10 +803,10 @@ __global__ void __launch_bounds__(kThreads, 1) attend_chunk_kernel(const __grid_
                     }
                 }
             }
-            const int64_t row = row_base + r;
+            const int64_t row = job.row_base + r;
             const float inv = row_l == 0.f ? 0.f : 1.f / row_l;
-            float *part = a.parts + (int64_t(blockIdx.x) * 2 + (sa == 0 ? 1 : 0)) * C::kPartFloats;
-            uint8_t *dst = static_cast<uint8_t *>(a.attn.out.data) + (sh.e.row0 + row / G) * a.attn.out.row_stride +
+            float *part = a.parts + (int64_t(blockIdx.x) * 2 + (job.sa == 0 ? 1 : 0)) * C::kPartFloats;
+            uint8_t *dst = static_cast<uint8_t *>(a.attn.out.data) + (e_.row0 + row / G) * a.attn.out.row_stride +
                            (h * G + row % G) * a.attn.out.head_stride;
             if (ok) {
 #pragma unroll
@@ -655,7 +819,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_chunk_kernel(const __grid_
                         for (int e = 0; e < 32; ++e)
                             if (nan_at[c] >> e & 1u) x[e] = 0x7fffffffu;
                     }
-                    if (r < t.rows) {
+                    if (r < rows) {
                         if (complete) {
 #pragma unroll
                             for (int e = 0; e < 4; ++e) {
@@ -672,25 +836,22 @@ __global__ void __launch_bounds__(kThreads, 1) attend_chunk_kernel(const __grid_
                         }
                     }
                 }
-                if (r < t.rows) {
+                if (r < rows) {
                     if (!complete) {
                         part[r] = row_m;
                         part[kJobRows + r] = row_l;
                     } else if (a.attn.lse) {
-                        a.attn.lse[(sh.e.row0 + row / G) * a.attn.n_heads + h * G + row % G] =
+                        a.attn.lse[(e_.row0 + row / G) * a.attn.n_heads + h * G + row % G] =
                             row_l == 0.f ? -INFINITY : (row_m + __log2f(row_l)) * (1.f / kLog2e);
                     }
                 }
             }
             tmem_fence_before();
         }
-        it += n;
-        it_g[0] += n;
-        if (two) it_g[1] += n;
-        if (!(sa == 0 && sb == t.steps)) {
+        if (!job.complete) {
             // parts of this job: shares first .. last; the one that arrives last joins them
-            const int first = int(((job_u0 + 1) * shares - 1) / total);
-            const int last = int(((job_u0 + t.steps) * shares - 1) / total);
+            const int first = int(((job.u0 + 1) * job.shares - 1) / job.total);
+            const int last = int(((job.u0 + job.t.steps) * job.shares - 1) / job.total);
             __threadfence();
             __syncthreads();
             if (tid == 0) s_last = !*gone && atomicAdd(&a.counters[first], 1u) == uint32_t(last - first);
@@ -698,63 +859,75 @@ __global__ void __launch_bounds__(kThreads, 1) attend_chunk_kernel(const __grid_
             if (s_last) {
                 __threadfence();
                 if (tid == 0) a.counters[first] = 0;
-                const int r = tid & (kJobRows - 1);
-                if (r < t.rows) {
-                    auto part_of = [&](int b) { return a.parts + (int64_t(b) * 2 + (b == first)) * C::kPartFloats; };
+                const int n_rows = job.t.rows, n_parts = last - first + 1;
+                // 32 elements of a row a thread and turn
+                for (int x = tid; x < kJobRows * (D / 32); x += kThreads) {
+                    const int r = x & (kJobRows - 1), c = x / kJobRows;
+                    if (r >= n_rows) continue;
+                    auto part_of = [&](int b) { return a.parts + (int64_t(first + b) * 2 + (b == 0)) * C::kPartFloats; };
                     float big = -INFINITY, sum = 0.f;
-                    for (int b = first; b <= last; ++b) big = fmaxf(big, __ldcg(part_of(b) + r));
-                    for (int b = first; b <= last; ++b) {
-                        const float mb = __ldcg(part_of(b) + r);
-                        sum += __ldcg(part_of(b) + kJobRows + r) * (mb == -INFINITY ? 0.f : exp2_of(mb - big));
+#pragma unroll 4
+                    for (int b = 0; b < n_parts; ++b) big = fmaxf(big, __ldcg(part_of(b) + r));
+                    float4 v[8];
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) v[e] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 2
+                    for (int b = 0; b < n_parts; ++b) {
+                        const float *p = part_of(b);
+                        const float mb = __ldcg(p + r), lb = __ldcg(p + kJobRows + r);
+                        const float f = mb == -INFINITY ? 0.f : exp2_of(mb - big);
+                        sum += lb * f;
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) {
+                            const float4 y = __ldcg(reinterpret_cast<const float4 *>(p + 2 * kJobRows) + int64_t(8 * c + e) * kJobRows + r);
+                            v[e].x += y.x * f; v[e].y += y.y * f; v[e].z += y.z * f; v[e].w += y.w * f;
+                        }
                     }
                     const float inv = sum == 0.f ? 0.f : 1.f / sum;
-                    const int64_t row = row_base + r;
-                    const int head = int(h * G + row % G);
-                    uint8_t *dst = static_cast<uint8_t *>(a.attn.out.data) + (sh.e.row0 + row / G) * a.attn.out.row_stride +
-                                   head * a.attn.out.head_stride;
-#pragma unroll 4
-                    for (int e = (tid / kJobRows) * 2; e < D / 4; e += 4) {  // 8 elements: two vectors of 4
-                        float v[8];
+                    const int64_t row = job.row_base + r;
+                    const int head = int(job.h * G + row % G);
+                    uint8_t *dst = static_cast<uint8_t *>(a.attn.out.data) + (job.e.row0 + row / G) * a.attn.out.row_stride +
+                                   head * a.attn.out.head_stride + 64 * c;
 #pragma unroll
-                        for (int x = 0; x < 8; ++x) v[x] = 0.f;
-                        for (int b = first; b <= last; ++b) {
-                            const float *p = part_of(b);
-                            const float mb = __ldcg(p + r);
-                            const float f = mb == -INFINITY ? 0.f : exp2_of(mb - big);
-#pragma unroll
-                            for (int x = 0; x < 2; ++x) {
-                                const float4 y = __ldcg(reinterpret_cast<const float4 *>(p + 2 * kJobRows) + int64_t(e + x) * kJobRows + r);
-                                v[4 * x] += y.x * f; v[4 * x + 1] += y.y * f; v[4 * x + 2] += y.z * f; v[4 * x + 3] += y.w * f;
-                            }
-                        }
-#pragma unroll
-                        for (int x = 0; x < 8; ++x) v[x] *= inv;
-                        if (4 * e < d) store8<TYPE>(dst + 8 * e, v);
+                    for (int e = 0; e < 4; ++e) {
+                        const float w[8] = {v[2 * e].x * inv, v[2 * e].y * inv, v[2 * e].z * inv, v[2 * e].w * inv,
+                                            v[2 * e + 1].x * inv, v[2 * e + 1].y * inv, v[2 * e + 1].z * inv, v[2 * e + 1].w * inv};
+                        if (32 * c + 8 * e < d) store8<TYPE>(dst + 16 * e, w);
                     }
-                    if (a.attn.lse && tid < kJobRows)
-                        a.attn.lse[(sh.e.row0 + row / G) * a.attn.n_heads + head] =
+                    if (a.attn.lse && c == 0)
+                        a.attn.lse[(job.e.row0 + row / G) * a.attn.n_heads + head] =
                             sum == 0.f ? -INFINITY : (big + __log2f(sum)) * (1.f / kLog2e);
                 }
             }
         }
         __syncthreads();  // Q and tensor memory are free again
         tmem_fence_after();
-        if (*gone) break;
-        off += n;
-        u += n;
+        if (tid == 0) {
+            job.it += job.n;
+            job.it_g[0] += job.n;
+            if (job.two) job.it_g[1] += job.n;
+            job.off += job.n;
+            job.u += job.n;
+        }
+        __syncthreads();
+        if (*gone || job.u >= job.u_end) break;
     }
     if (*gone) {
         if (tid == 0) report(a.report, KVL_ETIMEOUT, blockIdx.x);
-        if (warp == 12 && lane == 0) {  // let the products in flight end (bounded) before their memory goes
-            mbar_inval(bar + 8 * P_FULL);
-            mbar_init(bar + 8 * P_FULL, 1);
-            fence_mbar_init();
-            mma_commit(bar + 8 * P_FULL);
-            mbar_wait_bounded(bar + 8 * P_FULL, 0);
+        // let the products in flight end (bounded) before their memory goes, one issuing thread's after
+        // the other's
+        if (warp == 0) {
+            mma_commit(elect_one(), bar + 8 * LEAVE);
+            mbar_wait_bounded(bar + 8 * LEAVE, 0);
+        }
+        __syncthreads();
+        if (warp == 4) {
+            mma_commit(elect_one(), bar + 8 * LEAVE);
+            mbar_wait_bounded(bar + 8 * LEAVE, 1);
         }
     }
     __syncthreads();
-    if (warp == 12) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
+    if (warp == 8) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
 }
 
 template <int CODE, int TYPE, int D>
