@@ -17,6 +17,8 @@
 //
 // Every wait on a barrier is bounded: past the limit a flag is raised, the report says
 // KVL_ETIMEOUT, every role leaves, and the tensor memory is given back.
+#include <type_traits>
+
 #include "kvl_attend.cuh"
 
 namespace kvl {
@@ -39,7 +41,7 @@ constexpr float kSlack = 14.f, kHead = 4.f;
 
 // Scales and places of a step's groups; partial[w]: some row sees only a part of the two groups that
 // converting warp w filled.
-struct Places {
+struct alignas(16) Places {
     float ks[kGroups], lvs[kGroups], ivs[kGroups];
     int32_t t0[kGroups], nv[kGroups];
     int32_t partial[4];
@@ -83,9 +85,7 @@ __device__ __forceinline__ uint32_t elect_one()
     return r;
 }
 
-// Products are issued by a whole warp of which one lane (`one`) is elected: addresses and descriptors
-// stay uniform, so that they are kept in uniform registers and an issue takes few instructions.
-// Computed by a lone lane, each product cost 100 to 160 cycles of issue where it runs for 64.
+// Products, issued by the elected lane of a converged warp.
 __device__ __forceinline__ void mma_smem(uint32_t one, uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool add)
 {
     asm volatile(
@@ -152,6 +152,13 @@ __device__ __forceinline__ void tmem_st16(uint32_t at, const uint32_t (&r)[16])
         "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]),
         "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(at)
         : "memory");
+}
+
+__device__ __forceinline__ float max3(float a, float b, float c)
+{
+    float r;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
 }
 
 // Two floats in one register pair, and arithmetic on both at once.
@@ -250,7 +257,8 @@ __device__ __forceinline__ int64_t warp_steps(const AttendArgs &a, int32_t len, 
 struct Job {
     int64_t u, u_end, off;    // next unit, the share's end, units of the entry before u
     int64_t total, shares;
-    int64_t row_base, u0;     // the tile's first row, the job's first unit
+    int64_t u0;               // the job's first unit
+    int32_t row_base;         // the tile's first row
     Entry e;
     Tile t;
     int32_t entry, h, sa, n;  // KV head; steps [sa, sa + n) of the tile
@@ -306,10 +314,42 @@ __device__ __forceinline__ void next_job(const AttendArgs &a, Job &job, int lane
         job.sa = int(rest);
         job.n = int(min(int64_t(t.steps) - rest, job.u_end - job.u));
         job.u0 = job.u - rest;
-        job.row_base = int64_t(tile) * kJobRows;
+        job.row_base = tile * kJobRows;
         job.pos0 = e.len - e.fresh;
         job.two = t.rows > kTileRows;
         job.complete = job.n == t.steps;
+    }
+}
+
+// The products of tile g from K or V stage st, issued by a whole warp of which lane `one` is elected.
+// Kept short: the roles' loops together just fit the instruction cache, and with four copies of
+// these (a tile and stage each) the 512 rows on 31,232 took 295 us instead of 270.
+template <int D>
+__device__ __forceinline__ void issue_scores(uint32_t one, uint32_t sm, int g, uint32_t st)
+{
+    using C = Chunk<D>;
+    uint64_t q = matrix_desc(sm + C::kQ + g * C::kTileBytes, 16, 1024), k = matrix_desc(sm + C::kK + st * C::kTileBytes, 16, 1024);
+#pragma unroll 1
+    for (int x = 0; x < D / 64; ++x) {
+#pragma unroll
+        for (int y = 0; y < 4; ++y) mma_smem(one, g * 128, q + 2 * y, k + 2 * y, instr_desc(kSlots, false), x + y > 0);
+        q += kTileRows * 128 >> 4;
+        k += kTileRows * 128 >> 4;
+    }
+}
+
+template <int D>
+__device__ __forceinline__ void issue_values(uint32_t one, uint32_t sm, int g, uint32_t st, bool add)
+{
+    using C = Chunk<D>;
+    uint64_t v = matrix_desc(sm + C::kV + st * C::kTileBytes, kTileRows * 128, 1024);
+    uint32_t p = g * 128;
+#pragma unroll 1
+    for (int x = 0; x < kSlots / 64; ++x) {
+#pragma unroll
+        for (int y = 0; y < 4; ++y) mma_tmem(one, 256 + g * 128, p + y * 8, v + y * (2048 >> 4), instr_desc(D, true), add || x + y > 0);
+        p += 32;
+        v += 4 * 2048 >> 4;
     }
 }
 
@@ -412,7 +452,12 @@ __global__ void __launch_bounds__(kThreads, 1) attend_chunk_kernel(const __grid_
     tmem_fence_before();
     __syncthreads();
     tmem_fence_after();
-    const uint32_t tmem = __shfl_sync(0xffffffffu, s_tmem, 0);  // columns: S0 0, S1 128, O0 256, O1 384
+    constexpr uint32_t tmem = 0;  // columns: S0 0, S1 128, O0 256, O1 384
+    if (s_tmem != 0) {            // all 512 columns were asked for: they begin at 0
+        if (tid == 0) report(a.report, KVL_ECUDA, blockIdx.x);
+        if (warp == 8) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(s_tmem) : "memory");
+        return;
+    }
     volatile int *gone = &s_gone;
 
     const uint8_t *codes = static_cast<const uint8_t *>(a.cache.codes);
@@ -425,8 +470,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_chunk_kernel(const __grid_
 
         // ---- Q: each row scaled by a power of two into the range of a half (undone in s_cq)
         {
-            const int rows = job.t.rows, h = job.h, row0 = job.e.row0;
-            const int64_t row_base = job.row_base;
+            const int rows = job.t.rows, h = job.h, row0 = job.e.row0, row_base = job.row_base;
             constexpr int kLanes = D / 8, kPer = 32 / kLanes;  // lanes of a row, rows of a warp's vector
             const int at = (lane % kLanes) * 8;
 #pragma unroll 4
@@ -436,9 +480,9 @@ __global__ void __launch_bounds__(kThreads, 1) attend_chunk_kernel(const __grid_
 #pragma unroll
                 for (int x = 0; x < 8; ++x) v[x] = 0.f;
                 if (r < rows && at < d) {
-                    const int64_t row = row_base + r;
-                    load8<TYPE>(static_cast<const uint8_t *>(a.attn.q.data) + (row0 + row / G) * a.attn.q.row_stride +
-                                    (h * G + row % G) * a.attn.q.head_stride + 2 * at, v);
+                    const uint32_t row = row_base + r, tok = row / uint32_t(G);
+                    load8<TYPE>(static_cast<const uint8_t *>(a.attn.q.data) + int64_t(row0 + tok) * a.attn.q.row_stride +
+                                    int64_t(h * G + row - tok * G) * a.attn.q.head_stride + 2 * at, v);
                 }
                 float amax = 0.f;
 #pragma unroll
@@ -506,10 +550,11 @@ __global__ void __launch_bounds__(kThreads, 1) attend_chunk_kernel(const __grid_
             float ks, vs, ksn = 0.f, vsn = 1.f;
             scales(page, ks, vs);
             uint4 kreg[kVecs], vreg[kVecs];
-            auto fetch = [&](uint4 (&reg)[kVecs], int s, int base, bool v) {  // step s's codes, of this batch or the next
+            // This lane's place in the warp's two groups of a step (of this batch or the next), and its codes.
+            const uint8_t *half[2];
+            int valid[2];
+            auto look = [&](int s, int base) {
                 const bool ahead = s - base >= 16;
-                const uint8_t *half[2];
-                int valid[2];
 #pragma unroll
                 for (int y = 0; y < 2; ++y) {
                     const int from = ((s & 15) << 1) | y;
@@ -517,13 +562,15 @@ __global__ void __launch_bounds__(kThreads, 1) attend_chunk_kernel(const __grid_
                     const int tt = __shfl_sync(0xffffffffu, ahead ? t0n : t0, from);
                     valid[y] = __shfl_sync(0xffffffffu, ahead ? nvn : nv, from);
                     if (ch * 16 >= d) valid[y] = 0;
-                    half[y] = codes + (v ? v_plane_bytes : 0) + (((plane + max(pg, 0)) * B + tt % B) * H + h) * d + ch * 16;
+                    half[y] = codes + (((plane + max(pg, 0)) * B + tt % B) * H + h) * d + ch * 16;
                 }
+            };
+            auto fetch = [&](uint4 (&reg)[kVecs], int64_t plane_bytes) {
 #pragma unroll
                 for (int x = 0; x < kVecs; ++x) {
                     const int r = (x % (kVecs / 2)) * kPer + rw, y = x / (kVecs / 2);  // slot r of the warp's group y
                     reg[x] = make_uint4(0, 0, 0, 0);
-                    if (r < valid[y]) reg[x] = __ldg(reinterpret_cast<const uint4 *>(half[y] + int64_t(r) * H * d));
+                    if (r < valid[y]) reg[x] = __ldg(reinterpret_cast<const uint4 *>(half[y] + plane_bytes + int64_t(r) * H * d));
                 }
             };
             auto convert = [&](const uint4 (&reg)[kVecs], uint8_t *dst) {
@@ -540,8 +587,9 @@ __global__ void __launch_bounds__(kThreads, 1) attend_chunk_kernel(const __grid_
                     *reinterpret_cast<uint4 *>(p + (((un + 1) ^ (r & 7)) << 4)) = hi;
                 }
             };
-            fetch(kreg, 0, 0, false);
-            fetch(vreg, 0, 0, true);
+            look(0, 0);
+            fetch(kreg, 0);
+            fetch(vreg, v_plane_bytes);
             int base = 0;
             for (int s = 0; s < n; ++s) {
                 if (s - base == 16) {
@@ -569,7 +617,10 @@ __global__ void __launch_bounds__(kThreads, 1) attend_chunk_kernel(const __grid_
                 fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(bar + 8 * (K_FULL + st));
-                if (s + 1 < n) fetch(kreg, s + 1, base, false);
+                if (s + 1 < n) {
+                    look(s + 1, base);
+                    fetch(kreg, 0);
+                }
                 if (CODE == KVL_CODE_FLOAT && partial) {
                     // NaN codes of a step that some rows see in part would reach the others as 0 * NaN:
                     // they leave the products here and come back where the rows are written
@@ -592,7 +643,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_chunk_kernel(const __grid_
                 fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(bar + 8 * (V_FULL + st));
-                if (s + 1 < n) fetch(vreg, s + 1, base, true);
+                if (s + 1 < n) fetch(vreg, v_plane_bytes);
             }
         } else if (warp < 4 || job.two) {
             // ---- softmax: row r of the job, TMEM lane r % 128
@@ -603,7 +654,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_chunk_kernel(const __grid_
             const int n = job.n;
             int lo, hi;
             {
-                const int pos = job.pos0 + int((job.row_base + r) / G), len = job.e.len;
+                const int pos = job.pos0 + int(uint32_t(job.row_base + r) / uint32_t(G)), len = job.e.len;
                 hi = a.attn.causal ? min(len, pos + 1) : len;
                 lo = a.attn.window > 0 ? max(0, pos - a.attn.window + 1) : 0;
                 if (r >= job.t.rows) { lo = job.t.all_lo; hi = job.t.all_hi; }
@@ -621,14 +672,8 @@ __global__ void __launch_bounds__(kThreads, 1) attend_chunk_kernel(const __grid_
                 const uint32_t k = it_u + s, st = k % kStages;
                 if (!__all_sync(0xffffffffu, wait_bar(bar + 8 * (K_FULL + st), (k / kStages) & 1, gone))) return;
                 tmem_fence_after();
-                const uint64_t qa = matrix_desc(sm + C::kQ + g * C::kTileBytes, 16, 1024);
-                const uint64_t ka = matrix_desc(sm + C::kK + st * C::kTileBytes, 16, 1024);
                 const uint32_t one = elect_one();
-#pragma unroll
-                for (int x = 0; x < D / 16; ++x) {
-                    const uint32_t o = ((x >> 2) * (kTileRows * 128) + (x & 3) * 32) >> 4;
-                    mma_smem(one, tmem + g * 128, qa + o, ka + o, instr_desc(kSlots, false), x > 0);
-                }
+                issue_scores<D>(one, sm, g, st);
                 mma_commit(one, bar + 8 * (S_FULL + g));
                 if (one) mbar_arrive(bar + 8 * (S_FULL + g));
                 done(one, K_EMPTY + st);
@@ -637,12 +682,8 @@ __global__ void __launch_bounds__(kThreads, 1) attend_chunk_kernel(const __grid_
                 const uint32_t k = it_u + s, st = k % kStages;
                 if (!__all_sync(0xffffffffu, wait_bar(bar + 8 * (V_FULL + st), (k / kStages) & 1, gone))) return;
                 tmem_fence_after();
-                const uint64_t va = matrix_desc(sm + C::kV + st * C::kTileBytes, kTileRows * 128, 1024);
                 const uint32_t one = elect_one();
-#pragma unroll
-                for (int x = 0; x < kSlots / 16; ++x)
-                    mma_tmem(one, tmem + 256 + g * 128, tmem + g * 128 + x * 8, va + x * (2048 >> 4), instr_desc(D, true),
-                             s > 0 || x > 0);
+                issue_values<D>(one, sm, g, st, s > 0);
                 mma_commit(one, bar + 8 * (PV_DONE + g));
                 done(one, V_EMPTY + st);
             };
@@ -655,109 +696,134 @@ __global__ void __launch_bounds__(kThreads, 1) attend_chunk_kernel(const __grid_
                 tmem_fence_after();
                 const Places &pl = places[(it + s) % kPlaces];
                 const bool whole = !(pl.partial[0] | pl.partial[1] | pl.partial[2] | pl.partial[3]);
-                // The step's 128 scores of the row stay in registers.  x = score * f + b by groups; a group that the row does not see at all gets
-                // harmless ones (its page's scales may be anything).
-                uint32_t x0[32], x1[32], x2[32], x3[32];
-                auto seen = [&](int gi, int &first, int &past) {
-                    first = max(lo - pl.t0[gi], 0);
-                    past = min(hi - pl.t0[gi], pl.nv[gi]);
-                };
-                auto hide = [&](uint32_t (&x)[32], int gi) {  // scores of groups gi, gi + 1 that the row does not see
+                // The step's 128 scores of the row stay in registers; x = score * f + b by groups.  Steps that
+                // every row sees whole have code without branches of its own: with the masks' in
+                // it, the two passes took 1,900 cycles instead of 1,300.
+                auto weights = [&](auto whole_c) -> bool {
+                    constexpr bool kWhole = decltype(whole_c)::value;
+                    uint32_t x0[32], x1[32], x2[32], x3[32];
+                    auto hide = [&](uint32_t (&x)[32], int gi) {  // scores of groups gi, gi + 1 that the row does not see
 #pragma unroll
-                    for (int y = 0; y < 2; ++y) {
-                        int first, past;
-                        seen(gi + y, first, past);
+                        for (int y = 0; y < 2; ++y) {
+                            const int first = max(lo - pl.t0[gi + y], 0), past = min(hi - pl.t0[gi + y], pl.nv[gi + y]);
 #pragma unroll
-                        for (int e = 0; e < 16; ++e)
-                            if (e < first || e >= past) x[16 * y + e] = 0xff800000u;  // -infinity
+                            for (int e = 0; e < 16; ++e)
+                                if (e < first || e >= past) x[16 * y + e] = 0xff800000u;  // -infinity
+                        }
+                    };
+                    // f, b (and 1 / scale) of groups gi .. gi + 3; a group the row does not see at all gets
+                    // harmless ones, as its page's scales may be anything
+                    auto factors = [&](int gi, float (&f)[4], float (&b)[4], float (&iv)[4]) {
+                        const float4 k4 = *reinterpret_cast<const float4 *>(pl.ks + gi), l4 = *reinterpret_cast<const float4 *>(pl.lvs + gi);
+                        const float4 i4 = *reinterpret_cast<const float4 *>(pl.ivs + gi);
+                        f[0] = k4.x * cq; f[1] = k4.y * cq; f[2] = k4.z * cq; f[3] = k4.w * cq;
+                        b[0] = l4.x; b[1] = l4.y; b[2] = l4.z; b[3] = l4.w;
+                        iv[0] = i4.x; iv[1] = i4.y; iv[2] = i4.z; iv[3] = i4.w;
+                        if constexpr (!kWhole) {
+#pragma unroll
+                            for (int y = 0; y < 4; ++y) {
+                                f[y] = f[y] < 1e-37f ? 1e-37f : f[y];  // keeps -infinity * f from being a NaN
+                                const int first = max(lo - pl.t0[gi + y], 0), past = min(hi - pl.t0[gi + y], pl.nv[gi + y]);
+                                if (past <= first) { f[y] = 1.f; b[y] = 0.f; iv[y] = 0.f; }
+                            }
+                        }
+                    };
+                    float big = -INFINITY;
+                    auto largest = [&](const uint32_t (&x)[32], float f0, float b0, float f1, float b1) {
+                        float top[2];
+#pragma unroll
+                        for (int y = 0; y < 2; ++y) {
+                            float u = __uint_as_float(x[16 * y]), v = __uint_as_float(x[16 * y + 1]);
+#pragma unroll
+                            for (int e = 2; e < 14; e += 4) {
+                                u = max3(u, __uint_as_float(x[16 * y + e]), __uint_as_float(x[16 * y + e + 1]));
+                                v = max3(v, __uint_as_float(x[16 * y + e + 2]), __uint_as_float(x[16 * y + e + 3]));
+                            }
+                            u = max3(u, __uint_as_float(x[16 * y + 14]), __uint_as_float(x[16 * y + 15]));
+                            top[y] = fmaxf(u, v);
+                        }
+                        // scales are not negative: a group's largest x comes from its largest score
+                        big = max3(big, fmaf(top[0], f0, b0), fmaf(top[1], f1, b1));
+                    };
+                    tmem_ld32(ts, x0);
+                    tmem_ld32(ts + 32, x1);
+                    tmem_wait_ld();
+                    tmem_ld32(ts + 64, x2);
+                    tmem_ld32(ts + 96, x3);
+                    if constexpr (!kWhole) { hide(x0, 0); hide(x1, 2); }
+                    {
+                        float f[4], b[4], iv[4];
+                        factors(0, f, b, iv);
+                        largest(x0, f[0], b[0], f[1], b[1]);
+                        largest(x1, f[2], b[2], f[3], b[3]);
                     }
-                };
-                auto factors = [&](int gi, float &f, float &b, float &iv) {
-                    f = pl.ks[gi] * cq;
-                    f = f < 1e-37f ? 1e-37f : f;  // keeps -infinity * f from being a NaN
-                    b = pl.lvs[gi];
-                    iv = pl.ivs[gi];
-                    if (!whole) {
-                        int first, past;
-                        seen(gi, first, past);
-                        if (past <= first) { f = 1.f; b = 0.f; iv = 0.f; }
+                    tmem_wait_ld();
+                    if constexpr (!kWhole) { hide(x2, 4); hide(x3, 6); }
+                    {
+                        float f[4], b[4], iv[4];
+                        factors(4, f, b, iv);
+                        largest(x2, f[0], b[0], f[1], b[1]);
+                        largest(x3, f[2], b[2], f[3], b[3]);
                     }
-                };
-                float big = -INFINITY;
-                auto largest = [&](const uint32_t (&x)[32], int gi) {
-#pragma unroll
-                    for (int y = 0; y < 2; ++y) {
-                        float top = fmaxf(__uint_as_float(x[16 * y]), __uint_as_float(x[16 * y + 1]));
-#pragma unroll
-                        for (int e = 2; e < 16; e += 2)
-                            top = fmaxf(top, fmaxf(__uint_as_float(x[16 * y + e]), __uint_as_float(x[16 * y + e + 1])));
-                        float f, b, iv;
-                        factors(gi + y, f, b, iv);
-                        big = fmaxf(big, fmaf(top, f, b));  // scales are not negative: the group's largest x
-                    }
-                };
-                tmem_ld32(ts, x0);
-                tmem_ld32(ts + 32, x1);
-                tmem_wait_ld();
-                tmem_ld32(ts + 64, x2);
-                tmem_ld32(ts + 96, x3);
-                if (!whole) { hide(x0, 0); hide(x1, 2); }
-                largest(x0, 0);
-                largest(x1, 2);
-                tmem_wait_ld();
-                if (!whole) { hide(x2, 4); hide(x3, 6); }
-                largest(x2, 4);
-                largest(x3, 6);
-                const bool grow = big > row_m + kSlack || (row_m == -INFINITY && big > -INFINITY);
-                if (__any_sync(0xffffffffu, grow)) {
-                    const float m = grow ? big + kHead : row_m;
-                    const float f = grow ? exp2_of(row_m - m) : 1.f;  // 0 from a first maximum
-                    row_l *= f;
-                    row_m = m;
-                    if (s > 0) {
-                        ok = __all_sync(0xffffffffu, wait_bar(bar + 8 * (PV_DONE + g), ph ^ 1, gone));
-                        if (!ok) break;
-                        tmem_fence_after();
+                    const bool grow = big > row_m + kSlack || (row_m == -INFINITY && big > -INFINITY);
+                    if (__any_sync(0xffffffffu, grow)) {
+                        const float m = grow ? big + kHead : row_m;
+                        const float f = grow ? exp2_of(row_m - m) : 1.f;  // 0 from a first maximum
+                        row_l *= f;
+                        row_m = m;
+                        if (s > 0) {
+                            if (!__all_sync(0xffffffffu, wait_bar(bar + 8 * (PV_DONE + g), ph ^ 1, gone))) return false;
+                            tmem_fence_after();
 #pragma unroll 1
-                        for (int c = 0; c < D / 8; ++c) {  // 8 at a time: the scores stay in their registers
-                            uint32_t x[8];
-                            tmem_ld8(to + 8 * c, x);
-                            tmem_wait_ld();
+                            for (int c = 0; c < D / 8; ++c) {  // 8 at a time: the scores stay in their registers
+                                uint32_t x[8];
+                                tmem_ld8(to + 8 * c, x);
+                                tmem_wait_ld();
 #pragma unroll
-                            for (int e = 0; e < 8; ++e) x[e] = __float_as_uint(__uint_as_float(x[e]) * f);
-                            tmem_st8(to + 8 * c, x);
+                                for (int e = 0; e < 8; ++e) x[e] = __float_as_uint(__uint_as_float(x[e]) * f);
+                                tmem_st8(to + 8 * c, x);
+                            }
                         }
                     }
-                }
-                const float ref = row_m == -INFINITY ? 0.f : row_m;
-                auto weigh = [&](const uint32_t (&x)[32], int c) {
-                    uint32_t p[16];
+                    const float ref = row_m == -INFINITY ? 0.f : row_m;
+                    auto weigh = [&](const uint32_t (&x)[32], int c, float f0, float b0, float i0, float f1, float b1, float i1) {
+                        uint32_t p[16];
 #pragma unroll
-                    for (int y = 0; y < 2; ++y) {
-                        float f, b, iv;
-                        factors(2 * c + y, f, b, iv);
-                        const uint64_t ff = pair_of(f, f), bb = pair_of(b - ref, b - ref);
-                        uint64_t s0 = 0, s1 = 0;  // two pairs of partial sums
+                        for (int y = 0; y < 2; ++y) {
+                            const uint64_t ff = y ? pair_of(f1, f1) : pair_of(f0, f0), bb = y ? pair_of(b1, b1) : pair_of(b0, b0);
+                            uint64_t s0 = 0, s1 = 0;  // two pairs of partial sums
 #pragma unroll
-                        for (int e = 0; e < 16; e += 4) {
-                            float2 u = split_pair(fma_pair(pair_of(__uint_as_float(x[16 * y + e]), __uint_as_float(x[16 * y + e + 1])), ff, bb));
-                            float2 v = split_pair(fma_pair(pair_of(__uint_as_float(x[16 * y + e + 2]), __uint_as_float(x[16 * y + e + 3])), ff, bb));
-                            u.x = exp2_of(u.x); u.y = exp2_of(u.y); v.x = exp2_of(v.x); v.y = exp2_of(v.y);
-                            s0 = add_pair(s0, pair_of(u.x, u.y));
-                            s1 = add_pair(s1, pair_of(v.x, v.y));
-                            p[8 * y + e / 2] = pack2<KVL_TYPE_HALF>(u.x, u.y);
-                            p[8 * y + e / 2 + 1] = pack2<KVL_TYPE_HALF>(v.x, v.y);
+                            for (int e = 0; e < 16; e += 4) {
+                                float2 u = split_pair(fma_pair(pair_of(__uint_as_float(x[16 * y + e]), __uint_as_float(x[16 * y + e + 1])), ff, bb));
+                                float2 v = split_pair(fma_pair(pair_of(__uint_as_float(x[16 * y + e + 2]), __uint_as_float(x[16 * y + e + 3])), ff, bb));
+                                u.x = exp2_of(u.x); u.y = exp2_of(u.y); v.x = exp2_of(v.x); v.y = exp2_of(v.y);
+                                s0 = add_pair(s0, pair_of(u.x, u.y));
+                                s1 = add_pair(s1, pair_of(v.x, v.y));
+                                p[8 * y + e / 2] = pack2<KVL_TYPE_HALF>(u.x, u.y);
+                                p[8 * y + e / 2 + 1] = pack2<KVL_TYPE_HALF>(v.x, v.y);
+                            }
+                            const float2 sum = split_pair(add_pair(s0, s1));
+                            row_l = fmaf(sum.x + sum.y, y ? i1 : i0, row_l);
                         }
-                        const float2 sum = split_pair(add_pair(s0, s1));
-                        row_l = fmaf(sum.x + sum.y, iv, row_l);
+                        tmem_st16(ts + 16 * c, p);
+                    };
+                    asm volatile("" ::: "memory");  // the groups' factors are read again rather than kept in registers
+                    {
+                        float f[4], b[4], iv[4];
+                        factors(0, f, b, iv);
+                        weigh(x0, 0, f[0], b[0] - ref, iv[0], f[1], b[1] - ref, iv[1]);
+                        weigh(x1, 1, f[2], b[2] - ref, iv[2], f[3], b[3] - ref, iv[3]);
                     }
-                    tmem_st16(ts + 16 * c, p);
+                    {
+                        float f[4], b[4], iv[4];
+                        factors(4, f, b, iv);
+                        weigh(x2, 2, f[0], b[0] - ref, iv[0], f[1], b[1] - ref, iv[1]);
+                        weigh(x3, 3, f[2], b[2] - ref, iv[2], f[3], b[3] - ref, iv[3]);
+                    }
+                    return true;
                 };
-                asm volatile("" ::: "memory");  // the groups' factors are read again rather than kept in registers
-                weigh(x0, 0);
-                weigh(x1, 1);
-                weigh(x2, 2);
-                weigh(x3, 3);
+                ok = whole ? weights(std::true_type{}) : weights(std::false_type{});
+                if (!ok) break;
                 tmem_wait_st();
                 tmem_fence_before();
                 __syncwarp();
@@ -803,11 +869,12 @@ __global__ void __launch_bounds__(kThreads, 1) attend_chunk_kernel(const __grid_
                     }
                 }
             }
-            const int64_t row = job.row_base + r;
+            const uint32_t row = job.row_base + r, tok = row / uint32_t(G);
+            const int64_t out_row = e_.row0 + tok;
+            const int head = h * G + int(row - tok * G);
             const float inv = row_l == 0.f ? 0.f : 1.f / row_l;
             float *part = a.parts + (int64_t(blockIdx.x) * 2 + (job.sa == 0 ? 1 : 0)) * C::kPartFloats;
-            uint8_t *dst = static_cast<uint8_t *>(a.attn.out.data) + (e_.row0 + row / G) * a.attn.out.row_stride +
-                           (h * G + row % G) * a.attn.out.head_stride;
+            uint8_t *dst = static_cast<uint8_t *>(a.attn.out.data) + out_row * a.attn.out.row_stride + head * a.attn.out.head_stride;
             if (ok) {
 #pragma unroll
                 for (int c = 0; c < D / 32; ++c) {
@@ -841,7 +908,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_chunk_kernel(const __grid_
                         part[r] = row_m;
                         part[kJobRows + r] = row_l;
                     } else if (a.attn.lse) {
-                        a.attn.lse[(e_.row0 + row / G) * a.attn.n_heads + h * G + row % G] =
+                        a.attn.lse[out_row * a.attn.n_heads + head] =
                             row_l == 0.f ? -INFINITY : (row_m + __log2f(row_l)) * (1.f / kLog2e);
                     }
                 }
@@ -884,9 +951,10 @@ __global__ void __launch_bounds__(kThreads, 1) attend_chunk_kernel(const __grid_
                         }
                     }
                     const float inv = sum == 0.f ? 0.f : 1.f / sum;
-                    const int64_t row = job.row_base + r;
-                    const int head = int(job.h * G + row % G);
-                    uint8_t *dst = static_cast<uint8_t *>(a.attn.out.data) + (job.e.row0 + row / G) * a.attn.out.row_stride +
+                    const uint32_t row = job.row_base + r, tok = row / uint32_t(G);
+                    const int64_t out_row = job.e.row0 + tok;
+                    const int head = job.h * G + int(row - tok * G);
+                    uint8_t *dst = static_cast<uint8_t *>(a.attn.out.data) + out_row * a.attn.out.row_stride +
                                    head * a.attn.out.head_stride + 64 * c;
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
@@ -895,7 +963,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_chunk_kernel(const __grid_
                         if (32 * c + 8 * e < d) store8<TYPE>(dst + 16 * e, w);
                     }
                     if (a.attn.lse && c == 0)
-                        a.attn.lse[(job.e.row0 + row / G) * a.attn.n_heads + head] =
+                        a.attn.lse[out_row * a.attn.n_heads + head] =
                             sum == 0.f ? -INFINITY : (big + __log2f(sum)) * (1.f / kLog2e);
                 }
             }
