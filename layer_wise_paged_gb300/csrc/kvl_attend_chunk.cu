@@ -58,7 +58,7 @@ struct Chunk {
 };
 
 // Barriers (each in its own 8 bytes).
-enum Bar { K_FULL = 0, K_EMPTY = 2, V_FULL = 4, V_EMPTY = 6, S_FULL = 8, P_FULL = 10, PV_DONE = 12, TURN = 14, LEAVE = 16, BARS = 17 };
+enum Bar { K_FULL = 0, K_EMPTY = 2, V_FULL = 4, V_EMPTY = 6, S_FULL = 8, PV_DONE = 10, LEAVE = 12, BARS = 13 };
 
 // ---- tensor-core wrappers -------------------------------------------------------------------
 
@@ -153,6 +153,14 @@ __device__ __forceinline__ void tmem_st16(uint32_t at, const uint32_t (&r)[16])
         "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(at)
         : "memory");
 }
+
+// Named barriers between warps of a softmax warpgroup (1 + g: its weights are written; the issuing warp
+// waits, the others only arrive) and between the two issuing warps (3 + g: tile g's turn).  They are
+// not in shared memory, where an access takes 200 cycles while products stream their operands.
+template <int N>
+__device__ __forceinline__ void meet_wait(int id) { asm volatile("bar.sync %0, %1;" ::"r"(id), "n"(N) : "memory"); }
+template <int N>
+__device__ __forceinline__ void meet_arrive(int id) { asm volatile("bar.arrive %0, %1;" ::"r"(id), "n"(N) : "memory"); }
 
 __device__ __forceinline__ float max3(float a, float b, float c)
 {
@@ -437,9 +445,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_chunk_kernel(const __grid_
         for (int g = 0; g < 2; ++g) {
             mbar_init(bar + 8 * (S_FULL + g), 2);   // product done, and the issuing thread (which has seen the
                                                     // step's places: K_FULL's release reaches the softmax by it)
-            mbar_init(bar + 8 * (P_FULL + g), 4);   // the tile's softmax warps
             mbar_init(bar + 8 * (PV_DONE + g), 1);
-            mbar_init(bar + 8 * (TURN + g), 1);     // the other tile's products of the step before are issued
         }
         mbar_init(bar + 8 * LEAVE, 1);
         fence_mbar_init();
@@ -650,7 +656,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_chunk_kernel(const __grid_
             const int g = warp >> 2, r = tid & 255;  // (uniform: warp is)
             const uint32_t lanes = uint32_t(warp & 3) << 21;  // lane 32 (warp % 4), in bits 16 and up
             const uint32_t ts = tmem + lanes + g * 128, to = tmem + lanes + 256 + g * 128;
-            const uint32_t it = job.it, it_g1 = job.it_g[1], it_g = g ? it_g1 : job.it_g[0];
+            const uint32_t it = job.it, it_g = g ? job.it_g[1] : job.it_g[0];
             const int n = job.n;
             int lo, hi;
             {
@@ -668,26 +674,29 @@ __global__ void __launch_bounds__(kThreads, 1) attend_chunk_kernel(const __grid_
                 mma_commit(one, bar + 8 * which);
                 if (!job.two && one) mbar_arrive(bar + 8 * which);  // for the tile without rows
             };
+            auto await = [&](int which, int s) {  // K or V of step s is converted
+                const uint32_t k = it_u + s;
+                return bool(__all_sync(0xffffffffu, wait_bar(bar + 8 * (which + k % kStages), (k / kStages) & 1, gone)));
+            };
             auto scores = [&](int s) {  // S = Q K^T of step s
-                const uint32_t k = it_u + s, st = k % kStages;
-                if (!__all_sync(0xffffffffu, wait_bar(bar + 8 * (K_FULL + st), (k / kStages) & 1, gone))) return;
-                tmem_fence_after();
+                const uint32_t st = (it_u + s) % kStages;
                 const uint32_t one = elect_one();
                 issue_scores<D>(one, sm, g, st);
                 mma_commit(one, bar + 8 * (S_FULL + g));
-                if (one) mbar_arrive(bar + 8 * (S_FULL + g));
                 done(one, K_EMPTY + st);
+                if (one) mbar_arrive(bar + 8 * (S_FULL + g));
             };
             auto values = [&](int s) {  // O += P V of step s
-                const uint32_t k = it_u + s, st = k % kStages;
-                if (!__all_sync(0xffffffffu, wait_bar(bar + 8 * (V_FULL + st), (k / kStages) & 1, gone))) return;
-                tmem_fence_after();
+                const uint32_t st = (it_u + s) % kStages;
                 const uint32_t one = elect_one();
                 issue_values<D>(one, sm, g, st, s > 0);
                 mma_commit(one, bar + 8 * (PV_DONE + g));
                 done(one, V_EMPTY + st);
             };
-            if (leads) scores(0);
+            if (leads && await(K_FULL, 0)) {
+                tmem_fence_after();
+                scores(0);
+            }
             bool ok = true;
             for (int s = 0; s < n; ++s) {
                 const uint32_t ph = (it_g + s) & 1;
@@ -711,21 +720,30 @@ __global__ void __launch_bounds__(kThreads, 1) attend_chunk_kernel(const __grid_
                                 if (e < first || e >= past) x[16 * y + e] = 0xff800000u;  // -infinity
                         }
                     };
-                    // f, b (and 1 / scale) of groups gi .. gi + 3; a group the row does not see at all gets
-                    // harmless ones, as its page's scales may be anything
-                    auto factors = [&](int gi, float (&f)[4], float (&b)[4], float (&iv)[4]) {
-                        const float4 k4 = *reinterpret_cast<const float4 *>(pl.ks + gi), l4 = *reinterpret_cast<const float4 *>(pl.lvs + gi);
-                        const float4 i4 = *reinterpret_cast<const float4 *>(pl.ivs + gi);
-                        f[0] = k4.x * cq; f[1] = k4.y * cq; f[2] = k4.z * cq; f[3] = k4.w * cq;
-                        b[0] = l4.x; b[1] = l4.y; b[2] = l4.z; b[3] = l4.w;
+                    // f and b of the groups; a group the row does not see at all gets harmless ones, as its
+                    // page's scales may be anything
+                    float f[kGroups], b[kGroups], iv[4];
+#pragma unroll
+                    for (int y = 0; y < kGroups; y += 4) {
+                        const float4 k4 = *reinterpret_cast<const float4 *>(pl.ks + y), l4 = *reinterpret_cast<const float4 *>(pl.lvs + y);
+                        f[y] = k4.x * cq; f[y + 1] = k4.y * cq; f[y + 2] = k4.z * cq; f[y + 3] = k4.w * cq;
+                        b[y] = l4.x; b[y + 1] = l4.y; b[y + 2] = l4.z; b[y + 3] = l4.w;
+                    }
+                    auto unseen = [&](int y) { return min(hi - pl.t0[y], pl.nv[y]) <= max(lo - pl.t0[y], 0); };
+                    if constexpr (!kWhole) {
+#pragma unroll
+                        for (int y = 0; y < kGroups; ++y) {
+                            f[y] = f[y] < 1e-37f ? 1e-37f : f[y];  // keeps -infinity * f from being a NaN
+                            if (unseen(y)) { f[y] = 1.f; b[y] = 0.f; }
+                        }
+                    }
+                    auto inverses = [&](int y) {  // 1 / scale of groups y .. y + 3
+                        const float4 i4 = *reinterpret_cast<const float4 *>(pl.ivs + y);
                         iv[0] = i4.x; iv[1] = i4.y; iv[2] = i4.z; iv[3] = i4.w;
                         if constexpr (!kWhole) {
 #pragma unroll
-                            for (int y = 0; y < 4; ++y) {
-                                f[y] = f[y] < 1e-37f ? 1e-37f : f[y];  // keeps -infinity * f from being a NaN
-                                const int first = max(lo - pl.t0[gi + y], 0), past = min(hi - pl.t0[gi + y], pl.nv[gi + y]);
-                                if (past <= first) { f[y] = 1.f; b[y] = 0.f; iv[y] = 0.f; }
-                            }
+                            for (int x = 0; x < 4; ++x)
+                                if (unseen(y + x)) iv[x] = 0.f;
                         }
                     };
                     float big = -INFINITY;
@@ -751,20 +769,13 @@ __global__ void __launch_bounds__(kThreads, 1) attend_chunk_kernel(const __grid_
                     tmem_ld32(ts + 64, x2);
                     tmem_ld32(ts + 96, x3);
                     if constexpr (!kWhole) { hide(x0, 0); hide(x1, 2); }
-                    {
-                        float f[4], b[4], iv[4];
-                        factors(0, f, b, iv);
-                        largest(x0, f[0], b[0], f[1], b[1]);
-                        largest(x1, f[2], b[2], f[3], b[3]);
-                    }
+                    largest(x0, f[0], b[0], f[1], b[1]);
+                    largest(x1, f[2], b[2], f[3], b[3]);
                     tmem_wait_ld();
                     if constexpr (!kWhole) { hide(x2, 4); hide(x3, 6); }
-                    {
-                        float f[4], b[4], iv[4];
-                        factors(4, f, b, iv);
-                        largest(x2, f[0], b[0], f[1], b[1]);
-                        largest(x3, f[2], b[2], f[3], b[3]);
-                    }
+                    largest(x2, f[4], b[4], f[5], b[5]);
+                    largest(x3, f[6], b[6], f[7], b[7]);
+                    inverses(0);
                     const bool grow = big > row_m + kSlack || (row_m == -INFINITY && big > -INFINITY);
                     if (__any_sync(0xffffffffu, grow)) {
                         const float m = grow ? big + kHead : row_m;
@@ -807,36 +818,40 @@ __global__ void __launch_bounds__(kThreads, 1) attend_chunk_kernel(const __grid_
                         }
                         tmem_st16(ts + 16 * c, p);
                     };
-                    asm volatile("" ::: "memory");  // the groups' factors are read again rather than kept in registers
-                    {
-                        float f[4], b[4], iv[4];
-                        factors(0, f, b, iv);
-                        weigh(x0, 0, f[0], b[0] - ref, iv[0], f[1], b[1] - ref, iv[1]);
-                        weigh(x1, 1, f[2], b[2] - ref, iv[2], f[3], b[3] - ref, iv[3]);
-                    }
-                    {
-                        float f[4], b[4], iv[4];
-                        factors(4, f, b, iv);
-                        weigh(x2, 2, f[0], b[0] - ref, iv[0], f[1], b[1] - ref, iv[1]);
-                        weigh(x3, 3, f[2], b[2] - ref, iv[2], f[3], b[3] - ref, iv[3]);
-                    }
+#pragma unroll
+                    for (int y = 0; y < kGroups; ++y) b[y] -= ref;
+                    weigh(x0, 0, f[0], b[0], iv[0], f[1], b[1], iv[1]);
+                    const float iv2 = iv[2], iv3 = iv[3];
+                    inverses(4);
+                    weigh(x1, 1, f[2], b[2], iv2, f[3], b[3], iv3);
+                    weigh(x2, 2, f[4], b[4], iv[0], f[5], b[5], iv[1]);
+                    weigh(x3, 3, f[6], b[6], iv[2], f[7], b[7], iv[3]);
                     return true;
                 };
                 ok = whole ? weights(std::true_type{}) : weights(std::false_type{});
                 if (!ok) break;
                 tmem_wait_st();
                 tmem_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(bar + 8 * (P_FULL + g));
-                if (leads && __all_sync(0xffffffffu, wait_bar(bar + 8 * (P_FULL + g), ph, gone))) {
-                    // The tiles take turns: a tile's two products run one after the other, not mixed with the
-                    // other tile's, so one tile is at its softmax while the other is at its products
-                    // (mixed, both wait for both: 341 us instead of 233 for 512 rows on 31,232).
-                    const uint32_t turn = it_g1 + s - (g == 0);
-                    if (job.two && (g == 1 || s > 0) && !__all_sync(0xffffffffu, wait_bar(bar + 8 * (TURN + g), turn & 1, gone))) break;
-                    values(s);
-                    if (s + 1 < n) scores(s + 1);
-                    if (job.two && lane == 0) mbar_arrive(bar + 8 * (TURN + 1 - g));
+                if (!leads) {
+                    meet_arrive<128>(1 + g);
+                    continue;
+                }
+                const bool more = s + 1 < n;
+                if (!(ok = await(V_FULL, s) && (!more || await(K_FULL, s + 1)))) break;
+                meet_wait<128>(1 + g);
+                // The tiles take turns: a tile's two products run one after the other, not mixed with the
+                // other tile's, so one tile is at its softmax while the other is at its products.
+                if (job.two && (g == 1 || s > 0)) meet_wait<64>(3 + g);
+                tmem_fence_after();
+                values(s);
+                if (more) scores(s + 1);
+                if (job.two && (g == 0 || more)) meet_arrive<64>(4 - g);
+            }
+            if (!ok) {  // given up: nobody is left waiting for this warp
+                if (leads) {
+                    if (job.two) meet_arrive<64>(4 - g);
+                } else {
+                    meet_arrive<128>(1 + g);
                 }
             }
             if (ok) {
