@@ -49,6 +49,15 @@ __device__ __forceinline__ int32_t group_of(int32_t token, int32_t B, int32_t pe
 
 __device__ __forceinline__ int64_t units_of(const Cost &c, int H) { return int64_t(H) * c.tiles * c.groups; }
 
+// 16 bytes into shared memory; zeros where !ok (src has to be a valid address all the same).
+__device__ __forceinline__ void copy_async16(uint32_t dst, const void *src, bool ok)
+{
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(ok ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void copy_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copy_async_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+
 // 2^x; -infinity gives 0.
 __device__ __forceinline__ float exp2_of(float x)
 {

@@ -32,7 +32,10 @@ constexpr int kGroups = kSlots / kGroup;    // 8
 constexpr int kStages = 2;
 constexpr int kPlaces = 4;                  // steps whose scales are kept (see place_full)
 constexpr int kBatch = 512;                 // entries whose steps are held at a time
-constexpr int kStepsPerCta = 2;             // a share is at least this many steps
+// Units of a share: a job's steps, and kJobCost before them for starting it (finding it, loading Q,
+// filling the pipeline).
+constexpr int kJobCost = 4;
+constexpr int kStepsPerCta = kJobCost + 2;  // a share is at least this many units
 // A row's reference is set kHead above its largest x so far and moved only when an x passes it by
 // kSlack: weights up to 2^14 are halves still, and those below 2^-14 keep 2^-25 of the largest
 // weight's 2^-4 or more.  With the reference at the maximum and a slack of 8, one of a warpgroup's
@@ -250,11 +253,11 @@ __device__ __forceinline__ int32_t tiles_of(const AttendArgs &a, const Entry &e)
     return rows > a.max_rows ? (rows + kJobRows - 1) / kJobRows : 0;
 }
 
-// Steps of one KV head of an entry, all tiles: a warp's lanes take a tile each.
-__device__ __forceinline__ int64_t warp_steps(const AttendArgs &a, int32_t len, int32_t fresh, int32_t tiles, int lane)
+// Units of one KV head of an entry, all tiles: a warp's lanes take a tile each.
+__device__ __forceinline__ int64_t warp_units(const AttendArgs &a, int32_t len, int32_t fresh, int32_t tiles, int lane)
 {
     int64_t n = 0;
-    for (int t = lane; t < tiles; t += 32) n += tile_of(a, len, fresh, t).steps;
+    for (int t = lane; t < tiles; t += 32) n += tile_of(a, len, fresh, t).steps + kJobCost;
 #pragma unroll
     for (int o = 16; o; o >>= 1) n += __shfl_xor_sync(0xffffffffu, n, o);
     return n;
@@ -265,7 +268,8 @@ __device__ __forceinline__ int64_t warp_steps(const AttendArgs &a, int32_t len, 
 struct Job {
     int64_t u, u_end, off;    // next unit, the share's end, units of the entry before u
     int64_t total, shares;
-    int64_t u0;               // the job's first unit
+    int64_t u0;               // the unit of the job's first step
+    int32_t taken;            // units of the job in this share
     int32_t row_base;         // the tile's first row
     Entry e;
     Tile t;
@@ -276,7 +280,8 @@ struct Job {
     bool complete;            // the share holds the whole job
 };
 
-// The job that holds unit job.u; called by one whole warp.
+// The job that holds unit job.u, of which this share has the units from there on; n = 0 where they are
+// only units before its steps.  Called by one whole warp.
 __device__ __forceinline__ void next_job(const AttendArgs &a, Job &job, int lane)
 {
     const int H = a.cache.n_kv_heads, B = a.cache.block_tokens;
@@ -284,19 +289,19 @@ __device__ __forceinline__ void next_job(const AttendArgs &a, Job &job, int lane
     int entry = job.entry;
     Entry e = load_entry(a.seqs, B, entry, nullptr);
     int32_t tiles = tiles_of(a, e);
-    int64_t steps = warp_steps(a, e.len, e.fresh, tiles, lane);
-    while (off >= H * steps) {
-        off -= H * steps;
+    int64_t units = warp_units(a, e.len, e.fresh, tiles, lane);
+    while (off >= H * units) {
+        off -= H * units;
         e = load_entry(a.seqs, B, ++entry, nullptr);
         tiles = tiles_of(a, e);
-        steps = warp_steps(a, e.len, e.fresh, tiles, lane);
+        units = warp_units(a, e.len, e.fresh, tiles, lane);
     }
-    const int h = int(off / steps);
-    int64_t rest = off - h * steps;
-    // the tile whose steps hold `rest`: 32 tiles at a time
+    const int h = int(off / units);
+    int64_t rest = off - h * units;
+    // the tile whose units hold `rest`: 32 tiles at a time
     int tile = 0;
     for (int base = 0; base < tiles; base += 32) {
-        const int n = base + lane < tiles ? tile_of(a, e.len, e.fresh, base + lane).steps : 0;
+        const int n = base + lane < tiles ? tile_of(a, e.len, e.fresh, base + lane).steps + kJobCost : 0;
         int sum = n;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -314,14 +319,16 @@ __device__ __forceinline__ void next_job(const AttendArgs &a, Job &job, int lane
     }
     if (lane == 0) {
         const Tile t = tile_of(a, e.len, e.fresh, tile);
+        const int64_t taken = min(int64_t(t.steps + kJobCost) - rest, job.u_end - job.u);
         job.off = off;
         job.entry = entry;
         job.e = e;
         job.t = t;
         job.h = h;
-        job.sa = int(rest);
-        job.n = int(min(int64_t(t.steps) - rest, job.u_end - job.u));
-        job.u0 = job.u - rest;
+        job.sa = max(0, int(rest) - kJobCost);
+        job.n = max(0, int(rest + taken) - kJobCost) - job.sa;
+        job.taken = int(taken);
+        job.u0 = job.u - rest + kJobCost;
         job.row_base = tile * kJobRows;
         job.pos0 = e.len - e.fresh;
         job.two = t.rows > kTileRows;
@@ -369,7 +376,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_chunk_kernel(const __grid_
     __shared__ __align__(8) unsigned long long bars[BARS];
     __shared__ Places places[kPlaces];
     __shared__ float s_cq[kJobRows];
-    __shared__ uint32_t s_steps[kBatch];
+    __shared__ uint32_t s_units[kBatch];
     __shared__ Job job;
     __shared__ int s_last, s_gone, s_nan;
     __shared__ uint32_t s_tmem;
@@ -389,14 +396,14 @@ __global__ void __launch_bounds__(kThreads, 1) attend_chunk_kernel(const __grid_
                 __syncthreads();
                 for (int i = warp; i < n; i += kThreads / 32) {
                     const Entry e = load_entry(a.seqs, B, base + i, pass == 0 && blockIdx.x == 0 && lane == 0 ? a.report : nullptr);
-                    const int64_t steps = warp_steps(a, e.len, e.fresh, tiles_of(a, e), lane);
-                    if (lane == 0) s_steps[i] = uint32_t(min(steps, int64_t(0xffffffffu)));
+                    const int64_t units = warp_units(a, e.len, e.fresh, tiles_of(a, e), lane);
+                    if (lane == 0) s_units[i] = uint32_t(min(units, int64_t(0xffffffffu)));
                 }
                 __syncthreads();
             }
             // 32 lanes scan the batch; every warp does, and finds the same
             for (int i = 0; i < n; i += 32) {
-                int64_t x = i + lane < n ? int64_t(s_steps[i + lane]) * H : 0, sum = x;
+                int64_t x = i + lane < n ? int64_t(s_units[i + lane]) * H : 0, sum = x;
 #pragma unroll
                 for (int o = 1; o < 32; o <<= 1) {
                     const int64_t y = __shfl_up_sync(0xffffffffu, sum, o);
@@ -473,28 +480,49 @@ __global__ void __launch_bounds__(kThreads, 1) attend_chunk_kernel(const __grid_
         if (warp == 0) next_job(a, job, lane);
         if (tid == 0) s_nan = 0;
         __syncthreads();
+        if (job.n == 0) {  // its steps are the next share's
+            if (job.u + job.taken >= job.u_end) break;
+            __syncthreads();
+            if (tid == 0) {
+                job.off += job.taken;
+                job.u += job.taken;
+            }
+            __syncthreads();
+            continue;
+        }
 
         // ---- Q: each row scaled by a power of two into the range of a half (undone in s_cq)
         {
             const int rows = job.t.rows, h = job.h, row0 = job.e.row0, row_base = job.row_base;
             constexpr int kLanes = D / 8, kPer = 32 / kLanes;  // lanes of a row, rows of a warp's vector
             const int at = (lane % kLanes) * 8;
-#pragma unroll 4
-            for (int r0 = warp * kPer; r0 < kJobRows; r0 += kThreads / 32 * kPer) {
-                const int r = r0 + lane / kLanes;
+            constexpr int kTurns = (kJobRows / kPer + kThreads / 32 - 1) / (kThreads / 32);
+            // All rows come by asynchronous copies into the (free) K and V stages, each vector to the thread
+            // that takes it on from there: short loops, as this code runs once a job and is fetched anew.
+            const uint32_t stage = sm + C::kK + tid * 16;
+#pragma unroll 1
+            for (int x = 0; x < kTurns; ++x) {
+                const int r = (warp + x * (kThreads / 32)) * kPer + lane / kLanes;
+                const bool ok = r < rows && at < d;
+                const uint32_t row = ok ? row_base + r : 0, tok = row / uint32_t(G);
+                copy_async16(stage + x * (kThreads * 16),
+                             static_cast<const uint8_t *>(a.attn.q.data) + int64_t(row0 + tok) * a.attn.q.row_stride +
+                                 int64_t(h * G + row - tok * G) * a.attn.q.head_stride + (ok ? 2 * at : 0), ok);
+            }
+            copy_async_commit();
+            copy_async_wait<0>();
+#pragma unroll 1
+            for (int x = 0; x < kTurns; ++x) {
+                const int r = (warp + x * (kThreads / 32)) * kPer + lane / kLanes;
+                const uint4 raw = ld_shared_v4(stage + x * (kThreads * 16));
                 float v[8];
-#pragma unroll
-                for (int x = 0; x < 8; ++x) v[x] = 0.f;
-                if (r < rows && at < d) {
-                    const uint32_t row = row_base + r, tok = row / uint32_t(G);
-                    load8<TYPE>(static_cast<const uint8_t *>(a.attn.q.data) + int64_t(row0 + tok) * a.attn.q.row_stride +
-                                    int64_t(h * G + row - tok * G) * a.attn.q.head_stride + 2 * at, v);
-                }
+                load8<TYPE>(reinterpret_cast<const uint8_t *>(&raw), v);
                 float amax = 0.f;
 #pragma unroll
-                for (int x = 0; x < 8; ++x) amax = fmaxf(amax, fabsf(v[x]));
+                for (int y = 0; y < 8; ++y) amax = fmaxf(amax, fabsf(v[y]));
 #pragma unroll
                 for (int o = kLanes / 2; o; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+                if (r >= kJobRows) continue;
                 const uint32_t ex = (__float_as_uint(amax) >> 23) & 0xffu;
                 const bool plain = ex < 2 || ex > 252;
                 const float up = plain ? 1.f : __uint_as_float((254u - ex) << 23);
@@ -989,8 +1017,8 @@ __global__ void __launch_bounds__(kThreads, 1) attend_chunk_kernel(const __grid_
             job.it += job.n;
             job.it_g[0] += job.n;
             if (job.two) job.it_g[1] += job.n;
-            job.off += job.n;
-            job.u += job.n;
+            job.off += job.taken;
+            job.u += job.taken;
         }
         __syncthreads();
         if (*gone || job.u >= job.u_end) break;
