@@ -63,12 +63,12 @@ extern "C" kvl_status kvl_attend(const kvl_cache *cache, int32_t layer, const kv
     // which launches can be left out.
     const int64_t bound = attn->max_new > 0 && attn->max_new < seqs->n_rows ? attn->max_new : seqs->n_rows;
     const int64_t most = bound * (attn->n_heads / cache->n_kv_heads);
-    if (cache->head_dim > 128 || most <= kChunkRows) return launch_attend_rows(a, sms, stream);
+    if (cache->head_dim > 128 || most <= kChunkRows) return launch_attend_rows(a, most, sms, stream);
     if (seqs->n_seq == 1) {
         a.max_rows = 0;
         return launch_attend_chunk(a, sms, stream);
     }
     a.max_rows = kChunkRows;
     s = launch_attend_chunk(a, sms, stream);
-    return s ? s : launch_attend_rows(a, sms, stream);
+    return s ? s : launch_attend_rows(a, kChunkRows, sms, stream);
 }

@@ -73,7 +73,8 @@ __device__ __forceinline__ float v_scale(float s) { return s < kTinyScale ? kTin
 }  // namespace
 
 size_t attend_rows_part_bytes(int head_dim);  // for each SM
-kvl_status launch_attend_rows(const AttendArgs &a, int sms, void *stream);
+// most: a bound on the rows (as max_rows) of an entry, which chooses the row tile.
+kvl_status launch_attend_rows(const AttendArgs &a, int64_t most, int sms, void *stream);
 size_t attend_chunk_part_bytes(int head_dim);
 kvl_status launch_attend_chunk(const AttendArgs &a, int sms, void *stream);
 

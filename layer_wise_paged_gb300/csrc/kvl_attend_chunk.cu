@@ -613,8 +613,10 @@ __global__ void __launch_bounds__(kThreads, 1) attend_chunk_kernel(const __grid_
                     const int r = cw * 32 + x * kPer + rw;
                     const uint32_t w[4] = {reg[x].x, reg[x].y, reg[x].z, reg[x].w};
                     uint4 lo, hi;
-                    lo.x = codes_lo<CODE>(w[0]); lo.y = codes_hi<CODE>(w[0]); lo.z = codes_lo<CODE>(w[1]); lo.w = codes_hi<CODE>(w[1]);
-                    hi.x = codes_lo<CODE>(w[2]); hi.y = codes_hi<CODE>(w[2]); hi.z = codes_lo<CODE>(w[3]); hi.w = codes_hi<CODE>(w[3]);
+                    codes_of<CODE>(w[0], lo.x, lo.y);
+                    codes_of<CODE>(w[1], lo.z, lo.w);
+                    codes_of<CODE>(w[2], hi.x, hi.y);
+                    codes_of<CODE>(w[3], hi.z, hi.w);
                     uint8_t *p = dst + (ch >> 2) * (kTileRows * 128) + r * 128;
                     const int un = (ch & 3) * 2;
                     *reinterpret_cast<uint4 *>(p + ((un ^ (r & 7)) << 4)) = lo;

@@ -24,17 +24,18 @@
 namespace kvl {
 namespace {
 
-constexpr int kWarps = 8;
+constexpr int kWarps = 6;
 constexpr int kThreads = kWarps * 32;
-constexpr int kStages = 3;
-constexpr int kCtasPerSm = 2;
-constexpr int kUnitsPerCta = 16;  // a share is at least two groups a warp
+constexpr int kPair = 2;          // groups a warp takes at a time
+constexpr int kStages = 2;        // pairs in its ring: one worked on, one on its way
+constexpr int kCtasPerSm = 2;     // 12 warps an SM: 168 registers a thread, 192 KB of rings at d = 128
+constexpr int kUnitsPerCta = kPair * kWarps;  // a share is at least a pair for each warp
 
 template <int D, int NT>
 struct Shape {
     static constexpr int kRows = 8 * NT;
     static constexpr int kGroupBytes = kGroup * D;            // K or V of a group
-    static constexpr int kRing = kStages * 2 * kGroupBytes;   // one warp's ring
+    static constexpr int kRing = kStages * kPair * 2 * kGroupBytes;  // one warp's ring
     static constexpr int kORow = D + 4;                       // floats; the pad spreads rows over banks
     static constexpr int kOBytes = kRows * kORow * 4;         // one warp's O, over its ring
     static constexpr int kWarpBytes = kRing > kOBytes ? kRing : kOBytes;
@@ -99,7 +100,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attend_rows_kernel(const
     using S = Shape<D, NT>;
     constexpr int kRows = S::kRows, kChunks = D / 16, kLaneBytes = D / 8;
     extern __shared__ __align__(128) uint8_t smem[];
-    __shared__ int64_t s_scan[kWarps], s_off;
+    __shared__ int64_t s_scan[kWarps], s_off, s_u, s_end;
     __shared__ int s_entry, s_last;
     __shared__ float s_m[kWarps][kRows], s_l[kWarps][kRows], s_cq[kRows];
 
@@ -129,20 +130,37 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attend_rows_kernel(const
     }
     const int64_t shares = min(int64_t(gridDim.x), (total + kUnitsPerCta - 1) / kUnitsPerCta);
     if (int64_t(blockIdx.x) >= shares) return;
-    int64_t u = total * blockIdx.x / shares;
-    const int64_t u_end = total * (blockIdx.x + 1) / shares;
-    if (u >= before && u < before + mine) {
-        int64_t at = before;
-        int i = i0;
-        for (; i < i1; ++i) {
-            const int64_t n = units_of(cost_of<NT>(a, i, nullptr), H);
-            if (u < at + n) break;
-            at += n;
+    // The share's first unit and the next share's: where one falls inside a job of few groups it moves to
+    // the job's start (small jobs are not split; what a job's parts are does not change by it).
+    int64_t u = total * blockIdx.x / shares, u_end = total * (blockIdx.x + 1) / shares;
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+        const int64_t x = k ? u_end : u;
+        if (x >= before && x < before + mine) {
+            int64_t at = before, n = 0;
+            Cost q;
+            int i = i0;
+            for (; i < i1; ++i) {
+                q = cost_of<NT>(a, i, nullptr);
+                n = units_of(q, H);
+                if (x < at + n) break;
+                at += n;
+            }
+            int64_t off = x - at;
+            if (q.groups <= kUnitsPerCta) off -= off % q.groups;
+            if (k) {
+                s_end = at + off;
+            } else {
+                s_entry = i;
+                s_off = off;
+                s_u = at + off;
+            }
         }
-        s_entry = i;
-        s_off = u - at;
     }
+    if (tid == 0 && u_end == total) s_end = total;
     __syncthreads();
+    u = s_u;
+    u_end = s_end;
     int entry = s_entry;
     int64_t off = s_off;  // units of the entry before u
     Cost c = cost_of<NT>(a, entry, nullptr);
@@ -165,15 +183,16 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attend_rows_kernel(const
         const int rows = min(kRows, c.e.fresh * G - tile * kRows);
         const int pos0 = c.e.len - c.e.fresh;
 
-        // ---- groups of this warp: ga + warp + kWarps * k.  Lane k holds the k-th's page, scales
-        // and place; the next 32 are fetched while these are worked on.
-        const int count = (gb - ga - warp + kWarps - 1) / kWarps;  // may be <= 0
-        auto place_of = [&](int k, int &t0, int &nv) -> int32_t {  // page of the k-th group, -1: none
+        // ---- groups of this warp: pair k holds ga + 2 (warp + kWarps k) and the next.  Lane l looks after
+        // group l % 2 of pair l / 2 of a batch of 16: its page, scales and place; the next batch's are
+        // fetched while this one is worked on.
+        const int count = (gb - ga - kPair * warp + kPair * kWarps - 1) / (kPair * kWarps);  // may be <= 0
+        auto place_of = [&](int k, int &t0, int &nv) -> int32_t {  // page of this lane's group of pair k, -1: none
             t0 = 0;
             nv = 0;
-            if (k >= count) return -1;
-            const int g = c.g0 + ga + warp + kWarps * k;
-            const int blk = g / per_block, slot = (g - blk * per_block) * kGroup;
+            const int g = ga + kPair * (warp + kWarps * k) + (lane & 1);
+            if (g >= gb) return -1;
+            const int blk = (c.g0 + g) / per_block, slot = (c.g0 + g - blk * per_block) * kGroup;
             t0 = blk * B + slot;
             nv = min(min(kGroup, B - slot), c.e.len - t0);
             if (nv <= 0) return -1;
@@ -185,17 +204,19 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attend_rows_kernel(const
             }
             return page;
         };
-        auto scales_of = [&](int32_t page, float &ks, float &vs) {
-            ks = 0.f;
-            vs = 1.f;
+        auto scales_of = [&](int32_t page, float &ks, float &lvs, float &ivs) {
+            ks = 1.f;
+            float vs = 1.f;
             if (page >= 0) {
                 ks = __ldg(a.cache.scales + (plane + page) * H + h);
                 vs = v_scale(__ldg(a.cache.scales + (plane + N + page) * H + h));
             }
+            lvs = __log2f(vs);
+            ivs = __fdividef(1.f, vs);
         };
         int t0_l, nv_l, t0_n, nv_n;
-        int32_t page_l = place_of(lane, t0_l, nv_l), page_n = -1;
-        float ks_l, vs_l, ks_n = 0.f, vs_n = 1.f;
+        int32_t page_l = place_of(lane >> 1, t0_l, nv_l), page_n = -1;
+        float ks_l, lvs_l, ivs_l, ks_n = 1.f, lvs_n = 0.f, ivs_n = 1.f;
 
         // ---- Q: each row scaled by a power of two into the range of a half (undone in s_cq)
         for (int r = warp; r < kRows; r += kWarps) {
@@ -234,8 +255,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attend_rows_kernel(const
                     __floats2half2_rn(v[2 * x] * up, v[2 * x + 1] * up);
             if (lane == 0) s_cq[r] = a.attn.sm_scale * kLog2e * down;
         }
-        scales_of(page_l, ks_l, vs_l);
-        page_n = place_of(32 + lane, t0_n, nv_n);
+        scales_of(page_l, ks_l, lvs_l, ivs_l);
+        page_n = place_of(16 + (lane >> 1), t0_n, nv_n);
         __syncthreads();
 
         // visible tokens of this lane's columns (rows 2kk, 2kk + 1 of each tile of 8) and of all rows
@@ -265,56 +286,71 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attend_rows_kernel(const
             for (int x = 0; x < kChunks; ++x) o[t][x][0] = o[t][x][1] = o[t][x][2] = o[t][x][3] = 0.f;
         }
 
-        // start of the k-th group's copies: its page is lane k%32's, of these 32 or the next
+        // start of pair k's copies (its pages are of this batch or the next)
         int base_k = 0;
-        auto load_group = [&](int k) {
+        const int row_l = lane / kChunks, ch_l = lane % kChunks;  // this lane's row and 16 bytes of a 512-byte instruction
+        const int row_bytes = H * d;
+        auto load_pair = [&](int k) {
             if (k < count) {
-                const bool ahead = k - base_k >= 32;
-                const int32_t page = __shfl_sync(0xffffffffu, ahead ? page_n : page_l, k & 31);
-                const int t0 = __shfl_sync(0xffffffffu, ahead ? t0_n : t0_l, k & 31);
-                const int nv = __shfl_sync(0xffffffffu, ahead ? nv_n : nv_l, k & 31);
-                const uint32_t dst = ring + (k % kStages) * (2 * S::kGroupBytes);
-                const uint8_t *src = codes + (((plane + max(page, 0)) * B + t0 % B) * H + h) * d;
+                const bool ahead = k - base_k >= 16;
+                const uint32_t dst = ring + (k % kStages) * (kPair * 2 * S::kGroupBytes);
 #pragma unroll
-                for (int x = 0; x < D / 32; ++x) {  // 512 bytes an instruction
-                    const int id = x * 32 + lane, r = id / kChunks, ch = id % kChunks;
-                    const bool ok = r < nv && ch * 16 < d;
-                    const uint8_t *p = src + (ok ? int64_t(r) * H * d + ch * 16 : 0);
-                    copy_async16(dst + k_at<D>(r, ch), p, ok);
-                    copy_async16(dst + S::kGroupBytes + v_at<D>(r, ch), p + v_plane_bytes, ok);
+                for (int y = 0; y < kPair; ++y) {
+                    const int from = ((k & 15) << 1) | y;
+                    const int32_t page = __shfl_sync(0xffffffffu, ahead ? page_n : page_l, from);
+                    const int t0 = __shfl_sync(0xffffffffu, ahead ? t0_n : t0_l, from);
+                    const int nv = __shfl_sync(0xffffffffu, ahead ? nv_n : nv_l, from);
+                    const uint8_t *src = codes + (((plane + max(page, 0)) * B + t0 % B) * H + h) * d;
+                    const uint32_t dk = dst + y * (2 * S::kGroupBytes);
+#pragma unroll
+                    for (int x = 0; x < D / 32; ++x) {
+                        const int r = x * (32 / kChunks) + row_l;
+                        const bool ok = r < nv && (D == 256 || ch_l * 16 < d);
+                        const uint8_t *p = src + (ok ? r * row_bytes + ch_l * 16 : 0);
+                        copy_async16(dk + k_at<D>(r, ch_l), p, ok);
+                        copy_async16(dk + S::kGroupBytes + v_at<D>(r, ch_l), p + v_plane_bytes, ok);
+                    }
                 }
             }
             copy_async_commit();
         };
 #pragma unroll
-        for (int k = 0; k < kStages - 1; ++k) load_group(k);
+        for (int k = 0; k < kStages - 1; ++k) load_pair(k);
 
         for (int k = 0; k < count; ++k) {
-            if (k - base_k == 32) {
-                base_k += 32;
-                page_l = page_n; t0_l = t0_n; nv_l = nv_n; ks_l = ks_n; vs_l = vs_n;
-                page_n = place_of(base_k + 32 + lane, t0_n, nv_n);
+            if (k - base_k == 16) {
+                base_k += 16;
+                page_l = page_n; t0_l = t0_n; nv_l = nv_n; ks_l = ks_n; lvs_l = lvs_n; ivs_l = ivs_n;
+                page_n = place_of(base_k + 16 + (lane >> 1), t0_n, nv_n);
             }
-            if (k - base_k == 8) scales_of(page_n, ks_n, vs_n);
-            copy_async_wait<kStages - 2>();
+            if (k - base_k == 6) scales_of(page_n, ks_n, lvs_n, ivs_n);
+            load_pair(k + kStages - 1);
+            copy_async_wait<kStages - 1>();
             __syncwarp();
-            load_group(k + kStages - 1);
-            const int t0 = __shfl_sync(0xffffffffu, t0_l, k & 31), nv = __shfl_sync(0xffffffffu, nv_l, k & 31);
-            const float ks = __shfl_sync(0xffffffffu, ks_l, k & 31), vs = __shfl_sync(0xffffffffu, vs_l, k & 31);
-            const float ivs = __fdividef(1.f, vs), lvs = __log2f(vs);
-            const uint8_t *kt = smem + (ring - smem_u32(smem)) + (k % kStages) * (2 * S::kGroupBytes);
-            const uint8_t *vt = kt + S::kGroupBytes;
+            float ks[kPair], lvs[kPair], ivs[kPair];
+            int t0[kPair], nv[kPair];
+            bool whole = true;
+#pragma unroll
+            for (int y = 0; y < kPair; ++y) {
+                const int from = ((k & 15) << 1) | y;
+                t0[y] = __shfl_sync(0xffffffffu, t0_l, from);
+                nv[y] = __shfl_sync(0xffffffffu, nv_l, from);
+                ks[y] = __shfl_sync(0xffffffffu, ks_l, from);
+                lvs[y] = __shfl_sync(0xffffffffu, lvs_l, from);
+                ivs[y] = __shfl_sync(0xffffffffu, ivs_l, from);
+                whole = whole && nv[y] == kGroup && t0[y] >= all_lo && t0[y] + kGroup <= all_hi;
+            }
+            const uint8_t *kt = smem + (ring - smem_u32(smem)) + (k % kStages) * (kPair * 2 * S::kGroupBytes);
 
             // ---- S^T = K Q^T
-            float s[NT][4];
+            float s[NT][kPair][4];
 #pragma unroll
-            for (int t = 0; t < NT; ++t) s[t][0] = s[t][1] = s[t][2] = s[t][3] = 0.f;
+            for (int t = 0; t < NT; ++t)
+#pragma unroll
+                for (int y = 0; y < kPair; ++y) s[t][y][0] = s[t][y][1] = s[t][y][2] = s[t][y][3] = 0.f;
 #pragma unroll
             for (int i = 0; i < D / 64; ++i) {
                 const int ch = kk + 4 * i;
-                const uint4 ka = *reinterpret_cast<const uint4 *>(kt + k_at<D>(nn, ch));
-                const uint4 kb = *reinterpret_cast<const uint4 *>(kt + k_at<D>(nn + 8, ch));
-                const uint32_t wa[4] = {ka.x, ka.y, ka.z, ka.w}, wb[4] = {kb.x, kb.y, kb.z, kb.w};
                 uint32_t q[NT][8];
 #pragma unroll
                 for (int t = 0; t < NT; ++t) {
@@ -324,35 +360,46 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attend_rows_kernel(const
                     q[t][4] = y.x; q[t][5] = y.y; q[t][6] = y.z; q[t][7] = y.w;
                 }
 #pragma unroll
-                for (int w = 0; w < 4; ++w) {
-                    const uint32_t a0 = codes_lo<CODE>(wa[w]), a1 = codes_lo<CODE>(wb[w]);
-                    const uint32_t a2 = codes_hi<CODE>(wa[w]), a3 = codes_hi<CODE>(wb[w]);
+                for (int y = 0; y < kPair; ++y) {
+                    const uint8_t *kg = kt + y * (2 * S::kGroupBytes);
+                    const uint4 ka = *reinterpret_cast<const uint4 *>(kg + k_at<D>(nn, ch));
+                    const uint4 kb = *reinterpret_cast<const uint4 *>(kg + k_at<D>(nn + 8, ch));
+                    const uint32_t wa[4] = {ka.x, ka.y, ka.z, ka.w}, wb[4] = {kb.x, kb.y, kb.z, kb.w};
 #pragma unroll
-                    for (int t = 0; t < NT; ++t) mma16816(s[t], a0, a1, a2, a3, q[t][2 * w], q[t][2 * w + 1]);
+                    for (int w = 0; w < 4; ++w) {
+                        uint32_t a0, a1, a2, a3;
+                        codes_of<CODE>(wa[w], a0, a2);
+                        codes_of<CODE>(wb[w], a1, a3);
+#pragma unroll
+                        for (int t = 0; t < NT; ++t) mma16816(s[t][y], a0, a1, a2, a3, q[t][2 * w], q[t][2 * w + 1]);
+                    }
                 }
             }
 
-            // ---- softmax over tokens nn, nn + 8 of columns 2kk, 2kk + 1
-            const bool whole = nv == kGroup && t0 >= all_lo && t0 + kGroup <= all_hi;
+            // ---- softmax over tokens nn, nn + 8 of each group, of columns 2kk, 2kk + 1
             bool grew = false;
             float mn[NT][2];
 #pragma unroll
             for (int t = 0; t < NT; ++t) {
+                float v[2] = {-INFINITY, -INFINITY};
 #pragma unroll
-                for (int x = 0; x < 4; ++x) {
-                    s[t][x] = fmaf(s[t][x], ks * cq[t][x & 1], lvs);
-                    if (!whole) {
-                        const int r = nn + 8 * (x >> 1);
-                        if (r >= nv || t0 + r < lo[t][x & 1] || t0 + r >= hi[t][x & 1]) s[t][x] = -INFINITY;
+                for (int y = 0; y < kPair; ++y) {
+#pragma unroll
+                    for (int x = 0; x < 4; ++x) {
+                        s[t][y][x] = fmaf(s[t][y][x], ks[y] * cq[t][x & 1], lvs[y]);
+                        if (!whole) {
+                            const int r = nn + 8 * (x >> 1);
+                            if (r >= nv[y] || t0[y] + r < lo[t][x & 1] || t0[y] + r >= hi[t][x & 1]) s[t][y][x] = -INFINITY;
+                        }
+                        v[x & 1] = fmaxf(v[x & 1], s[t][y][x]);
                     }
                 }
 #pragma unroll
                 for (int x = 0; x < 2; ++x) {
-                    float v = fmaxf(s[t][x], s[t][x + 2]);
-                    v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 4));
-                    v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 8));
-                    v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 16));
-                    mn[t][x] = fmaxf(m[t][x], v);
+                    v[x] = fmaxf(v[x], __shfl_xor_sync(0xffffffffu, v[x], 4));
+                    v[x] = fmaxf(v[x], __shfl_xor_sync(0xffffffffu, v[x], 8));
+                    v[x] = fmaxf(v[x], __shfl_xor_sync(0xffffffffu, v[x], 16));
+                    mn[t][x] = fmaxf(m[t][x], v[x]);
                     grew |= mn[t][x] > m[t][x];
                 }
             }
@@ -371,85 +418,96 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attend_rows_kernel(const
                         }
                     }
             }
-            uint32_t p0[NT], p1[NT];
+            uint32_t p0[NT][kPair], p1[NT][kPair];
 #pragma unroll
-            for (int t = 0; t < NT; ++t) {
-                float w[4];
+            for (int t = 0; t < NT; ++t)
 #pragma unroll
-                for (int x = 0; x < 4; ++x) {
-                    const float ref = m[t][x & 1] == -INFINITY ? 0.f : m[t][x & 1];
-                    w[x] = exp2_of(s[t][x] - ref);
-                    if (whole) l[t][x & 1] = fmaf(w[x], ivs, l[t][x & 1]);
-                    else if (s[t][x] != -INFINITY) l[t][x & 1] = fmaf(w[x], ivs, l[t][x & 1]);
+                for (int y = 0; y < kPair; ++y) {
+                    float w[4];
+#pragma unroll
+                    for (int x = 0; x < 4; ++x) {
+                        const float ref = m[t][x & 1] == -INFINITY ? 0.f : m[t][x & 1];
+                        w[x] = exp2_of(s[t][y][x] - ref);
+                        if (whole || s[t][y][x] != -INFINITY) l[t][x & 1] = fmaf(w[x], ivs[y], l[t][x & 1]);
+                    }
+                    p0[t][y] = transpose8x8(pack2<KVL_TYPE_HALF>(w[0], w[1]));
+                    p1[t][y] = transpose8x8(pack2<KVL_TYPE_HALF>(w[2], w[3]));
                 }
-                p0[t] = transpose8x8(pack2<KVL_TYPE_HALF>(w[0], w[1]));
-                p1[t] = transpose8x8(pack2<KVL_TYPE_HALF>(w[2], w[3]));
-            }
 
             // ---- O^T += V^T P^T: tokens 2kk, 2kk + 1, 2kk + 8, 2kk + 9, elements from nn * D/8 on
-            uint32_t vw[4][kLaneBytes / 4];
 #pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                const int row = 2 * kk + (r & 1) + 8 * (r >> 1);
-                if constexpr (D == 64) {
-                    const uint2 x = *reinterpret_cast<const uint2 *>(vt + v_at<D>(row, nn >> 1) + 8 * (nn & 1));
-                    vw[r][0] = x.x; vw[r][1] = x.y;
-                } else {
+            for (int y = 0; y < kPair; ++y) {
+                const uint8_t *vt = kt + y * (2 * S::kGroupBytes) + S::kGroupBytes;
+                uint32_t vw[4][kLaneBytes / 4];
 #pragma unroll
-                    for (int y = 0; y < D / 128; ++y) {
-                        const uint4 x = *reinterpret_cast<const uint4 *>(vt + v_at<D>(row, nn * (D / 128) + y));
-                        vw[r][4 * y] = x.x; vw[r][4 * y + 1] = x.y; vw[r][4 * y + 2] = x.z; vw[r][4 * y + 3] = x.w;
-                    }
-                }
-            }
-            // a NaN in a token that some rows do not see must not reach them through 0 * NaN
-            uint32_t nan_words = 0;
-            if (CODE == KVL_CODE_FLOAT && !whole) {
+                for (int r = 0; r < 4; ++r) {
+                    const int row = 2 * kk + (r & 1) + 8 * (r >> 1);
+                    if constexpr (D == 64) {
+                        const uint2 x = *reinterpret_cast<const uint2 *>(vt + v_at<D>(row, nn >> 1) + 8 * (nn & 1));
+                        vw[r][0] = x.x; vw[r][1] = x.y;
+                    } else {
 #pragma unroll
-                for (int r = 0; r < 4; ++r)
-#pragma unroll
-                    for (int x = 0; x < kLaneBytes / 4; ++x)
-                        nan_words |= __vcmpeq4(vw[r][x] & 0x7f7f7f7fu, 0x7f7f7f7fu);
-            }
-            const bool has_nan = CODE == KVL_CODE_FLOAT && !whole && __any_sync(0xffffffffu, nan_words != 0);
-#pragma unroll
-            for (int x = 0; x < kLaneBytes / 4; ++x) {
-#pragma unroll
-                for (int y = 0; y < 2; ++y) {  // elements 4x + 2y, 4x + 2y + 1 of the lane's run
-                    const uint32_t u0 = __byte_perm(vw[0][x], vw[1][x], y ? 0x7362 : 0x5140);
-                    const uint32_t u1 = __byte_perm(vw[2][x], vw[3][x], y ? 0x7362 : 0x5140);
-                    uint32_t a0 = codes_lo<CODE>(u0), a1 = codes_hi<CODE>(u0), a2 = codes_lo<CODE>(u1), a3 = codes_hi<CODE>(u1);
-                    if (has_nan) {
-                        // NaN codes leave the product; a second one of NaN marks with the rows' view of
-                        // the tokens tells which results they belong to
-                        auto split = [](uint32_t &v) {
-                            uint32_t mark = 0;  // a converted NaN code has every exponent bit set
-                            if ((v & 0x7c00u) == 0x7c00u) mark |= 0xffffu;
-                            if ((v & 0x7c000000u) == 0x7c000000u) mark |= 0xffff0000u;
-                            v &= ~mark;
-                            return mark & 0x3c003c00u;  // 1.0
-                        };
-                        const uint32_t n0 = split(a0), n1 = split(a1), n2 = split(a2), n3 = split(a3);
-#pragma unroll
-                        for (int t = 0; t < NT; ++t) {
-                            uint32_t see[2];
-#pragma unroll
-                            for (int z = 0; z < 2; ++z) {
-                                const uint32_t v0 = s[t][2 * z] != -INFINITY ? 0x3c00u : 0u;
-                                const uint32_t v1 = s[t][2 * z + 1] != -INFINITY ? 0x3c000000u : 0u;
-                                see[z] = transpose8x8(v0 | v1);
-                            }
-                            float z[4] = {0.f, 0.f, 0.f, 0.f};
-                            mma16816(z, n0, n1, n2, n3, see[0], see[1]);
-#pragma unroll
-                            for (int q = 0; q < 4; ++q)
-                                if (z[q] > 0.f) o[t][2 * x + y][q] = NAN;
+                        for (int z = 0; z < D / 128; ++z) {
+                            const uint4 x = *reinterpret_cast<const uint4 *>(vt + v_at<D>(row, nn * (D / 128) + z));
+                            vw[r][4 * z] = x.x; vw[r][4 * z + 1] = x.y; vw[r][4 * z + 2] = x.z; vw[r][4 * z + 3] = x.w;
                         }
                     }
-#pragma unroll
-                    for (int t = 0; t < NT; ++t) mma16816(o[t][2 * x + y], a0, a1, a2, a3, p0[t], p1[t]);
                 }
+                // a NaN in a token that some rows do not see must not reach them through 0 * NaN
+                bool has_nan = false;
+                if (CODE == KVL_CODE_FLOAT && !whole) {
+                    uint32_t nan_words = 0;
+#pragma unroll
+                    for (int r = 0; r < 4; ++r)
+#pragma unroll
+                        for (int x = 0; x < kLaneBytes / 4; ++x) nan_words |= __vcmpeq4(vw[r][x] & 0x7f7f7f7fu, 0x7f7f7f7fu);
+                    has_nan = __any_sync(0xffffffffu, nan_words != 0);
+                }
+                if (has_nan) {
+                    // NaN codes leave the product; a product of NaN marks with the rows' view of the tokens
+                    // tells which results they belong to
+#pragma unroll
+                    for (int x = 0; x < kLaneBytes / 4; ++x) {
+                        uint32_t w[4];
+#pragma unroll
+                        for (int r = 0; r < 4; ++r) {
+                            const uint32_t bad = __vcmpeq4(vw[r][x] & 0x7f7f7f7fu, 0x7f7f7f7fu);
+                            w[r] = bad & 0x38383838u;  // marks: the code of 1
+                            vw[r][x] &= ~bad;
+                        }
+#pragma unroll
+                        for (int z = 0; z < 2; ++z) {
+                            uint32_t n0, n1, n2, n3;
+                            codes_of<CODE>(__byte_perm(w[0], w[1], z ? 0x7362 : 0x5140), n0, n1);
+                            codes_of<CODE>(__byte_perm(w[2], w[3], z ? 0x7362 : 0x5140), n2, n3);
+#pragma unroll
+                            for (int t = 0; t < NT; ++t) {
+                                uint32_t see[2];
+#pragma unroll
+                                for (int u2 = 0; u2 < 2; ++u2)
+                                    see[u2] = transpose8x8((s[t][y][2 * u2] != -INFINITY ? 0x3c00u : 0u) |
+                                                           (s[t][y][2 * u2 + 1] != -INFINITY ? 0x3c000000u : 0u));
+                                float hit[4] = {0.f, 0.f, 0.f, 0.f};
+                                mma16816(hit, n0, n1, n2, n3, see[0], see[1]);
+#pragma unroll
+                                for (int q = 0; q < 4; ++q)
+                                    if (hit[q] > 0.f) o[t][2 * x + z][q] = NAN;
+                            }
+                        }
+                    }
+                }
+#pragma unroll
+                for (int x = 0; x < kLaneBytes / 4; ++x)
+#pragma unroll
+                    for (int z = 0; z < 2; ++z) {  // elements 4x + 2z, 4x + 2z + 1 of the lane's run
+                        uint32_t a0, a1, a2, a3;
+                        codes_of<CODE>(__byte_perm(vw[0][x], vw[1][x], z ? 0x7362 : 0x5140), a0, a1);
+                        codes_of<CODE>(__byte_perm(vw[2][x], vw[3][x], z ? 0x7362 : 0x5140), a2, a3);
+#pragma unroll
+                        for (int t = 0; t < NT; ++t) mma16816(o[t][2 * x + z], a0, a1, a2, a3, p0[t][y], p1[t][y]);
+                    }
             }
+            __syncwarp();  // the stage may be filled again
         }
         copy_async_wait<0>();
         __syncwarp();
@@ -559,15 +617,24 @@ kvl_status launch_rows(const AttendArgs &a, int sms, void *stream)
 {
     static std::atomic<unsigned long long> ready[kMaxDevices];
     if (!allow_smem(attend_rows_kernel<CODE, TYPE, D, NT>, ready, Shape<D, NT>::kSmem)) return KVL_ECUDA;
-    attend_rows_kernel<CODE, TYPE, D, NT><<<sms * kCtasPerSm, kThreads, Shape<D, NT>::kSmem, static_cast<cudaStream_t>(stream)>>>(a);
+    // (rings of 256 elements leave room for one CTA an SM)
+    const int ctas = sms * (2 * Shape<D, NT>::kSmem <= 220 * 1024 ? kCtasPerSm : 1);
+    attend_rows_kernel<CODE, TYPE, D, NT><<<ctas, kThreads, Shape<D, NT>::kSmem, static_cast<cudaStream_t>(stream)>>>(a);
     return launch_status();
 }
 
+// Row tiles of 8, 16 or 32 by the bound on an entry's rows: a tile's tokens are read and converted once.
+// 32 rows of 128 elements would not leave a warp its registers, nor 16 of 256.
 template <int CODE, int TYPE>
-kvl_status launch_rows_dim(const AttendArgs &a, int sms, void *stream)
+kvl_status launch_rows_dim(const AttendArgs &a, int64_t most, int sms, void *stream)
 {
-    if (a.cache.head_dim <= 64) return launch_rows<CODE, TYPE, 64, 1>(a, sms, stream);
-    if (a.cache.head_dim <= 128) return launch_rows<CODE, TYPE, 128, 1>(a, sms, stream);
+    if (a.cache.head_dim <= 64) {
+        if (most <= 8) return launch_rows<CODE, TYPE, 64, 1>(a, sms, stream);
+        if (most <= 16) return launch_rows<CODE, TYPE, 64, 2>(a, sms, stream);
+        return launch_rows<CODE, TYPE, 64, 4>(a, sms, stream);
+    }
+    if (a.cache.head_dim <= 128)
+        return most <= 8 ? launch_rows<CODE, TYPE, 128, 1>(a, sms, stream) : launch_rows<CODE, TYPE, 128, 2>(a, sms, stream);
     return launch_rows<CODE, TYPE, 256, 1>(a, sms, stream);
 }
 
@@ -575,18 +642,18 @@ kvl_status launch_rows_dim(const AttendArgs &a, int sms, void *stream)
 
 size_t attend_rows_part_bytes(int head_dim)
 {
-    const int D = head_dim <= 64 ? 64 : head_dim <= 128 ? 128 : 256;
-    return size_t(2) * kCtasPerSm * (8 * (D + 2)) * sizeof(float);
+    const int D = head_dim <= 64 ? 64 : head_dim <= 128 ? 128 : 256, rows = head_dim <= 64 ? 32 : head_dim <= 128 ? 16 : 8;
+    return size_t(2) * kCtasPerSm * (rows * (D + 2)) * sizeof(float);
 }
 
-kvl_status launch_attend_rows(const AttendArgs &a, int sms, void *stream)
+kvl_status launch_attend_rows(const AttendArgs &a, int64_t most, int sms, void *stream)
 {
     const bool bf = a.attn.type == KVL_TYPE_BFLOAT;
     if (a.cache.code_type == KVL_CODE_FLOAT)
-        return bf ? launch_rows_dim<KVL_CODE_FLOAT, KVL_TYPE_BFLOAT>(a, sms, stream)
-                  : launch_rows_dim<KVL_CODE_FLOAT, KVL_TYPE_HALF>(a, sms, stream);
-    return bf ? launch_rows_dim<KVL_CODE_INT, KVL_TYPE_BFLOAT>(a, sms, stream)
-              : launch_rows_dim<KVL_CODE_INT, KVL_TYPE_HALF>(a, sms, stream);
+        return bf ? launch_rows_dim<KVL_CODE_FLOAT, KVL_TYPE_BFLOAT>(a, most, sms, stream)
+                  : launch_rows_dim<KVL_CODE_FLOAT, KVL_TYPE_HALF>(a, most, sms, stream);
+    return bf ? launch_rows_dim<KVL_CODE_INT, KVL_TYPE_BFLOAT>(a, most, sms, stream)
+              : launch_rows_dim<KVL_CODE_INT, KVL_TYPE_HALF>(a, most, sms, stream);
 }
 
 }  // namespace kvl

@@ -199,36 +199,22 @@ __device__ __forceinline__ float of_code(uint32_t c)
         return float(int8_t(c));
 }
 
-__device__ __forceinline__ uint32_t cvt_e4m3x2_f16x2(uint32_t two_codes)
-{
-    uint32_t r;
-    asm("{\n\t.reg .b16 h;\n\tcvt.u16.u32 h, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, h;\n\t}" : "=r"(r) : "r"(two_codes));
-    return r;
-}
-
-// The codes in the low (high) half of w as two halves: exact for both code types.
-// An integer code c is read as the half 1024 + (c + 128), of which 1152 is taken.
+// The four codes of w as halves, two and two: exact for both code types.  An integer code c is read as
+// the half 1024 + (c + 128), of which 1152 is taken.
 template <int CODE>
-__device__ __forceinline__ uint32_t codes_lo(uint32_t w)
+__device__ __forceinline__ void codes_of(uint32_t w, uint32_t &lo, uint32_t &hi)
 {
     if constexpr (CODE == KVL_CODE_FLOAT) {
-        return cvt_e4m3x2_f16x2(w & 0xffffu);
+        asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, l;\n\tcvt.rn.f16x2.e4m3x2 %1, h;\n\t}"
+            : "=r"(lo), "=r"(hi)
+            : "r"(w));
     } else {
-        const uint32_t u = __byte_perm(w ^ 0x80808080u, 0x64646464u, 0x5140);
-        const __half2 h = __hsub2(*reinterpret_cast<const __half2 *>(&u), __half2half2(__ushort_as_half(0x6480)));
-        return *reinterpret_cast<const uint32_t *>(&h);
-    }
-}
-
-template <int CODE>
-__device__ __forceinline__ uint32_t codes_hi(uint32_t w)
-{
-    if constexpr (CODE == KVL_CODE_FLOAT) {
-        return cvt_e4m3x2_f16x2(w >> 16);
-    } else {
-        const uint32_t u = __byte_perm(w ^ 0x80808080u, 0x64646464u, 0x5342);
-        const __half2 h = __hsub2(*reinterpret_cast<const __half2 *>(&u), __half2half2(__ushort_as_half(0x6480)));
-        return *reinterpret_cast<const uint32_t *>(&h);
+        const uint32_t x = w ^ 0x80808080u;
+        const uint32_t u = __byte_perm(x, 0x64646464u, 0x5140), v = __byte_perm(x, 0x64646464u, 0x5342);
+        const __half2 bias = __half2half2(__ushort_as_half(0x6480));
+        const __half2 a = __hsub2(*reinterpret_cast<const __half2 *>(&u), bias), b = __hsub2(*reinterpret_cast<const __half2 *>(&v), bias);
+        lo = *reinterpret_cast<const uint32_t *>(&a);
+        hi = *reinterpret_cast<const uint32_t *>(&b);
     }
 }
 
