@@ -34,6 +34,29 @@ namespace {
 
 constexpr int kGroup = 16;
 
+// What stands for m in the exponent is a reference, set kHead above a row's largest x so far and moved
+// only when an x passes it by kSlack: weights up to 2^14 are halves still, and those below 2^-14 keep
+// 2^-25 of a largest weight that is 2^-4 or more.  So a row's sums are rescaled about once.  (With the
+// reference at the maximum and a slack of 8, one of the 128 rows that the tensor-memory kernel steps
+// together moved in most steps and held the others up for 1,000 cycles.)
+constexpr float kSlack = 14.f, kHead = 4.f;
+
+// `total` units cut into `shares` contiguous parts whose sizes differ by at most one.  Units are counted
+// in 32 bits (a call whose units do not fit, some 10^10 tokens, is refused), as 64-bit divisions would
+// be the longest part of a small call's start.
+struct Cut {
+    uint32_t total, shares, size, rest;  // the first `rest` shares hold size + 1 units
+    __device__ __forceinline__ Cut() {}
+    __device__ __forceinline__ Cut(uint32_t t, uint32_t s) : total(t), shares(s), size(t / s), rest(t - t / s * s) {}
+    __device__ __forceinline__ uint32_t start(uint32_t b) const { return b * size + min(b, rest); }
+    __device__ __forceinline__ uint32_t share_of(uint32_t u) const
+    {
+        const uint32_t large = rest * (size + 1);
+        return u < large ? u / (size + 1) : rest + (u - large) / size;
+    }
+};
+constexpr uint64_t kMostUnits = uint64_t(1) << 31;
+
 // What one batch entry costs: `tiles` row tiles for each KV head, each walking the groups
 // [g0, g0 + groups).
 struct Cost {
@@ -47,7 +70,6 @@ __device__ __forceinline__ int32_t group_of(int32_t token, int32_t B, int32_t pe
     return b * per_block + (token - b * B) / kGroup;
 }
 
-__device__ __forceinline__ int64_t units_of(const Cost &c, int H) { return int64_t(H) * c.tiles * c.groups; }
 
 // 16 bytes into shared memory; zeros where !ok (src has to be a valid address all the same).
 __device__ __forceinline__ void copy_async16(uint32_t dst, const void *src, bool ok)

@@ -36,11 +36,6 @@ constexpr int kBatch = 512;                 // entries whose steps are held at a
 // filling the pipeline).
 constexpr int kJobCost = 4;
 constexpr int kStepsPerCta = kJobCost + 2;  // a share is at least this many units
-// A row's reference is set kHead above its largest x so far and moved only when an x passes it by
-// kSlack: weights up to 2^14 are halves still, and those below 2^-14 keep 2^-25 of the largest
-// weight's 2^-4 or more.  With the reference at the maximum and a slack of 8, one of a warpgroup's
-// 128 rows moved in most steps and held the others up for 1,000 cycles.
-constexpr float kSlack = 14.f, kHead = 4.f;
 
 // Scales and places of a step's groups; partial[w]: some row sees only a part of the two groups that
 // converting warp w filled.
@@ -254,21 +249,21 @@ __device__ __forceinline__ int32_t tiles_of(const AttendArgs &a, const Entry &e)
 }
 
 // Units of one KV head of an entry, all tiles: a warp's lanes take a tile each.
-__device__ __forceinline__ int64_t warp_units(const AttendArgs &a, int32_t len, int32_t fresh, int32_t tiles, int lane)
+__device__ __forceinline__ uint32_t warp_units(const AttendArgs &a, int32_t len, int32_t fresh, int32_t tiles, int lane)
 {
-    int64_t n = 0;
+    uint64_t n = 0;
     for (int t = lane; t < tiles; t += 32) n += tile_of(a, len, fresh, t).steps + kJobCost;
 #pragma unroll
     for (int o = 16; o; o >>= 1) n += __shfl_xor_sync(0xffffffffu, n, o);
-    return n;
+    return uint32_t(min(n, kMostUnits));
 }
 
 // Where a CTA stands in its share, and the job it works on: in shared memory, so that the roles' loops
 // hold only what they use in registers.
 struct Job {
-    int64_t u, u_end, off;    // next unit, the share's end, units of the entry before u
-    int64_t total, shares;
-    int64_t u0;               // the unit of the job's first step
+    Cut cut;
+    uint32_t u, u_end, off;   // next unit, the share's end, units of the entry before u
+    uint32_t u0;              // the unit of the job's first step
     int32_t taken;            // units of the job in this share
     int32_t row_base;         // the tile's first row
     Entry e;
@@ -285,11 +280,11 @@ struct Job {
 __device__ __forceinline__ void next_job(const AttendArgs &a, Job &job, int lane)
 {
     const int H = a.cache.n_kv_heads, B = a.cache.block_tokens;
-    int64_t off = job.off;
+    uint32_t off = job.off;
     int entry = job.entry;
     Entry e = load_entry(a.seqs, B, entry, nullptr);
     int32_t tiles = tiles_of(a, e);
-    int64_t units = warp_units(a, e.len, e.fresh, tiles, lane);
+    uint32_t units = warp_units(a, e.len, e.fresh, tiles, lane);
     while (off >= H * units) {
         off -= H * units;
         e = load_entry(a.seqs, B, ++entry, nullptr);
@@ -297,7 +292,7 @@ __device__ __forceinline__ void next_job(const AttendArgs &a, Job &job, int lane
         units = warp_units(a, e.len, e.fresh, tiles, lane);
     }
     const int h = int(off / units);
-    int64_t rest = off - h * units;
+    uint32_t rest = off - h * units;
     // the tile whose units hold `rest`: 32 tiles at a time
     int tile = 0;
     for (int base = 0; base < tiles; base += 32) {
@@ -308,7 +303,7 @@ __device__ __forceinline__ void next_job(const AttendArgs &a, Job &job, int lane
             const int y = __shfl_up_sync(0xffffffffu, sum, o);
             if (lane >= o) sum += y;
         }
-        const unsigned past = __ballot_sync(0xffffffffu, rest < sum);
+        const unsigned past = __ballot_sync(0xffffffffu, rest < uint32_t(sum));
         if (past) {
             const int l = __ffs(past) - 1;
             tile = base + l;
@@ -319,7 +314,7 @@ __device__ __forceinline__ void next_job(const AttendArgs &a, Job &job, int lane
     }
     if (lane == 0) {
         const Tile t = tile_of(a, e.len, e.fresh, tile);
-        const int64_t taken = min(int64_t(t.steps + kJobCost) - rest, job.u_end - job.u);
+        const uint32_t taken = min(t.steps + kJobCost - rest, job.u_end - job.u);
         job.off = off;
         job.entry = entry;
         job.e = e;
@@ -388,7 +383,9 @@ __global__ void __launch_bounds__(kThreads, 1) attend_chunk_kernel(const __grid_
 
     // ---- this CTA's share of the steps: the entries' steps a batch at a time (entry i of a batch by
     // warp i % 12, its tiles by the lanes), their sum, then the entry that holds the share's first
-    int64_t total = 0, shares = 0, u = -1, before = 0;
+    uint64_t before = 0;
+    uint32_t u = 0;
+    Cut cut;
     for (int pass = 0; pass < 2; ++pass) {
         for (int base = 0; base < a.seqs.n_seq; base += kBatch) {
             const int n = min(kBatch, a.seqs.n_seq - base);
@@ -396,31 +393,30 @@ __global__ void __launch_bounds__(kThreads, 1) attend_chunk_kernel(const __grid_
                 __syncthreads();
                 for (int i = warp; i < n; i += kThreads / 32) {
                     const Entry e = load_entry(a.seqs, B, base + i, pass == 0 && blockIdx.x == 0 && lane == 0 ? a.report : nullptr);
-                    const int64_t units = warp_units(a, e.len, e.fresh, tiles_of(a, e), lane);
-                    if (lane == 0) s_units[i] = uint32_t(min(units, int64_t(0xffffffffu)));
+                    const uint32_t units = warp_units(a, e.len, e.fresh, tiles_of(a, e), lane);
+                    if (lane == 0) s_units[i] = units;
                 }
                 __syncthreads();
             }
             // 32 lanes scan the batch; every warp does, and finds the same
             for (int i = 0; i < n; i += 32) {
-                int64_t x = i + lane < n ? int64_t(s_units[i + lane]) * H : 0, sum = x;
+                uint64_t x = i + lane < n ? uint64_t(s_units[i + lane]) * H : 0, sum = x;
 #pragma unroll
                 for (int o = 1; o < 32; o <<= 1) {
-                    const int64_t y = __shfl_up_sync(0xffffffffu, sum, o);
+                    const uint64_t y = __shfl_up_sync(0xffffffffu, sum, o);
                     if (lane >= o) sum += y;
                 }
                 if (pass == 1) {
                     const unsigned past = __ballot_sync(0xffffffffu, u < before + sum);
                     if (past) {
                         const int l = __ffs(past) - 1;
-                        const int64_t at = before + __shfl_sync(0xffffffffu, sum - x, l);
+                        const uint32_t at = uint32_t(before + __shfl_sync(0xffffffffu, sum - x, l));
                         if (tid == 0) {
                             job.entry = base + i + l;
                             job.off = u - at;
                             job.u = u;
-                            job.u_end = total * (blockIdx.x + 1) / shares;
-                            job.total = total;
-                            job.shares = shares;
+                            job.u_end = cut.start(blockIdx.x + 1);
+                            job.cut = cut;
                             job.it = job.it_g[0] = job.it_g[1] = 0;
                         }
                         base = a.seqs.n_seq;  // found: leave both loops
@@ -431,10 +427,13 @@ __global__ void __launch_bounds__(kThreads, 1) attend_chunk_kernel(const __grid_
             }
         }
         if (pass == 0) {
-            total = before;
-            shares = min(int64_t(gridDim.x), (total + kStepsPerCta - 1) / kStepsPerCta);
-            if (int64_t(blockIdx.x) >= shares) return;
-            u = total * blockIdx.x / shares;
+            if (before == 0 || before >= kMostUnits) {
+                if (before && blockIdx.x == 0 && tid == 0) report(a.report, KVL_ERANGE, a.seqs.n_seq);
+                return;
+            }
+            cut = Cut(uint32_t(before), min(gridDim.x, (uint32_t(before) + kStepsPerCta - 1) / kStepsPerCta));
+            if (blockIdx.x >= cut.shares) return;
+            u = cut.start(blockIdx.x);
             before = 0;
         }
     }
@@ -962,8 +961,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_chunk_kernel(const __grid_
         }
         if (!job.complete) {
             // parts of this job: shares first .. last; the one that arrives last joins them
-            const int first = int(((job.u0 + 1) * job.shares - 1) / job.total);
-            const int last = int(((job.u0 + job.t.steps) * job.shares - 1) / job.total);
+            const int first = int(job.cut.share_of(job.u0)), last = int(job.cut.share_of(job.u0 + job.t.steps - 1));
             __threadfence();
             __syncthreads();
             if (tid == 0) s_last = !*gone && atomicAdd(&a.counters[first], 1u) == uint32_t(last - first);

@@ -29,7 +29,12 @@ constexpr int kThreads = kWarps * 32;
 constexpr int kPair = 2;          // groups a warp takes at a time
 constexpr int kStages = 2;        // pairs in its ring: one worked on, one on its way
 constexpr int kCtasPerSm = 2;     // 12 warps an SM: 168 registers a thread, 192 KB of rings at d = 128
-constexpr int kUnitsPerCta = kPair * kWarps;  // a share is at least a pair for each warp
+// Units of a share: a job's groups, and kJobCost before them for starting and joining it.  A share is at
+// least kUnitsPerCta, and a job of at most kSmallJob groups is not split: joining the parts takes as
+// long as some 70 groups (one token of 777: 8 CTAs and 13 us instead of 33 CTAs and 16).
+constexpr int kJobCost = 16;
+constexpr int kUnitsPerCta = 40;
+constexpr int kSmallJob = 72;
 
 template <int D, int NT>
 struct Shape {
@@ -100,7 +105,9 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attend_rows_kernel(const
     using S = Shape<D, NT>;
     constexpr int kRows = S::kRows, kChunks = D / 16, kLaneBytes = D / 8;
     extern __shared__ __align__(128) uint8_t smem[];
-    __shared__ int64_t s_scan[kWarps], s_off, s_u, s_end;
+    __shared__ uint64_t s_scan[kWarps];
+    __shared__ uint32_t s_off, s_u[2];
+    __shared__ Cost s_cost;
     __shared__ int s_entry, s_last;
     __shared__ float s_m[kWarps][kRows], s_l[kWarps][kRows], s_cq[kRows];
 
@@ -112,58 +119,65 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attend_rows_kernel(const
     // ---- this CTA's share of the units ----
     const int n_seq = a.seqs.n_seq, per_thread = (n_seq + kThreads - 1) / kThreads;
     const int i0 = min(n_seq, tid * per_thread), i1 = min(n_seq, i0 + per_thread);
-    int64_t mine = 0;
-    for (int i = i0; i < i1; ++i) mine += units_of(cost_of<NT>(a, i, blockIdx.x == 0 ? a.report : nullptr), H);
-    int64_t scan = mine;
+    auto units_of = [&](const Cost &q) { return uint64_t(H * q.tiles) * uint32_t(q.groups + kJobCost); };
+    Cost c;  // of the thread's last entry; kept where it is the only one
+    uint64_t mine = 0;
+    for (int i = i0; i < i1; ++i) {
+        c = cost_of<NT>(a, i, blockIdx.x == 0 ? a.report : nullptr);
+        mine += units_of(c);
+    }
+    uint64_t scan = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-        const int64_t y = __shfl_up_sync(0xffffffffu, scan, o);
+        const uint64_t y = __shfl_up_sync(0xffffffffu, scan, o);
         if (lane >= o) scan += y;
     }
     if (lane == 31) s_scan[warp] = scan;
     __syncthreads();
-    int64_t before = scan - mine, total = 0;
+    uint64_t before = scan - mine, total = 0;
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) {
         if (w < warp) before += s_scan[w];
         total += s_scan[w];
     }
-    const int64_t shares = min(int64_t(gridDim.x), (total + kUnitsPerCta - 1) / kUnitsPerCta);
-    if (int64_t(blockIdx.x) >= shares) return;
-    // The share's first unit and the next share's: where one falls inside a job of few groups it moves to
-    // the job's start (small jobs are not split; what a job's parts are does not change by it).
-    int64_t u = total * blockIdx.x / shares, u_end = total * (blockIdx.x + 1) / shares;
-#pragma unroll
+    if (total == 0 || total >= kMostUnits) {
+        if (total && blockIdx.x == 0 && tid == 0) report(a.report, KVL_ERANGE, n_seq);
+        return;
+    }
+    const Cut cut(uint32_t(total), min(gridDim.x, (uint32_t(total) + kUnitsPerCta - 1) / kUnitsPerCta));
+    if (blockIdx.x >= cut.shares) return;
+    // The share's first unit and the next share's: where one falls inside a small job it moves to the
+    // job's start.
+#pragma unroll 1
     for (int k = 0; k < 2; ++k) {
-        const int64_t x = k ? u_end : u;
+        const uint64_t x = cut.start(blockIdx.x + k);
         if (x >= before && x < before + mine) {
-            int64_t at = before, n = 0;
-            Cost q;
+            uint64_t at = before;
             int i = i0;
-            for (; i < i1; ++i) {
-                q = cost_of<NT>(a, i, nullptr);
-                n = units_of(q, H);
-                if (x < at + n) break;
-                at += n;
-            }
-            int64_t off = x - at;
-            if (q.groups <= kUnitsPerCta) off -= off % q.groups;
-            if (k) {
-                s_end = at + off;
-            } else {
+            if (per_thread > 1)
+                for (;; ++i) {
+                    c = cost_of<NT>(a, i, nullptr);
+                    if (x < at + units_of(c)) break;
+                    at += units_of(c);
+                }
+            uint32_t in = uint32_t(x - at);
+            if (c.groups <= kSmallJob) in -= in % (c.groups + kJobCost);
+            if (k == 0) {
                 s_entry = i;
-                s_off = off;
-                s_u = at + off;
+                s_off = in;
+                s_cost = c;
             }
+            s_u[k] = uint32_t(at) + in;
+        } else if (tid == 0 && x == total) {
+            s_u[k] = uint32_t(total);
         }
     }
-    if (tid == 0 && u_end == total) s_end = total;
     __syncthreads();
-    u = s_u;
-    u_end = s_end;
+    uint32_t u = s_u[0];
+    const uint32_t u_end = s_u[1];
     int entry = s_entry;
-    int64_t off = s_off;  // units of the entry before u
-    Cost c = cost_of<NT>(a, entry, nullptr);
+    uint32_t off = s_off;  // units of the entry before u
+    c = s_cost;
 
     const uint32_t ring = smem_u32(smem) + S::kQBytes + warp * S::kWarpBytes;
     __half *sq = reinterpret_cast<__half *>(smem);
@@ -171,14 +185,18 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attend_rows_kernel(const
     const int64_t plane = int64_t(a.layer) * 2 * N, v_plane_bytes = N * B * H * d;
 
     while (u < u_end) {
-        while (off >= units_of(c, H)) {  // on to the entry that holds unit u
-            off -= units_of(c, H);
+        while (off >= units_of(c)) {  // on to the entry that holds unit u
+            off -= uint32_t(units_of(c));
             c = cost_of<NT>(a, ++entry, nullptr);
         }
-        const int job = int(off / c.groups);
-        const int ga = int(off - int64_t(job) * c.groups);
-        const int gb = int(min(int64_t(c.groups), ga + (u_end - u)));
-        const int64_t job_u0 = u - ga;
+        const uint32_t per_job = c.groups + kJobCost;
+        const int job = int(off / per_job), in = int(off - job * per_job);
+        const int taken = int(min(per_job - in, u_end - u));
+        const int ga = max(0, in - kJobCost), gb = max(0, in + taken - kJobCost);
+        const uint32_t group0 = u - in + kJobCost;  // the unit of the job's first group
+        off += taken;
+        u += taken;
+        if (ga == gb) continue;  // its groups are the next share's
         const int h = job / c.tiles, tile = job - h * c.tiles;
         const int rows = min(kRows, c.e.fresh * G - tile * kRows);
         const int pos0 = c.e.len - c.e.fresh;
@@ -217,6 +235,37 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attend_rows_kernel(const
         int t0_l, nv_l, t0_n, nv_n;
         int32_t page_l = place_of(lane >> 1, t0_l, nv_l), page_n = -1;
         float ks_l, lvs_l, ivs_l, ks_n = 1.f, lvs_n = 0.f, ivs_n = 1.f;
+
+        // start of pair k's copies (its pages are of this batch or the next)
+        int base_k = 0;
+        const int row_l = lane / kChunks, ch_l = lane % kChunks;  // this lane's row and 16 bytes of a 512-byte instruction
+        const int row_bytes = H * d;
+        auto load_pair = [&](int k) {
+            if (k < count) {
+                const bool ahead = k - base_k >= 16;
+                const uint32_t dst = ring + (k % kStages) * (kPair * 2 * S::kGroupBytes);
+#pragma unroll
+                for (int y = 0; y < kPair; ++y) {
+                    const int from = ((k & 15) << 1) | y;
+                    const int32_t page = __shfl_sync(0xffffffffu, ahead ? page_n : page_l, from);
+                    const int t0 = __shfl_sync(0xffffffffu, ahead ? t0_n : t0_l, from);
+                    const int nv = __shfl_sync(0xffffffffu, ahead ? nv_n : nv_l, from);
+                    const uint8_t *src = codes + (((plane + max(page, 0)) * B + t0 % B) * H + h) * d;
+                    const uint32_t dk = dst + y * (2 * S::kGroupBytes);
+#pragma unroll
+                    for (int x = 0; x < D / 32; ++x) {
+                        const int r = x * (32 / kChunks) + row_l;
+                        const bool ok = r < nv && (D == 256 || ch_l * 16 < d);
+                        const uint8_t *p = src + (ok ? r * row_bytes + ch_l * 16 : 0);
+                        copy_async16(dk + k_at<D>(r, ch_l), p, ok);
+                        copy_async16(dk + S::kGroupBytes + v_at<D>(r, ch_l), p + v_plane_bytes, ok);
+                    }
+                }
+            }
+            copy_async_commit();
+        };
+#pragma unroll
+        for (int k = 0; k < kStages - 1; ++k) load_pair(k);
 
         // ---- Q: each row scaled by a power of two into the range of a half (undone in s_cq)
         for (int r = warp; r < kRows; r += kWarps) {
@@ -286,37 +335,6 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attend_rows_kernel(const
             for (int x = 0; x < kChunks; ++x) o[t][x][0] = o[t][x][1] = o[t][x][2] = o[t][x][3] = 0.f;
         }
 
-        // start of pair k's copies (its pages are of this batch or the next)
-        int base_k = 0;
-        const int row_l = lane / kChunks, ch_l = lane % kChunks;  // this lane's row and 16 bytes of a 512-byte instruction
-        const int row_bytes = H * d;
-        auto load_pair = [&](int k) {
-            if (k < count) {
-                const bool ahead = k - base_k >= 16;
-                const uint32_t dst = ring + (k % kStages) * (kPair * 2 * S::kGroupBytes);
-#pragma unroll
-                for (int y = 0; y < kPair; ++y) {
-                    const int from = ((k & 15) << 1) | y;
-                    const int32_t page = __shfl_sync(0xffffffffu, ahead ? page_n : page_l, from);
-                    const int t0 = __shfl_sync(0xffffffffu, ahead ? t0_n : t0_l, from);
-                    const int nv = __shfl_sync(0xffffffffu, ahead ? nv_n : nv_l, from);
-                    const uint8_t *src = codes + (((plane + max(page, 0)) * B + t0 % B) * H + h) * d;
-                    const uint32_t dk = dst + y * (2 * S::kGroupBytes);
-#pragma unroll
-                    for (int x = 0; x < D / 32; ++x) {
-                        const int r = x * (32 / kChunks) + row_l;
-                        const bool ok = r < nv && (D == 256 || ch_l * 16 < d);
-                        const uint8_t *p = src + (ok ? r * row_bytes + ch_l * 16 : 0);
-                        copy_async16(dk + k_at<D>(r, ch_l), p, ok);
-                        copy_async16(dk + S::kGroupBytes + v_at<D>(r, ch_l), p + v_plane_bytes, ok);
-                    }
-                }
-            }
-            copy_async_commit();
-        };
-#pragma unroll
-        for (int k = 0; k < kStages - 1; ++k) load_pair(k);
-
         for (int k = 0; k < count; ++k) {
             if (k - base_k == 16) {
                 base_k += 16;
@@ -376,12 +394,13 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attend_rows_kernel(const
                 }
             }
 
-            // ---- softmax over tokens nn, nn + 8 of each group, of columns 2kk, 2kk + 1
+            // ---- softmax over tokens nn, nn + 8 of each group, of columns 2kk, 2kk + 1.  Only a score that
+            // has outgrown its column's reference makes the lanes compare theirs.
             bool grew = false;
-            float mn[NT][2];
+            float top[NT][2];
 #pragma unroll
             for (int t = 0; t < NT; ++t) {
-                float v[2] = {-INFINITY, -INFINITY};
+                top[t][0] = top[t][1] = -INFINITY;
 #pragma unroll
                 for (int y = 0; y < kPair; ++y) {
 #pragma unroll
@@ -391,25 +410,23 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attend_rows_kernel(const
                             const int r = nn + 8 * (x >> 1);
                             if (r >= nv[y] || t0[y] + r < lo[t][x & 1] || t0[y] + r >= hi[t][x & 1]) s[t][y][x] = -INFINITY;
                         }
-                        v[x & 1] = fmaxf(v[x & 1], s[t][y][x]);
+                        top[t][x & 1] = fmaxf(top[t][x & 1], s[t][y][x]);
                     }
                 }
-#pragma unroll
-                for (int x = 0; x < 2; ++x) {
-                    v[x] = fmaxf(v[x], __shfl_xor_sync(0xffffffffu, v[x], 4));
-                    v[x] = fmaxf(v[x], __shfl_xor_sync(0xffffffffu, v[x], 8));
-                    v[x] = fmaxf(v[x], __shfl_xor_sync(0xffffffffu, v[x], 16));
-                    mn[t][x] = fmaxf(m[t][x], v[x]);
-                    grew |= mn[t][x] > m[t][x];
-                }
+                grew = grew || top[t][0] > m[t][0] + kSlack || top[t][1] > m[t][1] + kSlack;
             }
             if (__any_sync(0xffffffffu, grew)) {
 #pragma unroll
                 for (int t = 0; t < NT; ++t)
 #pragma unroll
                     for (int x = 0; x < 2; ++x) {
-                        const float f = mn[t][x] == -INFINITY ? 1.f : exp2_of(m[t][x] - mn[t][x]);
-                        m[t][x] = mn[t][x];
+                        float v = top[t][x];
+                        v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 4));
+                        v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 8));
+                        v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 16));
+                        if (v <= m[t][x] + kSlack || v == -INFINITY) continue;
+                        const float f = exp2_of(m[t][x] - (v + kHead));
+                        m[t][x] = v + kHead;
                         l[t][x] *= f;
 #pragma unroll
                         for (int j = 0; j < kChunks; ++j) {
@@ -577,8 +594,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attend_rows_kernel(const
         }
         if (!complete) {
             // parts of this job: shares first .. last; the one that arrives last joins them
-            const int first = int(((job_u0 + 1) * shares - 1) / total);
-            const int last = int(((job_u0 + c.groups) * shares - 1) / total);
+            const int first = int(cut.share_of(group0)), last = int(cut.share_of(group0 + c.groups - 1));
             __threadfence();
             __syncthreads();
             if (tid == 0) s_last = atomicAdd(&a.counters[first], 1u) == uint32_t(last - first);
@@ -586,29 +602,43 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attend_rows_kernel(const
             if (s_last) {
                 __threadfence();
                 if (tid == 0) a.counters[first] = 0;
+                // factors of the parts' rows into shared memory (over the rings), all loads at once; then
+                // every thread adds up four elements of a row over the parts
+                const int n_parts = last - first + 1;
+                float *fac = reinterpret_cast<float *>(smem + S::kQBytes), *sums = fac + n_parts * kRows;
+                auto part_of = [&](int b) { return a.parts + (int64_t(first + b) * 2 + (b == 0)) * S::kPartFloats; };
+                for (int x = tid; x < n_parts * kRows; x += kThreads) {
+                    const int b = x / kRows, r = x % kRows;
+                    fac[x] = r < rows ? __ldcg(part_of(b) + r) : 0.f;
+                    sums[x] = r < rows ? __ldcg(part_of(b) + kRows + r) : 0.f;
+                }
+                __syncthreads();
+                if (tid < rows) {
+                    float big = -INFINITY, sum = 0.f;
+                    for (int b = 0; b < n_parts; ++b) big = fmaxf(big, fac[b * kRows + tid]);
+                    for (int b = 0; b < n_parts; ++b) {
+                        const float mb = fac[b * kRows + tid], f = mb == -INFINITY ? 0.f : exp2_of(mb - big);
+                        fac[b * kRows + tid] = f;
+                        sum += sums[b * kRows + tid] * f;
+                    }
+                    s_m[0][tid] = big;
+                    s_l[0][tid] = sum;
+                }
+                __syncthreads();
                 for (int x = tid; x < rows * (D / 4); x += kThreads) {
                     const int r = x / (D / 4), e = (x % (D / 4)) * 4;
-                    float big = -INFINITY;
-                    for (int b = first; b <= last; ++b)
-                        big = fmaxf(big, __ldcg(a.parts + (int64_t(b) * 2 + (b == first)) * S::kPartFloats + r));
                     float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-                    float sum = 0.f;
-#pragma unroll 4
-                    for (int b = first; b <= last; ++b) {
-                        const float *p = a.parts + (int64_t(b) * 2 + (b == first)) * S::kPartFloats;
-                        const float mb = __ldcg(p + r), lb = __ldcg(p + kRows + r);
-                        const float4 y = __ldcg(reinterpret_cast<const float4 *>(p + 2 * kRows + r * D + e));
-                        const float f = mb == -INFINITY ? 0.f : exp2_of(mb - big);
+#pragma unroll 8
+                    for (int b = 0; b < n_parts; ++b) {
+                        const float4 y = __ldcg(reinterpret_cast<const float4 *>(part_of(b) + 2 * kRows + r * D + e));
+                        const float f = fac[b * kRows + r];
                         v.x += y.x * f; v.y += y.y * f; v.z += y.z * f; v.w += y.w * f;
-                        sum += lb * f;
                     }
-                    finish(r, e, v, big, sum);
+                    finish(r, e, v, s_m[0][r], s_l[0][r]);
                 }
             }
         }
         __syncthreads();  // Q, the rings and the joined results are free again
-        off += gb - ga;
-        u += gb - ga;
     }
 }
 
@@ -623,15 +653,14 @@ kvl_status launch_rows(const AttendArgs &a, int sms, void *stream)
     return launch_status();
 }
 
-// Row tiles of 8, 16 or 32 by the bound on an entry's rows: a tile's tokens are read and converted once.
-// 32 rows of 128 elements would not leave a warp its registers, nor 16 of 256.
+// Row tiles of 8 or 16 by the bound on an entry's rows: a tile's tokens are read and converted once.
+// 16 rows of 256 elements would not leave a warp its registers.
 template <int CODE, int TYPE>
 kvl_status launch_rows_dim(const AttendArgs &a, int64_t most, int sms, void *stream)
 {
     if (a.cache.head_dim <= 64) {
         if (most <= 8) return launch_rows<CODE, TYPE, 64, 1>(a, sms, stream);
-        if (most <= 16) return launch_rows<CODE, TYPE, 64, 2>(a, sms, stream);
-        return launch_rows<CODE, TYPE, 64, 4>(a, sms, stream);
+        return launch_rows<CODE, TYPE, 64, 2>(a, sms, stream);
     }
     if (a.cache.head_dim <= 128)
         return most <= 8 ? launch_rows<CODE, TYPE, 128, 1>(a, sms, stream) : launch_rows<CODE, TYPE, 128, 2>(a, sms, stream);
@@ -642,7 +671,7 @@ kvl_status launch_rows_dim(const AttendArgs &a, int64_t most, int sms, void *str
 
 size_t attend_rows_part_bytes(int head_dim)
 {
-    const int D = head_dim <= 64 ? 64 : head_dim <= 128 ? 128 : 256, rows = head_dim <= 64 ? 32 : head_dim <= 128 ? 16 : 8;
+    const int D = head_dim <= 64 ? 64 : head_dim <= 128 ? 128 : 256, rows = head_dim <= 128 ? 16 : 8;
     return size_t(2) * kCtasPerSm * (rows * (D + 2)) * sizeof(float);
 }
 
