@@ -14,14 +14,16 @@ from __future__ import annotations
 
 import ctypes
 import math
+import threading
 
 import numpy as np
 import torch
 
+from . import lib as _lib
 from . import (KVL_ATTEND_ZERO_BYTES, KVL_CODE_FLOAT, KVL_CODE_INT, KVL_REPORT_BYTES, KVL_ROPE_BASE,
                KVL_ROPE_LINEAR, KVL_ROPE_PLAIN, KVL_ROPE_WAVELENGTH, KVL_TYPE_BFLOAT, KVL_TYPE_FLOAT,
                KVL_TYPE_HALF, check, kvl_attention, kvl_cache, kvl_pages, kvl_read_status,
-               kvl_rope, kvl_rows, kvl_sequences, lib)
+               kvl_rope, kvl_rows, kvl_sequences)
 
 CODES = {"e4m3": KVL_CODE_FLOAT, "int8": KVL_CODE_INT}
 TYPES = {torch.bfloat16: KVL_TYPE_BFLOAT, torch.float16: KVL_TYPE_HALF, torch.float32: KVL_TYPE_FLOAT}
@@ -29,9 +31,12 @@ ROPE_KINDS = {"plain": KVL_ROPE_PLAIN, "linear": KVL_ROPE_LINEAR, "base": KVL_RO
               "wavelength": KVL_ROPE_WAVELENGTH}
 
 
-def _stream(stream):
+_raw_stream = torch._C._cuda_getCurrentRawStream  # torch.cuda.current_stream without its Stream object (5 us)
+
+
+def _stream(stream, device=0):
     if stream is None:
-        return torch.cuda.current_stream().cuda_stream
+        return _raw_stream(device)
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
@@ -47,9 +52,9 @@ def _ints(t, name, n=None):
     return t.data_ptr()
 
 
-def _rows(t, name, heads, dim):
-    """kvl_rows of a [rows, heads, dim] tensor."""
-    if not t.is_cuda or t.dim() != 3 or t.dtype not in TYPES:
+def _rows(r, t, name, heads, dim):
+    """Fill the kvl_rows `r` with a [rows, heads, dim] tensor."""
+    if t.dim() != 3 or not t.is_cuda or t.dtype not in TYPES:
         raise ValueError(f"{name}: a [rows, heads, dim] device tensor of bf16, f16 or f32")
     _, h, d = t.shape
     if h != heads or d != dim:
@@ -58,7 +63,28 @@ def _rows(t, name, heads, dim):
     if s2 != 1:
         raise ValueError(f"{name}: the last dimension is contiguous")
     z = t.element_size()
-    return kvl_rows(t.data_ptr(), s0 * z, s1 * z)
+    r.data, r.row_stride, r.head_stride = t.data_ptr(), s0 * z, s1 * z
+
+
+class _Args(threading.local):
+    """The C structs of a call, each thread's own: filling their fields takes a few hundred nanoseconds
+    where making them anew takes microseconds."""
+
+    def __init__(self, cache=None):
+        self.a, self.b = kvl_rows(), kvl_rows()
+        self.attn = kvl_attention()
+        # (views into the struct: q and out are filled in place)
+        self.q, self.out = self.attn.q, self.attn.out
+        self.seqs = kvl_sequences()
+        self.src, self.dst, self.heads = (kvl_rows * 4)(), (kvl_rows * 4)(), (ctypes.c_int32 * 4)()
+        self.sets = [(self.src[i], self.dst[i]) for i in range(4)]
+        if cache is not None:
+            p = cache._p
+            self.seqs.n_slots, self.seqs.table_stride = cache.n_slots, cache.tables.shape[1]
+            self.seqs.tables, self.seqs.lens = p.tables, p.lens
+
+
+_args = _Args()
 
 
 def _flat(t, dtype, shape, name):
@@ -90,7 +116,7 @@ def rope_frequencies(rot_dim, base=10000.0, kind="plain", factor=1.0, low=1.0, h
     if kind not in ROPE_KINDS or rot_dim <= 0 or rot_dim % 2:
         raise ValueError(f"kind: one of {sorted(ROPE_KINDS)}; rot_dim: a positive even number")
     f, g = np.zeros(rot_dim // 2, np.float32), ctypes.c_float(1.0)
-    check(lib().kvl_rotary_frequencies(ROPE_KINDS[kind], base, rot_dim // 2, factor, low, high, trained_context,
+    check(_lib().kvl_rotary_frequencies(ROPE_KINDS[kind], base, rot_dim // 2, factor, low, high, trained_context,
                                        int(bool(scale_gain)), f.ctypes.data, ctypes.byref(g)), "kvl_rotary_frequencies")
     return f, g.value
 
@@ -99,18 +125,20 @@ def rotary(rope, positions, pairs, inverse=False, stream=None):
     """Turn each (x, y) of `pairs` (y may be x), [rows, heads, dim] tensors of one type, by
     int32 `positions` [rows], in one launch.  inverse: the gradient of x from that of y."""
     n = len(pairs)
-    if n == 0:
-        raise ValueError("pairs: at least one (source, destination)")
+    if not 1 <= n <= 4:
+        raise ValueError("pairs: one to four (source, destination)")
     x0 = pairs[0][0]
     rows, _, dim = x0.shape
-    src, dst, heads = (kvl_rows * n)(), (kvl_rows * n)(), (ctypes.c_int32 * n)()
+    c, heads = _args, _args.heads
     for i, (x, y) in enumerate(pairs):
-        if x.dtype is not x0.dtype or y.dtype is not x0.dtype or x.shape != y.shape or x.shape[0] != rows:
+        if x.dtype is not x0.dtype or y.dtype is not x0.dtype or x.shape[0] != rows or y.shape[0] != rows:
             raise ValueError("pairs: tensors of one type, with the same rows")
         h = heads[i] = x.shape[1]
-        src[i], dst[i] = _rows(x, "source", h, dim), _rows(y, "destination", h, dim)
-    check(lib().kvl_rotary(rope._ref, rows, dim, TYPES[x0.dtype], _ints(positions, "positions", rows), n, src, dst,
-                           heads, int(bool(inverse)), _stream(stream)), "kvl_rotary")
+        src, dst = c.sets[i]
+        _rows(src, x, "source", h, dim)
+        _rows(dst, y, "destination", h, dim)
+    check(_lib().kvl_rotary(rope._ref, rows, dim, TYPES[x0.dtype], _ints(positions, "positions", rows), n, c.src, c.dst,
+                            heads, 1 if inverse else 0, _stream(stream, x0.get_device())), "kvl_rotary")
 
 
 class QuantCache:
@@ -134,7 +162,7 @@ class QuantCache:
         _ints(refs, "refs", N)
         self.codes, self.scales, self.tables, self.lens, self.refs, self.code = codes, scales, tables, lens, refs, code
         self.n_layers, self.pool_blocks, self.block_tokens, self.n_kv_heads, self.head_dim = L, N, B, H, d
-        self.device = codes.device
+        self.device, self._index = codes.device, codes.get_device()
         self.pairs = torch.empty((N, 2), dtype=torch.int32, device=self.device) if pairs is None else pairs
         # the report and, unless given, the number of pairs
         own = torch.zeros(KVL_REPORT_BYTES + 16, dtype=torch.uint8, device=self.device)
@@ -143,7 +171,7 @@ class QuantCache:
         _flat(self.pairs, torch.int32, (N, 2), "pairs")
         _ints(self.n_pairs, "n_pairs", 1)
         self.n_slots = tables.shape[0]
-        self._lib = lib()
+        self._lib = _lib()
         self._c = kvl_cache(L, H, d, B, N, CODES[code], 0, codes.data_ptr(), scales.data_ptr())
         self._p = kvl_pages(N, B, self.n_slots, tables.shape[1], tables.data_ptr(), lens.data_ptr(), refs.data_ptr(),
                             self.pairs.data_ptr(), self.n_pairs.data_ptr())
@@ -153,6 +181,7 @@ class QuantCache:
             raise ValueError(f"no such cache: head_dim {d} (a multiple of 16 up to 256), block_tokens {B}, {H} heads")
         self._ws = {}  # a workspace for each stream: calls on two streams may run at the same time
         self._scale = 1.0 / math.sqrt(d)
+        self._args = _Args(self)
         self._report = self.report.data_ptr()
         self.reset_status()
 
@@ -169,23 +198,28 @@ class QuantCache:
         return cls(codes, scales, tables, lens, refs, code=code)
 
     # -- rows -----------------------------------------------------------------
-    def _seqs(self, starts, slots, n_rows):
+    def _seqs(self, c, starts, slots, n_rows):
         n = starts.shape[0] - 1
         if n < 0 or (slots is None and n > self.n_slots):
             raise ValueError(f"starts: one more entry than there are sequences, of which there are {self.n_slots}")
-        return kvl_sequences(n, self.n_slots, n_rows, self.tables.shape[1], self._p.tables, None, self._p.lens,
-                             None if slots is None else _ints(slots, "slots", n), _ints(starts, "starts"))
+        s = c.seqs
+        s.n_seq, s.n_rows, s.starts = n, n_rows, _ints(starts, "starts")
+        s.slots = None if slots is None else _ints(slots, "slots", n)
+        return s
 
     def append(self, layer, k, v, starts, rope=None, slots=None, stream=None):
         """Quantise fresh k, v [rows, H, d] into the pages of `layer`: rows starts[i] ..
         starts[i + 1] are the last tokens of sequence slots[i] (or i).  rope: turn k by the
         tokens' positions first."""
-        if k.dtype is not v.dtype or k.shape != v.shape:
+        n_rows, dtype, c = k.shape[0], k.dtype, self._args
+        if dtype is not v.dtype or n_rows != v.shape[0]:
             raise ValueError("k, v: one type and shape")
-        kr, vr = _rows(k, "k", self.n_kv_heads, self.head_dim), _rows(v, "v", self.n_kv_heads, self.head_dim)
-        check(self._lib.kvl_cache_append(self._cache, layer, self._seqs(starts, slots, k.shape[0]), TYPES[k.dtype],
-                                         kr, vr, None if rope is None else rope._ref, self._report, _stream(stream)),
-              "kvl_cache_append")
+        _rows(c.a, k, "k", self.n_kv_heads, self.head_dim)
+        _rows(c.b, v, "v", self.n_kv_heads, self.head_dim)
+        r = self._lib.kvl_cache_append(self._cache, layer, self._seqs(c, starts, slots, n_rows), TYPES[dtype], c.a, c.b,
+                                       None if rope is None else rope._ref, self._report, _stream(stream, self._index))
+        if r:
+            check(r, "kvl_cache_append")
 
     def attend(self, layer, q, starts, out=None, lse=None, sm_scale=None, causal=True, window=0, slots=None,
                max_new=0, stream=None):
@@ -193,30 +227,39 @@ class QuantCache:
         sequences' tokens in `layer`; returns out [rows, n_heads, d].  lse: float32 [rows, n_heads]
         that receives the logarithms of the softmax sums.  max_new: a bound the caller knows on the
         rows of any one sequence."""
-        n_rows, heads = q.shape[0], q.shape[1]
-        qr = _rows(q, "q", heads, self.head_dim)
+        n_rows, heads, _ = q.shape
+        dtype, c = q.dtype, self._args
+        _rows(c.q, q, "q", heads, self.head_dim)
         if out is None:
-            out = torch.empty((n_rows, heads, self.head_dim), dtype=q.dtype, device=q.device)
-        elif out.dtype is not q.dtype or out.shape[0] != n_rows:
+            out = torch.empty((n_rows, heads, self.head_dim), dtype=dtype, device=q.device)
+        elif out.dtype is not dtype or out.shape[0] != n_rows:
             raise ValueError("out: the type and shape of q")
-        if lse is not None:
+        _rows(c.out, out, "out", heads, self.head_dim)
+        a = c.attn
+        if lse is None:
+            a.lse = None
+        else:
             _flat(lse, torch.float32, (n_rows, heads), "lse")
-        st = _stream(stream)
+            a.lse = lse.data_ptr()
+        st = _stream(stream, self._index)
         ws = self._ws.get(st)
         if ws is None:
             ws = self._workspace(st)
-        a = kvl_attention(qr, _rows(out, "out", heads, self.head_dim), None if lse is None else lse.data_ptr(), heads, TYPES[q.dtype],
-                          self._scale if sm_scale is None else sm_scale, int(bool(causal)), window, max_new)
-        check(self._lib.kvl_attend(self._cache, layer, self._seqs(starts, slots, n_rows), a, ws.data_ptr(),
-                                   self._ws_bytes, self._report, st), "kvl_attend")
+        a.n_heads, a.type, a.sm_scale = heads, TYPES[dtype], self._scale if sm_scale is None else sm_scale
+        a.causal, a.window, a.max_new = 1 if causal else 0, window, max_new
+        r = self._lib.kvl_attend(self._cache, layer, self._seqs(c, starts, slots, n_rows), a, ws[1], self._ws_bytes,
+                                 self._report, st)
+        if r:
+            check(r, "kvl_attend")
         return out
 
     def _workspace(self, st):
-        ws = torch.empty(self._ws_bytes, dtype=torch.uint8, device=self.device)
+        # allocated on its own stream: memory just freed on another may still be in use there
         with torch.cuda.stream(torch.cuda.ExternalStream(st) if st else torch.cuda.default_stream()):
+            ws = torch.empty(self._ws_bytes, dtype=torch.uint8, device=self.device)
             ws[:KVL_ATTEND_ZERO_BYTES].zero_()
-        self._ws[st] = ws
-        return ws
+        self._ws[st] = ws, ws.data_ptr()
+        return self._ws[st]
 
     # -- pages ----------------------------------------------------------------
     def extend(self, slots, counts, stream=None):
@@ -224,32 +267,32 @@ class QuantCache:
         appended (a shared last page is replaced by a copy)."""
         n = slots.shape[0]
         check(self._lib.kvl_pages_extend(self._pages, n, _ints(slots, "slots"), _ints(counts, "counts", n),
-                                         self._report, _stream(stream)), "kvl_pages_extend")
+                                         self._report, _stream(stream, self._index)), "kvl_pages_extend")
 
     def fork(self, parents, children, stream=None):
         """children[i] (empty) becomes a copy of parents[i] that shares its pages."""
         n = parents.shape[0]
         check(self._lib.kvl_pages_fork(self._pages, n, _ints(parents, "parents"), _ints(children, "children", n),
-                                       self._report, _stream(stream)), "kvl_pages_fork")
+                                       self._report, _stream(stream, self._index)), "kvl_pages_fork")
 
     def free(self, slots, stream=None):
         """The sequences of `slots` end; their pages lose a reference."""
         check(self._lib.kvl_pages_free(self._pages, slots.shape[0], _ints(slots, "slots"), self._report,
-                                       _stream(stream)), "kvl_pages_free")
+                                       _stream(stream, self._index)), "kvl_pages_free")
 
     def compact(self, stream=None):
         """Renumber the live pages into the lowest numbers; ``copy_pages`` moves them."""
-        check(self._lib.kvl_pages_compact(self._pages, self._report, _stream(stream)), "kvl_pages_compact")
+        check(self._lib.kvl_pages_compact(self._pages, self._report, _stream(stream, self._index)), "kvl_pages_compact")
 
     def copy_pages(self, stream=None):
         """Make the copies that the last extend or compact asked for (every layer)."""
         check(self._lib.kvl_pages_copy(self._cache, self._p.pairs, self._p.n_pairs, self.pool_blocks, self._report,
-                                       _stream(stream)), "kvl_pages_copy")
+                                       _stream(stream, self._index)), "kvl_pages_copy")
 
     # -- status ---------------------------------------------------------------
     def status(self, stream=None):
         """(code, detail) of the problems recorded so far (synchronises)."""
-        return kvl_read_status(self._report, _stream(stream))
+        return kvl_read_status(self._report, _stream(stream, self._index))
 
     def reset_status(self, stream=None):
-        check(self._lib.kvl_report_reset(self._report, _stream(stream)), "kvl_report_reset")
+        check(self._lib.kvl_report_reset(self._report, _stream(stream, self._index)), "kvl_report_reset")
