@@ -4,11 +4,11 @@
 //   inverse: sin negated (the transposed map; with gain it is the gradient, without it also
 //   the inverse).
 //
-// Bound by HBM: each element is read and written once.  A row's cosines and sines serve all
-// its heads, so a CTA takes kRowsPerCta rows, its threads first work out the rows' pairs into
-// shared memory (one pair each), then stream the heads in 16-byte vectors: a thread turns VEC
-// pairs, i.e. one vector (interleaved) or two (halves, n_freq elements apart), and the
-// elements after the pairs are copied as vectors.
+// Bound by HBM: each element is read and written once.  A CTA takes tiles of a few rows, whose angles
+// its threads work out into shared memory (a pair each); then a thread keeps one vector position of a
+// head (16 bytes of pairs, or two such vectors n_freq elements apart, or 16 bytes of what follows the
+// pairs) and walks the tile's heads, kAhead at a time, so no index is divided and enough loads are in
+// flight; the first of them leave before the angles are worked out.
 #include <cmath>
 #include <cstring>
 
@@ -26,27 +26,38 @@ struct RotaryArgs {
     int64_t n_rows;
     int32_t n_freq, head_dim, interleaved, inverse;
     float gain;
-    int32_t rows_per_cta;
+    int32_t tile_rows;
+    int32_t rest_vecs;  // vectors after a head's pairs that have to be copied
+    bool copy_rest;     // some destination is not its source
     int32_t n_sets;
     int32_t heads_end[kMaxSets];  // heads of the sets, summed
     kvl_rows src[kMaxSets], dst[kMaxSets];
-    int32_t copy_rest[kMaxSets];  // the elements after the pairs have to be copied
 };
 
-// VEC elements at p, as floats and back.  VEC * element size is 8 or 16 bytes.
+// VEC elements as they are in memory (16 or 8 bytes), and as floats.
 template <int TYPE, int VEC>
-__device__ __forceinline__ void load_vec(const uint8_t *p, float (&v)[VEC])
+struct RawVec {
+    using type = uint4;
+};
+template <>
+struct RawVec<KVL_TYPE_BFLOAT, 4> {
+    using type = uint2;
+};
+template <>
+struct RawVec<KVL_TYPE_HALF, 4> {
+    using type = uint2;
+};
+
+template <int TYPE, int VEC>
+__device__ __forceinline__ void to_floats(const typename RawVec<TYPE, VEC>::type &raw, float (&v)[VEC])
 {
+    const uint32_t *u = reinterpret_cast<const uint32_t *>(&raw);
     if constexpr (TYPE == KVL_TYPE_FLOAT) {
-        const float4 a = *reinterpret_cast<const float4 *>(p);
-        v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-    } else if constexpr (VEC == 8) {
-        load8<TYPE>(p, v);
-    } else {
-        const uint2 w = *reinterpret_cast<const uint2 *>(p);
-        const uint32_t u[2] = {w.x, w.y};
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
+        for (int i = 0; i < VEC; ++i) v[i] = __uint_as_float(u[i]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < VEC / 2; ++i) {
             if constexpr (TYPE == KVL_TYPE_BFLOAT) {
                 v[2 * i] = __uint_as_float(u[i] << 16);
                 v[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
@@ -71,79 +82,125 @@ __device__ __forceinline__ void store_vec(uint8_t *p, const float (&v)[VEC])
     }
 }
 
-template <int TYPE, int VEC>
-__global__ void __launch_bounds__(kThreads) rotary_kernel(const __grid_constant__ RotaryArgs a)
+template <int TYPE, int VEC, bool INTERLEAVED>
+__global__ void __launch_bounds__(kThreads, 4) rotary_kernel(const __grid_constant__ RotaryArgs a)
 {
-    constexpr int kSize = TYPE == KVL_TYPE_FLOAT ? 4 : 2;
-    extern __shared__ float2 turns[];  // [rows][n_freq] (cos, sin) with the gain
-    const int64_t row0 = int64_t(blockIdx.x) * a.rows_per_cta;
-    const int rows = int(min(int64_t(a.rows_per_cta), a.n_rows - row0));
-    for (int i = threadIdx.x; i < rows * a.n_freq; i += kThreads) {
-        const int r = i / a.n_freq, f = i - r * a.n_freq;
-        float2 cs = cos_sin_of(a.positions[row0 + r], a.inv_freq[f]);
-        cs.x *= a.gain;
-        cs.y *= a.inverse ? -a.gain : a.gain;
-        turns[i] = cs;
-    }
-    __syncthreads();
-    // an item: one vector of a head's pairs (halves: and its partner), or of its rest
-    const int per_pairs = a.interleaved ? 2 * a.n_freq / VEC : a.n_freq / VEC;
-    const int per_head = per_pairs + (a.head_dim - 2 * a.n_freq) / VEC;
+    constexpr int kSize = TYPE == KVL_TYPE_FLOAT ? 4 : 2, kAhead = INTERLEAVED ? 4 : 2;
+    using Raw = typename RawVec<TYPE, VEC>::type;
+    extern __shared__ __align__(16) float turns[];  // [rows][2][n_freq]: cosines, sines, with the gain
     const int heads = a.heads_end[a.n_sets - 1];
-    const int per_row = heads * per_head, total = rows * per_row;
-    for (int i = threadIdx.x; i < total; i += kThreads) {
-        const int r = i / per_row, rest = i - r * per_row;
-        int h = rest / per_head;
-        const int v = rest - h * per_head;
-        int s = 0;
-        while (h >= a.heads_end[s]) ++s;
-        if (s) h -= a.heads_end[s - 1];
-        const uint8_t *x = static_cast<const uint8_t *>(a.src[s].data) + (row0 + r) * a.src[s].row_stride +
-                           h * a.src[s].head_stride;
-        uint8_t *y = static_cast<uint8_t *>(a.dst[s].data) + (row0 + r) * a.dst[s].row_stride +
-                     h * a.dst[s].head_stride;
-        if (v >= per_pairs) {
-            if (!a.copy_rest[s]) continue;
-            const int at = (2 * a.n_freq + (v - per_pairs) * VEC) * kSize;
-            float u[VEC];
-            load_vec<TYPE, VEC>(x + at, u);
-            store_vec<TYPE, VEC>(y + at, u);
-        } else if (a.interleaved) {
-            const float2 *t = turns + r * a.n_freq + v * (VEC / 2);
-            float u[VEC], w[VEC];
-            load_vec<TYPE, VEC>(x + v * VEC * kSize, u);
+    const int per_pairs = INTERLEAVED ? 2 * a.n_freq / VEC : a.n_freq / VEC;  // vectors (or two) of a head's pairs
+    const int per_head = per_pairs + a.rest_vecs;
+    const int groups = kThreads / per_head;  // heads the CTA is at side by side
+    const int v = threadIdx.x % per_head, g = threadIdx.x / per_head;
+    const bool pairs = v < per_pairs;
+    const int at = (pairs ? v * VEC : 2 * a.n_freq + (v - per_pairs) * VEC) * kSize;
+    const int far = a.n_freq * kSize;  // from a half's vector to the other half's
+
+    for (int64_t row0 = int64_t(blockIdx.x) * a.tile_rows; row0 < a.n_rows; row0 += int64_t(gridDim.x) * a.tile_rows) {
+        const int rows = int(min(int64_t(a.tile_rows), a.n_rows - row0));
+        Raw u[kAhead], w[kAhead];
+        uint8_t *y[kAhead];
+        int turn[kAhead];
+        int r = 0, h = g;  // this thread's next head of the tile
+        auto load = [&]() {
 #pragma unroll
-            for (int k = 0; k < VEC / 2; ++k) {
-                w[2 * k] = u[2 * k] * t[k].x - u[2 * k + 1] * t[k].y;
-                w[2 * k + 1] = u[2 * k + 1] * t[k].x + u[2 * k] * t[k].y;
-            }
-            store_vec<TYPE, VEC>(y + v * VEC * kSize, w);
-        } else {
-            const float2 *t = turns + r * a.n_freq + v * VEC;
-            float u[VEC], w[VEC];
-            load_vec<TYPE, VEC>(x + v * VEC * kSize, u);
-            load_vec<TYPE, VEC>(x + (a.n_freq + v * VEC) * kSize, w);
+            for (int i = 0; i < kAhead; ++i) {
+                while (h >= heads && r < rows) {
+                    h -= heads;
+                    ++r;
+                }
+                y[i] = nullptr;
+                if (g < groups && r < rows) {
+                    int s = 0;
 #pragma unroll
-            for (int k = 0; k < VEC; ++k) {
-                const float p = u[k], q = w[k];
-                u[k] = p * t[k].x - q * t[k].y;
-                w[k] = q * t[k].x + p * t[k].y;
+                    for (int k = 0; k < kMaxSets - 1; ++k) s += k < a.n_sets - 1 && h >= a.heads_end[k];
+                    const int in = h - (s ? a.heads_end[s - 1] : 0);
+                    const uint8_t *x = static_cast<const uint8_t *>(a.src[s].data) + (row0 + r) * a.src[s].row_stride + in * a.src[s].head_stride + at;
+                    y[i] = static_cast<uint8_t *>(a.dst[s].data) + (row0 + r) * a.dst[s].row_stride + in * a.dst[s].head_stride + at;
+                    turn[i] = r * 2 * a.n_freq;
+                    u[i] = *reinterpret_cast<const Raw *>(x);
+                    if (!INTERLEAVED && pairs) w[i] = *reinterpret_cast<const Raw *>(x + far);
+                }
+                h += groups;
             }
-            store_vec<TYPE, VEC>(y + v * VEC * kSize, u);
-            store_vec<TYPE, VEC>(y + (a.n_freq + v * VEC) * kSize, w);
+        };
+        load();
+        for (int t = threadIdx.x; t < rows * a.n_freq; t += kThreads) {
+            const int q = t / a.n_freq, f = t - q * a.n_freq;
+            const float2 cs = cos_sin_of(a.positions[row0 + q], a.inv_freq[f]);
+            turns[q * 2 * a.n_freq + f] = cs.x * a.gain;
+            turns[(q * 2 + 1) * a.n_freq + f] = a.inverse ? -cs.y * a.gain : cs.y * a.gain;
         }
+        __syncthreads();
+        while (y[0]) {  // a thread's heads come in order: none is left when the first of a turn is none
+#pragma unroll
+            for (int i = 0; i < kAhead; ++i) {
+                if (!y[i]) continue;
+                if (!pairs) {
+                    *reinterpret_cast<Raw *>(y[i]) = u[i];
+                    continue;
+                }
+                constexpr int n = INTERLEAVED ? VEC / 2 : VEC;
+                float c[n], s[n];
+                if constexpr (n >= 4) {
+#pragma unroll
+                    for (int k = 0; k < n; k += 4) {
+                        const float4 c4 = *reinterpret_cast<const float4 *>(turns + turn[i] + v * n + k);
+                        const float4 s4 = *reinterpret_cast<const float4 *>(turns + turn[i] + a.n_freq + v * n + k);
+                        c[k] = c4.x; c[k + 1] = c4.y; c[k + 2] = c4.z; c[k + 3] = c4.w;
+                        s[k] = s4.x; s[k + 1] = s4.y; s[k + 2] = s4.z; s[k + 3] = s4.w;
+                    }
+                } else {
+#pragma unroll
+                    for (int k = 0; k < n; ++k) {
+                        c[k] = turns[turn[i] + v * n + k];
+                        s[k] = turns[turn[i] + a.n_freq + v * n + k];
+                    }
+                }
+                float p[VEC], o[VEC];
+                to_floats<TYPE, VEC>(u[i], p);
+                if constexpr (INTERLEAVED) {
+#pragma unroll
+                    for (int k = 0; k < n; ++k) {
+                        o[2 * k] = p[2 * k] * c[k] - p[2 * k + 1] * s[k];
+                        o[2 * k + 1] = p[2 * k + 1] * c[k] + p[2 * k] * s[k];
+                    }
+                    store_vec<TYPE, VEC>(y[i], o);
+                } else {
+                    float q[VEC];
+                    to_floats<TYPE, VEC>(w[i], q);
+#pragma unroll
+                    for (int k = 0; k < VEC; ++k) o[k] = p[k] * c[k] - q[k] * s[k];
+                    store_vec<TYPE, VEC>(y[i], o);
+#pragma unroll
+                    for (int k = 0; k < VEC; ++k) o[k] = q[k] * c[k] + p[k] * s[k];
+                    store_vec<TYPE, VEC>(y[i] + far, o);
+                }
+            }
+            load();
+        }
+        __syncthreads();  // the angles are free again
     }
 }
 
 template <int TYPE, int VEC>
 kvl_status launch_rotary(RotaryArgs &a, void *stream)
 {
-    // Few rows: one a CTA, so that they spread over the SMs; many: four, so that the
-    // threads' first pass (one pair each) has all of them at work.
-    a.rows_per_cta = a.n_rows < 1024 ? 1 : 4;
-    const int64_t grid = ceil_div64(a.n_rows, a.rows_per_cta);
-    rotary_kernel<TYPE, VEC><<<unsigned(grid), kThreads, size_t(a.rows_per_cta) * a.n_freq * sizeof(float2),
-                               static_cast<cudaStream_t>(stream)>>>(a);
+    const int sms = sm_count();
+    if (sms <= 0) return KVL_ECUDA;
+    a.rest_vecs = a.copy_rest ? (a.head_dim - 2 * a.n_freq) / VEC : 0;
+    // Few rows: one a CTA, so that they spread over the SMs; many: tiles of four on a grid that fills the GPU
+    // once, so that most of the threads have an angle to work out and CTAs start only once.
+    const int64_t most = int64_t(sms) * 4;
+    a.tile_rows = a.n_rows <= most ? 1 : 4;
+    const int64_t tiles = ceil_div64(a.n_rows, a.tile_rows);
+    const unsigned grid = unsigned(tiles < most ? tiles : most);
+    const size_t smem = size_t(a.tile_rows) * 2 * a.n_freq * sizeof(float);
+    if (a.interleaved)
+        rotary_kernel<TYPE, VEC, true><<<grid, kThreads, smem, static_cast<cudaStream_t>(stream)>>>(a);
+    else
+        rotary_kernel<TYPE, VEC, false><<<grid, kThreads, smem, static_cast<cudaStream_t>(stream)>>>(a);
     return launch_status();
 }
 
@@ -184,7 +241,7 @@ extern "C" kvl_status kvl_rotary(const kvl_rope *rope, int64_t n_rows, int32_t h
             return KVL_EINVAL;
         a.src[i] = src[i];
         a.dst[i] = dst[i];
-        a.copy_rest[i] = !same;
+        a.copy_rest = a.copy_rest || !same;  // (in place the copy writes what is there)
     }
     a.inv_freq = rope->inv_freq;
     a.positions = positions;
