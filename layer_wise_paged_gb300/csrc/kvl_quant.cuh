@@ -180,23 +180,20 @@ __device__ __forceinline__ void store8(uint8_t *p, const float (&v)[8])
 
 // ---- codes -------------------------------------------------------------------------------
 
-// The nearest code (ties to even) of a value already scaled, clamped to the largest one.
+// The nearest codes (ties to even) of four values already scaled, clamped to the largest one; a NaN
+// becomes the NaN code (float) or 0 (int).
 template <int CODE>
-__device__ __forceinline__ uint32_t to_code(float x)
+__device__ __forceinline__ uint32_t to_codes4(float a, float b, float c, float d)
 {
-    if constexpr (CODE == KVL_CODE_FLOAT)
-        return __nv_cvt_float_to_fp8(x, __NV_SATFINITE, __NV_E4M3);
-    else  // a NaN fails both comparisons of the clamp's inner minimum and becomes 0
-        return uint32_t(__float2int_rn(x != x ? 0.f : fminf(fmaxf(x, -127.f), 127.f))) & 0xffu;
-}
-
-template <int CODE>
-__device__ __forceinline__ float of_code(uint32_t c)
-{
-    if constexpr (CODE == KVL_CODE_FLOAT)
-        return __half2float(__half(__nv_cvt_fp8_to_halfraw(__nv_fp8_storage_t(c), __NV_E4M3)));
-    else
-        return float(int8_t(c));
+    if constexpr (CODE == KVL_CODE_FLOAT) {
+        uint32_t r;
+        asm("{\n\t.reg .b16 l, h;\n\tcvt.rn.satfinite.e4m3x2.f32 l, %2, %1;\n\tcvt.rn.satfinite.e4m3x2.f32 h, %4, %3;\n\t"
+            "mov.b32 %0, {l, h};\n\t}" : "=r"(r) : "f"(a), "f"(b), "f"(c), "f"(d));
+        return r;
+    } else {
+        auto one = [](float x) { return uint32_t(__float2int_rn(x != x ? 0.f : fminf(fmaxf(x, -127.f), 127.f))) & 0xffu; };
+        return one(a) | one(b) << 8 | one(c) << 16 | one(d) << 24;
+    }
 }
 
 // The four codes of w as halves, two and two: exact for both code types.  An integer code c is read as
