@@ -16,34 +16,30 @@ constexpr int kThreads = 1024;
 constexpr int kPerThread = 8;
 constexpr int kTile = kThreads * kPerThread;
 
-// Exclusive prefix sum over the CTA's threads; `total` receives the sum.  Every thread of the
-// CTA calls it; scratch holds 33 ints.
-__device__ __forceinline__ int block_scan(int x, int *scratch, int &total)
+// Exclusive prefix sum over the CTA's threads (of int, or of two packed in 64 bits); `total` receives the
+// sum.  Every thread of the CTA calls it; scratch holds 32 values, and two calls in a row need
+// different ones (or a barrier between them).
+template <typename T>
+__device__ __forceinline__ T block_scan(T x, T *scratch, T &total)
 {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    int y = x;
+    T y = x;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-        const int z = __shfl_up_sync(0xffffffffu, y, o);
+        const T z = __shfl_up_sync(0xffffffffu, y, o);
         if (lane >= o) y += z;
     }
-    __syncthreads();  // readers of the previous call's scratch
     if (lane == 31) scratch[warp] = y;
     __syncthreads();
-    if (warp == 0) {
-        const int s = lane < int(blockDim.x >> 5) ? scratch[lane] : 0;
-        int t = s;
+    T sums = scratch[lane];  // kThreads / 32 = 32 of them: every warp adds them up for itself
 #pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int z = __shfl_up_sync(0xffffffffu, t, o);
-            if (lane >= o) t += z;
-        }
-        scratch[lane] = t - s;
-        if (lane == 31) scratch[32] = t;
+    for (int o = 1; o < 32; o <<= 1) {
+        const T z = __shfl_up_sync(0xffffffffu, sums, o);
+        if (lane >= o) sums += z;
     }
-    __syncthreads();
-    total = scratch[32];
-    return scratch[warp] + y - x;
+    total = __shfl_sync(0xffffffffu, sums, 31);
+    const T before = __shfl_sync(0xffffffffu, sums, warp ? warp - 1 : 0);
+    return (warp ? before : T(0)) + y - x;
 }
 
 // The counts of this thread's kPerThread pages of the tile at `base` (1 past the end).
@@ -106,7 +102,8 @@ __global__ void __launch_bounds__(kThreads) extend_kernel(kvl_pages p, int32_t n
                                                           const int32_t *counts, void *rep)
 {
     extern __shared__ uint32_t named[];  // one bit a slot
-    __shared__ int scratch[33];
+    __shared__ int scan_a[32], scan_b[32];
+    __shared__ long long scan_need[32];
     __shared__ int s_prefix[kThreads], s_first[kThreads], s_slot[kThreads];
     __shared__ int s_bad;
     const int tid = threadIdx.x;
@@ -114,11 +111,15 @@ __global__ void __launch_bounds__(kThreads) extend_kernel(kvl_pages p, int32_t n
     if (tid == 0) s_bad = 0;
     __syncthreads();
 
-    // 1. what the batch needs, and whether it may have it
+    // 1. what the batch needs (pages in the low half of a sum, copies in the high one), and whether it
+    // may have it
+    const Need nothing = {0, 0, 0, 0, 0, -1, KVL_OK};
+    Need q = nothing;
+    long long prefix = 0, want = 0;  // of the (last) chunk of entries
     int64_t need = 0;
     for (int base = 0; base < n; base += kThreads) {
         const int i = base + tid;
-        Need q = {0, 0, 0, 0, 0, -1, KVL_OK};
+        q = nothing;
         if (i < n) {
             q = need_of(p, slots, counts, i);
             if (q.error == KVL_OK && (atomicOr(&named[q.slot >> 5], 1u << (q.slot & 31)) >> (q.slot & 31) & 1u))
@@ -128,21 +129,26 @@ __global__ void __launch_bounds__(kThreads) extend_kernel(kvl_pages p, int32_t n
                 s_bad = 1;
             }
         }
-        int total;
-        block_scan(q.error ? 0 : q.pages, scratch, total);
-        need += total;
+        if (base) __syncthreads();  // readers of the chunk before
+        prefix = block_scan<long long>(q.error ? 0 : q.pages | (long long)(q.shared >= 0) << 32, scan_need, want);
+        need += want & 0xffffffffll;
     }
     __syncthreads();
     bool ok = s_bad == 0 && need <= p.pool_blocks;
     if (s_bad == 0 && need > p.pool_blocks && tid == 0) report(rep, KVL_ERANGE, n);
+    // the free pages: of a pool of one tile, their ranks stay for the second part
+    int r[kPerThread], mine = 0, rank = 0;
+    const bool one_tile = p.pool_blocks <= kTile;
     if (ok) {
         int64_t free_pages = 0;
         for (int64_t base = 0; base < p.pool_blocks && free_pages < need; base += kTile) {
-            int r[kPerThread], mine = 0, total;
+            int total;
+            mine = 0;
             load_refs(p.refs, base, p.pool_blocks, r);
 #pragma unroll
             for (int k = 0; k < kPerThread; ++k) mine += r[k] == 0;
-            block_scan(mine, scratch, total);
+            if (base) __syncthreads();
+            rank = block_scan<int>(mine, scan_a, total);
             free_pages += total;
         }
         if (free_pages < need) {
@@ -160,48 +166,52 @@ __global__ void __launch_bounds__(kThreads) extend_kernel(kvl_pages p, int32_t n
     int n_pairs = 0;
     for (int base = 0; base < n; base += kThreads) {
         const int i = base + tid;
-        Need q = {0, 0, 0, 0, 0, -1, KVL_OK};
-        if (i < n) q = need_of(p, slots, counts, i);
-        int want, copies;
-        const int prefix = block_scan(q.pages, scratch, want);
-        const int pair = block_scan(q.shared >= 0, scratch, copies);
-        s_prefix[tid] = prefix;
+        if (n > kThreads) {
+            q = i < n ? need_of(p, slots, counts, i) : nothing;
+            __syncthreads();
+            prefix = block_scan<long long>(q.pages | (long long)(q.shared >= 0) << 32, scan_need, want);
+        }
+        const int pages = int(want & 0xffffffffll), copies = int(want >> 32), pair = int(prefix >> 32);
+        s_prefix[tid] = int(prefix & 0xffffffffll);
         s_first[tid] = q.first;
         s_slot[tid] = q.slot;
         __syncthreads();
         int given = 0;
-        while (given < want && tile < p.pool_blocks) {
-            int r[kPerThread], mine = 0, total;
-            load_refs(p.refs, tile, p.pool_blocks, r);
+        while (given < pages && tile < p.pool_blocks) {
+            int total = pages;
+            if (!one_tile || base) {
+                mine = 0;
+                load_refs(p.refs, tile, p.pool_blocks, r);
 #pragma unroll
-            for (int k = 0; k < kPerThread; ++k) mine += r[k] == 0;
-            int rank = given + block_scan(mine, scratch, total);
+                for (int k = 0; k < kPerThread; ++k) mine += r[k] == 0;
+                rank = block_scan<int>(mine, scan_b, total);
+                __syncthreads();
+            }
+            int at = given + rank;
 #pragma unroll
             for (int k = 0; k < kPerThread; ++k) {
                 if (r[k] != 0) continue;
-                if (rank < want) {
-                    // the last entry whose prefix is at most rank (entries without need share
-                    // the prefix of the next one, so the last of equals is the one that needs)
+                if (at < pages) {
+                    // the last entry whose prefix is at most `at` (entries without need share the prefix
+                    // of the next one, so the last of equals is the one that needs)
                     int lo = 0, hi = kThreads;
                     while (hi - lo > 1) {
                         const int mid = (lo + hi) >> 1;
-                        if (s_prefix[mid] <= rank) lo = mid; else hi = mid;
+                        if (s_prefix[mid] <= at) lo = mid; else hi = mid;
                     }
                     const int64_t id = tile + int64_t(tid) * kPerThread + k;
-                    p.tables[s_slot[lo] * p.table_stride + s_first[lo] + (rank - s_prefix[lo])] = int32_t(id);
+                    p.tables[s_slot[lo] * p.table_stride + s_first[lo] + (at - s_prefix[lo])] = int32_t(id);
                     p.refs[id] = 1;
                 }
-                ++rank;
+                ++at;
             }
             given += total;
-            if (given < want) tile += kTile;  // otherwise the next entries go on in this tile
+            if (given < pages) tile += kTile;  // otherwise the next entries go on in this tile
         }
         __syncthreads();  // the tables and counts written above
         if (i < n) {
-            if (q.shared >= 0) {
-                reinterpret_cast<int2 *>(p.pairs)[n_pairs + pair] =
-                    make_int2(q.shared, p.tables[q.slot * p.table_stride + q.first]);
-            }
+            if (q.shared >= 0)
+                reinterpret_cast<int2 *>(p.pairs)[n_pairs + pair] = make_int2(q.shared, p.tables[q.slot * p.table_stride + q.first]);
             p.lens[q.slot] = q.len + q.count;
         }
         n_pairs += copies;
@@ -278,14 +288,16 @@ __global__ void __launch_bounds__(128) free_kernel(kvl_pages p, const int32_t *s
 
 __global__ void __launch_bounds__(kThreads) compact_kernel(kvl_pages p)
 {
-    __shared__ int scratch[33];
+    __shared__ int scan_a[32];
+    __shared__ long long scan_b[32];
     int64_t live = 0;
     for (int64_t base = 0; base < p.pool_blocks; base += kTile) {
         int r[kPerThread], mine = 0, total;
         load_refs(p.refs, base, p.pool_blocks, r);
 #pragma unroll
         for (int k = 0; k < kPerThread; ++k) mine += base + int64_t(threadIdx.x) * kPerThread + k < p.pool_blocks && r[k] > 0;
-        block_scan(mine, scratch, total);
+        if (base) __syncthreads();
+        block_scan<int>(mine, scan_a, total);
         live += total;
     }
     // free numbers below `live` and live pages from it on are equally many: both lists go
@@ -293,7 +305,8 @@ __global__ void __launch_bounds__(kThreads) compact_kernel(kvl_pages p)
     int2 *pairs = reinterpret_cast<int2 *>(p.pairs);
     int holes = 0, movers = 0;
     for (int64_t base = 0; base < p.pool_blocks; base += kTile) {
-        int r[kPerThread], h = 0, m = 0, n_holes, n_movers;
+        int r[kPerThread], h = 0, m = 0;
+        long long both;
         load_refs(p.refs, base, p.pool_blocks, r);
         const int64_t at = base + int64_t(threadIdx.x) * kPerThread;
 #pragma unroll
@@ -301,15 +314,16 @@ __global__ void __launch_bounds__(kThreads) compact_kernel(kvl_pages p)
             h += at + k < live && r[k] <= 0;
             m += at + k >= live && at + k < p.pool_blocks && r[k] > 0;
         }
-        int hr = holes + block_scan(h, scratch, n_holes);
-        int mr = movers + block_scan(m, scratch, n_movers);
+        if (base) __syncthreads();
+        const long long before = block_scan<long long>(h | (long long)m << 32, scan_b, both);
+        int hr = holes + int(before & 0xffffffffll), mr = movers + int(before >> 32);
 #pragma unroll
         for (int k = 0; k < kPerThread; ++k) {
             if (at + k < live && r[k] <= 0) pairs[hr++].y = int32_t(at + k);
             if (at + k >= live && at + k < p.pool_blocks && r[k] > 0) pairs[mr++].x = int32_t(at + k);
         }
-        holes += n_holes;
-        movers += n_movers;
+        holes += int(both & 0xffffffffll);
+        movers += int(both >> 32);
     }
     __syncthreads();
     for (int k = threadIdx.x; k < movers; k += kThreads) {
@@ -320,13 +334,21 @@ __global__ void __launch_bounds__(kThreads) compact_kernel(kvl_pages p)
     if (threadIdx.x == 0) *p.n_pairs = movers;
 }
 
-// Table entries that name a moved page follow it: the pairs are sorted by old number.
+// Table entries that name a moved page follow it: the pairs are sorted by old number, and searched in
+// shared memory where they fit (a search in memory is a dozen loads one after another).
+constexpr int kNamesHeld = 8192;
+
 __global__ void __launch_bounds__(256) rename_kernel(kvl_pages p, void *rep)
 {
+    __shared__ int32_t held[kNamesHeld];
     const int n = *p.n_pairs;
     if (n == 0) return;
     const int2 *pairs = reinterpret_cast<const int2 *>(p.pairs);
+    const bool in_shared = n <= kNamesHeld;
+    if (in_shared)
+        for (int k = threadIdx.x; k < n; k += 256) held[k] = pairs[k].x;
     const int32_t lowest = pairs[0].x;
+    __syncthreads();
     const int lane = threadIdx.x & 31;
     for (int s = blockIdx.x * 8 + int(threadIdx.x >> 5); s < p.n_slots; s += gridDim.x * 8) {
         const int32_t len = p.lens[s];
@@ -342,9 +364,10 @@ __global__ void __launch_bounds__(256) rename_kernel(kvl_pages p, void *rep)
             int lo = 0, hi = n;
             while (hi - lo > 1) {
                 const int mid = (lo + hi) >> 1;
-                if (pairs[mid].x <= id) lo = mid; else hi = mid;
+                if ((in_shared ? held[mid] : pairs[mid].x) <= id) lo = mid; else hi = mid;
             }
-            if (pairs[lo].x == id) *e = pairs[lo].y;
+            const int2 q = pairs[lo];
+            if (q.x == id) *e = q.y;
         }
     }
 }
