@@ -8,8 +8,10 @@ namespace kvl {
 namespace {
 
 // Entries with more rows than this (fresh tokens x query heads of a KV head) go to the tensor-memory
-// kernel.
-constexpr int kChunkRows = 64;
+// kernel, whose time hardly depends on them up to 256, while attend_rows' grows with each 16.  Measured
+// (us, rows / chunk; 8 KV heads, d = 128): 32 sequences of 2,048 tokens: 16 rows 53 / 100, 32 84 / 101,
+// 48 112 / 102, 64 143 / 102; one of 32,768: 32 rows 45 / 52, 64 67 / 53.
+constexpr int kChunkRows = 40;
 
 // SMs the workspace is sized for (a host without a device sizes it for a GB300).
 int workspace_sms()

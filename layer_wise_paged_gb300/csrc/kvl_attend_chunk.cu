@@ -33,8 +33,8 @@ constexpr int kStages = 2;
 constexpr int kPlaces = 4;                  // steps whose scales are kept (see place_full)
 constexpr int kBatch = 512;                 // entries whose steps are held at a time
 // Units of a share: a job's steps, and kJobCost before them for starting it (finding it, loading Q,
-// filling the pipeline).
-constexpr int kJobCost = 4;
+// filling the pipeline; prompts of a few jobs a CTA: 355 us, with 4 374, with 8 366, with none 520).
+constexpr int kJobCost = 6;
 constexpr int kStepsPerCta = kJobCost + 2;  // a share is at least this many units
 
 // Scales and places of a step's groups; partial[w]: some row sees only a part of the two groups that

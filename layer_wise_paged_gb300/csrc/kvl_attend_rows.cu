@@ -29,12 +29,14 @@ constexpr int kThreads = kWarps * 32;
 constexpr int kPair = 2;          // groups a warp takes at a time
 constexpr int kStages = 2;        // pairs in its ring: one worked on, one on its way
 constexpr int kCtasPerSm = 2;     // 12 warps an SM: 168 registers a thread, 192 KB of rings at d = 128
-// Units of a share: a job's groups, and kJobCost before them for starting and joining it.  A share is at
-// least kUnitsPerCta, and a job of at most kSmallJob groups is not split: joining the parts takes as
-// long as some 70 groups (one token of 777: 8 CTAs and 13 us instead of 33 CTAs and 16).
-constexpr int kJobCost = 16;
-constexpr int kUnitsPerCta = 40;
-constexpr int kSmallJob = 72;
+// Units of a share: a job's groups, and kJobCost before them for starting and joining it (8 to 64 rows of
+// 48 ragged sequences: 45 us, with a cost of 16 49; 256 sequences: 242 us and 249).  A share is at least
+// kUnitsPerCta (8 heads of 1,500 tokens: 13 us, with 40 18), and a job of at most kSmallJob groups is not
+// split, as its parts would have to be joined (one token of 777, 8 jobs of 49 groups: not split 15.9 us,
+// split 13.5; of 500, 32 groups: 11.5 either way; with nothing kept whole and shares of 40 17.6).
+constexpr int kJobCost = 48;
+constexpr int kUnitsPerCta = 12;
+constexpr int kSmallJob = 48;
 
 template <int D, int NT>
 struct Shape {
@@ -267,20 +269,31 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attend_rows_kernel(const
 #pragma unroll
         for (int k = 0; k < kStages - 1; ++k) load_pair(k);
 
-        // ---- Q: each row scaled by a power of two into the range of a half (undone in s_cq)
-        for (int r = warp; r < kRows; r += kWarps) {
-            const int row = tile * kRows + r;
+        // ---- Q: each row scaled by a power of two into the range of a half (undone in s_cq).  A warp's rows
+        // are all on their way before the first is looked at.
+        constexpr int kQTurns = (kRows + kWarps - 1) / kWarps;
+        uint32_t qraw[kQTurns][D / 64];
+#pragma unroll
+        for (int z = 0; z < kQTurns; ++z) {
+            const int r = warp + z * kWarps, row = tile * kRows + r;
             const bool ok = r < rows;
             const uint8_t *src = static_cast<const uint8_t *>(a.attn.q.data) +
                                  (int64_t(c.e.row0) + (ok ? row / G : 0)) * a.attn.q.row_stride +
                                  int64_t(h * G + (ok ? row % G : 0)) * a.attn.q.head_stride;
+#pragma unroll
+            for (int x = 0; x < D / 64; ++x) {
+                const int e = lane * 2 + 64 * x;
+                qraw[z][x] = ok && e < d ? *reinterpret_cast<const uint32_t *>(src + 2 * e) : 0;
+            }
+        }
+#pragma unroll
+        for (int z = 0; z < kQTurns; ++z) {
+            const int r = warp + z * kWarps;
             float v[D / 32];
             float amax = 0.f;
 #pragma unroll
             for (int x = 0; x < D / 64; ++x) {
-                const int e = lane * 2 + 64 * x;
-                uint32_t w = 0;
-                if (ok && e < d) w = *reinterpret_cast<const uint32_t *>(src + 2 * e);
+                const uint32_t w = qraw[z][x];
                 if constexpr (TYPE == KVL_TYPE_BFLOAT) {
                     v[2 * x] = __uint_as_float(w << 16);
                     v[2 * x + 1] = __uint_as_float(w & 0xffff0000u);
@@ -293,6 +306,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attend_rows_kernel(const
             }
 #pragma unroll
             for (int o = 16; o; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+            if (r >= kRows) break;
             // amax * up in [1, 2) (exact powers of two; a row of zeros or infinities stays)
             const uint32_t ex = (__float_as_uint(amax) >> 23) & 0xffu;
             const bool plain = ex < 2 || ex > 252;
