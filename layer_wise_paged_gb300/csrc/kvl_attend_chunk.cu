@@ -271,6 +271,7 @@ struct Job {
     int32_t entry, h, sa, n;  // KV head; steps [sa, sa + n) of the tile
     int32_t pos0;             // position of the entry's first fresh row
     int32_t two;              // the second half tile has rows
+    int32_t half;             // of s_cq
     uint32_t it, it_g[2];     // steps done by this CTA, and of each half tile: the barriers' phases
     bool complete;            // the share holds the whole job
 };
@@ -370,9 +371,9 @@ __global__ void __launch_bounds__(kThreads, 1) attend_chunk_kernel(const __grid_
     extern __shared__ uint8_t smem_raw[];
     __shared__ __align__(8) unsigned long long bars[BARS];
     __shared__ Places places[kPlaces];
-    __shared__ float s_cq[kJobRows];
+    __shared__ float s_cq[2][kJobRows];
     __shared__ uint32_t s_units[kBatch];
-    __shared__ Job job;
+    __shared__ Job job, next;
     __shared__ int s_last, s_gone, s_nan;
     __shared__ uint32_t s_tmem;
 
@@ -418,6 +419,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_chunk_kernel(const __grid_
                             job.u_end = cut.start(blockIdx.x + 1);
                             job.cut = cut;
                             job.it = job.it_g[0] = job.it_g[1] = 0;
+                            job.n = job.taken = job.two = job.half = 0;
                         }
                         base = a.seqs.n_seq;  // found: leave both loops
                         break;
@@ -475,75 +477,64 @@ __global__ void __launch_bounds__(kThreads, 1) attend_chunk_kernel(const __grid_
     const uint8_t *codes = static_cast<const uint8_t *>(a.cache.codes);
     const int64_t plane = int64_t(a.layer) * 2 * N, v_plane_bytes = N * B * H * d;
 
-    while (true) {
-        if (warp == 0) next_job(a, job, lane);
-        if (tid == 0) s_nan = 0;
-        __syncthreads();
-        if (job.n == 0) {  // its steps are the next share's
-            if (job.u + job.taken >= job.u_end) break;
-            __syncthreads();
-            if (tid == 0) {
-                job.off += job.taken;
-                job.u += job.taken;
-            }
-            __syncthreads();
-            continue;
+    // Q of the job in `next` to its place, by the converting warps: each row scaled by a power of two into
+    // the range of a half (undone in s_cq).  All rows come by asynchronous copies into the (free) K stages,
+    // each vector to the thread that takes it on from there.
+    auto load_q = [&] {
+        const int cw = warp - 8, rows = next.t.rows, h = next.h, row0 = next.e.row0, row_base = next.row_base;
+        float *cq = s_cq[next.half];
+        constexpr int kLanes = D / 8, kPer = 32 / kLanes;  // lanes of a row, rows of a warp's vector
+        const int at = (lane % kLanes) * 8;
+        const int turns = (next.two ? kJobRows : kTileRows) / (4 * kPer);
+        const uint32_t stage = sm + C::kK + (tid & 127) * 16;
+#pragma unroll 2
+        for (int x = 0; x < turns; ++x) {
+            const int r = (cw + x * 4) * kPer + lane / kLanes;
+            const bool ok = r < rows && at < d;
+            const uint32_t row = ok ? row_base + r : 0, tok = row / uint32_t(G);
+            copy_async16(stage + x * 2048,
+                         static_cast<const uint8_t *>(a.attn.q.data) + int64_t(row0 + tok) * a.attn.q.row_stride +
+                             int64_t(h * G + row - tok * G) * a.attn.q.head_stride + (ok ? 2 * at : 0), ok);
         }
-
-        // ---- Q: each row scaled by a power of two into the range of a half (undone in s_cq)
-        {
-            const int rows = job.t.rows, h = job.h, row0 = job.e.row0, row_base = job.row_base;
-            constexpr int kLanes = D / 8, kPer = 32 / kLanes;  // lanes of a row, rows of a warp's vector
-            const int at = (lane % kLanes) * 8;
-            constexpr int kTurns = (kJobRows / kPer + kThreads / 32 - 1) / (kThreads / 32);
-            // All rows come by asynchronous copies into the (free) K and V stages, each vector to the thread
-            // that takes it on from there: short loops, as this code runs once a job and is fetched anew.
-            const uint32_t stage = sm + C::kK + tid * 16;
-#pragma unroll 1
-            for (int x = 0; x < kTurns; ++x) {
-                const int r = (warp + x * (kThreads / 32)) * kPer + lane / kLanes;
-                const bool ok = r < rows && at < d;
-                const uint32_t row = ok ? row_base + r : 0, tok = row / uint32_t(G);
-                copy_async16(stage + x * (kThreads * 16),
-                             static_cast<const uint8_t *>(a.attn.q.data) + int64_t(row0 + tok) * a.attn.q.row_stride +
-                                 int64_t(h * G + row - tok * G) * a.attn.q.head_stride + (ok ? 2 * at : 0), ok);
-            }
-            copy_async_commit();
-            copy_async_wait<0>();
-#pragma unroll 1
-            for (int x = 0; x < kTurns; ++x) {
-                const int r = (warp + x * (kThreads / 32)) * kPer + lane / kLanes;
-                const uint4 raw = ld_shared_v4(stage + x * (kThreads * 16));
-                float v[8];
-                load8<TYPE>(reinterpret_cast<const uint8_t *>(&raw), v);
-                float amax = 0.f;
+        copy_async_commit();
+        copy_async_wait<0>();
+#pragma unroll 4
+        for (int x = 0; x < turns; ++x) {
+            const int r = (cw + x * 4) * kPer + lane / kLanes;
+            const uint4 raw = ld_shared_v4(stage + x * 2048);
+            float v[8];
+            load8<TYPE>(reinterpret_cast<const uint8_t *>(&raw), v);
+            float amax = 0.f;
 #pragma unroll
-                for (int y = 0; y < 8; ++y) amax = fmaxf(amax, fabsf(v[y]));
+            for (int y = 0; y < 8; ++y) amax = fmaxf(amax, fabsf(v[y]));
 #pragma unroll
-                for (int o = kLanes / 2; o; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-                if (r >= kJobRows) continue;
-                const uint32_t ex = (__float_as_uint(amax) >> 23) & 0xffu;
-                const bool plain = ex < 2 || ex > 252;
-                const float up = plain ? 1.f : __uint_as_float((254u - ex) << 23);
-                const float down = plain ? 1.f : __uint_as_float(ex << 23);
-                uint4 w;
-                w.x = pack2<KVL_TYPE_HALF>(v[0] * up, v[1] * up);
-                w.y = pack2<KVL_TYPE_HALF>(v[2] * up, v[3] * up);
-                w.z = pack2<KVL_TYPE_HALF>(v[4] * up, v[5] * up);
-                w.w = pack2<KVL_TYPE_HALF>(v[6] * up, v[7] * up);
-                const int rt = r & (kTileRows - 1), unit = at / 8;
-                *reinterpret_cast<uint4 *>(smem + C::kQ + (r / kTileRows) * C::kTileBytes + (unit >> 3) * (kTileRows * 128) +
-                                           rt * 128 + (((unit & 7) ^ (rt & 7)) << 4)) = w;
-                if (lane % kLanes == 0) s_cq[r] = a.attn.sm_scale * kLog2e * down;
-            }
+            for (int o = kLanes / 2; o; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+            const uint32_t ex = (__float_as_uint(amax) >> 23) & 0xffu;
+            const bool plain = ex < 2 || ex > 252;
+            const float up = plain ? 1.f : __uint_as_float((254u - ex) << 23);
+            const float down = plain ? 1.f : __uint_as_float(ex << 23);
+            uint4 w;
+            w.x = pack2<KVL_TYPE_HALF>(v[0] * up, v[1] * up);
+            w.y = pack2<KVL_TYPE_HALF>(v[2] * up, v[3] * up);
+            w.z = pack2<KVL_TYPE_HALF>(v[4] * up, v[5] * up);
+            w.w = pack2<KVL_TYPE_HALF>(v[6] * up, v[7] * up);
+            const int rt = r & (kTileRows - 1), unit = at / 8;
+            *reinterpret_cast<uint4 *>(smem + C::kQ + (r / kTileRows) * C::kTileBytes + (unit >> 3) * (kTileRows * 128) +
+                                       rt * 128 + (((unit & 7) ^ (rt & 7)) << 4)) = w;
+            if (lane % kLanes == 0) cq[r] = a.attn.sm_scale * kLog2e * down;
         }
         fence_proxy_async_smem();
-        __syncthreads();
+    };
 
+    // Each turn: the job's steps, beside which the converting warps find the next job and load its Q as
+    // soon as the last product that reads Q is done, so that only the first job (the first turn has no
+    // steps) waits for its Q.
+    while (true) {
         if (warp >= 8) {
             // ---- convert K and V
             const int cw = warp - 8, n = job.n, h = job.h, len = job.e.len;
             const uint32_t it = job.it;
+            if (n > 0) {
             const int32_t *table = job.e.table;
             const int g0 = job.t.g0 + job.sa * kGroups, g1 = job.t.g1, all_lo = job.t.all_lo, all_hi = job.t.all_hi;
             constexpr int kPer = 512 / D, kVecs = 32 / kPer;  // rows of a warp's vector, vectors of its 32 slots
@@ -680,7 +671,38 @@ __global__ void __launch_bounds__(kThreads, 1) attend_chunk_kernel(const __grid_
                 if (lane == 0) mbar_arrive(bar + 8 * (V_FULL + st));
                 if (s + 1 < n) fetch(vreg, v_plane_bytes);
             }
-        } else if (warp < 4 || job.two) {
+            }
+            // the stages of the two steps that would come next are free, so all of K's readers are done
+            const uint32_t k0 = it + n, k1 = k0 + 1;
+            const bool free = __all_sync(0xffffffffu, wait_bar(bar + 8 * (K_EMPTY + k0 % kStages), ((k0 / kStages) & 1) ^ 1, gone) &&
+                                                          wait_bar(bar + 8 * (K_EMPTY + k1 % kStages), ((k1 / kStages) & 1) ^ 1, gone));
+            if (warp == 8) {
+                if (lane == 0) {
+                    next = job;
+                    next.it += n;
+                    next.it_g[0] += n;
+                    if (job.two) next.it_g[1] += n;
+                    next.half ^= 1;
+                    next.n = 0;
+                }
+                __syncwarp();
+                while (free) {
+                    const uint32_t u0 = next.u + next.taken, off = next.off + next.taken;
+                    __syncwarp();
+                    if (u0 >= next.u_end) break;
+                    if (lane == 0) {
+                        next.u = u0;
+                        next.off = off;
+                    }
+                    __syncwarp();
+                    next_job(a, next, lane);
+                    __syncwarp();
+                    if (next.n > 0) break;  // (its steps may be the next share's)
+                }
+            }
+            meet_wait<128>(5);
+            if (free && next.n > 0) load_q();
+        } else if (job.n > 0 && (warp < 4 || job.two)) {
             // ---- softmax: row r of the job, TMEM lane r % 128
             const int g = warp >> 2, r = tid & 255;  // (uniform: warp is)
             const uint32_t lanes = uint32_t(warp & 3) << 21;  // lane 32 (warp % 4), in bits 16 and up
@@ -695,7 +717,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_chunk_kernel(const __grid_
                 if (r >= job.t.rows) { lo = job.t.all_lo; hi = job.t.all_hi; }
             }
             float row_m = -INFINITY, row_l = 0.f;
-            const float cq = s_cq[r];
+            const float cq = s_cq[job.half][r];
             // The warpgroup's first warp issues its tile's products.
             const bool leads = (warp & 3) == 0;
             const uint32_t it_u = __shfl_sync(0xffffffffu, it, 0);
@@ -959,7 +981,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_chunk_kernel(const __grid_
             }
             tmem_fence_before();
         }
-        if (!job.complete) {
+        if (job.n > 0 && !job.complete) {
             // parts of this job: shares first .. last; the one that arrives last joins them
             const int first = int(job.cut.share_of(job.u0)), last = int(job.cut.share_of(job.u0 + job.t.steps - 1));
             __threadfence();
@@ -1011,17 +1033,14 @@ __global__ void __launch_bounds__(kThreads, 1) attend_chunk_kernel(const __grid_
                 }
             }
         }
-        __syncthreads();  // Q and tensor memory are free again
+        __syncthreads();  // tensor memory is free again, the next job's Q in its place
         tmem_fence_after();
         if (tid == 0) {
-            job.it += job.n;
-            job.it_g[0] += job.n;
-            if (job.two) job.it_g[1] += job.n;
-            job.off += job.taken;
-            job.u += job.taken;
+            job = next;
+            s_nan = 0;
         }
         __syncthreads();
-        if (*gone || job.u >= job.u_end) break;
+        if (*gone || job.n == 0) break;
     }
     if (*gone) {
         if (tid == 0) report(a.report, KVL_ETIMEOUT, blockIdx.x);
