@@ -472,8 +472,11 @@ kvl_status kvl_cache_append(const kvl_cache *cache, int32_t layer, const kvl_seq
  * (slots past lens, pages past the sequence's end) are never part of a result, whatever they
  * hold.  Statistics and sums are held in 32 bits, probabilities enter the products in 16.
  * n_rows * (n_heads / H) is below 2^31 - 256.
+ * Scales are taken to be at least 0 (V scales below 1e-30 count as 1e-30).  A call with more work than
+ * 2^31 groups of 16 tokens (about 10^10 tokens, counted for each KV head and row tile) does nothing and
+ * the report says KVL_ERANGE.
  *   max_new   0, or a bound on the fresh rows of any entry that the caller knows; it chooses
- *             kernels, results do not depend on it */
+ *             kernels, so results depend on it in their rounding only */
 typedef struct kvl_attention {
     kvl_rows q;       /* n_rows rows of n_heads heads */
     kvl_rows out;     /* likewise; must not overlap q */

@@ -61,8 +61,8 @@ extern "C" kvl_status kvl_attend(const kvl_cache *cache, int32_t layer, const kv
     a.counters = static_cast<uint32_t *>(d_workspace);
     a.parts = reinterpret_cast<float *>(static_cast<uint8_t *>(d_workspace) + KVL_ATTEND_ZERO_BYTES);
     a.report = d_report;
-    // Which kernel an entry is worked by depends on its rows alone; the bound on them only tells
-    // which launches can be left out.
+    // Of a batch, each entry goes to the kernel that suits its rows; where the bound on them (or the only
+    // entry's rows) says that one kernel takes all, the other is not launched.
     const int64_t bound = attn->max_new > 0 && attn->max_new < seqs->n_rows ? attn->max_new : seqs->n_rows;
     const int64_t most = bound * (attn->n_heads / cache->n_kv_heads);
     if (cache->head_dim > 128 || most <= kChunkRows) return launch_attend_rows(a, most, sms, stream);

@@ -1,17 +1,21 @@
 // kvl_attend_chunk.cu -- attention of many rows a sequence: prompts and their chunks.
 //
-// Bound by the tensor cores: 4 d operations for each (row, visible token).  One CTA an SM takes
+// 4 d operations for each (row, visible token), which is above the tensor cores' floor for prompts; bound
+// by the chain product, softmax, product of a tile (512 tokens of 32 heads on 31,232: 222 us where the
+// products alone take 135; a tile's turn of 3,700 cycles is 1,700 of softmax, 1,230 of products and 800 of
+// handing over, and tensor memory has no columns for a second S of a tile).  One CTA an SM takes
 // 256 rows of one KV head (query heads of the head times tokens), two accumulator tiles of 128,
 // and walks the tokens 128 slots (8 groups) at a time:
 //   warps 0-3, 4-7   softmax of tile 0, tile 1: a thread a row.  S comes from tensor memory, P goes
-//                    back over it as halves, O is rescaled in place when the maximum has grown
-//                    by more than 2^8 since it was last set (rare after the first slots);
+//                    back over it as halves, O is rescaled in place when the maximum has outgrown
+//                    the reference (kSlack).  The first warp of each issues its tile's products:
+//                    O += P V of the step (P in tensor memory, V token-major), then S = Q K^T of
+//                    the next (both in shared memory, K-major); the tiles take turns, so one's
+//                    softmax runs under the other's products;
 //   warps 8-11       read K and V codes from the pages, convert them to halves (exact) and lay
 //                    them out in shared memory for the tensor cores (128-byte swizzle), two
-//                    stages each, with the groups' scales and places beside them;
-//   warp 12          one thread issues the products: S_g = Q_g K^T (both in shared memory, K-major)
-//                    and O_g += P_g V (P in tensor memory, V token-major), for g = 0, 1 in turn,
-//                    so one tile's softmax runs under the other tile's products.
+//                    stages each, with the groups' scales and places beside them; between jobs
+//                    they find the next one and lay out its Q.
 // A converted K or V stage serves 256 rows, which is what keeps the conversion (16 bytes in, 32
 // out a vector) small beside the products.
 //
@@ -757,8 +761,8 @@ __global__ void __launch_bounds__(kThreads, 1) attend_chunk_kernel(const __grid_
                 const Places &pl = places[(it + s) % kPlaces];
                 const bool whole = !(pl.partial[0] | pl.partial[1] | pl.partial[2] | pl.partial[3]);
                 // The step's 128 scores of the row stay in registers; x = score * f + b by groups.  Steps that
-                // every row sees whole have code without branches of its own: with the masks' in
-                // it, the two passes took 1,900 cycles instead of 1,300.
+                // every row sees whole have code of their own: with the masks' code for all, 512 tokens on
+                // 31,232 took 440 us instead of 240 (in an earlier form of this loop).
                 auto weights = [&](auto whole_c) -> bool {
                     constexpr bool kWhole = decltype(whole_c)::value;
                     uint32_t x0[32], x1[32], x2[32], x3[32];

@@ -1,10 +1,11 @@
 // kvl_attend_rows.cu -- attention of few rows a sequence: decoded tokens, drafted tokens.
 //
-// Bound by HBM: each cached byte is read once, and 2 * 8 multiply-adds a byte are far below the
-// tensor rate, so what counts is bytes in flight and few instructions a byte.
+// Each cached byte is read once, and 2 * 8 multiply-adds a byte are far below the tensor rate, so what counts
+// is bytes in flight and few instructions a byte (256 ragged sequences: 241 us, 5.5 TB/s with 42 % of the
+// issue slots used; one token of 128,000: 62 us, of which 8 pass before the first bytes have come).
 //
 // A warp takes 16 tokens of one KV head at a time from its own ring in shared memory (filled by
-// 16-byte asynchronous copies, kStages groups ahead, no barrier between warps) and computes the
+// 16-byte asynchronous copies, a pair of groups ahead, no barrier between warps) and computes the
 // transposed products with 16 x 8 x 16 tensor instructions:
 //   S^T [16 tokens x 8 rows] = K [16 x d] Q^T,   O^T [d x 8 rows] += V^T [d x 16] P^T.
 // Tokens (then elements of V) fill the 16-high operand and the rows, i.e. the query heads of
@@ -26,9 +27,10 @@ namespace {
 
 constexpr int kWarps = 6;
 constexpr int kThreads = kWarps * 32;
-constexpr int kPair = 2;          // groups a warp takes at a time
-constexpr int kStages = 2;        // pairs in its ring: one worked on, one on its way
-constexpr int kCtasPerSm = 2;     // 12 warps an SM: 168 registers a thread, 192 KB of rings at d = 128
+constexpr int kPair = 2;          // groups a warp takes at a time (4 at d = 64: 137 us for 256 sequences of 1,500, with 2 123)
+constexpr int kStages = 2;        // pairs in its ring: one worked on, one on its way (3 or 4 at d = 64: the same time)
+constexpr int kCtasPerSm = 2;     // 12 warps an SM: 168 registers a thread, 192 KB of rings at d = 128 (3 at
+                                  // d = 64: 142 us for those 123, as the registers run out)
 // Units of a share: a job's groups, and kJobCost before them for starting and joining it (8 to 64 rows of
 // 48 ragged sequences: 45 us, with a cost of 16 49; 256 sequences: 242 us and 249).  A share is at least
 // kUnitsPerCta (8 heads of 1,500 tokens: 13 us, with 40 18), and a job of at most kSmallJob groups is not
@@ -616,8 +618,10 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attend_rows_kernel(const
             if (s_last) {
                 __threadfence();
                 if (tid == 0) a.counters[first] = 0;
-                // factors of the parts' rows into shared memory (over the rings), all loads at once; then
-                // every thread adds up four elements of a row over the parts
+                // The parts' maxima and sums into shared memory (over the rings), all loads at once; a warp a
+                // row turns them into factors; then each warp adds up every kWarps-th part and the warps'
+                // sums are added up in order (one token of 128,000, 38 parts of 8 rows: 62.4 us; with a thread an
+                // element 64.9).
                 const int n_parts = last - first + 1;
                 float *fac = reinterpret_cast<float *>(smem + S::kQBytes), *sums = fac + n_parts * kRows;
                 auto part_of = [&](int b) { return a.parts + (int64_t(first + b) * 2 + (b == 0)) * S::kPartFloats; };
@@ -627,28 +631,54 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attend_rows_kernel(const
                     sums[x] = r < rows ? __ldcg(part_of(b) + kRows + r) : 0.f;
                 }
                 __syncthreads();
-                if (tid < rows) {
+                for (int r = warp; r < rows; r += kWarps) {
                     float big = -INFINITY, sum = 0.f;
-                    for (int b = 0; b < n_parts; ++b) big = fmaxf(big, fac[b * kRows + tid]);
-                    for (int b = 0; b < n_parts; ++b) {
-                        const float mb = fac[b * kRows + tid], f = mb == -INFINITY ? 0.f : exp2_of(mb - big);
-                        fac[b * kRows + tid] = f;
-                        sum += sums[b * kRows + tid] * f;
+                    for (int b = lane; b < n_parts; b += 32) big = fmaxf(big, fac[b * kRows + r]);
+#pragma unroll
+                    for (int x = 16; x; x >>= 1) big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, x));
+                    for (int b = lane; b < n_parts; b += 32) {
+                        const float mb = fac[b * kRows + r], f = mb == -INFINITY ? 0.f : exp2_of(mb - big);
+                        fac[b * kRows + r] = f;
+                        sum += sums[b * kRows + r] * f;
                     }
-                    s_m[0][tid] = big;
-                    s_l[0][tid] = sum;
+#pragma unroll
+                    for (int x = 16; x; x >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, x);
+                    if (lane == 0) {
+                        s_m[0][r] = big;
+                        s_l[0][r] = sum;
+                    }
                 }
+                __syncthreads();
+                constexpr int kVecs = kRows * (D / 4) / 32;  // vectors of a lane
+                float4 v[kVecs];
+#pragma unroll
+                for (int x = 0; x < kVecs; ++x) v[x] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 2
+                for (int b = warp; b < n_parts; b += kWarps) {
+                    const float *p = part_of(b) + 2 * kRows;
+#pragma unroll
+                    for (int x = 0; x < kVecs; ++x) {
+                        const int r = (x * 32 + lane) / (D / 4);
+                        if (r >= rows) continue;
+                        const float4 y = __ldcg(reinterpret_cast<const float4 *>(p) + x * 32 + lane);
+                        const float f = fac[b * kRows + r];
+                        v[x].x += y.x * f; v[x].y += y.y * f; v[x].z += y.z * f; v[x].w += y.w * f;
+                    }
+                }
+                __syncthreads();
+                float4 *all = reinterpret_cast<float4 *>(smem + S::kQBytes);  // over the factors
+#pragma unroll
+                for (int x = 0; x < kVecs; ++x) all[(warp * kVecs + x) * 32 + lane] = v[x];
                 __syncthreads();
                 for (int x = tid; x < rows * (D / 4); x += kThreads) {
                     const int r = x / (D / 4), e = (x % (D / 4)) * 4;
-                    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 8
-                    for (int b = 0; b < n_parts; ++b) {
-                        const float4 y = __ldcg(reinterpret_cast<const float4 *>(part_of(b) + 2 * kRows + r * D + e));
-                        const float f = fac[b * kRows + r];
-                        v.x += y.x * f; v.y += y.y * f; v.z += y.z * f; v.w += y.w * f;
+                    float4 y = all[x];
+#pragma unroll
+                    for (int w = 1; w < kWarps; ++w) {
+                        const float4 z = all[w * kVecs * 32 + x];
+                        y.x += z.x; y.y += z.y; y.z += z.z; y.w += z.w;
                     }
-                    finish(r, e, v, s_m[0][r], s_l[0][r]);
+                    finish(r, e, y, s_m[0][r], s_l[0][r]);
                 }
             }
         }
@@ -672,6 +702,8 @@ kvl_status launch_rows(const AttendArgs &a, int sms, void *stream)
 template <int CODE, int TYPE>
 kvl_status launch_rows_dim(const AttendArgs &a, int64_t most, int sms, void *stream)
 {
+    // Row tiles of 8 while they hold all rows, else of 16, so that the cache is read half as often (256 sequences
+    // of 1,500, 4 rows, d = 128: in tiles of 8 154 us, of 16 215; 40 of 3,000, 8 rows: 57 and 75).
     if (a.cache.head_dim <= 64) {
         if (most <= 8) return launch_rows<CODE, TYPE, 64, 1>(a, sms, stream);
         return launch_rows<CODE, TYPE, 64, 2>(a, sms, stream);
