@@ -77,3 +77,52 @@ def test_page_numbers_do_not_matter():
 def test_runs_twice_alike():
     from examples import branches
     assert branches.run()[0] == branches.run()[0]
+
+
+def test_step_in_a_graph():
+    """A decode step captured once and replayed leaves what the same steps leave call by call."""
+    from layer_wise_paged_gb300.cache import QuantCache, Rope, rotary
+
+    def make():
+        cache = QuantCache.empty(2, 2, 64, 16, 40, 4, 10)
+        rope = Rope.make(64)
+        slots = torch.arange(4, dtype=torch.int32, device="cuda")
+        ones = torch.ones_like(slots)
+        starts = torch.arange(5, dtype=torch.int32, device="cuda")
+        g = torch.Generator(device="cuda").manual_seed(3)
+        x = torch.randn(4, 8 + 2 + 2, 64, generator=g, device="cuda").to(torch.bfloat16)
+        q, out = torch.empty(4, 8, 64, dtype=torch.bfloat16, device="cuda"), torch.zeros(2, 4, 8, 64, dtype=torch.bfloat16,
+                                                                                      device="cuda")
+
+        def step():
+            rotary(rope, cache.lens, [(x[:, :8], q)])  # a token's position is the length before it
+            cache.extend(slots, ones)
+            cache.copy_pages()
+            for layer in range(2):
+                cache.append(layer, x[:, 8:10], x[:, 10:], starts, rope=rope)
+                cache.attend(layer, q, starts, out=out[layer], max_new=1)
+
+        return cache, out, step
+
+    side = torch.cuda.Stream()
+    a, out_a, step_a = make()
+    b, out_b, step_b = make()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        step_a()  # the workspace of this stream is made before the capture
+        step_b()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        step_a()
+    for _ in range(20):
+        graph.replay()
+    with torch.cuda.stream(side):
+        for _ in range(20):
+            step_b()
+    torch.cuda.synchronize()
+    assert a.status() == b.status() == (0, 0)
+    assert torch.equal(a.lens, b.lens) and int(a.lens[0]) == 21
+    assert torch.equal(a.tables, b.tables) and torch.equal(a.refs, b.refs)
+    assert torch.equal(a.codes, b.codes) and torch.equal(a.scales, b.scales)
+    assert torch.equal(out_a, out_b) and bool(out_a.any())
