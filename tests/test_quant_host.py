@@ -200,3 +200,15 @@ def test_rotary_frequencies(lib):
                 (3, 1e4, 4, 2.0, 1.0, 4.0, 0.0)):
         assert call(*bad, 0, ctypes.addressof(out), None) == kvl.KVL_EINVAL, bad
     assert call(0, 1e4, 4, 1.0, 1.0, 4.0, 8192.0, 0, None, None) == kvl.KVL_EINVAL
+
+
+def test_attend_refuses_rows_past_32_bits(lib):
+    """Rows of a KV head (rows times grouped heads) are counted in 32 bits."""
+    c = cache()
+    need = lib.kvl_attend_workspace_bytes(c)
+    group = 64
+    rows = (2**31 - 256) // group
+    a = attention(n_heads=c.n_kv_heads * group)
+    assert lib.kvl_attend(c, 0, seqs(n_rows=rows), a, FAKE, need, FAKE, None) == kvl.KVL_EINVAL
+    # one row fewer gets past this check, to that of the workspace
+    assert lib.kvl_attend(c, 0, seqs(n_rows=rows - 1), a, FAKE + 8, need, FAKE, None) == kvl.KVL_EALIGN
