@@ -6,7 +6,7 @@
 // one CTA that walks the counts in tiles of kTile pages with block-wide prefix sums
 // (bound by latency: a few microseconds); fork and free are one CTA a sequence (atomic adds,
 // whose order does not show); copy moves whole pages with bulk copies through a ring of
-// shared-memory stages (bound by HBM, as the copy kernels of kvl_copy.cu are).
+// shared-memory stages, small ones a warp each (bound by HBM, as the copy kernels of kvl_copy.cu are).
 #include "kvl_quant.cuh"
 
 namespace kvl {
@@ -473,6 +473,57 @@ __global__ void __launch_bounds__(kCopyThreads) copy_pages_kernel(const __grid_c
     bulk_wait_all();
 }
 
+// Small pages: a warp a page and plane, 16 bytes a lane, as one thread that issues bulk copies takes 0.8 us a
+// unit, however small.  Measured (us, lanes / bulk copies; bytes of a page's plane of one layer): 1 KB x
+// 128,000 68 / 663, 4 KB x 128,000 211 / 660, 8 KB x 38,400 125 / 198; 16 KB x 32,000 192 / 177, 32 KB x
+// 4,800 61 / 51.
+constexpr int kSmallThreads = 256, kSmallCtasPerSm = 8;
+constexpr int64_t kSmallPage = 8192;
+
+__global__ void __launch_bounds__(kSmallThreads, kSmallCtasPerSm) copy_small_pages_kernel(const __grid_constant__ CopyPagesArgs a)
+{
+    int64_t n = *a.n_pairs;
+    if (n < 0 || n > a.max_pairs) {
+        if (blockIdx.x == 0 && threadIdx.x == 0) report(a.report, KVL_ERANGE, n);
+        n = n < 0 ? 0 : a.max_pairs;
+    }
+    const int64_t planes = int64_t(a.c.n_layers) * 2, N = a.c.pool_blocks;
+    const int H = a.c.n_kv_heads, lane = threadIdx.x & 31, page_bytes = int(a.page_bytes);
+    // unit u: pair u / planes, layer and plane u % planes
+    const int64_t u = int64_t(blockIdx.x) * (kSmallThreads / 32) + (threadIdx.x >> 5);
+    const int64_t step = int64_t(gridDim.x) * (kSmallThreads / 32), dk = step / planes, dlp = step - dk * planes;
+    int64_t k = u / planes, lp = u - k * planes;
+    while (k < n) {
+        int2 q;
+        if (pair_of(a, k, q)) {
+            const uint8_t *src = static_cast<const uint8_t *>(a.c.codes) + (lp * N + q.x) * a.page_bytes;
+            uint8_t *dst = static_cast<uint8_t *>(a.c.codes) + (lp * N + q.y) * a.page_bytes;
+            const float *from = a.c.scales + (lp * N + q.x) * H;
+            float *to = a.c.scales + (lp * N + q.y) * H;
+            const float first = lane < H ? from[lane] : 0.f;  // on its way with the codes
+            for (int at = lane * 16; at < page_bytes; at += 4 * 512) {
+                uint4 v[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    if (at + 512 * i < page_bytes) v[i] = *reinterpret_cast<const uint4 *>(src + at + 512 * i);
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    if (at + 512 * i < page_bytes) *reinterpret_cast<uint4 *>(dst + at + 512 * i) = v[i];
+            }
+            if (lane < H) to[lane] = first;
+            for (int h = lane + 32; h < H; h += 32) to[h] = from[h];
+        } else if (lane == 0) {
+            report(a.report, KVL_ERANGE, k);
+        }
+        k += dk;
+        lp += dlp;
+        if (lp >= planes) {
+            lp -= planes;
+            ++k;
+        }
+    }
+}
+
 inline kvl_status check_pages(const kvl_pages *p)
 {
     if (!p || p->pool_blocks <= 0 || p->pool_blocks > INT32_MAX || p->block_tokens <= 0 || p->n_slots <= 0 ||
@@ -563,10 +614,14 @@ extern "C" kvl_status kvl_pages_copy(const kvl_cache *cache, const int32_t *pair
     if (chunks > INT32_MAX) return KVL_EINVAL;
     a.chunks = int32_t(chunks);
     a.report = d_report;
-    static std::atomic<unsigned long long> ready[kMaxDevices];
-    if (!allow_smem(copy_pages_kernel, ready, kCopyStages * kStageBytes)) return KVL_ECUDA;
     const int sms = sm_count();
     if (sms <= 0) return KVL_ECUDA;
+    if (a.page_bytes <= kSmallPage) {
+        copy_small_pages_kernel<<<sms * kSmallCtasPerSm, kSmallThreads, 0, static_cast<cudaStream_t>(stream)>>>(a);
+        return launch_status();
+    }
+    static std::atomic<unsigned long long> ready[kMaxDevices];
+    if (!allow_smem(copy_pages_kernel, ready, kCopyStages * kStageBytes)) return KVL_ECUDA;
     copy_pages_kernel<<<sms, kCopyThreads, kCopyStages * kStageBytes, static_cast<cudaStream_t>(stream)>>>(a);
     return launch_status();
 }
