@@ -259,7 +259,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attend_rows_kernel(const
 #pragma unroll
                     for (int x = 0; x < D / 32; ++x) {
                         const int r = x * (32 / kChunks) + row_l;
-                        const bool ok = r < nv && (D == 256 || ch_l * 16 < d);
+                        const bool ok = r < nv && ch_l * 16 < d;  // (past the head lies the next one, or the end of the pool)
                         const uint8_t *p = src + (ok ? r * row_bytes + ch_l * 16 : 0);
                         copy_async16(dk + k_at<D>(r, ch_l), p, ok);
                         copy_async16(dk + S::kGroupBytes + v_at<D>(r, ch_l), p + v_plane_bytes, ok);
