@@ -2,13 +2,15 @@
 // and how a call's work is cut into equal shares.
 //
 // Both kernels compute, for a row with scores s_j = sm_scale q.K_j over the visible tokens,
-//   x_j = s_j log2(e) + log2(vs_j),  m = max x_j,  w_j = 2^(x_j - m),
+//   x_j = s_j log2(e) + log2(vs_j),  w_j = 2^(x_j - m),
 //   O = sum w_j codeV_j,  l = sum w_j / vs_j,   out = O / l,   lse = ln(l) + m ln(2),
 // with vs_j the V scale of token j's page: w_j 2^m / vs_j is the probability's numerator.  The
-// V scale rides in the exponent, so the products take the codes as they are, and w_j lies in
-// [0, 1] with 1 at the token that counts most: as a 16-bit half it has 11 significant bits
-// wherever it matters (below 2^-14 of the largest weight an absolute error of 2^-25).  The
-// maximum, l, O and every score are 32-bit.
+// V scale rides in the exponent, so the products take the codes as they are.  m is a reference near
+// the largest x_j (kHead, kSlack below).  w_j enters its product as a 16-bit half, which the tensor
+// cores take with exact halves of the codes: 11 significant bits down to 2^-14, an absolute error of
+// 2^-25 below.  The largest w_j of a row is 2^4 or more, so that is 2^-29 of it.  Bfloats would hold
+// every weight but with 8 bits.  l sums the weights before they are rounded.  The reference, l, O and
+// every score are 32-bit.
 //
 // Slots come in groups of 16, each within one page (a page whose size is no multiple of 16
 // ends in a part of a group), so a group has one K and one V scale and 16 consecutive rows.
@@ -34,12 +36,14 @@ namespace {
 
 constexpr int kGroup = 16;
 
-// What stands for m in the exponent is a reference, set kHead above a row's largest x so far and moved
-// only when an x passes it by kSlack: weights up to 2^14 are halves still, and those below 2^-14 keep
-// 2^-25 of a largest weight that is 2^-4 or more.  So a row's sums are rescaled about once.  (With the
-// reference at the maximum and a slack of 8, one of the 128 rows that the tensor-memory kernel steps
-// together moved in most steps and held the others up for 1,000 cycles.)
-constexpr float kSlack = 14.f, kHead = 4.f;
+// The reference m is set kHead above a row's largest x so far, that is below it, and moved only when an x
+// passes it by kSlack.  So weights stay below 2^15.5 (a half holds 2^15.99; half a bit is left for the
+// rounding of x), the largest is 2^4 or more, and a row's sums are rescaled about once: one of the 128
+// rows that the tensor-memory kernel steps together holds the others up for 1,000 cycles.  Both sides
+// (512 tokens on 31,232; prompts; us): -4 and 15.5 222.5 348, -4 and 15 224.5 350, -6 and 15 235 361, -8
+// and 15 252 385.  With the reference above the largest x (4 and 14: 221.8 346) weights of 2^-21 of the
+// largest were lost, and with them up to a fifth of what a long tail gives beside a peak.
+constexpr float kSlack = 15.5f, kHead = -4.f;
 
 // `total` units cut into `shares` contiguous parts whose sizes differ by at most one.  Units are counted
 // in 32 bits (a call whose units do not fit, some 10^10 tokens, is refused), as 64-bit divisions would

@@ -62,3 +62,51 @@ def test_another_heads_nan_stays_there(d, code, B):
 def test_append_to_heads_between_128_and_256(d, B):
     dev, want = A.run([43, 11, 90], [11, 1, 60], 2, d, B, "e4m3", BF)
     assert torch.equal(dev.scales.cpu(), want["scales"]) and torch.equal(dev.codes.cpu(), want["codes"])
+
+
+# ---- small weights beside a large one -----------------------------------------------------------------
+
+@pytest.mark.parametrize("share", [0.5, 0.8, 0.95])
+@pytest.mark.parametrize("tokens,new,seqs", [(131072, 64, 320), (131072, 2, 320), (131072, 64, 1), (20000, 130, 3)])
+def test_long_tail_beside_a_peak(tokens, new, seqs, share):
+    """The first token holds `share` of the softmax and has no V; a long tail whose V is about 1 holds the
+    rest, each token far below 2^-14 of the largest weight.  Many sequences (that share their pages) keep a
+    row in one CTA, so that all of its tail stands beside the peak.
+
+    A weight enters its product as a half with 2^4 or more for the largest of the row, so it is off by
+    2^-11 of itself, or by 2^-25 (2^-29 of the largest) where it is a subnormal half; out is rounded
+    to 2^-8 of itself, and a score is a sum of two products in 32 bits (72 roundings of 2^-23 bound it)."""
+    d, B = 64, 16
+    g = torch.Generator().manual_seed(tokens + new)
+    cache = Q.make_cache(12, 1, 1, d, B, [1], spare=0)  # (its tensors are replaced)
+    N = tokens // B
+    codes = torch.zeros((1, 2, N, B, 1, d), dtype=torch.uint8)
+    k = torch.zeros((N * B, d))
+    k[1:, 1] = torch.rand(tokens - 1, generator=g) * 2 - 1
+    k[0, 0] = 440.0 / 16
+    v = torch.zeros((N * B, d))
+    v[1:] = 1.0 + 0.25 * torch.rand((tokens - 1, 1), generator=g)
+    codes[0, 0, :, :, 0] = Q.to_codes(k * 16, "e4m3").view(N, B, d)
+    codes[0, 1, :, :, 0] = Q.to_codes(v * 16, "e4m3").view(N, B, d)
+    kd, vd = (Q.of_codes(codes[0, p], "e4m3").view(N * B, d) / 16 for p in (0, 1))
+    top = math.log(share / (1 - share) * tokens * math.sinh(1.0))  # the tail's mean of exp is sinh(1)
+    q = torch.zeros((new, 1, d))
+    q[:, 0, 0] = top * 8 / float(kd[0, 0])
+    q[:, 0, 1] = 8.0
+    q = q.to(BF)
+    perm = torch.randperm(N, generator=g)
+    pool = torch.empty_like(codes)
+    pool[:, :, perm] = codes
+    from layer_wise_paged_gb300.cache import QuantCache
+    dev = QuantCache(pool.cuda(), torch.full((1, 2, N, 1), 1 / 16).cuda(), perm.int().expand(seqs, N).contiguous().cuda(),
+                     torch.full((seqs,), tokens).int().cuda(), torch.full((N,), seqs, dtype=torch.int32, device="cuda"))
+    starts = (torch.arange(seqs + 1) * new).int().cuda()
+    out = dev.attend(0, q.repeat(seqs, 1, 1).cuda(), starts, max_new=new).view(seqs, new, d).cpu().double()
+    s = (q[:, 0].double() @ kd.T) / 8.0
+    s.masked_fill_(torch.arange(tokens)[None] > torch.arange(tokens - new, tokens)[:, None], -math.inf)
+    p = torch.softmax(s, -1)
+    want = p @ vd
+    assert 0.5 * (1 - share) < float(want.min()) and float(want.max()) < 2.5 * (1 - share)
+    ds = 72 * 2.0 ** -23 * float(q.double().abs().max() * kd.abs().max() / 8)
+    tol = (2.0 ** -8 + 2.0 ** -11 + 2 * ds) * want + tokens * 2.0 ** -29 * p.amax(-1, keepdim=True) * 1.25
+    assert float(((out - want).abs() - tol).max()) <= 0, float(((out - want).abs() / want).max())
