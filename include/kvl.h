@@ -495,6 +495,10 @@ typedef struct kvl_attention {
  * need a workspace each. */
 #define KVL_ATTEND_ZERO_BYTES 16384
 size_t kvl_attend_workspace_bytes(const kvl_cache *cache);
+/* The number of the stream capture that `stream` is in, unique in the process; 0: none.  Zeroing a
+ * workspace inside a capture happens when the graph runs and not before: such a workspace belongs to
+ * that graph alone. */
+uint64_t kvl_capture_id(void *stream);
 kvl_status kvl_attend(const kvl_cache *cache, int32_t layer, const kvl_sequences *seqs,
                       const kvl_attention *attn, void *d_workspace, size_t workspace_bytes,
                       void *d_report, void *stream);

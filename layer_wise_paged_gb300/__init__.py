@@ -116,6 +116,7 @@ def lib():
                                              ctypes.c_double, ctypes.c_double, i32, vp, P(ctypes.c_float)]
         L.kvl_cache_append.argtypes = [cp, i32, sp, i32, rp, rp, op, vp, vp]
         L.kvl_attend_workspace_bytes.argtypes, L.kvl_attend_workspace_bytes.restype = [cp], sz
+        L.kvl_capture_id.argtypes, L.kvl_capture_id.restype = [vp], ctypes.c_uint64
         L.kvl_attend.argtypes = [cp, i32, sp, P(kvl_attention), vp, sz, vp, vp]
         L.kvl_pages_extend.argtypes = [pg, i32, vp, vp, vp, vp]
         L.kvl_pages_fork.argtypes = [pg, i32, vp, vp, vp, vp]

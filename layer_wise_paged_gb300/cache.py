@@ -179,7 +179,10 @@ class QuantCache:
         self._ws_bytes = int(self._lib.kvl_attend_workspace_bytes(self._cache))
         if self._ws_bytes == 0:
             raise ValueError(f"no such cache: head_dim {d} (a multiple of 16 up to 256), block_tokens {B}, {H} heads")
-        self._ws = {}  # a workspace for each stream: calls on two streams may run at the same time
+        # a workspace for each stream (calls on two streams may run at the same time), and one for the newest
+        # capture on it (the graph may run beside them)
+        self._ws, self._ws_captured = {}, {}
+        self._capture_id = self._lib.kvl_capture_id
         self._scale = 1.0 / math.sqrt(d)
         self._args = _Args(self)
         self._report = self.report.data_ptr()
@@ -226,7 +229,11 @@ class QuantCache:
         """Attention of fresh rows q [rows, n_heads, d] (laid out as append's) over their
         sequences' tokens in `layer`; returns out [rows, n_heads, d].  lse: float32 [rows, n_heads]
         that receives the logarithms of the softmax sums.  max_new: a bound the caller knows on the
-        rows of any one sequence."""
+        rows of any one sequence.
+
+        Calls of one stream share a workspace, kept here.  Calls captured into a graph (torch.cuda.graph) have one
+        of that graph's own memory, which each run of the graph clears first: graphs may run in any
+        order, or beside each other and other calls where they have memory pools of their own."""
         n_rows, heads, _ = q.shape
         dtype, c = q.dtype, self._args
         _rows(c.q, q, "q", heads, self.head_dim)
@@ -242,9 +249,11 @@ class QuantCache:
             _flat(lse, torch.float32, (n_rows, heads), "lse")
             a.lse = lse.data_ptr()
         st = _stream(stream, self._index)
-        ws = self._ws.get(st)
-        if ws is None:
-            ws = self._workspace(st)
+        capture = self._capture_id(st)
+        held = self._ws_captured if capture else self._ws
+        ws = held.get(st)
+        if ws is None or ws[0] != capture:
+            ws = self._workspace(held, st, capture)
         a.n_heads, a.type, a.sm_scale = heads, TYPES[dtype], self._scale if sm_scale is None else sm_scale
         a.causal, a.window, a.max_new = 1 if causal else 0, window, max_new
         r = self._lib.kvl_attend(self._cache, layer, self._seqs(c, starts, slots, n_rows), a, ws[1], self._ws_bytes,
@@ -253,13 +262,14 @@ class QuantCache:
             check(r, "kvl_attend")
         return out
 
-    def _workspace(self, st):
-        # allocated on its own stream: memory just freed on another may still be in use there
+    def _workspace(self, held, st, capture):
+        # Allocated on its own stream: memory just freed on another may still be in use there.  In a capture
+        # the zeroing is a part of the graph, and the memory its pool's, as the graph's temporaries are.
         with torch.cuda.stream(torch.cuda.ExternalStream(st) if st else torch.cuda.default_stream()):
             ws = torch.empty(self._ws_bytes, dtype=torch.uint8, device=self.device)
             ws[:KVL_ATTEND_ZERO_BYTES].zero_()
-        self._ws[st] = ws, ws.data_ptr()
-        return self._ws[st]
+        held[st] = capture, ws.data_ptr(), ws
+        return held[st]
 
     # -- pages ----------------------------------------------------------------
     def extend(self, slots, counts, stream=None):

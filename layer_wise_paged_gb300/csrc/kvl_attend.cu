@@ -32,6 +32,17 @@ extern "C" size_t kvl_attend_workspace_bytes(const kvl_cache *cache)
     return KVL_ATTEND_ZERO_BYTES + size_t(workspace_sms()) * (rows > chunk ? rows : chunk);
 }
 
+extern "C" uint64_t kvl_capture_id(void *stream)
+{
+    cudaStreamCaptureStatus status = cudaStreamCaptureStatusNone;
+    unsigned long long id = 0;
+    if (cudaStreamGetCaptureInfo(static_cast<cudaStream_t>(stream), &status, &id) != cudaSuccess) {
+        cudaGetLastError();  // (the legacy stream beside a capture of another: not in one itself)
+        return 0;
+    }
+    return status == cudaStreamCaptureStatusNone ? 0 : id;
+}
+
 extern "C" kvl_status kvl_attend(const kvl_cache *cache, int32_t layer, const kvl_sequences *seqs,
                                  const kvl_attention *attn, void *d_workspace, size_t workspace_bytes,
                                  void *d_report, void *stream)

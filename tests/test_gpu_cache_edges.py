@@ -110,3 +110,97 @@ def test_long_tail_beside_a_peak(tokens, new, seqs, share):
     ds = 72 * 2.0 ** -23 * float(q.double().abs().max() * kd.abs().max() / 8)
     tol = (2.0 ** -8 + 2.0 ** -11 + 2 * ds) * want + tokens * 2.0 ** -29 * p.amax(-1, keepdim=True) * 1.25
     assert float(((out - want).abs() - tol).max()) <= 0, float(((out - want).abs() / want).max())
+
+
+# ---- captures -------------------------------------------------------------------------------------
+
+def _long_cache(seed=21):
+    """Sequences that are cut over several CTAs, queries of one and of 70 tokens, and their results."""
+    cache = Q.make_cache(seed, 1, 2, 64, 16, [6000, 9000])
+    dev = Q.on_gpu(cache)
+    g = torch.Generator().manual_seed(seed)
+    calls = []
+    for new in (1, 70):
+        q = torch.randn((2 * new, 4, 64), generator=g).to(BF).cuda()
+        starts = torch.tensor([0, new, 2 * new]).int().cuda()
+        calls.append((q, starts, new, dev.attend(0, q, starts, max_new=new)))
+    torch.cuda.synchronize()
+    return dev, calls
+
+
+def _attend_all(dev, calls, outs):
+    for (q, starts, new, _), out in zip(calls, outs):
+        dev.attend(0, q, starts, out=out, max_new=new)
+
+
+def _outs(calls):
+    return [torch.zeros_like(want) for _, _, _, want in calls]
+
+
+def _dirty_pool():
+    """A graph whose memory pool holds free memory full of ones."""
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        big = torch.empty(1 << 28, dtype=torch.uint8, device="cuda")
+        big.fill_(255)
+    graph.replay()
+    torch.cuda.synchronize()
+    del big
+    return graph
+
+
+def test_second_capture_runs_without_the_first():
+    """Two captures in a row on the same stream, without a call there before; only the second is run."""
+    dev, calls = _long_cache()
+    dirty = _dirty_pool()
+    graphs, outs = [torch.cuda.CUDAGraph() for _ in range(2)], [_outs(calls) for _ in range(2)]
+    for graph, out in zip(graphs, outs):
+        with torch.cuda.graph(graph, pool=dirty.pool()):
+            _attend_all(dev, calls, out)
+    for _ in range(3):
+        graphs[1].replay()
+    torch.cuda.synchronize()
+    for (_, _, _, want), first, second in zip(calls, *outs):
+        assert not bool(first.any())
+        assert torch.equal(second, want)
+    graphs[0].replay()
+    torch.cuda.synchronize()
+    for (_, _, _, want), first in zip(calls, outs[0]):
+        assert torch.equal(first, want)
+    assert dev.status() == (0, 0)
+
+
+def test_calls_on_a_stream_after_a_capture_that_never_ran():
+    dev, calls = _long_cache()
+    dirty = _dirty_pool()
+    graph, stream, never, outs = torch.cuda.CUDAGraph(), torch.cuda.Stream(), _outs(calls), _outs(calls)
+    with torch.cuda.graph(graph, pool=dirty.pool(), stream=stream):
+        _attend_all(dev, calls, never)
+    with torch.cuda.stream(stream):
+        _attend_all(dev, calls, outs)
+    torch.cuda.synchronize()
+    for (_, _, _, want), out, no in zip(calls, outs, never):
+        assert torch.equal(out, want) and not bool(no.any())
+
+
+def test_two_graphs_and_calls_at_the_same_time():
+    """Graphs captured on one stream, run on two others beside calls on the capture's stream."""
+    dev, calls = _long_cache()
+    side = torch.cuda.Stream()
+    graphs, outs = [torch.cuda.CUDAGraph() for _ in range(2)], [_outs(calls) for _ in range(3)]
+    for graph, out in zip(graphs, outs):
+        with torch.cuda.graph(graph, stream=side):
+            _attend_all(dev, calls, out)
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in graphs]
+    for _ in range(30):
+        for graph, stream in zip(graphs, streams):
+            with torch.cuda.stream(stream):
+                graph.replay()
+        with torch.cuda.stream(side):
+            _attend_all(dev, calls, outs[2])
+    torch.cuda.synchronize()
+    for out in outs:
+        for (_, _, _, want), x in zip(calls, out):
+            assert torch.equal(x, want)
+    assert dev.status() == (0, 0)
