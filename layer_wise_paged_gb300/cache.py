@@ -31,7 +31,9 @@ ROPE_KINDS = {"plain": KVL_ROPE_PLAIN, "linear": KVL_ROPE_LINEAR, "base": KVL_RO
               "wavelength": KVL_ROPE_WAVELENGTH}
 
 
-_raw_stream = torch._C._cuda_getCurrentRawStream  # torch.cuda.current_stream without its Stream object (5 us)
+# torch.cuda.current_stream without its Stream object (5 us), where torch has it
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda device: torch.cuda.current_stream(device).cuda_stream)
 
 
 def _stream(stream, device=0):
