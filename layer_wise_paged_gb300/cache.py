@@ -36,7 +36,19 @@ _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
     lambda device: torch.cuda.current_stream(device).cuda_stream)
 
 
-def _stream(stream, device=0):
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+_several = None  # whether there is another device than the current one (asked at the first call)
+
+
+def _stream(stream, device):
+    """The handle of the stream a call goes to.  The library launches on the current device, whatever
+    the tensors' is."""
+    global _several
+    if _several is None:
+        _several = torch.cuda.device_count() > 1
+    if _several and _current_device() != device:
+        raise ValueError(f"the tensors are on cuda:{device}, which is not the current device: call within "
+                         f"torch.cuda.device({device})")
     if stream is None:
         return _raw_stream(device)
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
@@ -267,7 +279,8 @@ class QuantCache:
     def _workspace(self, held, st, capture):
         # Allocated on its own stream: memory just freed on another may still be in use there.  In a capture
         # the zeroing is a part of the graph, and the memory its pool's, as the graph's temporaries are.
-        with torch.cuda.stream(torch.cuda.ExternalStream(st) if st else torch.cuda.default_stream()):
+        on = self.device
+        with torch.cuda.stream(torch.cuda.ExternalStream(st, device=on) if st else torch.cuda.default_stream(on)):
             ws = torch.empty(self._ws_bytes, dtype=torch.uint8, device=self.device)
             ws[:KVL_ATTEND_ZERO_BYTES].zero_()
         held[st] = capture, ws.data_ptr(), ws
