@@ -241,7 +241,8 @@ class QuantCache:
     def attend(self, layer, q, starts, out=None, lse=None, sm_scale=None, causal=True, window=0, slots=None,
                max_new=0, stream=None):
         """Attention of fresh rows q [rows, n_heads, d] (laid out as append's) over their
-        sequences' tokens in `layer`; returns out [rows, n_heads, d].  lse: float32 [rows, n_heads]
+        sequences' tokens in `layer`; returns out [rows, n_heads, d], which belongs to the call's
+        stream where it is made here.  lse: float32 [rows, n_heads]
         that receives the logarithms of the softmax sums.  max_new: a bound the caller knows on the
         rows of any one sequence.
 
@@ -251,8 +252,14 @@ class QuantCache:
         n_rows, heads, _ = q.shape
         dtype, c = q.dtype, self._args
         _rows(c.q, q, "q", heads, self.head_dim)
+        st = _stream(stream, self._index)
         if out is None:
-            out = torch.empty((n_rows, heads, self.head_dim), dtype=dtype, device=q.device)
+            shape = n_rows, heads, self.head_dim
+            if stream is None:
+                out = torch.empty(shape, dtype=dtype, device=q.device)
+            else:
+                with self._on(st):
+                    out = torch.empty(shape, dtype=dtype, device=q.device)
         elif out.dtype is not dtype or out.shape[0] != n_rows:
             raise ValueError("out: the type and shape of q")
         _rows(c.out, out, "out", heads, self.head_dim)
@@ -262,7 +269,6 @@ class QuantCache:
         else:
             _flat(lse, torch.float32, (n_rows, heads), "lse")
             a.lse = lse.data_ptr()
-        st = _stream(stream, self._index)
         capture = self._capture_id(st)
         held = self._ws_captured if capture else self._ws
         ws = held.get(st)
@@ -276,11 +282,16 @@ class QuantCache:
             check(r, "kvl_attend")
         return out
 
-    def _workspace(self, held, st, capture):
-        # Allocated on its own stream: memory just freed on another may still be in use there.  In a capture
-        # the zeroing is a part of the graph, and the memory its pool's, as the graph's temporaries are.
+    def _on(self, st):
+        """Allocations for calls on stream `st` are made on it: memory just freed on another may still be
+        in use there."""
         on = self.device
-        with torch.cuda.stream(torch.cuda.ExternalStream(st, device=on) if st else torch.cuda.default_stream(on)):
+        return torch.cuda.stream(torch.cuda.ExternalStream(st, device=on) if st else torch.cuda.default_stream(on))
+
+    def _workspace(self, held, st, capture):
+        # In a capture the zeroing is a part of the graph, and the memory its pool's, as the graph's
+        # temporaries are.
+        with self._on(st):
             ws = torch.empty(self._ws_bytes, dtype=torch.uint8, device=self.device)
             ws[:KVL_ATTEND_ZERO_BYTES].zero_()
         held[st] = capture, ws.data_ptr(), ws

@@ -204,3 +204,27 @@ def test_two_graphs_and_calls_at_the_same_time():
         for (_, _, _, want), x in zip(calls, out):
             assert torch.equal(x, want)
     assert dev.status() == (0, 0)
+
+
+# ---- streams ----------------------------------------------------------------------------------------
+
+def test_result_made_for_another_stream():
+    """The result of a call on a given stream is that stream's memory: not a block that was just freed on the
+    current one, where work on it is still to come."""
+    dev, calls = _long_cache()
+    side = torch.cuda.Stream()
+    q, starts, new, want = calls[1]
+    for cycles in (1000, 200_000_000):  # (the first time its kernels are loaded, which waits for the GPU)
+        dev.attend(0, q, starts, out=torch.empty_like(want), max_new=new, stream=side)
+        torch.cuda.synchronize()
+        freed = torch.empty_like(want)
+        torch.cuda._sleep(cycles)  # 0.1 s of the current stream, behind which it still writes `freed`
+        freed.fill_(7.0)
+        del freed
+        out = dev.attend(0, q, starts, max_new=new, stream=side)
+        torch.cuda.synchronize()
+        assert torch.equal(out, want)
+        del out
+    out = dev.attend(0, q, starts, max_new=new, stream=torch.cuda.default_stream())
+    torch.cuda.synchronize()
+    assert torch.equal(out, want)
