@@ -68,6 +68,13 @@ struct Cost {
     int32_t tiles, g0, groups;
 };
 
+// The first token a row at position `pos` sees, j > pos - window.  (A row stands before token 0 where an
+// entry has more rows than tokens; window may be as large as an int.)
+__device__ __forceinline__ int32_t first_seen(const AttendArgs &a, int32_t pos)
+{
+    return a.attn.window > 0 ? max(0, max(0, pos) - a.attn.window + 1) : 0;
+}
+
 __device__ __forceinline__ int32_t group_of(int32_t token, int32_t B, int32_t per_block)
 {
     const int32_t b = token / B;

@@ -234,9 +234,9 @@ __device__ __forceinline__ Tile tile_of(const AttendArgs &a, int32_t len, int32_
     const int pos0 = len - fresh;
     const int first = pos0 + int(row0 / uint32_t(G)), last = pos0 + int((row0 + t.rows - 1) / uint32_t(G));
     const int hi = a.attn.causal ? min(len, last + 1) : len;
-    const int lo = a.attn.window > 0 ? max(0, first - a.attn.window + 1) : 0;
+    const int lo = first_seen(a, first);
     t.all_hi = a.attn.causal ? min(len, first + 1) : len;
-    t.all_lo = a.attn.window > 0 ? max(0, last - a.attn.window + 1) : 0;
+    t.all_lo = first_seen(a, last);
     t.g0 = t.g1 = 0;
     if (hi > lo) {
         t.g0 = group_of(lo, B, per_block);
@@ -717,7 +717,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_chunk_kernel(const __grid_
             {
                 const int pos = job.pos0 + int(uint32_t(job.row_base + r) / uint32_t(G)), len = job.e.len;
                 hi = a.attn.causal ? min(len, pos + 1) : len;
-                lo = a.attn.window > 0 ? max(0, pos - a.attn.window + 1) : 0;
+                lo = first_seen(a, pos);
                 if (r >= job.t.rows) { lo = job.t.all_lo; hi = job.t.all_hi; }
             }
             float row_m = -INFINITY, row_l = 0.f;

@@ -96,7 +96,7 @@ __device__ __forceinline__ Cost cost_of(const AttendArgs &a, int i, void *rep)
     c.e = load_entry(a.seqs, B, i, rep);
     const int64_t rows = int64_t(c.e.fresh) * (a.attn.n_heads / a.cache.n_kv_heads);
     c.tiles = rows > a.max_rows ? 0 : int32_t((rows + 8 * NT - 1) / (8 * NT));
-    const int32_t lo = a.attn.window > 0 ? max(0, c.e.len - c.e.fresh - a.attn.window + 1) : 0;
+    const int32_t lo = first_seen(a, c.e.len - c.e.fresh);
     c.g0 = group_of(lo, B, per_block);
     // a sequence of no tokens is one group of none: its rows still get their zeros
     c.groups = max(1, c.e.len > 0 ? group_of(c.e.len - 1, B, per_block) + 1 - c.g0 : 0);
@@ -329,7 +329,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attend_rows_kernel(const
         float cq[NT][2];
         const int first_pos = pos0 + (tile * kRows) / G, last_pos = pos0 + (tile * kRows + rows - 1) / G;
         const int all_hi = a.attn.causal ? min(c.e.len, first_pos + 1) : c.e.len;
-        const int all_lo = a.attn.window > 0 ? max(0, last_pos - a.attn.window + 1) : 0;
+        const int all_lo = first_seen(a, last_pos);
 #pragma unroll
         for (int t = 0; t < NT; ++t)
 #pragma unroll
@@ -337,7 +337,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attend_rows_kernel(const
                 const int r = 8 * t + 2 * kk + x;
                 const int pos = pos0 + (tile * kRows + r) / G;
                 hi[t][x] = a.attn.causal ? min(c.e.len, pos + 1) : c.e.len;
-                lo[t][x] = a.attn.window > 0 ? max(0, pos - a.attn.window + 1) : 0;
+                lo[t][x] = first_seen(a, pos);
                 if (r >= rows) { lo[t][x] = 0; hi[t][x] = c.e.len; }
                 cq[t][x] = s_cq[r];
             }

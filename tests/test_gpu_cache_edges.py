@@ -228,3 +228,14 @@ def test_result_made_for_another_stream():
     out = dev.attend(0, q, starts, max_new=new, stream=torch.cuda.default_stream())
     torch.cuda.synchronize()
     assert torch.equal(out, want)
+
+
+# ---- windows ----------------------------------------------------------------------------------------
+
+@pytest.mark.parametrize("window", [1, 19, 2 ** 30, 2 ** 31 - 1])
+@pytest.mark.parametrize("lens,new", [([2, 40], [5, 3]), ([20, 33], [60, 33])])
+def test_windows_up_to_the_largest(lens, new, window):
+    """Also where an entry has more rows than tokens, so that its first rows stand before token 0."""
+    out, lse, (o, z, to, tz) = T.run(T.case(lens, new, window=window))
+    T.near(out, o, to, "out")
+    T.near(lse, z, tz, "lse")
