@@ -37,6 +37,7 @@ _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
 
 
 _current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+_MOST = 2 ** 31 - 1
 _several = None  # whether there is another device than the current one (asked at the first call)
 
 
@@ -269,6 +270,8 @@ class QuantCache:
         else:
             _flat(lse, torch.float32, (n_rows, heads), "lse")
             a.lse = lse.data_ptr()
+        if not (-_MOST <= window <= _MOST and -_MOST <= max_new <= _MOST):  # (a C int would wrap round)
+            raise ValueError("window, max_new: 32-bit numbers")
         capture = self._capture_id(st)
         held = self._ws_captured if capture else self._ws
         ws = held.get(st)

@@ -239,3 +239,13 @@ def test_windows_up_to_the_largest(lens, new, window):
     out, lse, (o, z, to, tz) = T.run(T.case(lens, new, window=window))
     T.near(out, o, to, "out")
     T.near(lse, z, tz, "lse")
+
+
+@pytest.mark.parametrize("name", ["window", "max_new"])
+@pytest.mark.parametrize("n", [2 ** 31, 2 ** 32 + 5, -2 ** 32 + 5])
+def test_numbers_past_32_bits_are_refused(name, n):
+    """They do not wrap round to another window."""
+    dev = Q.on_gpu(Q.make_cache(1, 1, 2, 64, 16, [40]))
+    q, starts = torch.zeros((1, 4, 64), dtype=BF, device="cuda"), torch.tensor([0, 1]).int().cuda()
+    with pytest.raises(ValueError, match="32-bit"):
+        dev.attend(0, q, starts, **{name: n})
