@@ -472,9 +472,11 @@ kvl_status kvl_cache_append(const kvl_cache *cache, int32_t layer, const kvl_seq
  * (slots past lens, pages past the sequence's end) are never part of a result, whatever they
  * hold.  Statistics and sums are held in 32 bits, probabilities enter the products in 16.
  * n_rows * (n_heads / H) is below 2^31 - 256.
- * Scales are taken to be at least 0 (V scales below 1e-30 count as 1e-30).  A call with more work than
- * 2^31 groups of 16 tokens (about 10^10 tokens, counted for each KV head and row tile) does nothing and
- * the report says KVL_ERANGE.
+ * Scales are taken to be at least 0.  A V scale of at most 1e-30, that of a page of zeros, counts as
+ * 2^-80.  A token's part is lost where its probability times its V scale is below 2^-126 of the largest
+ * such product of the row (so none above 2^-30 of the largest probability while V scales are at most 2^16).
+ * A call with more work than 2^31 groups of 16 tokens (about 10^10 tokens, counted for each KV head and
+ * row tile) does nothing and the report says KVL_ERANGE.
  *   max_new   0, or a bound on the fresh rows of any entry that the caller knows; it chooses
  *             kernels, so results depend on it in their rounding only */
 typedef struct kvl_attention {

@@ -99,9 +99,11 @@ __device__ __forceinline__ float exp2_of(float x)
     return r;
 }
 
-// The V scale of a page as the kernels use it: at least the smallest an append writes (a page
-// of zeros whose scale is 0 contributes nothing either way); a NaN stays.
-__device__ __forceinline__ float v_scale(float s) { return s < kTinyScale ? kTinyScale : s; }
+// The V scale of a page as the kernels use it.  Up to the smallest that an append writes, i.e. for a page
+// of zeros, any positive one gives the same result, and 2^-80 keeps weights and sums in range: a weight
+// 2^(x - m) is lost below 2^-126, which a scale of 1e-30 beside one of 2^20 reached at 2^-15 of the
+// largest probability, and l, which divides by the scale, stays finite.  A NaN stays.
+__device__ __forceinline__ float v_scale(float s) { return s <= kTinyScale ? 0x1p-80f : s; }
 
 }  // namespace
 

@@ -249,3 +249,60 @@ def test_numbers_past_32_bits_are_refused(name, n):
     q, starts = torch.zeros((1, 4, 64), dtype=BF, device="cuda"), torch.tensor([0, 1]).int().cuda()
     with pytest.raises(ValueError, match="32-bit"):
         dev.attend(0, q, starts, **{name: n})
+
+
+# ---- V scales far apart ---------------------------------------------------------------------------------
+
+@pytest.mark.parametrize("zero_scale", [1e-30, 0.0])
+@pytest.mark.parametrize("new", [1, 64])
+def test_pages_of_zeros_beside_large_values(new, zero_scale):
+    """Pages whose V is zero (append gives them the smallest scale, an empty cache holds 0) count in the
+    softmax however large the other pages' V scales are."""
+    tokens, d = 4000 + new, 64
+    cache = Q.make_cache(13, 1, 1, d, 16, [tokens], spare=0)
+    k = torch.zeros((tokens + 16, d))
+    k[16:, 0] = -15 * math.log(2.0)
+    pages = cache["tables"][0, :-(-tokens // 16)].long()
+    n = len(pages)
+    cache["codes"][:] = 0
+    cache["codes"][0, 0, pages, :, 0] = Q.to_codes(k[:n * 16] * 16, "e4m3").view(n, 16, d)
+    cache["scales"][0, 0] = 1 / 16
+    cache["scales"][0, 1] = zero_scale
+    cache["codes"][0, 1, pages[0]] = Q.to_codes(1 + torch.rand((16, 1, d), generator=torch.Generator().manual_seed(1)), "e4m3")
+    cache["scales"][0, 1, pages[0]] = 2.0 ** 20
+    q = torch.zeros((new, 1, d))
+    q[:, 0, 0] = 8.0
+    q, starts = q.to(BF), torch.tensor([0, new]).int()
+    dev = Q.on_gpu(cache)
+    lse = torch.zeros((new, 1), device="cuda")
+    out = dev.attend(0, q.cuda(), starts.cuda(), lse=lse, max_new=new)
+    o, z, to, tz = Q.attend(cache, 0, q, starts, [0], 1 / 8.0, True, 0)
+    T.near(out.cpu().double(), o, to, "out")
+    T.near(lse.cpu().double(), z, tz, "lse")
+
+
+@pytest.mark.parametrize("new", [1, 64])
+def test_softmax_sums_of_a_cache_of_zeros(new):
+    """V zero everywhere, and scores that grow along the sequence: the sums stay finite."""
+    tokens, d = 40000, 64
+    cache = Q.make_cache(14, 1, 1, d, 16, [tokens], spare=0)
+    pages = cache["tables"][0, :tokens // 16].long()
+    k = torch.zeros((tokens, d))
+    k[1024:, 0] = 7.0
+    cache["codes"][:] = 0
+    cache["codes"][0, 0, pages, :, 0] = Q.to_codes(k * 16, "e4m3").view(-1, 16, d)
+    cache["scales"][0, 0], cache["scales"][0, 1] = 1 / 16, 1e-30
+    q = torch.zeros((new, 1, d))
+    q[:, 0, 0] = 8.0
+    q = q.to(BF)
+    # one sequence would be cut over all CTAs: 320 that share their pages are not
+    from layer_wise_paged_gb300.cache import QuantCache
+    dev = QuantCache(cache["codes"].cuda(), cache["scales"].cuda(), cache["tables"].expand(320, -1).contiguous().cuda(),
+                     torch.full((320,), tokens).int().cuda(), cache["refs"].cuda() * 320)
+    lse = torch.zeros((320 * new, 1), device="cuda")
+    out = dev.attend(0, q.repeat(320, 1, 1).cuda(), (torch.arange(321) * new).int().cuda(), lse=lse, max_new=new)
+    kd = Q.of_codes(Q.to_codes(k[:, 0] * 16, "e4m3"), "e4m3") / 16
+    seen = torch.arange(tokens)[None] <= torch.arange(tokens - new, tokens)[:, None]
+    want = torch.logsumexp(torch.where(seen, kd[None], torch.full_like(kd, -math.inf)[None]), -1)
+    assert not bool(out.any())
+    assert float((lse.view(320, new).cpu().double() - want).abs().max()) < 1e-4
