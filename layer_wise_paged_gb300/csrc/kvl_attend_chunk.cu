@@ -19,11 +19,13 @@
 // A converted K or V stage serves 256 rows, which is what keeps the conversion (16 bytes in, 32
 // out a vector) small beside the products.
 //
-// Every wait on a barrier is bounded: past the limit a flag is raised, the report says
-// KVL_ETIMEOUT, every role leaves, and the tensor memory is given back.
+// Every wait on a memory barrier is bounded, and a warp's lanes go on or give up together: past the limit a
+// flag is raised, the report says KVL_ETIMEOUT, every role leaves in an order that leaves no warp waiting at a
+// named barrier (kvl_attend_meet.cuh), and the tensor memory is given back.
 #include <type_traits>
 
 #include "kvl_attend.cuh"
+#include "kvl_attend_meet.cuh"
 
 namespace kvl {
 namespace {
@@ -156,13 +158,14 @@ __device__ __forceinline__ void tmem_st16(uint32_t at, const uint32_t (&r)[16])
         : "memory");
 }
 
-// Named barriers between warps of a softmax warpgroup (1 + g: its weights are written; the issuing warp
-// waits, the others only arrive) and between the two issuing warps (3 + g: tile g's turn).  They are
-// not in shared memory, where an access takes 200 cycles while products stream their operands.
-template <int N>
-__device__ __forceinline__ void meet_wait(int id) { asm volatile("bar.sync %0, %1;" ::"r"(id), "n"(N) : "memory"); }
-template <int N>
-__device__ __forceinline__ void meet_arrive(int id) { asm volatile("bar.arrive %0, %1;" ::"r"(id), "n"(N) : "memory"); }
+// Named barriers (kvl_attend_meet.cuh).  They are not in shared memory, where an access takes 200 cycles
+// while products stream their operands.
+struct Meet {
+    template <int N>
+    __device__ __forceinline__ void wait(int id) const { asm volatile("bar.sync %0, %1;" ::"r"(id), "n"(N) : "memory"); }
+    template <int N>
+    __device__ __forceinline__ void arrive(int id) const { asm volatile("bar.arrive %0, %1;" ::"r"(id), "n"(N) : "memory"); }
+};
 
 __device__ __forceinline__ float max3(float a, float b, float c)
 {
@@ -477,6 +480,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_chunk_kernel(const __grid_
         return;
     }
     volatile int *gone = &s_gone;
+    const Meet meet;
 
     const uint8_t *codes = static_cast<const uint8_t *>(a.cache.codes);
     const int64_t plane = int64_t(a.layer) * 2 * N, v_plane_bytes = N * B * H * d;
@@ -632,7 +636,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_chunk_kernel(const __grid_
                 const int two_lanes = (s & 15) << 1;
                 const bool here = (lane & ~1) == two_lanes;
                 const bool partial = __any_sync(0xffffffffu, here && !(nv == kGroup && t0 >= all_lo && t0 + kGroup <= all_hi));
-                if (!wait_bar(bar + 8 * (K_EMPTY + st), ph ^ 1, gone)) break;
+                if (!__all_sync(0xffffffffu, wait_bar(bar + 8 * (K_EMPTY + st), ph ^ 1, gone))) break;  // (the lanes go or stay together)
                 Places &pl = places[k % kPlaces];
                 if (here) {
                     const int g = cw * 2 + (lane & 1);
@@ -668,7 +672,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_chunk_kernel(const __grid_
                     }
                     if (any) s_nan = 1;
                 }
-                if (!wait_bar(bar + 8 * (V_EMPTY + st), ph ^ 1, gone)) break;
+                if (!__all_sync(0xffffffffu, wait_bar(bar + 8 * (V_EMPTY + st), ph ^ 1, gone))) break;
                 convert(vreg, smem + C::kV + st * C::kTileBytes);
                 fence_proxy_async_smem();
                 __syncwarp();
@@ -704,7 +708,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_chunk_kernel(const __grid_
                     if (next.n > 0) break;  // (its steps may be the next share's)
                 }
             }
-            meet_wait<128>(5);
+            meet.wait<128>(kQBar);
             if (free && next.n > 0) load_q();
         } else if (job.n > 0 && (warp < 4 || job.two)) {
             // ---- softmax: row r of the job, TMEM lane r % 128
@@ -753,7 +757,8 @@ __global__ void __launch_bounds__(kThreads, 1) attend_chunk_kernel(const __grid_
                 scores(0);
             }
             bool ok = true;
-            for (int s = 0; s < n; ++s) {
+            int s = 0;
+            for (; s < n; ++s) {
                 const uint32_t ph = (it_g + s) & 1;
                 ok = __all_sync(0xffffffffu, wait_bar(bar + 8 * (S_FULL + g), ph, gone));
                 if (!ok) break;
@@ -888,27 +893,21 @@ __global__ void __launch_bounds__(kThreads, 1) attend_chunk_kernel(const __grid_
                 tmem_wait_st();
                 tmem_fence_before();
                 if (!leads) {
-                    meet_arrive<128>(1 + g);
+                    meet.arrive<128>(weights_bar(g, ph));
                     continue;
                 }
                 const bool more = s + 1 < n;
                 if (!(ok = await(V_FULL, s) && (!more || await(K_FULL, s + 1)))) break;
-                meet_wait<128>(1 + g);
+                meet.wait<128>(weights_bar(g, ph));
                 // The tiles take turns: a tile's two products run one after the other, not mixed with the
                 // other tile's, so one tile is at its softmax while the other is at its products.
-                if (job.two && (g == 1 || s > 0)) meet_wait<64>(3 + g);
+                if (job.two && (g == 1 || s > 0)) meet.wait<64>(turn_bar(g));
                 tmem_fence_after();
                 values(s);
                 if (more) scores(s + 1);
-                if (job.two && (g == 0 || more)) meet_arrive<64>(4 - g);
+                if (job.two && (g == 0 || more)) meet.arrive<64>(turn_bar(1 - g));
             }
-            if (!ok) {  // given up: nobody is left waiting for this warp
-                if (leads) {
-                    if (job.two) meet_arrive<64>(4 - g);
-                } else {
-                    meet_arrive<128>(1 + g);
-                }
-            }
+            if (!ok) leave_steps(meet, leads, job.two, g, it_g, s, n);
             if (ok) {
                 ok = __all_sync(0xffffffffu, wait_bar(bar + 8 * (PV_DONE + g), (it_g + n - 1) & 1, gone));
                 tmem_fence_after();
