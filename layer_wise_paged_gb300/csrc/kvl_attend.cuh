@@ -16,6 +16,7 @@
 // ends in a part of a group), so a group has one K and one V scale and 16 consecutive rows.
 #pragma once
 
+#include "kvl_attend_shares.cuh"
 #include "kvl_quant.cuh"
 
 namespace kvl {
@@ -45,21 +46,7 @@ constexpr int kGroup = 16;
 // largest were lost, and with them up to a fifth of what a long tail gives beside a peak.
 constexpr float kSlack = 15.5f, kHead = -4.f;
 
-// `total` units cut into `shares` contiguous parts whose sizes differ by at most one.  Units are counted
-// in 32 bits (a call whose units do not fit, some 10^10 tokens, is refused), as 64-bit divisions would
-// be the longest part of a small call's start.
-struct Cut {
-    uint32_t total, shares, size, rest;  // the first `rest` shares hold size + 1 units
-    __device__ __forceinline__ Cut() {}
-    __device__ __forceinline__ Cut(uint32_t t, uint32_t s) : total(t), shares(s), size(t / s), rest(t - t / s * s) {}
-    __device__ __forceinline__ uint32_t start(uint32_t b) const { return b * size + min(b, rest); }
-    __device__ __forceinline__ uint32_t share_of(uint32_t u) const
-    {
-        const uint32_t large = rest * (size + 1);
-        return u < large ? u / (size + 1) : rest + (u - large) / size;
-    }
-};
-constexpr uint64_t kMostUnits = uint64_t(1) << 31;
+constexpr uint64_t kMostUnits = uint64_t(1) << 31;  // see Cut
 
 // What one batch entry costs: `tiles` row tiles for each KV head, each walking the groups
 // [g0, g0 + groups).

@@ -339,6 +339,34 @@ __device__ __forceinline__ void next_job(const AttendArgs &a, Job &job, int lane
     }
 }
 
+// A part of `job` has come, or will not come; by one thread.  Whether it is to join the parts.
+__device__ __forceinline__ bool arrive_part(const AttendArgs &a, const Job &job, bool no_result)
+{
+    const uint32_t first = job.cut.share_of(job.u0), last = job.cut.share_of(job.u0 + job.t.steps - 1);
+    const Arrival x = arrival(atomicAdd(&a.counters[first], no_result ? 1 + kNoResult : 1), last - first + 1, no_result);
+    if (x.last) a.counters[first] = 0;
+    return x.join;
+}
+
+// The jobs of the share that have not been begun will not come: `job` (if n > 0) and those after it.  By one
+// whole warp of a CTA that gives up.  (Not inlined: its code in the roles' would cost 3 us of 350.)
+__device__ __noinline__ void arrive_without_result(const AttendArgs &a, Job &job, int lane)
+{
+    while (true) {
+        if (lane == 0 && job.n > 0 && !job.complete) arrive_part(a, job, true);
+        const uint32_t u = job.u + job.taken, off = job.off + job.taken;
+        __syncwarp();
+        if (u >= job.u_end) break;
+        if (lane == 0) {
+            job.u = u;
+            job.off = off;
+        }
+        __syncwarp();
+        next_job(a, job, lane);
+        __syncwarp();
+    }
+}
+
 // The products of tile g from K or V stage st, issued by a whole warp of which lane `one` is elected.
 // Kept short: the roles' loops together just fit the instruction cache, and with four copies of
 // these (a tile and stage each) the 512 rows on 31,232 took 295 us instead of 270.
@@ -476,6 +504,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_chunk_kernel(const __grid_
     constexpr uint32_t tmem = 0;  // columns: S0 0, S1 128, O0 256, O1 384
     if (s_tmem != 0) {            // all 512 columns were asked for: they begin at 0
         if (tid == 0) report(a.report, KVL_ECUDA, blockIdx.x);
+        if (warp == 8) arrive_without_result(a, job, lane);
         if (warp == 8) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(s_tmem) : "memory");
         return;
     }
@@ -989,11 +1018,10 @@ __global__ void __launch_bounds__(kThreads, 1) attend_chunk_kernel(const __grid_
             const int first = int(job.cut.share_of(job.u0)), last = int(job.cut.share_of(job.u0 + job.t.steps - 1));
             __threadfence();
             __syncthreads();
-            if (tid == 0) s_last = !*gone && atomicAdd(&a.counters[first], 1u) == uint32_t(last - first);
+            if (tid == 0) s_last = arrive_part(a, job, *gone);
             __syncthreads();
             if (s_last) {
                 __threadfence();
-                if (tid == 0) a.counters[first] = 0;
                 const int n_rows = job.t.rows, n_parts = last - first + 1;
                 // 32 elements of a row a thread and turn
                 for (int x = tid; x < kJobRows * (D / 32); x += kThreads) {
@@ -1047,6 +1075,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_chunk_kernel(const __grid_
     }
     if (*gone) {
         if (tid == 0) report(a.report, KVL_ETIMEOUT, blockIdx.x);
+        if (warp == 8) arrive_without_result(a, job, lane);
         // let the products in flight end (bounded) before their memory goes, one issuing thread's after
         // the other's
         if (warp == 0) {

@@ -27,3 +27,8 @@ def _run(tmp_path, name, *args):
 def test_no_warp_is_left_waiting(tmp_path):
     """Whichever wait runs out, and whenever, every softmax warp comes to the end of its steps."""
     assert "meet: ok" in _run(tmp_path, "attend_meet")
+
+
+def test_counters_are_zero_after_shares_that_gave_up(tmp_path):
+    """A job's parts are joined once if all came, never otherwise, and its counter is cleared either way."""
+    assert "shares: ok" in _run(tmp_path, "attend_shares")
