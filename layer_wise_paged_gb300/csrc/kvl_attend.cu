@@ -9,8 +9,14 @@ namespace {
 
 // Entries with more rows than this (fresh tokens x query heads of a KV head) go to the tensor-memory
 // kernel, whose time hardly depends on them up to 256, while attend_rows' grows with each 16.  Measured
-// (us, rows / chunk; 8 KV heads, d = 128): 32 sequences of 2,048 tokens: 16 rows 53 / 100, 32 84 / 101,
-// 48 112 / 102, 64 143 / 102; one of 32,768: 32 rows 45 / 52, 64 67 / 53.
+// (us, rows / chunk; 8 KV heads, e4m3; int8 the same within 3 %):
+//   32 sequences of 2,048 tokens   d = 128: 32 rows 85 / 92, 40 115 / 92, 48 116 / 93
+//                                  d = 64: 16 rows 33 / 70, 32 52 / 70, 40 72 / 70, 64 90 / 70
+//   one of 32,768                  d = 128: 32 rows 42 / 51, 48 54 / 51, 64 66 / 53
+//                                  d = 64: 32 rows 31 / 38, 40 38 / 39, 48 37 / 39, 64 45 / 39
+//   4 of 500                       40 rows, d = 128: 18 / 29, d = 64: 14 / 25
+//   16 of 1,000                    36 rows, d = 128: 42 / 43, d = 64 (4 heads): 23 / 29
+// At 33 to 40 rows large batches would gain up to a fifth by the chunk kernel, small ones lose a half.
 constexpr int kChunkRows = 40;
 
 // SMs the workspace is sized for (a host without a device sizes it for a GB300).

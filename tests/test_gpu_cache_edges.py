@@ -306,3 +306,16 @@ def test_softmax_sums_of_a_cache_of_zeros(new):
     want = torch.logsumexp(torch.where(seen, kd[None], torch.full_like(kd, -math.inf)[None]), -1)
     assert not bool(out.any())
     assert float((lse.view(320, new).cpu().double() - want).abs().max()) < 1e-4
+
+
+# ---- sizes where the choice of kernel changes -----------------------------------------------------------
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("rows", [31, 32, 33, 40, 41, 64])
+def test_rows_around_the_choice_of_kernel(rows, d):
+    """In a batch whose entries lie on both sides, and as the only entry."""
+    for new in ([rows, 1, 70], [rows]):
+        c = T.case([100, 40, 90][:len(new)], new, heads=2, kv_heads=2, d=d)
+        out, lse, (o, z, to, tz) = T.run(c)
+        T.near(out, o, to, "out")
+        T.near(lse, z, tz, "lse")
