@@ -457,7 +457,8 @@ kvl_status kvl_rotary_frequencies(int32_t kind, double base, int32_t n_freq, dou
  *   a fresh element's code is round(clamp(x * (1/scale'))), to nearest, ties to even.
  * max|x| is over finite elements; an infinity takes the largest code of its sign, a NaN
  * the NaN code (float) or 0 (int).  With a rope (NULL: none) K is turned by its cache
- * position first, in 32 bits.  Pages of different entries that receive rows must differ
+ * position first, in 32 bits; its n_freq is a multiple of 8 (kvl_rotary, which takes multiples
+ * of 4, can turn other keys beforehand).  Pages of different entries that receive rows must differ
  * (kvl_pages_extend sees to it).  type: of the rows, KVL_TYPE_*. */
 kvl_status kvl_cache_append(const kvl_cache *cache, int32_t layer, const kvl_sequences *seqs,
                             int32_t type, const kvl_rows *k, const kvl_rows *v,

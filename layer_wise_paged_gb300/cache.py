@@ -228,7 +228,7 @@ class QuantCache:
     def append(self, layer, k, v, starts, rope=None, slots=None, stream=None):
         """Quantise fresh k, v [rows, H, d] into the pages of `layer`: rows starts[i] ..
         starts[i + 1] are the last tokens of sequence slots[i] (or i).  rope: turn k by the
-        tokens' positions first."""
+        tokens' positions first (a multiple of 8 pairs; ``rotary`` turns keys of other numbers beforehand)."""
         n_rows, dtype, c = k.shape[0], k.dtype, self._args
         if dtype is not v.dtype or n_rows != v.shape[0]:
             raise ValueError("k, v: one type and shape")

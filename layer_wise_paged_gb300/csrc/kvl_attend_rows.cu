@@ -35,7 +35,10 @@ constexpr int kCtasPerSm = 2;     // 12 warps an SM: 168 registers a thread, 192
 // 48 ragged sequences: 45 us, with a cost of 16 49; 256 sequences: 242 us and 249).  A share is at least
 // kUnitsPerCta (8 heads of 1,500 tokens: 13 us, with 40 18), and a job of at most kSmallJob groups is not
 // split, as its parts would have to be joined (one token of 777, 8 jobs of 49 groups: not split 15.9 us,
-// split 13.5; of 500, 32 groups: 11.5 either way; with nothing kept whole and shares of 40 17.6).
+// split 13.5; of 500, 32 groups: 11.5 either way; with nothing kept whole and shares of 40 17.6).  The same
+// values serve d = 64: 16 rows of 48 sequences of 3,000 (int8) 35.1 us, with a cost of 16 35.5, of 96 39.0;
+// 256 sequences of 1,500 122.5 with any; one token of 1,500 10.5, with shares of 40 13.0, with jobs of up to
+// 96 groups whole 14.6, with none whole 10.5.
 constexpr int kJobCost = 48;
 constexpr int kUnitsPerCta = 12;
 constexpr int kSmallJob = 48;
