@@ -319,3 +319,87 @@ def test_rows_around_the_choice_of_kernel(rows, d):
         out, lse, (o, z, to, tz) = T.run(c)
         T.near(out, o, to, "out")
         T.near(lse, z, tz, "lse")
+
+
+# ---- append with the turn -------------------------------------------------------------------------------
+
+def _turned(lens, new, H, d, B, rot, interleaved, code, dtype=BF):
+    g = torch.Generator().manual_seed(rot + d)
+    cache = Q.make_cache(8, 1, H, d, B, lens, code=code, poison=False)
+    starts = torch.tensor([0] + new).cumsum(0).int()
+    k, v = (torch.randn((sum(new), H, d), generator=g).to(dtype) for _ in range(2))
+    from layer_wise_paged_gb300.cache import Rope
+    rope = Rope.make(rot, base=500000.0, interleaved=interleaved)
+    pos = torch.cat([torch.arange(n - m, n) for n, m in zip(lens, new)])
+    return cache, starts, k, v, rope, pos
+
+
+@pytest.mark.parametrize("interleaved", [False, True])
+@pytest.mark.parametrize("rot,d,B", [(128, 128, 16), (48, 80, 24), (64, 64, 200), (192, 192, 16)])
+def test_int8_keys_turned_on_their_way(rot, d, B, interleaved):
+    """The turned key is right to 2^-20 of its pair, so its code is the nearest integer of the exact key over the
+    scale, or one beside it where the quotient lies within 127 * 2^-18 of a half; values differ
+    by half a step and that much."""
+    lens, new, H = [300, 131], [290, 3], 2
+    cache, starts, k, v, rope, pos = _turned(lens, new, H, d, B, rot, interleaved, "int8")
+    dev = Q.on_gpu(cache)
+    dev.append(0, k.cuda(), v.cuda(), starts.cuda(), rope=rope)
+    assert dev.status() == (0, 0)
+    turned = Q.turn(k, pos, rope.inv_freq.cpu(), interleaved)
+    for i, (n, m) in enumerate(zip(lens, new)):
+        for t in range(m):
+            page, slot = int(cache["tables"][i, (n - m + t) // B]), (n - m + t) % B
+            s = dev.scales[0, 0, page].cpu().double()[:, None]
+            got = Q.of_codes(dev.codes[0, 0, page, slot].cpu(), "int8") * s
+            assert ((got - turned[int(starts[i]) + t]).abs() <= s * (0.5 + 127 * 2.0 ** -18)).all()
+    Q.append(cache, 0, turned, v, starts, range(2))
+    assert torch.allclose(dev.scales.cpu(), cache["scales"], rtol=2.0 ** -20)
+    step = (Q.of_codes(dev.codes.cpu(), "int8") - Q.of_codes(cache["codes"], "int8")).abs()
+    assert float(step.max()) <= 1 and float((step > 0).double().mean()) < 1e-3
+    assert torch.equal(dev.codes[0, 1].cpu(), cache["codes"][0, 1])  # V is not turned
+
+
+@pytest.mark.parametrize("code", ["e4m3", "int8"])
+def test_pairs_that_append_does_not_take(code):
+    """24 turned elements of 96: append refuses 12 pairs (not a multiple of 8); rotary takes them, in place, and
+    append the turned keys."""
+    from layer_wise_paged_gb300.cache import rotary
+    cache, starts, k, v, rope, pos = _turned([40, 9], [30, 9], 2, 96, 16, 24, False, code, dtype=F32)
+    dev = Q.on_gpu(cache)
+    kd, vd, sd = k.cuda(), v.cuda(), starts.cuda()
+    with pytest.raises(kvl.KvlError):
+        dev.append(0, kd, vd, sd, rope=rope)
+    rotary(rope, pos.int().cuda(), [(kd, kd)])
+    dev.append(0, kd, vd, sd)
+    assert dev.status() == (0, 0)
+    Q.append(cache, 0, kd.cpu(), v, starts, range(2))
+    assert torch.equal(dev.codes.cpu(), cache["codes"]) and torch.equal(dev.scales.cpu(), cache["scales"])
+
+
+# ---- large batches of many rows ---------------------------------------------------------------------------
+
+@pytest.mark.parametrize("code,window", [("e4m3", 0), ("int8", 200)])
+def test_many_sequences_of_many_rows(code, window):
+    """300 entries of 150 rows: each CTA has several jobs, whole and in parts.  Tolerance as in
+    tests/test_gpu_attend.py's batches: the output's rounding and 2^-9 of the magnitudes it sums."""
+    seqs, new = 300, 150
+    g = torch.Generator().manual_seed(9)
+    lens = [max(new, int(x)) for x in torch.randint(1, 900, (seqs,), generator=g)]
+    cache = Q.make_cache(3, 1, 2, 64, 16, lens, code=code)
+    dev = Q.on_gpu(cache)
+    q = torch.randn((seqs * new, 4, 64), generator=g).to(BF).cuda()
+    starts = (torch.arange(seqs + 1) * new).int().cuda()
+    out = dev.attend(0, q, starts, max_new=new, window=window)
+    assert torch.equal(out, dev.attend(0, q, starts, max_new=new, window=window)), "two calls differ"
+    assert dev.status() == (0, 0)
+    for i in sorted({0, 1, 100, 151, 222, seqs - 1}):
+        K, V = (Q.tokens(cache, 0, p, i, lens[i]).cuda() for p in (0, 1))
+        s = torch.einsum("thd,khd->thk", q[i * new:(i + 1) * new].double(), K.repeat_interleave(2, 1)) / 8.0
+        pos = torch.arange(lens[i] - new, lens[i], device="cuda")[:, None]
+        at = torch.arange(lens[i], device="cuda")[None]
+        hidden = at > pos if not window else (at > pos) | (at <= pos - window)
+        p = torch.softmax(s.masked_fill(hidden[:, None], -math.inf), -1)
+        want = torch.einsum("thk,khd->thd", p, V.repeat_interleave(2, 1))
+        mag = torch.einsum("thk,khd->thd", p, V.abs().repeat_interleave(2, 1))
+        tol = 2.0 ** -8 * want.abs() + 2.0 ** -9 * mag + 1e-4
+        assert float(((out[i * new:(i + 1) * new].double() - want).abs() - tol).max()) <= 0
