@@ -93,7 +93,7 @@ __device__ __forceinline__ void floats_of(const Raw4<TYPE> &r, float *v)
 
 // Lanes of a row: LPR, each holding 8 elements; 32 / LPR rows a vector.  Three CTAs an SM (80 registers a
 // thread, past which the forms of 16 lanes spill 230 to 340 bytes and those of 8 28 to 40; even so
-// 31,001 tokens of 8 heads of 128 take 58.5 us, 3.2 TB/s, with two 65.6, with four, which spill more, 70.7;
+// 31,001 tokens of 8 heads of 128 take 59 us, 3.2 TB/s, with two 65.6, with four, which spill more, 70.7;
 // 64 sequences of 100 and d = 64: 14.8, 16.8 and 14.6); rows of 32 lanes hold twice as much and get one
 // (255 registers, 16 bytes spilled).
 template <int TYPE, int CODE, int LPR>

@@ -1,9 +1,9 @@
 // kvl_attend_chunk.cu -- attention of many rows a sequence: prompts and their chunks.
 //
 // 4 d operations for each (row, visible token), which is above the tensor cores' floor for prompts; bound
-// by the chain product, softmax, product of a tile (512 tokens of 32 heads on 31,232: 222 us where the
+// by the chain product, softmax, product of a tile (512 tokens of 32 heads on 31,232: 223 us where the
 // products alone take 135; a tile's turn of 3,700 cycles is 1,700 of softmax, 1,230 of products and 800 of
-// handing over, and tensor memory has no columns for a second S of a tile).  One CTA an SM takes
+// handing over, and at d = 128 tensor memory has no columns for a second S of 128 slots).  One CTA an SM takes
 // 256 rows of one KV head (query heads of the head times tokens), two accumulator tiles of 128,
 // and walks the tokens 128 slots (8 groups) at a time:
 //   warps 0-3, 4-7   softmax of tile 0, tile 1: a thread a row.  S comes from tensor memory, P goes
@@ -515,7 +515,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_chunk_kernel(const __grid_
     const int64_t plane = int64_t(a.layer) * 2 * N, v_plane_bytes = N * B * H * d;
 
     // Q of the job in `next` to its place, by the converting warps: each row scaled by a power of two into
-    // the range of a half (undone in s_cq).  All rows come by asynchronous copies into the (free) K stages,
+    // the range of a half (undone in s_cq), as in attend_rows.  All rows come by asynchronous copies into the (free) K stages,
     // each vector to the thread that takes it on from there.
     auto load_q = [&] {
         const int cw = warp - 8, rows = next.t.rows, h = next.h, row0 = next.e.row0, row_base = next.row_base;

@@ -1,8 +1,8 @@
 // kvl_attend_rows.cu -- attention of few rows a sequence: decoded tokens, drafted tokens.
 //
 // Each cached byte is read once, and 2 * 8 multiply-adds a byte are far below the tensor rate, so what counts
-// is bytes in flight and few instructions a byte (256 ragged sequences: 241 us, 5.5 TB/s with 42 % of the
-// issue slots used; one token of 128,000: 62 us, of which 8 pass before the first bytes have come).
+// is bytes in flight and few instructions a byte (256 ragged sequences: 242 us, 5.4 TB/s with 42 % of the
+// issue slots used; one token of 128,000: 61 us, of which 8 pass before the first bytes have come).
 //
 // A warp takes 16 tokens of one KV head at a time from its own ring in shared memory (filled by
 // 16-byte asynchronous copies, a pair of groups ahead, no barrier between warps) and computes the
@@ -274,8 +274,9 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attend_rows_kernel(const
 #pragma unroll
         for (int k = 0; k < kStages - 1; ++k) load_pair(k);
 
-        // ---- Q: each row scaled by a power of two into the range of a half (undone in s_cq).  A warp's rows
-        // are all on their way before the first is looked at.
+        // ---- Q: each row scaled by a power of two into the range of a half (undone in s_cq), which is exact
+        // but for elements below 2^-14 of the row's largest (2^-25 of it at most).  A warp's rows are all on
+        // their way before the first is looked at.
         constexpr int kQTurns = (kRows + kWarps - 1) / kWarps;
         uint32_t qraw[kQTurns][D / 64];
 #pragma unroll
