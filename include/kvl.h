@@ -469,14 +469,16 @@ kvl_status kvl_cache_append(const kvl_cache *cache, int32_t layer, const kvl_seq
  * + t; query head h reads KV head h / (n_heads / H).  With s_j = sm_scale * (q . K_j):
  *   visible: 0 <= j < lens, j <= p if causal, j > p - window if window > 0;
  *   out = sum_j softmax(s)_j V_j,  lse = log(sum_j exp(s_j)) (natural, optional).
- * A row that sees nothing gets out = 0 and lse = -infinity.  Cached bytes that no row sees
- * (slots past lens, pages past the sequence's end) are never part of a result, whatever they
- * hold.  Statistics and sums are held in 32 bits, probabilities enter the products in 16.
- * n_rows * (n_heads / H) is below 2^31 - 256.
- * Scales are taken to be at least 0.  A V scale of at most 1e-30, that of a page of zeros, counts as
- * 2^-80.  A token's part is lost where its probability times its V scale is below 2^-126 of the largest
- * such product of the row (so none above 2^-30 of the largest probability while V scales are at most 2^16).
- * A call with more work than 2^31 groups of 16 tokens (about 10^10 tokens, counted for each KV head and
+ * A row that sees nothing, or only scores of -infinity, gets out = 0 and lse = -infinity.  Cached
+ * bytes that no row sees (slots past lens, pages past the sequence's end) are never part of a
+ * result, whatever they hold.
+ * Statistics and sums are held in 32 bits.  A token's probability times its V scale enters the
+ * product as a half: right to 2^-11 of itself, or to 2^-29 of the largest such product of the row.
+ * Scales are taken to be finite and at least 0 (one that is NaN, where a row sees it, makes the
+ * row's out and lse NaN).  A V scale of at most 1e-30, that of a page of zeros, counts as 2^-80.  A
+ * token's part is lost where its probability times its V scale is below 2^-126 of the largest such
+ * product of the row (so none above 2^-30 of the largest probability while V scales are at most 2^16).
+ * n_rows * (n_heads / H) is below 2^31 - 256.  A call with more work than 2^31 groups of 16 tokens (about 10^10 tokens, counted for each KV head and
  * row tile) does nothing and the report says KVL_ERANGE.
  *   max_new   0, or a bound on the fresh rows of any entry that the caller knows; it chooses
  *             kernels, so results depend on it in their rounding only */
