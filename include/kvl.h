@@ -478,8 +478,9 @@ kvl_status kvl_cache_append(const kvl_cache *cache, int32_t layer, const kvl_seq
  * row's out and lse NaN).  A V scale of at most 1e-30, that of a page of zeros, counts as 2^-80.  A
  * token's part is lost where its probability times its V scale is below 2^-126 of the largest such
  * product of the row (so none above 2^-30 of the largest probability while V scales are at most 2^16).
- * n_rows * (n_heads / H) is below 2^31 - 256.  A call with more work than 2^31 groups of 16 tokens (about 10^10 tokens, counted for each KV head and
- * row tile) does nothing and the report says KVL_ERANGE.
+ * n_rows * (n_heads / H) is below 2^31 - 256.  A call with more work than 2^31 groups of 16 tokens
+ * (about 10^10 tokens, counted for each KV head and row tile) does nothing and the report says
+ * KVL_ERANGE.
  *   max_new   0, or a bound on the fresh rows of any entry that the caller knows; it chooses
  *             kernels, so results depend on it in their rounding only */
 typedef struct kvl_attention {
