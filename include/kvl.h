@@ -509,6 +509,65 @@ kvl_status kvl_attend(const kvl_cache *cache, int32_t layer, const kvl_sequences
                       const kvl_attention *attn, void *d_workspace, size_t workspace_bytes,
                       void *d_report, void *stream);
 
+/* kvl_attend_shared -- attention of a batch whose sequences share prefixes, as forks do: the same results as
+ * kvl_attend, but the tokens that a group of entries shares are read once for the rows of all of them.
+ *   groups   entries groups[g] .. groups[g + 1] of the batch are group g (ascending; entries outside all groups
+ *            share nothing, a group may be empty)
+ *   tokens   the first tokens[g] tokens of every sequence of group g are in the same pages: those of the group's
+ *            first sequence are read.  (After kvl_pages_fork and _extend that holds of a parent's whole
+ *            pages; a partly filled last one is replaced by copies.)
+ * Every row sees all shared tokens: tokens[g] is at most lens - (fresh rows) of each entry with rows.  An entry for
+ * which it is more is left out, its rows not written, and reported (KVL_ERANGE with its number); so are the
+ * entries of a group that is bad: reported with the group's number, KVL_EINVAL for its range, KVL_ERANGE for
+ * more shared tokens than its first sequence holds.  A call with a window, or whose entries may have more than 40 rows (bound by max_new, times
+ * n_heads / H), reads every entry's own table, as kvl_attend does.
+ * d_workspace is kvl_attend's; d_parts (16-byte aligned) needs no preparation and holds nothing between calls. */
+typedef struct kvl_shared {
+    int32_t n_groups; /* at most 1048576 */
+    int32_t reserved; /* 0 */
+    const int32_t *groups; /* device, n_groups + 1 */
+    const int32_t *tokens; /* device, n_groups */
+} kvl_shared;
+
+size_t kvl_attend_shared_parts_bytes(const kvl_cache *cache, int64_t n_rows, int32_t n_heads);
+kvl_status kvl_attend_shared(const kvl_cache *cache, int32_t layer, const kvl_sequences *seqs,
+                             const kvl_shared *shared, const kvl_attention *attn, void *d_workspace,
+                             size_t workspace_bytes, void *d_parts, size_t parts_bytes, void *d_report,
+                             void *stream);
+
+/* kvl_weigh -- how much attention each cached token received: for every token j that an entry's sequence holds,
+ *   mass_out[slot][j] = mass_in[slot][j] + sum over fresh rows t and query heads h that see j of
+ *                       exp(sm_scale * (q_th . K_j) - lse_th)
+ * with rows, visibility and sm_scale as kvl_attend's and lse as it returned them, so each term is the probability
+ * that row t's head h gave token j.  With begin != 0 the fresh tokens' mass_in counts as 0 (a step's first call;
+ * the layers after it add).  A row whose lse is infinite gives nothing.  mass_out may be mass_in; entries without
+ * fresh rows, and what lies past a sequence's tokens, are not written.  Slots of a call must differ.  Sums are in
+ * 32 bits and come out the same every time.  A sequence longer than a row of masses is left out (KVL_ERANGE).
+ * Scales are taken to be finite.  d_workspace (16-byte aligned) needs no preparation and holds nothing between
+ * calls; kvl_weigh_workspace_bytes is 0 for bad arguments. */
+typedef struct kvl_weighing {
+    kvl_rows q;             /* n_rows rows of n_heads heads */
+    const float *lse;       /* [n_rows][n_heads] */
+    const float *mass_in;   /* [n_slots][in_stride] */
+    float *mass_out;        /* [n_slots][out_stride] */
+    int64_t in_stride, out_stride;
+    int64_t tokens;         /* that a row of masses has room for (at most the strides, but for one slot) */
+    int32_t n_heads;        /* a multiple of n_kv_heads */
+    int32_t type;           /* KVL_TYPE_BFLOAT or KVL_TYPE_HALF, of q */
+    float sm_scale;
+    int32_t causal;         /* 0 or 1 */
+    int32_t window;         /* 0: none; > 0 needs causal */
+    int32_t max_new;        /* 0, or a bound on the fresh rows of any entry; chooses kernels */
+    int32_t begin;          /* 0 or 1 */
+    int32_t reserved;       /* 0 */
+} kvl_weighing;
+
+size_t kvl_weigh_workspace_bytes(const kvl_cache *cache, int32_t n_seq, int64_t n_rows, int32_t n_heads,
+                                 int32_t max_new);
+kvl_status kvl_weigh(const kvl_cache *cache, int32_t layer, const kvl_sequences *seqs,
+                     const kvl_weighing *weighing, void *d_workspace, size_t workspace_bytes, void *d_report,
+                     void *stream);
+
 /* Page bookkeeping, all of it in device memory, without a host in the loop.
  * refs[b] counts the table entries of live sequences that name page b (0: free); slot s
  * holds lens[s] tokens in the pages tables[s*table_stride ...], ceil(lens[s] / B) of them;
@@ -558,12 +617,52 @@ kvl_status kvl_pages_compact(const kvl_pages *pages, void *d_report, void *strea
 kvl_status kvl_pages_copy(const kvl_cache *cache, const int32_t *pairs, const int32_t *d_n_pairs,
                           int64_t max_pairs, void *d_report, void *stream);
 
+/* kvl_pages_evict -- shorten slots[i] (n of them, distinct) to keep[i] tokens.  A sequence that holds no more stays
+ * as it is.  Else it keeps its first f = min(first, keep) tokens, its last r = min(recent, keep - f) and, of
+ * those between, the keep - f - r of the largest mass; of equal masses the first ones, a NaN counting as less
+ * than any number, and all as equal where mass is NULL.  The kept tokens stay in order: the k-th becomes token
+ * k.  Its masses move along, and the rest of its row of masses becomes 0.  Pages before f / B stay; the tokens from there on go
+ * to fresh pages (the lowest free numbers, in batch order), whose codes kvl_tokens_move brings before anything
+ * else is done to the pages, and the pages they were in lose a reference.
+ * If a slot is bad (KVL_EINVAL), named twice (KVL_EDUP) or too long for its table or masses, or there are too few
+ * free pages (pages freed by this call do not count; KVL_ERANGE with detail n), nothing is changed.
+ * A key keeps the rotary position it was turned by, while attention counts positions from the
+ * sequence's shortened start: later keys are turned by their own positions before they are appended. */
+typedef struct kvl_eviction {
+    const int32_t *keep;  /* device, n */
+    float *mass;          /* NULL, or [n_slots][mass_stride] */
+    int64_t mass_stride;
+    int64_t tokens;       /* that a row of masses has room for (at most the stride, but for one slot) */
+    int32_t first;
+    int32_t recent;
+} kvl_eviction;
+
+/* What an eviction asks to be moved (device arrays, written by kvl_pages_evict). */
+typedef struct kvl_moves {
+    int32_t *from; /* [N][B][2]: (page, slot) of each token of a fresh page; a page of -1: none; 8-byte aligned */
+    int32_t *to;   /* [N]: the fresh pages */
+    int32_t *at;   /* [n_slots + 1]: where each entry's begin in `to` */
+    int32_t *n;    /* their number */
+} kvl_moves;
+
+kvl_status kvl_pages_evict(const kvl_pages *pages, int32_t n, const int32_t *slots, const kvl_eviction *eviction,
+                           const kvl_moves *moves, void *d_report, void *stream);
+
+/* kvl_tokens_move -- bring the codes of an eviction's tokens, all layers, K and V: for each fresh page and head
+ *   scale' = the largest scale of the pages that its tokens come from,
+ *   code'  = round(code * (scale / scale')) in 32 bits, to nearest, ties to even; tokens whose scale is scale'
+ *            keep their codes.
+ * Slots of a page that receive no token are not written.  max_pages: pages that `to` has room for. */
+kvl_status kvl_tokens_move(const kvl_cache *cache, const kvl_moves *moves, int64_t max_pages, void *d_report,
+                           void *stream);
+
 /* Human-readable name of a status code (static string). */
 const char *kvl_status_string(kvl_status s);
 
 /* Kernel launches one call of each entry point makes (for launch accounting):
  * which = 0 plan, 1 slice, 2 merge-scatter, 3 gather / scatter-back, 4 rotary, 5 append,
- * 6 attend (at most), 7 pages extend, 8 fork, 9 free, 10 compact, 11 copy. */
+ * 6 attend (at most), 7 pages extend, 8 fork, 9 free, 10 compact, 11 copy, 12 attend_shared (at
+ * most), 13 weigh (at most), 14 evict, 15 tokens move. */
 int32_t kvl_launches_per_call(int32_t which);
 
 #ifdef __cplusplus

@@ -71,6 +71,14 @@ kvl_attention = _struct("kvl_attention", [
 kvl_pages = _struct("kvl_pages", [
     ("pool_blocks", _i64), ("block_tokens", _i32), ("n_slots", _i32), ("table_stride", _i64),
     ("tables", _ptr), ("lens", _ptr), ("refs", _ptr), ("pairs", _ptr), ("n_pairs", _ptr)])
+kvl_shared = _struct("kvl_shared", [("n_groups", _i32), ("reserved", _i32), ("groups", _ptr), ("tokens", _ptr)])
+kvl_weighing = _struct("kvl_weighing", [
+    ("q", kvl_rows), ("lse", _ptr), ("mass_in", _ptr), ("mass_out", _ptr), ("in_stride", _i64), ("out_stride", _i64),
+    ("tokens", _i64), ("n_heads", _i32), ("type", _i32), ("sm_scale", _f32), ("causal", _i32), ("window", _i32), ("max_new", _i32),
+    ("begin", _i32), ("reserved", _i32)])
+kvl_eviction = _struct("kvl_eviction", [("keep", _ptr), ("mass", _ptr), ("mass_stride", _i64), ("tokens", _i64),
+                                        ("first", _i32), ("recent", _i32)])
+kvl_moves = _struct("kvl_moves", [("from_", _ptr), ("to", _ptr), ("at", _ptr), ("n", _ptr)])
 
 
 # struct kvl_request, 112 bytes, field for field
@@ -123,6 +131,14 @@ def lib():
         L.kvl_pages_free.argtypes = [pg, i32, vp, vp, vp]
         L.kvl_pages_compact.argtypes = [pg, vp, vp]
         L.kvl_pages_copy.argtypes = [cp, vp, vp, i64, vp, vp]
+        L.kvl_attend_shared_parts_bytes.argtypes, L.kvl_attend_shared_parts_bytes.restype = [cp, i64, i32], sz
+        L.kvl_attend_shared.argtypes = [cp, i32, sp, P(kvl_shared), P(kvl_attention), vp, sz, vp, sz, vp, vp]
+        L.kvl_weigh_workspace_bytes.argtypes, L.kvl_weigh_workspace_bytes.restype = [cp, i32, i64, i32, i32], sz
+        L.kvl_weigh.argtypes = [cp, i32, sp, P(kvl_weighing), vp, sz, vp, vp]
+        L.kvl_pages_evict.argtypes = [pg, i32, vp, P(kvl_eviction), P(kvl_moves), vp, vp]
+        L.kvl_tokens_move.argtypes = [cp, P(kvl_moves), i64, vp, vp]
+        for f in (L.kvl_attend_shared, L.kvl_weigh, L.kvl_pages_evict, L.kvl_tokens_move):
+            f.restype = i32
         for f in (L.kvl_report_reset, L.kvl_rotary, L.kvl_rotary_frequencies, L.kvl_cache_append, L.kvl_attend,
                   L.kvl_pages_extend, L.kvl_pages_fork, L.kvl_pages_free, L.kvl_pages_compact, L.kvl_pages_copy):
             f.restype = i32
@@ -266,7 +282,8 @@ def pack_requests(requests, *, hit_base=0, miss_base=0, obj_base=0, src_table_ba
     return out[:len(requests)] if requests else out[:0]
 
 
-__all__ = ["kvl_cache", "kvl_sequences", "kvl_rows", "kvl_rope", "kvl_attention", "kvl_pages", "build", "lib", "geom", "kvl_geom", "kvl_launch", "KVL_LAUNCH_HOST_SRC",
+__all__ = ["kvl_cache", "kvl_sequences", "kvl_rows", "kvl_rope", "kvl_attention", "kvl_pages", "kvl_shared",
+           "kvl_weighing", "kvl_eviction", "kvl_moves", "build", "lib", "geom", "kvl_geom", "kvl_launch", "KVL_LAUNCH_HOST_SRC",
            "KVL_LAUNCH_HOST_DST", "REQUEST_DTYPE", "pack_requests", "check",
            "KvlError", "kvl_plan_bytes", "kvl_plan_layout", "kvl_batch_plan", "kvl_batch_plan_static_scratch",
            "kvl_slice_layer",

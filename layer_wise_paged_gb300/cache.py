@@ -1,7 +1,7 @@
 """An 8-bit paged KV cache bound to torch device tensors: marshalling around the C ABI.
 
 ``QuantCache`` holds the codes, scales and page bookkeeping of a cache and forwards each
-step (append, attend, extend, fork, free, compact, page copies) to libkvl.so;
+step (append, attend, attend_shared, weigh, extend, fork, free, compact, page copies, evict, token moves) to libkvl.so;
 ``rotary`` turns rows of heads by their positions.  No step runs here, nothing
 synchronises, and every call enqueues on the current stream unless it is given one.
 Device-side problems (a page number out of range, too few free pages) are read with
@@ -22,8 +22,8 @@ import torch
 from . import lib as _lib
 from . import (KVL_ATTEND_ZERO_BYTES, KVL_CODE_FLOAT, KVL_CODE_INT, KVL_REPORT_BYTES, KVL_ROPE_BASE,
                KVL_ROPE_LINEAR, KVL_ROPE_PLAIN, KVL_ROPE_WAVELENGTH, KVL_TYPE_BFLOAT, KVL_TYPE_FLOAT,
-               KVL_TYPE_HALF, check, kvl_attention, kvl_cache, kvl_pages, kvl_read_status,
-               kvl_rope, kvl_rows, kvl_sequences)
+               KVL_TYPE_HALF, check, kvl_attention, kvl_cache, kvl_eviction, kvl_moves, kvl_pages, kvl_read_status,
+               kvl_rope, kvl_rows, kvl_sequences, kvl_shared, kvl_weighing)
 
 CODES = {"e4m3": KVL_CODE_FLOAT, "int8": KVL_CODE_INT}
 TYPES = {torch.bfloat16: KVL_TYPE_BFLOAT, torch.float16: KVL_TYPE_HALF, torch.float32: KVL_TYPE_FLOAT}
@@ -91,6 +91,8 @@ class _Args(threading.local):
         # (views into the struct: q and out are filled in place)
         self.q, self.out = self.attn.q, self.attn.out
         self.seqs = kvl_sequences()
+        self.shared, self.weighing, self.eviction = kvl_shared(), kvl_weighing(), kvl_eviction()
+        self.weighing_q = self.weighing.q
         self.src, self.dst, self.heads = (kvl_rows * 4)(), (kvl_rows * 4)(), (ctypes.c_int32 * 4)()
         self.sets = [(self.src[i], self.dst[i]) for i in range(4)]
         if cache is not None:
@@ -200,6 +202,7 @@ class QuantCache:
         self._capture_id = self._lib.kvl_capture_id
         self._scale = 1.0 / math.sqrt(d)
         self._args = _Args(self)
+        self._moved = None
         self._report = self.report.data_ptr()
         self.reset_status()
 
@@ -250,10 +253,83 @@ class QuantCache:
         Calls of one stream share a workspace, kept here.  Calls captured into a graph (torch.cuda.graph) have one
         of that graph's own memory, which each run of the graph clears first: graphs may run in any
         order, or beside each other and other calls where they have memory pools of their own."""
+        st = _stream(stream, self._index)
+        out, ws = self._attention(q, out, lse, sm_scale, causal, window, max_new, stream, st)
+        c = self._args
+        r = self._lib.kvl_attend(self._cache, layer, self._seqs(c, starts, slots, q.shape[0]), c.attn, ws, self._ws_bytes,
+                                 self._report, st)
+        if r:
+            check(r, "kvl_attend")
+        return out
+
+    def attend_shared(self, layer, q, starts, groups, shared, out=None, lse=None, sm_scale=None, causal=True, window=0,
+                      slots=None, max_new=0, stream=None):
+        """``attend`` of a batch whose sequences share prefixes (forks of one prompt): entries groups[g] ..
+        groups[g + 1] (int32, n_groups + 1) have their first shared[g] tokens (int32, n_groups) in the same
+        pages, which are read once for the rows of all of them.  After ``fork`` and ``extend`` that holds of
+        the parent's whole pages: shared = length // block_tokens * block_tokens.  Give max_new: entries
+        that may have more than 40 rows (times heads of a KV head), or a window, are computed as by ``attend``."""
+        n_groups = shared.shape[0]
+        st = _stream(stream, self._index)
+        out, ws = self._attention(q, out, lse, sm_scale, causal, window, max_new, stream, st)
+        c = self._args
+        g = c.shared
+        g.n_groups, g.groups, g.tokens = n_groups, _ints(groups, "groups", n_groups + 1), _ints(shared, "shared")
+        n_rows, heads, _ = q.shape
+        n = self._lib.kvl_attend_shared_parts_bytes(self._cache, n_rows, heads)
+        parts = self._scratch(n, stream, st)
+        r = self._lib.kvl_attend_shared(self._cache, layer, self._seqs(c, starts, slots, n_rows), g, c.attn, ws,
+                                        self._ws_bytes, parts.data_ptr(), n, self._report, st)
+        if r:
+            check(r, "kvl_attend_shared")
+        return out
+
+    def weigh(self, layer, q, starts, lse, mass, out=None, begin=False, sm_scale=None, causal=True, window=0, slots=None,
+              max_new=0, stream=None):
+        """Add to mass (float32 [slots, tokens]) what each cached token of the batch's sequences received from the
+        fresh rows q in `layer`: the sum over rows and query heads of exp(sm_scale q.K - lse), with the lse that
+        ``attend`` returned for them.  begin: the fresh tokens' masses start from zero (the first layer
+        weighed in a step).  out: the sums go there, mass is left as it is.  Slots of a call differ."""
+        n_rows, heads, _ = q.shape
+        dtype, c = q.dtype, self._args
+        w = c.weighing
+        _rows(c.weighing_q, q, "q", heads, self.head_dim)
+        _flat(lse, torch.float32, (n_rows, heads), "lse")
+        w.lse = lse.data_ptr()
+        w.mass_in, w.in_stride = self._mass(mass, "mass")
+        w.mass_out, w.out_stride = (w.mass_in, w.in_stride) if out is None else self._mass(out, "out")
+        w.tokens = mass.shape[1] if out is None else min(mass.shape[1], out.shape[1])
+        if not (-_MOST <= window <= _MOST and -_MOST <= max_new <= _MOST):
+            raise ValueError("window, max_new: 32-bit numbers")
+        w.n_heads, w.type, w.sm_scale = heads, TYPES[dtype], self._scale if sm_scale is None else sm_scale
+        w.causal, w.window, w.max_new, w.begin = 1 if causal else 0, window, max_new, 1 if begin else 0
+        st = _stream(stream, self._index)
+        s = self._seqs(c, starts, slots, n_rows)
+        n = self._lib.kvl_weigh_workspace_bytes(self._cache, s.n_seq, n_rows, heads, max(0, max_new))
+        ws = self._scratch(n, stream, st)
+        r = self._lib.kvl_weigh(self._cache, layer, s, w, ws.data_ptr(), n, self._report, st)
+        if r:
+            check(r, "kvl_weigh")
+        return mass if out is None else out
+
+    def _mass(self, t, name):
+        if t.dtype is not torch.float32 or not t.is_cuda or t.dim() != 2 or t.shape[0] != self.n_slots or \
+                t.shape[1] == 0 or (t.shape[1] > 1 and t.stride(1) != 1) or (t.shape[0] > 1 and t.stride(0) < t.shape[1]):
+            raise ValueError(f"{name}: float32 [{self.n_slots}, tokens] in device memory, rows contiguous")
+        return t.data_ptr(), max(t.stride(0), t.shape[1])
+
+    def _scratch(self, n, stream, st):
+        """Memory of one call, which is its stream's."""
+        if stream is None:
+            return torch.empty(n, dtype=torch.uint8, device=self.device)
+        with self._on(st):
+            return torch.empty(n, dtype=torch.uint8, device=self.device)
+
+    def _attention(self, q, out, lse, sm_scale, causal, window, max_new, stream, st):
+        """Fill this thread's kvl_attention; (out, the workspace's address)."""
         n_rows, heads, _ = q.shape
         dtype, c = q.dtype, self._args
         _rows(c.q, q, "q", heads, self.head_dim)
-        st = _stream(stream, self._index)
         if out is None:
             shape = n_rows, heads, self.head_dim
             if stream is None:
@@ -279,11 +355,7 @@ class QuantCache:
             ws = self._workspace(held, st, capture)
         a.n_heads, a.type, a.sm_scale = heads, TYPES[dtype], self._scale if sm_scale is None else sm_scale
         a.causal, a.window, a.max_new = 1 if causal else 0, window, max_new
-        r = self._lib.kvl_attend(self._cache, layer, self._seqs(c, starts, slots, n_rows), a, ws[1], self._ws_bytes,
-                                 self._report, st)
-        if r:
-            check(r, "kvl_attend")
-        return out
+        return out, ws[1]
 
     def _on(self, st):
         """Allocations for calls on stream `st` are made on it: memory just freed on another may still be
@@ -327,6 +399,39 @@ class QuantCache:
         """Make the copies that the last extend or compact asked for (every layer)."""
         check(self._lib.kvl_pages_copy(self._cache, self._p.pairs, self._p.n_pairs, self.pool_blocks, self._report,
                                        _stream(stream, self._index)), "kvl_pages_copy")
+
+    def evict(self, slots, keep, mass=None, first=0, recent=0, stream=None):
+        """Shorten sequence slots[i] to keep[i] tokens (int32) where it holds more: its first `first`, its last `recent`
+        and the heaviest of the rest by mass (float32 [slots, tokens], as ``weigh`` makes it; None: all weigh the
+        same), in order.  Their masses move along, the rest of their rows becomes 0.  Make ``move_tokens`` before anything else is done with the
+        pages.  A key keeps the rotary position it was turned by: turn later ones by their own positions
+        (``rotary``) and append them without a rope."""
+        n, c = slots.shape[0], self._args
+        if not (-_MOST <= first <= _MOST and -_MOST <= recent <= _MOST):
+            raise ValueError("first, recent: 32-bit numbers")
+        e = c.eviction
+        e.keep, e.first, e.recent = _ints(keep, "keep", n), first, recent
+        e.mass, e.mass_stride = (None, 0) if mass is None else self._mass(mass, "mass")
+        e.tokens = 0 if mass is None else mass.shape[1]
+        st = _stream(stream, self._index)
+        check(self._lib.kvl_pages_evict(self._pages, n, _ints(slots, "slots"), e, self._moves(st), self._report, st),
+              "kvl_pages_evict")
+
+    def move_tokens(self, stream=None):
+        """Move the tokens that the last evict kept into their fresh pages (every layer)."""
+        st = _stream(stream, self._index)
+        check(self._lib.kvl_tokens_move(self._cache, self._moves(st), self.pool_blocks, self._report, st), "kvl_tokens_move")
+
+    def _moves(self, st):
+        if self._moved is None:  # 8 bytes a token of the pool, at the first eviction
+            with self._on(st):
+                N = self.pool_blocks
+                words = torch.empty(2 * N * self.block_tokens + N + self.n_slots + 2, dtype=torch.int32, device=self.device)
+                words[-1:].zero_()  # nothing to move
+            at = words.data_ptr()
+            to = at + 8 * N * self.block_tokens
+            self._moved = kvl_moves(at, to, to + 4 * N, to + 4 * (N + self.n_slots + 1)), words
+        return self._moved[0]
 
     # -- status ---------------------------------------------------------------
     def status(self, stream=None):

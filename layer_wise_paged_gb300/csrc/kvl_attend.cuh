@@ -31,6 +31,10 @@ struct AttendArgs {
     uint32_t *counters;
     float *parts;      // partial results of rows split over CTAs
     void *report;
+    // attention over a shared prefix only
+    kvl_shared shared;
+    float *row_o;      // [n_rows][n_heads][64, 128 or 256]: O of the rows over the shared tokens
+    float *row_ml;     // [n_rows][n_heads][2]: their references and sums
 };
 
 namespace {
@@ -53,6 +57,7 @@ constexpr uint64_t kMostUnits = uint64_t(1) << 31;  // see Cut
 struct Cost {
     Entry e;
     int32_t tiles, g0, groups;
+    int32_t lo;  // the first token any row sees
 };
 
 // The first token a row at position `pos` sees, j > pos - window.  (A row stands before token 0 where an
@@ -68,6 +73,48 @@ __device__ __forceinline__ int32_t group_of(int32_t token, int32_t B, int32_t pe
     return b * per_block + (token - b * B) / kGroup;
 }
 
+
+// Group g of a batch that shares prefixes, as one entry: the shared tokens in the pages of its first sequence, and
+// the rows of all of them.  len = 0 for a group that is left out.
+__device__ __forceinline__ Entry load_group(const AttendArgs &a, int32_t g, void *rep)
+{
+    Entry e = {nullptr, 0, 0, 0};
+    const int32_t i0 = a.shared.groups[g], i1 = a.shared.groups[g + 1], P = a.shared.tokens[g];
+    if (i0 < 0 || i1 < i0 || i1 > a.seqs.n_seq || P < 0) {
+        report(rep, KVL_EINVAL, g);
+        return e;
+    }
+    if (i0 == i1 || P == 0) return e;
+    const Entry f = load_entry(a.seqs, a.cache.block_tokens, i0, nullptr);  // (its own problems: where it is an entry)
+    const int32_t r0 = a.seqs.starts[i0], r1 = a.seqs.starts[i1];
+    if (!f.table || r0 < 0 || r1 < r0 || r1 > a.seqs.n_rows) return e;
+    if (P > f.len) {
+        report(rep, KVL_ERANGE, g);
+        return e;
+    }
+    e.table = f.table;
+    e.len = P;
+    e.fresh = r1 - r0;
+    e.row0 = r0;
+    return e;
+}
+
+// The tokens that entry i (resolved as e) shares with the others of its group.  An entry whose group is left out,
+// or one of whose rows does not see all of them, loses its rows.
+__device__ __forceinline__ int32_t shared_of(const AttendArgs &a, Entry &e, int32_t i, void *rep)
+{
+    int lo = -1, hi = a.shared.n_groups;  // the last group that begins at i or before
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (a.shared.groups[mid] <= i) lo = mid; else hi = mid;
+    }
+    if (e.fresh <= 0 || lo < 0 || i >= a.shared.groups[lo + 1] || a.shared.tokens[lo] == 0) return 0;
+    const Entry p = load_group(a, lo, nullptr);
+    if (p.len > 0 && p.len <= e.len - e.fresh && e.row0 >= p.row0 && e.row0 + e.fresh <= p.row0 + p.fresh) return p.len;
+    if (p.len > 0) report(rep, KVL_ERANGE, i);  // (a group reports itself)
+    e.len = e.fresh = 0;
+    return 0;
+}
 
 // 16 bytes into shared memory; zeros where !ok (src has to be a valid address all the same).
 __device__ __forceinline__ void copy_async16(uint32_t dst, const void *src, bool ok)
@@ -86,6 +133,23 @@ __device__ __forceinline__ float exp2_of(float x)
     return r;
 }
 
+__device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                         uint32_t b1)
+{
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+                 : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// Byte offset of 16-byte chunk c of row r in a group's K tile.  A lane reads it by rows lane/4 and chunks
+// lane%4 + 4i; the chunk is XORed so that the 8 lanes of a shared-memory phase hit 8 different
+// 16-byte columns of 128.
+template <int D>
+__device__ __forceinline__ uint32_t k_at(int r, int c)
+{
+    if constexpr (D == 64) return r * 64 + c * 16;
+    else return r * D + ((c ^ ((r & 1) << 2)) << 4);
+}
 // The V scale of a page as the kernels use it.  Up to the smallest that an append writes, i.e. for a page
 // of zeros, any positive one gives the same result, and 2^-80 keeps weights and sums in range: a weight
 // 2^(x - m) is lost below 2^-126, which a scale of 1e-30 beside one of 2^20 reached at 2^-15 of the
@@ -99,5 +163,13 @@ size_t attend_rows_part_bytes(int head_dim);  // for each SM
 kvl_status launch_attend_rows(const AttendArgs &a, int64_t most, int sms, void *stream);
 size_t attend_chunk_part_bytes(int head_dim);
 kvl_status launch_attend_chunk(const AttendArgs &a, int sms, void *stream);
+
+// Entries with more rows than this (fresh tokens x query heads of a KV head) go to the tensor-memory kernel.
+constexpr int kChunkRows = 40;
+// What attention's entry points check alike.  nothing: the call has no work.
+kvl_status check_attend(const kvl_cache *cache, int32_t layer, const kvl_sequences *seqs, const kvl_attention *attn,
+                        const void *d_workspace, size_t workspace_bytes, const void *d_report, bool *nothing);
+AttendArgs attend_args(const kvl_cache *cache, int32_t layer, const kvl_sequences *seqs, const kvl_attention *attn,
+                       void *d_workspace, void *d_report);
 
 }  // namespace kvl

@@ -1,0 +1,416 @@
+// kvl_evict.cu -- shorten sequences of a cache to the tokens that matter: which stay, where they go, and their
+// move into fresh pages.
+//
+// A sequence of len > keep tokens keeps its first f = min(first, keep), its last r = min(recent, keep - f) and, of
+// those between, the keep - f - r with the largest mass (of equals the first).  They keep their order: the k-th of
+// them becomes token k.  Pages before f / B stay; from there on the sequence gets fresh pages, so a page that a
+// fork still names is never written, sources and destinations are disjoint, and how many pages a batch needs does
+// not depend on the masses:
+//   plan    one CTA: checks, needs, and the lowest free numbers in batch order (as extend);
+//   select  a CTA a sequence: the smallest mass that stays by its digits (three passes of 11, 11 and 10 bits over
+//           order-preserving keys), then one walk in token order that gives each kept token its place, moves its
+//           mass and notes where its codes come from;
+//   move    all layers' codes, a warp 512 bytes of a row's width of one new page.
+#include "kvl_pages.cuh"
+
+namespace kvl {
+namespace {
+
+constexpr int kDigits = 2048;  // 11 bits
+constexpr int kRun = 4;        // tokens of a thread in a turn
+
+struct EvictArgs {
+    kvl_pages p;
+    kvl_eviction e;
+    kvl_moves m;
+    int32_t n;
+    const int32_t *slots;
+    void *report;
+};
+
+// What entry i asks for.
+struct Ask {
+    int32_t slot, len, keep;
+    int32_t stay;   // pages that stay
+    int32_t pages;  // fresh ones; 0 where the sequence is not shortened (or shortened to whole pages that stay)
+    int32_t error;
+    bool cut;
+};
+
+__device__ __forceinline__ Ask ask_of(const EvictArgs &a, int i)
+{
+    const int32_t B = a.p.block_tokens;
+    Ask q = {a.slots[i], 0, a.e.keep[i], 0, 0, KVL_OK, false};
+    if (q.slot < 0 || q.slot >= a.p.n_slots || q.keep < 0) {
+        q.error = KVL_EINVAL;
+        return q;
+    }
+    q.len = a.p.lens[q.slot];
+    if (q.len < 0 || ceil_div64(q.len, B) > a.p.table_stride || (a.e.mass && q.len > a.e.tokens)) {
+        q.error = KVL_ERANGE;
+        return q;
+    }
+    q.cut = q.len > q.keep;
+    q.stay = min(a.e.first, q.keep) / B;
+    if (q.cut) q.pages = int32_t(ceil_div64(q.keep, B)) - q.stay;
+    return q;
+}
+
+// at[i]: where entry i's pages begin in `to`; at[n]: -1 if nothing is done.
+__global__ void __launch_bounds__(kThreads) evict_plan_kernel(const __grid_constant__ EvictArgs a)
+{
+    extern __shared__ uint32_t named[];  // one bit a slot
+    __shared__ long long scan_need[32];
+    __shared__ int scan_free[32], s_bad;
+    const int tid = threadIdx.x;
+    for (int w = tid; w < (a.p.n_slots + 31) / 32; w += kThreads) named[w] = 0;
+    if (tid == 0) s_bad = 0;
+    __syncthreads();
+    long long need = 0;
+    for (int base = 0; base < a.n; base += kThreads) {
+        const int i = base + tid;
+        Ask q = {};
+        if (i < a.n) {
+            q = ask_of(a, i);
+            if (q.error == KVL_OK && (atomicOr(&named[q.slot >> 5], 1u << (q.slot & 31)) >> (q.slot & 31) & 1u))
+                q.error = KVL_EDUP;
+            if (q.error) {
+                report(a.report, q.error, i);
+                s_bad = 1;
+            }
+        }
+        long long total;
+        if (base) __syncthreads();  // readers of the scan before
+        const long long at = need + block_scan<long long>(q.pages, scan_need, total);
+        if (i < a.n) a.m.at[i] = int32_t(min(at, (long long)INT32_MAX));
+        need += total;
+    }
+    __syncthreads();
+    bool ok = s_bad == 0 && need <= a.p.pool_blocks;
+    if (ok) {
+        // are there that many?  (counted before any is taken)
+        long long held = 0;
+        for (int64_t base = 0; base < a.p.pool_blocks && held < need; base += kTile) {
+            int r[kPerThread], mine = 0, total;
+            load_refs(a.p.refs, base, a.p.pool_blocks, r);
+#pragma unroll
+            for (int k = 0; k < kPerThread; ++k) mine += r[k] == 0;
+            if (base) __syncthreads();
+            block_scan<int>(mine, scan_free, total);
+            held += total;
+        }
+        ok = held >= need;
+    }
+    if (!ok) {
+        if (tid == 0) {
+            if (s_bad == 0) report(a.report, KVL_ERANGE, a.n);
+            a.m.at[a.n] = -1;
+            *a.m.n = 0;
+        }
+        return;
+    }
+    long long given = 0;
+    for (int64_t base = 0; base < a.p.pool_blocks && given < need; base += kTile) {
+        int r[kPerThread], mine = 0, total;
+        load_refs(a.p.refs, base, a.p.pool_blocks, r);
+#pragma unroll
+        for (int k = 0; k < kPerThread; ++k) mine += r[k] == 0;
+        __syncthreads();
+        long long at = given + block_scan<int>(mine, scan_free, total);
+#pragma unroll
+        for (int k = 0; k < kPerThread; ++k) {
+            if (r[k] != 0) continue;
+            if (at < need) {
+                const int64_t id = base + int64_t(tid) * kPerThread + k;
+                a.m.to[at] = int32_t(id);
+                a.p.refs[id] = 1;
+            }
+            ++at;
+        }
+        given += total;
+    }
+    if (tid == 0) {
+        a.m.at[a.n] = int32_t(need);
+        *a.m.n = int32_t(need);
+    }
+}
+
+// Larger keys are larger masses; -0 is 0, and a NaN comes last.
+__device__ __forceinline__ uint32_t key_of(float x)
+{
+    if (x != x) return 0;
+    const uint32_t u = __float_as_uint(x + 0.f);
+    return u & 0x80000000u ? ~u : u | 0x80000000u;
+}
+
+__global__ void __launch_bounds__(kThreads) evict_select_kernel(const __grid_constant__ EvictArgs a)
+{
+    __shared__ uint32_t hist[kDigits];
+    __shared__ long long scan[32];
+    __shared__ int scan_bins[32];
+    __shared__ uint32_t s_digit, s_rest;
+    const int tid = threadIdx.x, i = blockIdx.x;
+    if (a.m.at[a.n] < 0) return;
+    const Ask q = ask_of(a, i);
+    if (!q.cut) return;
+    const int32_t B = a.p.block_tokens;
+    const int f = min(a.e.first, q.keep), r = min(a.e.recent, q.keep - f);
+    const int lo = f, hi = q.len - r;       // the tokens to choose from
+    const int take = q.keep - f - r;        // how many of them stay; fewer than there are
+    float *mass = a.e.mass ? a.e.mass + int64_t(q.slot) * a.e.mass_stride : nullptr;
+    int32_t *table = a.p.tables + int64_t(q.slot) * a.p.table_stride;
+
+    // ---- the smallest key that stays, and how many of those that equal it
+    uint32_t least = 0xffffffffu, equals = 0;
+    if (take > 0 && !mass) {
+        least = key_of(0.f);
+        equals = take;
+    } else if (take > 0) {
+        uint32_t known = 0, mask = 0, rest = take;  // the key's digits so far; its rank among those that have them
+#pragma unroll 1
+        for (int pass = 0; pass < 3; ++pass) {
+            const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0, bins = pass == 2 ? 1024 : 2048;
+            for (int x = tid; x < bins; x += kThreads) hist[x] = 0;
+            __syncthreads();
+            for (int j = lo + tid; j < hi; j += kThreads) {
+                const uint32_t k = key_of(mass[j]);
+                if ((k & mask) == known) atomicAdd(&hist[(k >> shift) & (bins - 1)], 1u);
+            }
+            __syncthreads();
+            // the digit at which the sum from the largest digit down reaches `rest`: two bins a thread
+            const int top = bins - 1 - 2 * tid;
+            const int c0 = 2 * tid < bins ? hist[top] : 0, c1 = 2 * tid + 1 < bins ? hist[top - 1] : 0;
+            int total;
+            const uint32_t before = block_scan<int>(c0 + c1, scan_bins, total);
+            if (before < rest && rest <= before + c0) {
+                s_digit = top;
+                s_rest = rest - before;
+            } else if (before + c0 < rest && rest <= before + c0 + c1) {
+                s_digit = top - 1;
+                s_rest = rest - before - c0;
+            }
+            __syncthreads();
+            known |= s_digit << shift;
+            mask |= uint32_t(bins - 1) << shift;
+            rest = s_rest;
+            __syncthreads();
+        }
+        least = known;
+        equals = rest;
+    }
+
+    // ---- places, masses, sources; a turn's masses are read before any is written, and a token moves down
+    const int64_t first_page = a.m.at[i];
+    long long kept = 0;  // tokens that stay before this turn; those that equal `least` in the high half
+    for (int base = 0; base < q.len; base += kThreads * kRun) {
+        const int j0 = base + tid * kRun;
+        float x[kRun];
+        bool sure[kRun], even[kRun];
+        int n_sure = 0, n_even = 0;
+#pragma unroll
+        for (int y = 0; y < kRun; ++y) {
+            const int j = j0 + y;
+            x[y] = mass && j < q.len ? mass[j] : 0.f;
+            const uint32_t k = key_of(x[y]);
+            const bool between = j >= lo && j < hi;
+            sure[y] = j < q.len && (!between || (take > 0 && k > least));
+            even[y] = between && take > 0 && k == least;
+            n_sure += sure[y];
+            n_even += even[y];
+        }
+        long long total;
+        const long long before = kept + block_scan<long long>(n_sure | (long long)n_even << 32, scan, total);
+        kept += total;
+        int s = int(before & 0xffffffffll), v = int(before >> 32);
+#pragma unroll
+        for (int y = 0; y < kRun; ++y) {
+            const int j = j0 + y;
+            if (sure[y] || (even[y] && v < int(equals))) {
+                const int k = s + min(v, int(equals)), at = k / B - q.stay;
+                if (mass) mass[k] = x[y];
+                if (at >= 0) {
+                    const int32_t page = table[j / B];
+                    const bool there = page >= 0 && page < a.p.pool_blocks;
+                    if (!there) report(a.report, KVL_ERANGE, i);
+                    reinterpret_cast<int2 *>(a.m.from)[(first_page + at) * B + k % B] = make_int2(there ? page : -1, j % B);
+                }
+            }
+            s += sure[y];
+            v += even[y];
+        }
+        __syncthreads();  // the scan's sums and the masses
+    }
+    if (mass)
+        for (int64_t j = q.keep + tid; j < a.e.tokens; j += kThreads) mass[j] = 0.f;
+    const int pages = int(ceil_div64(q.keep, B));
+    for (int64_t k = q.keep + tid; k < int64_t(pages) * B; k += kThreads)
+        if (q.pages > 0) reinterpret_cast<int2 *>(a.m.from)[(first_page + k / B - q.stay) * B + k % B] = make_int2(-1, 0);
+    // ---- the pages that go
+    const int held = int(ceil_div64(q.len, B));
+    for (int k = q.stay + tid; k < held; k += kThreads) {
+        const int32_t id = table[k];
+        if (id < 0 || id >= a.p.pool_blocks) {
+            report(a.report, KVL_ERANGE, i);
+        } else if (atomicSub(&a.p.refs[id], 1) <= 0) {
+            atomicAdd(&a.p.refs[id], 1);
+            report(a.report, KVL_EINVAL, i);
+        }
+    }
+    __syncthreads();
+    for (int k = q.stay + tid; k < pages; k += kThreads) table[k] = a.m.to[first_page + k - q.stay];
+    if (tid == 0) a.p.lens[q.slot] = q.keep;
+}
+
+// ---- codes -------------------------------------------------------------------------------------
+
+constexpr int kMoveThreads = 256, kMoveCtasPerSm = 4;
+constexpr int kHeld = 8;  // tokens whose codes a lane has on their way
+
+struct MoveArgs {
+    kvl_cache c;
+    kvl_moves m;
+    int64_t max_pages;
+    int32_t lanes;   // lanes of a row's slice: a power of two, 16 bytes each
+    int32_t slices;  // of a row of H * d bytes
+    void *report;
+};
+
+// scale' = the largest scale of the pages that a new page's tokens come from, for each head; code' =
+// round(code * (scale / scale')).  The tokens of the largest scale keep their codes bit for bit, so what a further
+// eviction rounds again is what came from smaller ones.
+template <int CODE>
+__global__ void __launch_bounds__(kMoveThreads, kMoveCtasPerSm) move_tokens_kernel(const __grid_constant__ MoveArgs a)
+{
+    int64_t n = *a.m.n;
+    if (n < 0 || n > a.max_pages) {
+        if (blockIdx.x == 0 && threadIdx.x == 0) report(a.report, KVL_ERANGE, n);
+        n = n < 0 ? 0 : a.max_pages;
+    }
+    const int64_t N = a.c.pool_blocks, planes = int64_t(a.c.n_layers) * 2;
+    const int B = a.c.block_tokens, H = a.c.n_kv_heads, d = a.c.head_dim, row_bytes = H * d;
+    const int lane = threadIdx.x & 31, per = 32 / a.lanes, rw = lane / a.lanes, ch = lane % a.lanes;
+    const int64_t units = n * planes * a.slices, step = int64_t(gridDim.x) * (kMoveThreads / 32);
+    for (int64_t u = int64_t(blockIdx.x) * (kMoveThreads / 32) + (threadIdx.x >> 5); u < units; u += step) {
+        const int64_t kp = u / a.slices, k = kp / planes, lp = kp - k * planes;
+        const int at = (int(u - kp * a.slices) * a.lanes + ch) * 16;  // this lane's bytes of a row
+        const bool mine = at < row_bytes;
+        const int32_t to = a.m.to[k];
+        if (to < 0 || to >= N) {
+            if (lane == 0) report(a.report, KVL_ERANGE, k);
+            continue;
+        }
+        const int h = mine ? at / d : 0;
+        const uint8_t *codes = static_cast<const uint8_t *>(a.c.codes) + lp * N * B * row_bytes + (mine ? at : 0);
+        const float *scales = a.c.scales + lp * N * H + h;
+        const int2 *from = reinterpret_cast<const int2 *>(a.m.from) + k * B;
+        auto source = [&](int slot) -> int2 {  // page and slot, a page of -1: none
+            const int2 x = slot < B ? from[slot] : make_int2(-1, 0);
+            return make_int2(x.x < N && x.y >= 0 && x.y < B ? x.x : -1, x.y);
+        };
+        float now = 0.f;
+        for (int s = rw; s < B; s += per) {
+            const int2 x = source(s);
+            if (x.x >= 0) now = fmaxf(now, scales[int64_t(x.x) * H]);
+        }
+        for (int o = a.lanes; o < 32; o <<= 1) now = fmaxf(now, __shfl_xor_sync(0xffffffffu, now, o));
+        for (int s0 = rw; s0 < B; s0 += per * kHeld) {
+            uint4 w[kHeld];
+            float was[kHeld];
+#pragma unroll
+            for (int y = 0; y < kHeld; ++y) {
+                const int2 x = source(s0 + y * per);
+                was[y] = -1.f;  // none
+                if (x.x >= 0 && mine) {
+                    w[y] = *reinterpret_cast<const uint4 *>(codes + (int64_t(x.x) * B + x.y) * row_bytes);
+                    was[y] = scales[int64_t(x.x) * H];
+                }
+            }
+#pragma unroll
+            for (int y = 0; y < kHeld; ++y) {
+                const int s = s0 + y * per;
+                if (was[y] == -1.f) continue;
+                if (was[y] != now) {
+                    const float ratio = __fdiv_rn(was[y], now);
+                    uint32_t z[4] = {w[y].x, w[y].y, w[y].z, w[y].w};
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        uint32_t l, g;
+                        codes_of<CODE>(z[i], l, g);
+                        const float2 p = __half22float2(*reinterpret_cast<const __half2 *>(&l)), q = __half22float2(*reinterpret_cast<const __half2 *>(&g));
+                        z[i] = to_codes4<CODE>(p.x * ratio, p.y * ratio, q.x * ratio, q.y * ratio);
+                    }
+                    w[y] = make_uint4(z[0], z[1], z[2], z[3]);
+                }
+                *reinterpret_cast<uint4 *>(static_cast<uint8_t *>(a.c.codes) + ((lp * N + to) * B + s) * row_bytes + at) = w[y];
+            }
+        }
+        if (mine && rw == 0 && at % d == 0) a.c.scales[(lp * N + to) * H + h] = now;
+    }
+}
+
+inline kvl_status check_moves(const kvl_moves *m)
+{
+    if (!m || !m->from || !m->to || !m->at || !m->n) return KVL_EINVAL;
+    if ((reinterpret_cast<uintptr_t>(m->from) & 7u) || misaligned4(m->to) || misaligned4(m->at) || misaligned4(m->n))
+        return KVL_EALIGN;
+    return KVL_OK;
+}
+
+}  // namespace
+}  // namespace kvl
+
+using namespace kvl;
+
+extern "C" kvl_status kvl_pages_evict(const kvl_pages *pages, int32_t n, const int32_t *slots,
+                                      const kvl_eviction *eviction, const kvl_moves *moves, void *d_report, void *stream)
+{
+    if (!eviction) return KVL_EINVAL;
+    kvl_status s = check_batch(pages, n, slots, eviction->keep, d_report);
+    if (!s) s = check_moves(moves);
+    if (s) return s;
+    if (eviction->first < 0 || eviction->recent < 0 || (eviction->mass && (eviction->tokens <= 0 || eviction->mass_stride < eviction->tokens))) return KVL_EINVAL;
+    if (misaligned4(eviction->mass)) return KVL_EALIGN;
+    EvictArgs a;
+    a.p = *pages;
+    a.e = *eviction;
+    a.m = *moves;
+    a.n = n;
+    a.slots = slots;
+    a.report = d_report;
+    static std::atomic<unsigned long long> ready[kMaxDevices];
+    const int smem = (pages->n_slots + 31) / 32 * 4;
+    if (smem > 32 * 1024 && !allow_smem(evict_plan_kernel, ready, (1 << 20) / 8)) return KVL_ECUDA;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    evict_plan_kernel<<<1, kThreads, smem, st>>>(a);
+    s = launch_status();
+    if (s || n == 0) return s;
+    evict_select_kernel<<<n, kThreads, 0, st>>>(a);
+    return launch_status();
+}
+
+extern "C" kvl_status kvl_tokens_move(const kvl_cache *cache, const kvl_moves *moves, int64_t max_pages,
+                                      void *d_report, void *stream)
+{
+    kvl_status s = check_cache(cache);
+    if (!s && (max_pages < 0 || max_pages > INT32_MAX)) s = KVL_EINVAL;
+    if (s || max_pages == 0) return s;
+    if ((s = check_moves(moves))) return s;
+    if (bad_report(d_report)) return KVL_EALIGN;
+    const int sms = sm_count();
+    if (sms <= 0) return KVL_ECUDA;
+    MoveArgs a;
+    a.c = *cache;
+    a.m = *moves;
+    a.max_pages = max_pages;
+    const int vectors = cache->n_kv_heads * cache->head_dim / 16;
+    a.lanes = 1;
+    while (a.lanes < 32 && a.lanes < vectors) a.lanes *= 2;
+    a.slices = (vectors + a.lanes - 1) / a.lanes;
+    a.report = d_report;
+    const int ctas = sms * kMoveCtasPerSm;
+    if (cache->code_type == KVL_CODE_FLOAT)
+        move_tokens_kernel<KVL_CODE_FLOAT><<<ctas, kMoveThreads, 0, static_cast<cudaStream_t>(stream)>>>(a);
+    else
+        move_tokens_kernel<KVL_CODE_INT><<<ctas, kMoveThreads, 0, static_cast<cudaStream_t>(stream)>>>(a);
+    return launch_status();
+}

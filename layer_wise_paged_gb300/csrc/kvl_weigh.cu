@@ -1,0 +1,59 @@
+// kvl_weigh.cu -- the entry points that weigh cached tokens: checks, choice of kernel.
+#include <cmath>
+
+#include "kvl_weigh.cuh"
+
+using namespace kvl;
+
+extern "C" size_t kvl_weigh_workspace_bytes(const kvl_cache *cache, int32_t n_seq, int64_t n_rows, int32_t n_heads,
+                                            int32_t max_new)
+{
+    if (check_cache(cache) != KVL_OK || n_seq < 0 || n_rows < 0 || n_rows > INT32_MAX || n_heads <= 0 || n_heads > 65535 ||
+        max_new < 0)
+        return 0;
+    return 16;
+}
+
+extern "C" kvl_status kvl_weigh(const kvl_cache *cache, int32_t layer, const kvl_sequences *seqs,
+                                const kvl_weighing *w, void *d_workspace, size_t workspace_bytes, void *d_report,
+                                void *stream)
+{
+    kvl_status s = check_cache(cache);
+    if (!s) s = check_sequences(seqs);
+    if (s) return s;
+    if (!w || layer < 0 || layer >= cache->n_layers) return KVL_EINVAL;
+    if (w->n_heads <= 0 || w->n_heads > 65535 || w->n_heads % cache->n_kv_heads ||
+        (w->type != KVL_TYPE_BFLOAT && w->type != KVL_TYPE_HALF) || !(w->sm_scale > 0.f && w->sm_scale < INFINITY) ||
+        (w->causal & ~1) || w->window < 0 || (w->window > 0 && !w->causal) || w->max_new < 0 || (w->begin & ~1) || w->reserved != 0)
+        return KVL_EINVAL;
+    if (seqs->n_rows * (w->n_heads / cache->n_kv_heads) > INT32_MAX - 256) return KVL_EINVAL;
+    if (bad_report(d_report)) return KVL_EALIGN;
+    if (seqs->n_seq == 0 || seqs->n_rows == 0) return KVL_OK;
+    if ((s = check_rows(&w->q))) return s;
+    if (!w->lse || !w->mass_in || !w->mass_out || w->tokens <= 0 || w->in_stride < w->tokens || w->out_stride < w->tokens) return KVL_EINVAL;
+    if (misaligned4(w->lse) || misaligned4(w->mass_in) || misaligned4(w->mass_out) || !aligned16(d_workspace)) return KVL_EALIGN;
+    if (!d_workspace || workspace_bytes < kvl_weigh_workspace_bytes(cache, seqs->n_seq, seqs->n_rows, w->n_heads, w->max_new))
+        return KVL_EINVAL;
+    const int sms = sm_count();
+    if (sms <= 0) return KVL_ECUDA;
+    WeighArgs a = {};
+    a.t.cache = *cache;
+    a.t.seqs = *seqs;
+    a.t.layer = layer;
+    a.t.report = d_report;
+    a.t.attn.q = w->q;
+    a.t.attn.n_heads = w->n_heads;
+    a.t.attn.type = w->type;
+    a.t.attn.sm_scale = w->sm_scale;
+    a.t.attn.causal = w->causal;
+    a.t.attn.window = w->window;
+    a.lse = w->lse;
+    a.mass_in = w->mass_in;
+    a.mass_out = w->mass_out;
+    a.in_stride = w->in_stride;
+    a.out_stride = w->out_stride;
+    a.tokens = w->tokens;
+    a.begin = w->begin;
+    const int64_t bound = w->max_new > 0 && w->max_new < seqs->n_rows ? w->max_new : seqs->n_rows;
+    return launch_weigh_rows(a, bound * (w->n_heads / cache->n_kv_heads), sms, stream);
+}
