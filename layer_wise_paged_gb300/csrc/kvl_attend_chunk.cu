@@ -26,6 +26,7 @@
 
 #include "kvl_attend.cuh"
 #include "kvl_attend_meet.cuh"
+#include "kvl_tcgen.cuh"
 
 namespace kvl {
 namespace {
@@ -64,100 +65,6 @@ struct Chunk {
 // Barriers (each in its own 8 bytes).
 enum Bar { K_FULL = 0, K_EMPTY = 2, V_FULL = 4, V_EMPTY = 6, S_FULL = 8, PV_DONE = 10, LEAVE = 12, BARS = 13 };
 
-// ---- tensor-core wrappers -------------------------------------------------------------------
-
-// Shared-memory matrix descriptor: 128-byte swizzle, addresses in 16-byte units.  K-major (rows of
-// 64 halves): `stride` between groups of 8 rows.  MN-major: `lead` between runs of 64 elements
-// of the non-contracted index, `stride` between groups of 8 contracted ones.
-__device__ __forceinline__ uint64_t matrix_desc(uint32_t addr, uint32_t lead, uint32_t stride)
-{
-    return uint64_t((addr >> 4) & 0x3fff) | (uint64_t(lead >> 4) << 16) | (uint64_t(stride >> 4) << 32) |
-           (uint64_t(1) << 46) | (uint64_t(2) << 61);
-}
-
-// Instruction descriptor: f32 accumulators, half operands, 128 x n; b_mn: B is MN-major.
-__host__ __device__ constexpr uint32_t instr_desc(int n, bool b_mn)
-{
-    return (1u << 4) | (uint32_t(b_mn) << 16) | (uint32_t(n >> 3) << 17) | (uint32_t(kTileRows >> 4) << 24);
-}
-
-// One lane of a converged warp, the same one every time.
-__device__ __forceinline__ uint32_t elect_one()
-{
-    uint32_t r;
-    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
-    return r;
-}
-
-// Products, issued by the elected lane of a converged warp.
-__device__ __forceinline__ void mma_smem(uint32_t one, uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool add)
-{
-    asm volatile(
-        "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
-        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d), "l"(a), "l"(b), "r"(idesc),
-        "r"(uint32_t(add)), "r"(one)
-        : "memory");
-}
-
-__device__ __forceinline__ void mma_tmem(uint32_t one, uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool add)
-{
-    asm volatile(
-        "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
-        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d), "r"(a), "l"(b), "r"(idesc),
-        "r"(uint32_t(add)), "r"(one)
-        : "memory");
-}
-
-// Arrives on the barrier when the products that the elected lane has issued so far have ended.
-__device__ __forceinline__ void mma_commit(uint32_t one, uint32_t bar)
-{
-    asm volatile(
-        "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %1, 0;\n\t"
-        "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(bar), "r"(one)
-        : "memory");
-}
-
-__device__ __forceinline__ void tmem_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
-__device__ __forceinline__ void tmem_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
-__device__ __forceinline__ void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
-__device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
-
-// 32 columns of this warp's 32 lanes.
-__device__ __forceinline__ void tmem_ld32(uint32_t at, uint32_t (&r)[32])
-{
-    asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
-        "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
-        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
-          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
-          "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
-          "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
-        : "r"(at));
-}
-
-__device__ __forceinline__ void tmem_ld8(uint32_t at, uint32_t (&r)[8])
-{
-    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
-                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
-                 : "r"(at));
-}
-
-__device__ __forceinline__ void tmem_st8(uint32_t at, const uint32_t (&r)[8])
-{
-    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%8], {%0,%1,%2,%3,%4,%5,%6,%7};" ::"r"(r[0]), "r"(r[1]), "r"(r[2]),
-                 "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(at)
-                 : "memory");
-}
-
-__device__ __forceinline__ void tmem_st16(uint32_t at, const uint32_t (&r)[16])
-{
-    asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15};" ::"r"(r[0]),
-        "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]),
-        "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(at)
-        : "memory");
-}
-
 // Named barriers (kvl_attend_meet.cuh).  They are not in shared memory, where an access takes 200 cycles
 // while products stream their operands.
 struct Meet {
@@ -166,57 +73,6 @@ struct Meet {
     template <int N>
     __device__ __forceinline__ void arrive(int id) const { asm volatile("bar.arrive %0, %1;" ::"r"(id), "n"(N) : "memory"); }
 };
-
-__device__ __forceinline__ float max3(float a, float b, float c)
-{
-    float r;
-    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
-    return r;
-}
-
-// Two floats in one register pair, and arithmetic on both at once.
-__device__ __forceinline__ uint64_t pair_of(float x, float y)
-{
-    uint64_t r;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(x), "f"(y));
-    return r;
-}
-__device__ __forceinline__ float2 split_pair(uint64_t x)
-{
-    float2 r;
-    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(x));
-    return r;
-}
-__device__ __forceinline__ uint64_t fma_pair(uint64_t a, uint64_t b, uint64_t c)
-{
-    uint64_t r;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-    return r;
-}
-__device__ __forceinline__ uint64_t add_pair(uint64_t a, uint64_t b)
-{
-    uint64_t r;
-    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-    return r;
-}
-
-// Bounded wait that also leaves when another role has given up.  The limit (kWaitLimitNs at the
-// highest clock) is looked at every 256 tries: reading the global timer on the way in cost up to a
-// thousand cycles after the barrier had completed.
-__device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, volatile int *gone)
-{
-    if (mbar_try_wait(bar, parity)) return true;
-    const long long t0 = clock64();
-    for (uint32_t tries = 1; !mbar_try_wait(bar, parity); ++tries) {
-        if (tries & 255) continue;
-        if (*gone) return false;
-        if (clock64() - t0 > 2 * static_cast<long long>(kWaitLimitNs)) {
-            *gone = 1;
-            return false;
-        }
-    }
-    return true;
-}
 
 // ---- work ------------------------------------------------------------------------------------
 

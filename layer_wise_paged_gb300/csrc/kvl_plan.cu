@@ -634,7 +634,7 @@ extern "C" int32_t kvl_launches_per_call(int32_t which)
     case 10: return 2;                  // compact: counts, then tables
     case 11: return 1;                  // copy
     case 12: return 2;                  // attend_shared: shared tokens, own tokens
-    case 13: return 1;                  // weigh
+    case 13: return 2;                  // weigh: rows, then their weights
     case 14: return 2;                  // evict: plan, select
     case 15: return 1;                  // tokens move
     default: return 0;

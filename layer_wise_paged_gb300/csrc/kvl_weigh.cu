@@ -5,13 +5,34 @@
 
 using namespace kvl;
 
+namespace {
+
+// Calls whose entries may have more rows than this go to the tensor-memory kernel.
+constexpr int kChunkRowsOfWeigh = 16;
+// (Past this many rows a KV head's steps would outlast the kernel's bounded waits.)
+constexpr int64_t kMostChunkRows = int64_t(1) << 26;
+
+bool by_chunks(const kvl_cache &c, int64_t n_rows, int n_heads, int max_new)
+{
+    const int64_t bound = max_new > 0 && max_new < n_rows ? max_new : n_rows, G = n_heads / c.n_kv_heads;
+    return c.head_dim <= 128 && bound * G > kChunkRowsOfWeigh && n_rows * G <= kMostChunkRows;
+}
+
+int workspace_sms()
+{
+    const int n = sm_count();
+    return n > 0 ? n : 152;
+}
+
+}  // namespace
+
 extern "C" size_t kvl_weigh_workspace_bytes(const kvl_cache *cache, int32_t n_seq, int64_t n_rows, int32_t n_heads,
                                             int32_t max_new)
 {
     if (check_cache(cache) != KVL_OK || n_seq < 0 || n_rows < 0 || n_rows > INT32_MAX || n_heads <= 0 || n_heads > 65535 ||
         max_new < 0)
         return 0;
-    return 16;
+    return by_chunks(*cache, n_rows, n_heads, max_new) ? weigh_chunk_bytes(*cache, n_seq, n_rows, n_heads, workspace_sms()) : 16;
 }
 
 extern "C" kvl_status kvl_weigh(const kvl_cache *cache, int32_t layer, const kvl_sequences *seqs,
@@ -54,6 +75,7 @@ extern "C" kvl_status kvl_weigh(const kvl_cache *cache, int32_t layer, const kvl
     a.out_stride = w->out_stride;
     a.tokens = w->tokens;
     a.begin = w->begin;
+    if (by_chunks(*cache, seqs->n_rows, w->n_heads, w->max_new)) return launch_weigh_chunk(a, d_workspace, sms, stream);
     const int64_t bound = w->max_new > 0 && w->max_new < seqs->n_rows ? w->max_new : seqs->n_rows;
     return launch_weigh_rows(a, bound * (w->n_heads / cache->n_kv_heads), sms, stream);
 }

@@ -22,5 +22,7 @@ struct WeighArgs {
 
 // most: a bound on the rows (fresh tokens x query heads of a KV head) of an entry, which chooses the row tile.
 kvl_status launch_weigh_rows(const WeighArgs &a, int64_t most, int sms, void *stream);
+size_t weigh_chunk_bytes(const kvl_cache &c, int n_seq, int64_t n_rows, int n_heads, int sms);
+kvl_status launch_weigh_chunk(const WeighArgs &a, void *d_workspace, int sms, void *stream);
 
 }  // namespace kvl
