@@ -7,17 +7,22 @@
 // fork still names is never written, sources and destinations are disjoint, and how many pages a batch needs does
 // not depend on the masses:
 //   plan    one CTA: checks, needs, and the lowest free numbers in batch order (as extend);
-//   select  a CTA a sequence: the smallest mass that stays by its digits (three passes of 11, 11 and 10 bits over
-//           order-preserving keys), then one walk in token order that gives each kept token its place, moves its
-//           mass and notes where its codes come from;
+//   select  a cluster of CTAs a sequence: the smallest mass that stays by its digits (three passes of 11, 11 and 10
+//           bits over order-preserving keys, histograms added up over the cluster), then one walk in token order
+//           that gives each kept token its place, moves its mass and notes where its codes come from;
 //   move    all layers' codes, a warp 512 bytes of a row's width of one new page.
+#include <algorithm>
+
+#include <cooperative_groups.h>
+
 #include "kvl_pages.cuh"
 
 namespace kvl {
 namespace {
 
 constexpr int kDigits = 2048;  // 11 bits
-constexpr int kRun = 4;        // tokens of a thread in a turn
+constexpr int kRun = 16;       // tokens of a thread in a round
+constexpr int kMostRanks = 8;  // CTAs of a sequence
 
 struct EvictArgs {
     kvl_pages p;
@@ -143,13 +148,20 @@ __device__ __forceinline__ uint32_t key_of(float x)
     return u & 0x80000000u ? ~u : u | 0x80000000u;
 }
 
+// A cluster of CTAs a sequence: a thread holds kRun tokens' masses in registers, so a sequence of up to kRun * 1024
+// tokens a CTA is read once (longer ones again for every pass, in rounds).
 __global__ void __launch_bounds__(kThreads) evict_select_kernel(const __grid_constant__ EvictArgs a)
 {
-    __shared__ uint32_t hist[kDigits];
+    __shared__ uint32_t hist[2][kDigits];
     __shared__ long long scan[32];
     __shared__ int scan_bins[32];
     __shared__ uint32_t s_digit, s_rest;
-    const int tid = threadIdx.x, i = blockIdx.x;
+    __shared__ uint32_t s_count[kRun * 32];  // of a round's 32 tokens: those that surely stay, those of the least mass << 16
+    __shared__ uint32_t s_before[kRun * 32];
+    __shared__ long long s_total;
+    const cooperative_groups::cluster_group cluster = cooperative_groups::this_cluster();
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int ranks = int(cluster.num_blocks()), rank = int(cluster.block_rank()), i = blockIdx.x / ranks;
     if (a.m.at[a.n] < 0) return;
     const Ask q = ask_of(a, i);
     if (!q.cut) return;
@@ -159,6 +171,18 @@ __global__ void __launch_bounds__(kThreads) evict_select_kernel(const __grid_con
     const int take = q.keep - f - r;        // how many of them stay; fewer than there are
     float *mass = a.e.mass ? a.e.mass + int64_t(q.slot) * a.e.mass_stride : nullptr;
     int32_t *table = a.p.tables + int64_t(q.slot) * a.p.table_stride;
+    const int64_t round = int64_t(ranks) * kThreads * kRun;
+    const int rounds = int(ceil_div64(q.len, round));
+    float x[kRun];
+    auto token = [&](int n, int y) { return n * round + (int64_t(rank) * kRun + y) * kThreads + tid; };
+    auto load = [&](int n) {
+#pragma unroll
+        for (int y = 0; y < kRun; ++y) {
+            const int64_t j = token(n, y);
+            x[y] = mass && j < q.len ? __ldcg(mass + j) : 0.f;
+        }
+    };
+    load(0);
 
     // ---- the smallest key that stays, and how many of those that equal it
     uint32_t least = 0xffffffffu, equals = 0;
@@ -167,19 +191,33 @@ __global__ void __launch_bounds__(kThreads) evict_select_kernel(const __grid_con
         equals = take;
     } else if (take > 0) {
         uint32_t known = 0, mask = 0, rest = take;  // the key's digits so far; its rank among those that have them
+        for (int z = tid; z < kDigits; z += kThreads) hist[0][z] = 0;
+        __syncthreads();
 #pragma unroll 1
         for (int pass = 0; pass < 3; ++pass) {
             const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0, bins = pass == 2 ? 1024 : 2048;
-            for (int x = tid; x < bins; x += kThreads) hist[x] = 0;
-            __syncthreads();
-            for (int j = lo + tid; j < hi; j += kThreads) {
-                const uint32_t k = key_of(mass[j]);
-                if ((k & mask) == known) atomicAdd(&hist[(k >> shift) & (bins - 1)], 1u);
+            uint32_t *mine = hist[pass & 1];
+#pragma unroll 1
+            for (int n = 0; n < rounds; ++n) {
+                if (rounds > 1) load(n);
+#pragma unroll
+                for (int y = 0; y < kRun; ++y) {
+                    const int64_t j = token(n, y);
+                    const uint32_t k = key_of(x[y]);
+                    if (j >= lo && j < hi && (k & mask) == known) atomicAdd(&mine[(k >> shift) & (bins - 1)], 1u);
+                }
             }
-            __syncthreads();
+            cluster.sync();
             // the digit at which the sum from the largest digit down reaches `rest`: two bins a thread
             const int top = bins - 1 - 2 * tid;
-            const int c0 = 2 * tid < bins ? hist[top] : 0, c1 = 2 * tid + 1 < bins ? hist[top - 1] : 0;
+            int c0 = 0, c1 = 0;
+            if (2 * tid < bins)
+                for (int z = 0; z < ranks; ++z) {
+                    const uint32_t *theirs = cluster.map_shared_rank(mine, z);
+                    c0 += theirs[top];
+                    c1 += theirs[top - 1];
+                }
+            for (int z = tid; z < kDigits; z += kThreads) hist[~pass & 1][z] = 0;  // (its readers have passed)
             int total;
             const uint32_t before = block_scan<int>(c0 + c1, scan_bins, total);
             if (before < rest && rest <= before + c0) {
@@ -199,34 +237,45 @@ __global__ void __launch_bounds__(kThreads) evict_select_kernel(const __grid_con
         equals = rest;
     }
 
-    // ---- places, masses, sources; a turn's masses are read before any is written, and a token moves down
+    // ---- places, masses, sources.  A round's masses are in registers before any is written, and a token moves down,
+    // never past tokens that a later round still reads.
     const int64_t first_page = a.m.at[i];
-    long long kept = 0;  // tokens that stay before this turn; those that equal `least` in the high half
-    for (int base = 0; base < q.len; base += kThreads * kRun) {
-        const int j0 = base + tid * kRun;
-        float x[kRun];
-        bool sure[kRun], even[kRun];
-        int n_sure = 0, n_even = 0;
+    long long kept = 0;  // tokens that stay before this round; those that equal `least` in the high half
+#pragma unroll 1
+    for (int n = 0; n < rounds; ++n) {
+        if (rounds > 1) load(n);
+        unsigned sure[kRun], even[kRun];
 #pragma unroll
         for (int y = 0; y < kRun; ++y) {
-            const int j = j0 + y;
-            x[y] = mass && j < q.len ? mass[j] : 0.f;
+            const int64_t j = token(n, y);
             const uint32_t k = key_of(x[y]);
             const bool between = j >= lo && j < hi;
-            sure[y] = j < q.len && (!between || (take > 0 && k > least));
-            even[y] = between && take > 0 && k == least;
-            n_sure += sure[y];
-            n_even += even[y];
+            sure[y] = __ballot_sync(0xffffffffu, j < q.len && (!between || (take > 0 && k > least)));
+            even[y] = __ballot_sync(0xffffffffu, between && take > 0 && k == least);
+            if (lane == 0) s_count[y * 32 + warp] = __popc(sure[y]) | __popc(even[y]) << 16;
         }
+        __syncthreads();
+        const uint32_t c = tid < kRun * 32 ? s_count[tid] : 0;
         long long total;
-        const long long before = kept + block_scan<long long>(n_sure | (long long)n_even << 32, scan, total);
-        kept += total;
-        int s = int(before & 0xffffffffll), v = int(before >> 32);
+        const long long b = block_scan<long long>((c & 0xffffu) | (long long)(c >> 16) << 32, scan, total);
+        if (tid < kRun * 32) s_before[tid] = uint32_t(b & 0xffff) | uint32_t(b >> 32) << 16;  // (each at most 16,384)
+        if (tid == 0) s_total = total;
+        cluster.sync();
+        long long all = 0, ahead = kept;
+        for (int z = 0; z < ranks; ++z) {
+            const long long t = *cluster.map_shared_rank(&s_total, z);
+            all += t;
+            if (z < rank) ahead += t;
+        }
+        kept += all;
 #pragma unroll
         for (int y = 0; y < kRun; ++y) {
-            const int j = j0 + y;
-            if (sure[y] || (even[y] && v < int(equals))) {
-                const int k = s + min(v, int(equals)), at = k / B - q.stay;
+            const uint32_t w = s_before[y * 32 + warp], below = (1u << lane) - 1;
+            const int s = int(ahead & 0xffffffffll) + int(w & 0xffffu) + __popc(sure[y] & below);
+            const int v = int(ahead >> 32) + int(w >> 16) + __popc(even[y] & below);
+            const bool stays = sure[y] >> lane & 1u, equal = even[y] >> lane & 1u;
+            if (stays || (equal && v < int(equals))) {
+                const int j = int(token(n, y)), k = s + min(v, int(equals)), at = k / B - q.stay;
                 if (mass) mass[k] = x[y];
                 if (at >= 0) {
                     const int32_t page = table[j / B];
@@ -235,19 +284,18 @@ __global__ void __launch_bounds__(kThreads) evict_select_kernel(const __grid_con
                     reinterpret_cast<int2 *>(a.m.from)[(first_page + at) * B + k % B] = make_int2(there ? page : -1, j % B);
                 }
             }
-            s += sure[y];
-            v += even[y];
         }
-        __syncthreads();  // the scan's sums and the masses
+        cluster.sync();  // the sums, and the masses
     }
+    const int me = rank * kThreads + tid, all = ranks * kThreads;
     if (mass)
-        for (int64_t j = q.keep + tid; j < a.e.tokens; j += kThreads) mass[j] = 0.f;
+        for (int64_t j = q.keep + me; j < a.e.tokens; j += all) mass[j] = 0.f;
     const int pages = int(ceil_div64(q.keep, B));
-    for (int64_t k = q.keep + tid; k < int64_t(pages) * B; k += kThreads)
+    for (int64_t k = q.keep + me; k < int64_t(pages) * B; k += all)
         if (q.pages > 0) reinterpret_cast<int2 *>(a.m.from)[(first_page + k / B - q.stay) * B + k % B] = make_int2(-1, 0);
     // ---- the pages that go
     const int held = int(ceil_div64(q.len, B));
-    for (int k = q.stay + tid; k < held; k += kThreads) {
+    for (int k = q.stay + me; k < held; k += all) {
         const int32_t id = table[k];
         if (id < 0 || id >= a.p.pool_blocks) {
             report(a.report, KVL_ERANGE, i);
@@ -256,9 +304,9 @@ __global__ void __launch_bounds__(kThreads) evict_select_kernel(const __grid_con
             report(a.report, KVL_EINVAL, i);
         }
     }
-    __syncthreads();
-    for (int k = q.stay + tid; k < pages; k += kThreads) table[k] = a.m.to[first_page + k - q.stay];
-    if (tid == 0) a.p.lens[q.slot] = q.keep;
+    cluster.sync();
+    for (int k = q.stay + me; k < pages; k += all) table[k] = a.m.to[first_page + k - q.stay];
+    if (me == 0) a.p.lens[q.slot] = q.keep;
 }
 
 // ---- codes -------------------------------------------------------------------------------------
@@ -272,12 +320,15 @@ struct MoveArgs {
     int64_t max_pages;
     int32_t lanes;   // lanes of a row's slice: a power of two, 16 bytes each
     int32_t slices;  // of a row of H * d bytes
+    int32_t parts;   // of a page's slots, `part` slots each
+    int32_t part;
     void *report;
 };
 
 // scale' = the largest scale of the pages that a new page's tokens come from, for each head; code' =
 // round(code * (scale / scale')).  The tokens of the largest scale keep their codes bit for bit, so what a further
-// eviction rounds again is what came from smaller ones.
+// eviction rounds again is what came from smaller ones.  A warp takes a part of a page's slots (whose scales it
+// looks at all the same) and a slice of their rows.
 template <int CODE>
 __global__ void __launch_bounds__(kMoveThreads, kMoveCtasPerSm) move_tokens_kernel(const __grid_constant__ MoveArgs a)
 {
@@ -289,40 +340,52 @@ __global__ void __launch_bounds__(kMoveThreads, kMoveCtasPerSm) move_tokens_kern
     const int64_t N = a.c.pool_blocks, planes = int64_t(a.c.n_layers) * 2;
     const int B = a.c.block_tokens, H = a.c.n_kv_heads, d = a.c.head_dim, row_bytes = H * d;
     const int lane = threadIdx.x & 31, per = 32 / a.lanes, rw = lane / a.lanes, ch = lane % a.lanes;
-    const int64_t units = n * planes * a.slices, step = int64_t(gridDim.x) * (kMoveThreads / 32);
+    const int64_t per_page = planes * a.slices * a.parts, units = n * per_page;
+    const int64_t step = int64_t(gridDim.x) * (kMoveThreads / 32);
     for (int64_t u = int64_t(blockIdx.x) * (kMoveThreads / 32) + (threadIdx.x >> 5); u < units; u += step) {
-        const int64_t kp = u / a.slices, k = kp / planes, lp = kp - k * planes;
-        const int at = (int(u - kp * a.slices) * a.lanes + ch) * 16;  // this lane's bytes of a row
+        const int64_t k = u / per_page;
+        uint32_t rest = uint32_t(u - k * per_page);  // (at most 2^31: checked on the host)
+        const uint32_t lp = rest / uint32_t(a.slices * a.parts);
+        rest -= lp * uint32_t(a.slices * a.parts);
+        const int slice = int(rest / uint32_t(a.parts)), s_first = int(rest - uint32_t(slice) * a.parts) * a.part;
+        const int first = slice * a.lanes * 16, at = first + ch * 16;  // the slice's bytes of a row, and this lane's
         const bool mine = at < row_bytes;
         const int32_t to = a.m.to[k];
         if (to < 0 || to >= N) {
             if (lane == 0) report(a.report, KVL_ERANGE, k);
             continue;
         }
-        const int h = mine ? at / d : 0;
+        const int h = mine ? at / d : 0, ha = first / d, hb = (min(first + a.lanes * 16, row_bytes) - 1) / d;  // heads of the slice
         const uint8_t *codes = static_cast<const uint8_t *>(a.c.codes) + lp * N * B * row_bytes + (mine ? at : 0);
-        const float *scales = a.c.scales + lp * N * H + h;
+        const float *scales = a.c.scales + lp * N * H;
         const int2 *from = reinterpret_cast<const int2 *>(a.m.from) + k * B;
         auto source = [&](int slot) -> int2 {  // page and slot, a page of -1: none
             const int2 x = slot < B ? from[slot] : make_int2(-1, 0);
             return make_int2(x.x < N && x.y >= 0 && x.y < B ? x.x : -1, x.y);
         };
+        // lane l looks at the scales of tokens l, l + 32, ... for each head of the slice
         float now = 0.f;
-        for (int s = rw; s < B; s += per) {
-            const int2 x = source(s);
-            if (x.x >= 0) now = fmaxf(now, scales[int64_t(x.x) * H]);
+        for (int s = 0; s < B; s += 32) {
+            const int32_t page = source(s + lane).x;
+#pragma unroll 4
+            for (int y = ha; y <= hb; ++y) {
+                const float v = page >= 0 ? scales[int64_t(page) * H + y] : 0.f;
+                const float top = __uint_as_float(__reduce_max_sync(0xffffffffu, v > 0.f ? __float_as_uint(v) : 0u));
+                if (y == h) now = fmaxf(now, top);
+            }
         }
-        for (int o = a.lanes; o < 32; o <<= 1) now = fmaxf(now, __shfl_xor_sync(0xffffffffu, now, o));
-        for (int s0 = rw; s0 < B; s0 += per * kHeld) {
+        const int s_past = min(B, s_first + a.part);
+        for (int s0 = s_first + rw; s0 - rw < s_past; s0 += per * kHeld) {
             uint4 w[kHeld];
             float was[kHeld];
 #pragma unroll
             for (int y = 0; y < kHeld; ++y) {
-                const int2 x = source(s0 + y * per);
+                const int s = s0 + y * per;
+                const int2 x = s < s_past ? source(s) : make_int2(-1, 0);
                 was[y] = -1.f;  // none
                 if (x.x >= 0 && mine) {
                     w[y] = *reinterpret_cast<const uint4 *>(codes + (int64_t(x.x) * B + x.y) * row_bytes);
-                    was[y] = scales[int64_t(x.x) * H];
+                    was[y] = scales[int64_t(x.x) * H + h];
                 }
             }
 #pragma unroll
@@ -341,10 +404,10 @@ __global__ void __launch_bounds__(kMoveThreads, kMoveCtasPerSm) move_tokens_kern
                     }
                     w[y] = make_uint4(z[0], z[1], z[2], z[3]);
                 }
-                *reinterpret_cast<uint4 *>(static_cast<uint8_t *>(a.c.codes) + ((lp * N + to) * B + s) * row_bytes + at) = w[y];
+                *reinterpret_cast<uint4 *>(static_cast<uint8_t *>(a.c.codes) + ((int64_t(lp) * N + to) * B + s) * row_bytes + at) = w[y];
             }
         }
-        if (mine && rw == 0 && at % d == 0) a.c.scales[(lp * N + to) * H + h] = now;
+        if (s_first == 0 && mine && rw == 0 && at % d == 0) a.c.scales[(int64_t(lp) * N + to) * H + h] = now;
     }
 }
 
@@ -384,8 +447,21 @@ extern "C" kvl_status kvl_pages_evict(const kvl_pages *pages, int32_t n, const i
     evict_plan_kernel<<<1, kThreads, smem, st>>>(a);
     s = launch_status();
     if (s || n == 0) return s;
-    evict_select_kernel<<<n, kThreads, 0, st>>>(a);
-    return launch_status();
+    // as many CTAs a sequence as hold the longest that the table has room for in their registers
+    const int64_t most = std::min(pages->table_stride * int64_t(pages->block_tokens), pages->pool_blocks * int64_t(pages->block_tokens));
+    unsigned ranks = 1;
+    while (ranks < kMostRanks && int64_t(ranks) * kThreads * kRun < most) ranks *= 2;
+    cudaLaunchAttribute cluster;
+    cluster.id = cudaLaunchAttributeClusterDimension;
+    cluster.val.clusterDim.x = ranks;
+    cluster.val.clusterDim.y = cluster.val.clusterDim.z = 1;
+    cudaLaunchConfig_t config = {};
+    config.gridDim = dim3(unsigned(n) * ranks);
+    config.blockDim = dim3(kThreads);
+    config.stream = st;
+    config.attrs = &cluster;
+    config.numAttrs = 1;
+    return cudaLaunchKernelEx(&config, evict_select_kernel, a) == cudaSuccess ? launch_status() : (cudaGetLastError(), KVL_ECUDA);
 }
 
 extern "C" kvl_status kvl_tokens_move(const kvl_cache *cache, const kvl_moves *moves, int64_t max_pages,
@@ -406,6 +482,9 @@ extern "C" kvl_status kvl_tokens_move(const kvl_cache *cache, const kvl_moves *m
     a.lanes = 1;
     while (a.lanes < 32 && a.lanes < vectors) a.lanes *= 2;
     a.slices = (vectors + a.lanes - 1) / a.lanes;
+    a.part = 2 * kHeld * (32 / a.lanes);
+    a.parts = int32_t((int64_t(cache->block_tokens) + a.part - 1) / a.part);
+    if (int64_t(cache->n_layers) * 2 * a.slices * a.parts > INT32_MAX) return KVL_EINVAL;
     a.report = d_report;
     const int ctas = sms * kMoveCtasPerSm;
     if (cache->code_type == KVL_CODE_FLOAT)
