@@ -529,7 +529,8 @@ typedef struct kvl_shared {
     const int32_t *tokens; /* device, n_groups */
 } kvl_shared;
 
-size_t kvl_attend_shared_parts_bytes(const kvl_cache *cache, int64_t n_rows, int32_t n_heads);
+size_t kvl_attend_shared_parts_bytes(const kvl_cache *cache, int32_t n_seq, int32_t n_groups, int64_t n_rows,
+                                     int32_t n_heads);
 kvl_status kvl_attend_shared(const kvl_cache *cache, int32_t layer, const kvl_sequences *seqs,
                              const kvl_shared *shared, const kvl_attention *attn, void *d_workspace,
                              size_t workspace_bytes, void *d_parts, size_t parts_bytes, void *d_report,

@@ -131,7 +131,7 @@ def lib():
         L.kvl_pages_free.argtypes = [pg, i32, vp, vp, vp]
         L.kvl_pages_compact.argtypes = [pg, vp, vp]
         L.kvl_pages_copy.argtypes = [cp, vp, vp, i64, vp, vp]
-        L.kvl_attend_shared_parts_bytes.argtypes, L.kvl_attend_shared_parts_bytes.restype = [cp, i64, i32], sz
+        L.kvl_attend_shared_parts_bytes.argtypes, L.kvl_attend_shared_parts_bytes.restype = [cp, i32, i32, i64, i32], sz
         L.kvl_attend_shared.argtypes = [cp, i32, sp, P(kvl_shared), P(kvl_attention), vp, sz, vp, sz, vp, vp]
         L.kvl_weigh_workspace_bytes.argtypes, L.kvl_weigh_workspace_bytes.restype = [cp, i32, i64, i32, i32], sz
         L.kvl_weigh.argtypes = [cp, i32, sp, P(kvl_weighing), vp, sz, vp, vp]

@@ -276,9 +276,10 @@ class QuantCache:
         g = c.shared
         g.n_groups, g.groups, g.tokens = n_groups, _ints(groups, "groups", n_groups + 1), _ints(shared, "shared")
         n_rows, heads, _ = q.shape
-        n = self._lib.kvl_attend_shared_parts_bytes(self._cache, n_rows, heads)
+        s = self._seqs(c, starts, slots, n_rows)
+        n = self._lib.kvl_attend_shared_parts_bytes(self._cache, s.n_seq, n_groups, n_rows, heads)
         parts = self._scratch(n, stream, st)
-        r = self._lib.kvl_attend_shared(self._cache, layer, self._seqs(c, starts, slots, n_rows), g, c.attn, ws,
+        r = self._lib.kvl_attend_shared(self._cache, layer, s, g, c.attn, ws,
                                         self._ws_bytes, parts.data_ptr(), n, self._report, st)
         if r:
             check(r, "kvl_attend_shared")

@@ -33,8 +33,14 @@ struct AttendArgs {
     void *report;
     // attention over a shared prefix only
     kvl_shared shared;
-    float *row_o;      // [n_rows][n_heads][64, 128 or 256]: O of the rows over the shared tokens
-    float *row_ml;     // [n_rows][n_heads][2]: their references and sums
+    int32_t *shared_done;  // 1: the shared tokens' results are there
+    int32_t *sharing;      // [n_seq] Sharing
+    float *row_o;          // [n_rows][n_heads][64, 128 or 256]: O of the rows over the shared tokens
+    float *row_ml;         // [n_rows][n_heads][2]: their references and sums
+    // where the tensor-memory kernel makes them (kvl_attend_prefix.cuh): rows of a tile (0: row_o has them)
+    int32_t prefix_rows, prefix_most;
+    int32_t *prefix_jobs;
+    float *prefix_parts;   // prefix_most of them
 };
 
 namespace {
@@ -57,7 +63,8 @@ constexpr uint64_t kMostUnits = uint64_t(1) << 31;  // see Cut
 struct Cost {
     Entry e;
     int32_t tiles, g0, groups;
-    int32_t lo;  // the first token any row sees
+    int32_t lo;            // the first token any row sees
+    int32_t group, row0;   // of a sequence that shares its first lo tokens: its group, and the group's first row
 };
 
 // The first token a row at position `pos` sees, j > pos - window.  (A row stands before token 0 where an
@@ -99,21 +106,38 @@ __device__ __forceinline__ Entry load_group(const AttendArgs &a, int32_t g, void
     return e;
 }
 
-// The tokens that entry i (resolved as e) shares with the others of its group.  An entry whose group is left out,
-// or one of whose rows does not see all of them, loses its rows.
-__device__ __forceinline__ int32_t shared_of(const AttendArgs &a, Entry &e, int32_t i, void *rep)
+// What an entry shares with the others of its group: its first `tokens` tokens (-1: the entry is left out), its
+// group and the group's first row.
+struct alignas(16) Sharing {
+    int32_t tokens, group, row0, reserved;
+};
+
+// An entry whose group is left out, or one of whose rows does not see all shared tokens, is left out.
+__device__ __forceinline__ Sharing sharing_of(const AttendArgs &a, int32_t i, void *rep)
 {
+    Sharing s = {0, 0, 0, 0};
+    const Entry e = load_entry(a.seqs, a.cache.block_tokens, i, nullptr);  // (reports itself where its own tokens are attended)
     int lo = -1, hi = a.shared.n_groups;  // the last group that begins at i or before
     while (hi - lo > 1) {
         const int mid = (lo + hi) >> 1;
         if (a.shared.groups[mid] <= i) lo = mid; else hi = mid;
     }
-    if (e.fresh <= 0 || lo < 0 || i >= a.shared.groups[lo + 1] || a.shared.tokens[lo] == 0) return 0;
+    if (e.fresh <= 0 || lo < 0 || i >= a.shared.groups[lo + 1] || a.shared.tokens[lo] == 0) return s;
     const Entry p = load_group(a, lo, nullptr);
-    if (p.len > 0 && p.len <= e.len - e.fresh && e.row0 >= p.row0 && e.row0 + e.fresh <= p.row0 + p.fresh) return p.len;
+    s.group = lo;
+    s.row0 = p.row0;
+    s.tokens = p.len;
+    if (p.len > 0 && p.len <= e.len - e.fresh && e.row0 >= p.row0 && e.row0 + e.fresh <= p.row0 + p.fresh) return s;
     if (p.len > 0) report(rep, KVL_ERANGE, i);  // (a group reports itself)
-    e.len = e.fresh = 0;
-    return 0;
+    s.tokens = -1;
+    return s;
+}
+
+// Every entry's sharing, looked up once by the kernel over the shared tokens for the one over the entries' own, which
+// would go through half a dozen loads one after another for each.
+__device__ __forceinline__ void resolve_entries(const AttendArgs &a, int first, int step)
+{
+    for (int i = first; i < a.seqs.n_seq; i += step) reinterpret_cast<Sharing *>(a.sharing)[i] = sharing_of(a, i, a.report);
 }
 
 // 16 bytes into shared memory; zeros where !ok (src has to be a valid address all the same).

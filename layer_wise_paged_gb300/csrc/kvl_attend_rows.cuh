@@ -29,6 +29,7 @@
 namespace kvl {
 namespace {
 
+constexpr int kMostParts = 160;  // of a row's shared tokens: no more than there are SMs
 constexpr int kWarps = 6;
 constexpr int kThreads = kWarps * 32;
 constexpr int kPair = 2;          // groups a warp takes at a time (4 at d = 64: 137 us for 256 sequences of 1,500, with 2 123)
@@ -93,7 +94,13 @@ __device__ __forceinline__ Cost cost_of(const AttendArgs &a, int i, void *rep)
         c.e = load_group(a, i, rep);
     } else {
         c.e = load_entry(a.seqs, B, i, rep);
-        if constexpr (PART == Part::own) c.lo = shared_of(a, c.e, i, rep);
+        if constexpr (PART == Part::own) {
+            const Sharing s = reinterpret_cast<const Sharing *>(a.sharing)[i];
+            c.lo = max(s.tokens, 0);
+            c.group = s.group;
+            c.row0 = s.row0;
+            if (s.tokens < 0) c.e.len = c.e.fresh = 0;
+        }
     }
     const int64_t rows = int64_t(c.e.fresh) * (a.attn.n_heads / a.cache.n_kv_heads);
     c.tiles = rows > a.max_rows ? 0 : int32_t((rows + 8 * NT - 1) / (8 * NT));
@@ -115,12 +122,27 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attend_rows_kernel(const
     __shared__ Cost s_cost;
     __shared__ int s_entry, s_last;
     __shared__ float s_m[kWarps][kRows], s_l[kWarps][kRows], s_cq[kRows];
+    // how a row's own tokens and the parts of the shared ones join
+    struct Join {
+        const float *o;   // the first part's values
+        int64_t step;     // to the next part's
+        int parts;        // -1: the shared tokens' results are missing
+        float own, big, sum;
+    };
+    constexpr bool kOwn = PART == Part::own;
+    __shared__ Join s_join[kOwn ? kRows : 1];
+    __shared__ float s_factor[kOwn ? kRows : 1][kOwn ? kMostParts : 1];
 
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, nn = lane >> 2, kk = lane & 3;
     const int H = a.cache.n_kv_heads, d = a.cache.head_dim, B = a.cache.block_tokens;
     const int G = a.attn.n_heads / H, per_block = (B + kGroup - 1) / kGroup;
     const int64_t N = a.cache.pool_blocks;
 
+    if constexpr (PART == Part::shared) {
+        allow_dependents_launch();
+        resolve_entries(a, int(blockIdx.x) * kThreads + tid, int(gridDim.x) * kThreads);
+    }
+    if constexpr (PART == Part::own) grid_dependency_wait();
     // ---- this CTA's share of the units ----
     const int n_seq = PART == Part::shared ? a.shared.n_groups : a.seqs.n_seq, per_thread = (n_seq + kThreads - 1) / kThreads;
     const int i0 = min(n_seq, tid * per_thread), i1 = min(n_seq, i0 + per_thread);
@@ -145,6 +167,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attend_rows_kernel(const
         if (w < warp) before += s_scan[w];
         total += s_scan[w];
     }
+    if constexpr (PART == Part::shared)
+        if (blockIdx.x == 0 && tid == 0) *a.shared_done = total < kMostUnits;
     if (total == 0 || total >= kMostUnits) {
         if (total && blockIdx.x == 0 && tid == 0) report(a.report, KVL_ERANGE, n_seq);
         return;
@@ -586,15 +610,18 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attend_rows_kernel(const
                 return;
             }
             if constexpr (PART == Part::own) {
-                if (c.lo > 0) {
-                    const int64_t at = t * a.attn.n_heads + head;
-                    const float4 y = *reinterpret_cast<const float4 *>(a.row_o + at * D + e);
-                    const float2 ml = *reinterpret_cast<const float2 *>(a.row_ml + at * 2);
-                    const float m = fmaxf(big, ml.x);
-                    const float f = big == -INFINITY ? 0.f : exp2_of(big - m), g = ml.x == -INFINITY ? 0.f : exp2_of(ml.x - m);
-                    v.x = v.x * f + y.x * g; v.y = v.y * f + y.y * g; v.z = v.z * f + y.z * g; v.w = v.w * f + y.w * g;
-                    sum = sum * f + ml.y * g;
-                    big = m;
+                // what the shared tokens gave: one result of the row, or parts of it, in order
+                const Join &j = s_join[r];
+                if (j.parts < 0) return;
+                v.x *= j.own; v.y *= j.own; v.z *= j.own; v.w *= j.own;
+                sum = j.sum;
+                big = j.big;
+                const float *o = j.o + e;
+#pragma unroll 8
+                for (int b = 0; b < j.parts; ++b) {
+                    const float g = s_factor[r][b];
+                    const float4 y = *reinterpret_cast<const float4 *>(o + b * j.step);
+                    v.x += y.x * g; v.y += y.y * g; v.z += y.z * g; v.w += y.w * g;
                 }
             }
             const float inv = sum == 0.f ? 0.f : 1.f / sum;  // 0: the row sees nothing
@@ -604,7 +631,61 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attend_rows_kernel(const
             if (e == 0 && a.attn.lse)
                 a.attn.lse[t * a.attn.n_heads + head] = sum == 0.f ? -INFINITY : (big + __log2f(sum)) * (1.f / kLog2e);
         };
+        // By a warp a row: the factors of row r's own tokens (reference big, sum of weights sum) and of the parts.
+        auto weigh_parts = [&](int r, float big, float sum) {
+            const int row = tile * kRows + r, head = h * G + row % G;
+            const int64_t t = int64_t(c.e.row0) + row / G;
+            const float *ml = nullptr;
+            Join j = {nullptr, 0, 0, 0.f, 0.f, 0.f};
+            int64_t ml_step = 1;  // from a reference to its sum
+            if (c.lo > 0 && a.prefix_rows == 0) {
+                const int64_t at = t * a.attn.n_heads + head;
+                ml = a.row_ml + at * 2;
+                j.o = a.row_o + at * D;
+                j.parts = 1;
+            } else if (c.lo > 0) {
+                const int R = a.prefix_rows, row_g = int(t - c.row0) * G + row % G, tile_g = row_g / R, r_g = row_g - tile_g * R;
+                const int64_t id = int64_t(c.row0) * G / R + c.group + tile_g;
+                const int2 p = reinterpret_cast<const int2 *>(a.prefix_jobs)[id * H + h];
+                // (not there if a wait ran out)
+                j.parts = p.x >= 0 && p.y >= 0 && p.y <= kMostParts && p.x <= a.prefix_most - p.y ? p.y : 0;
+                j.step = int64_t(R) * (D + 2);
+                ml = a.prefix_parts + (j.parts ? p.x : 0) * j.step + r_g;
+                ml_step = R;
+                j.o = ml - r_g + 2 * R + int64_t(r_g) * D;
+            }
+            float m = big;
+            for (int b = lane; b < j.parts; b += 32) m = fmaxf(m, ml[b * j.step]);
+#pragma unroll
+            for (int x = 16; x; x >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, x));
+            float all = 0.f;
+            for (int b = lane; b < j.parts; b += 32) {
+                const float mb = ml[b * j.step], f = mb == -INFINITY ? 0.f : exp2_of(mb - m);
+                s_factor[r][b] = f;
+                all += ml[b * j.step + ml_step] * f;
+            }
+#pragma unroll
+            for (int x = 16; x; x >>= 1) all += __shfl_xor_sync(0xffffffffu, all, x);
+            j.own = big == -INFINITY ? 0.f : exp2_of(big - m);
+            j.big = m;
+            j.sum = sum * j.own + all;
+            if (c.lo > 0 && !*a.shared_done) j.parts = -1;
+            if (lane == 0) s_join[r] = j;
+        };
         float *part = a.parts + (int64_t(blockIdx.x) * 2 + (ga == 0 ? 1 : 0)) * S::kPartFloats;
+        if constexpr (kOwn) {
+            if (complete) {
+                for (int r = warp; r < rows; r += kWarps) {
+                    float big = -INFINITY, sum = 0.f;
+#pragma unroll
+                    for (int w = 0; w < kWarps; ++w) big = fmaxf(big, s_m[w][r]);
+#pragma unroll
+                    for (int w = 0; w < kWarps; ++w) sum += s_m[w][r] == -INFINITY ? 0.f : s_l[w][r] * exp2_of(s_m[w][r] - big);
+                    weigh_parts(r, big, sum);
+                }
+                __syncthreads();
+            }
+        }
         for (int x = tid; x < rows * (D / 4); x += kThreads) {
             const int r = x / (D / 4), e = (x % (D / 4)) * 4;
             float big = -INFINITY;
@@ -669,6 +750,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attend_rows_kernel(const
                         s_m[0][r] = big;
                         s_l[0][r] = sum;
                     }
+                    if constexpr (kOwn) weigh_parts(r, big, sum);
                 }
                 __syncthreads();
                 constexpr int kVecs = kRows * (D / 4) / 32;  // vectors of a lane
@@ -715,6 +797,8 @@ kvl_status launch_rows(const AttendArgs &a, int sms, void *stream)
     if (!allow_smem(attend_rows_kernel<CODE, TYPE, D, NT, PART>, ready, Shape<D, NT>::kSmem)) return KVL_ECUDA;
     // (rings of 256 elements leave room for one CTA an SM)
     const int ctas = sms * (2 * Shape<D, NT>::kSmem <= 220 * 1024 ? kCtasPerSm : 1);
+    if constexpr (PART == Part::own)
+        return launch_behind(attend_rows_kernel<CODE, TYPE, D, NT, PART>, ctas, kThreads, Shape<D, NT>::kSmem, stream, a);
     attend_rows_kernel<CODE, TYPE, D, NT, PART><<<ctas, kThreads, Shape<D, NT>::kSmem, static_cast<cudaStream_t>(stream)>>>(a);
     return launch_status();
 }

@@ -24,10 +24,26 @@ constexpr int kDigits = 2048;  // 11 bits
 constexpr int kRun = 16;       // tokens of a thread in a round
 constexpr int kMostRanks = 8;  // CTAs of a sequence
 
+// n / d for 0 <= n < 2^31 by one product: the quotient of n and 2^(31 + s) / d rounded up, s = ceil(log2(d)).
+struct Divider {
+    uint32_t factor;
+    int32_t shift, d;
+    explicit Divider(int32_t by) : d(by)
+    {
+        int s = 0;
+        while ((int64_t(1) << s) < by) ++s;
+        shift = 31 + s;
+        factor = uint32_t(((uint64_t(1) << shift) + by - 1) / by);
+    }
+    Divider() = default;
+    __device__ __forceinline__ int32_t operator()(int32_t n) const { return int32_t((uint64_t(uint32_t(n)) * factor) >> shift); }
+};
+
 struct EvictArgs {
     kvl_pages p;
     kvl_eviction e;
     kvl_moves m;
+    Divider by_block;
     int32_t n;
     const int32_t *slots;
     void *report;
@@ -68,6 +84,7 @@ __global__ void __launch_bounds__(kThreads) evict_plan_kernel(const __grid_const
     __shared__ long long scan_need[32];
     __shared__ int scan_free[32], s_bad;
     const int tid = threadIdx.x;
+    allow_dependents_launch();
     for (int w = tid; w < (a.p.n_slots + 31) / 32; w += kThreads) named[w] = 0;
     if (tid == 0) s_bad = 0;
     __syncthreads();
@@ -162,6 +179,8 @@ __global__ void __launch_bounds__(kThreads) evict_select_kernel(const __grid_con
     const cooperative_groups::cluster_group cluster = cooperative_groups::this_cluster();
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int ranks = int(cluster.num_blocks()), rank = int(cluster.block_rank()), i = blockIdx.x / ranks;
+    grid_dependency_wait();
+    allow_dependents_launch();
     if (a.m.at[a.n] < 0) return;
     const Ask q = ask_of(a, i);
     if (!q.cut) return;
@@ -275,13 +294,14 @@ __global__ void __launch_bounds__(kThreads) evict_select_kernel(const __grid_con
             const int v = int(ahead >> 32) + int(w >> 16) + __popc(even[y] & below);
             const bool stays = sure[y] >> lane & 1u, equal = even[y] >> lane & 1u;
             if (stays || (equal && v < int(equals))) {
-                const int j = int(token(n, y)), k = s + min(v, int(equals)), at = k / B - q.stay;
+                const int j = int(token(n, y)), k = s + min(v, int(equals)), k_blk = a.by_block(k), at = k_blk - q.stay;
                 if (mass) mass[k] = x[y];
                 if (at >= 0) {
-                    const int32_t page = table[j / B];
+                    const int j_blk = a.by_block(j);
+                    const int32_t page = table[j_blk];
                     const bool there = page >= 0 && page < a.p.pool_blocks;
                     if (!there) report(a.report, KVL_ERANGE, i);
-                    reinterpret_cast<int2 *>(a.m.from)[(first_page + at) * B + k % B] = make_int2(there ? page : -1, j % B);
+                    reinterpret_cast<int2 *>(a.m.from)[(first_page + at) * B + k - k_blk * B] = make_int2(there ? page : -1, j - j_blk * B);
                 }
             }
         }
@@ -320,18 +340,43 @@ struct MoveArgs {
     int64_t max_pages;
     int32_t lanes;   // lanes of a row's slice: a power of two, 16 bytes each
     int32_t slices;  // of a row of H * d bytes
-    int32_t parts;   // of a page's slots, `part` slots each
+    int32_t parts;   // of a page's slots, `part` slots (at most 32) each
     int32_t part;
     void *report;
 };
 
+// round(code * ratio) of four codes, 0 <= ratio <= 1, the product rounded to 32 bits first.
+template <int CODE>
+__device__ __forceinline__ uint32_t turn4(uint32_t w, float ratio)
+{
+    if constexpr (CODE == KVL_CODE_FLOAT) {
+        uint32_t l, g;
+        codes_of<CODE>(w, l, g);
+        const float2 p = __half22float2(*reinterpret_cast<const __half2 *>(&l)), q = __half22float2(*reinterpret_cast<const __half2 *>(&g));
+        return to_codes4<CODE>(p.x * ratio, p.y * ratio, q.x * ratio, q.y * ratio);
+    } else {
+        // A code c is read as the float 2^23 + (c + 128), of which 2^23 + 128 is taken; adding 1.5 * 2^23 rounds the
+        // product to a whole number, which is the sum's lowest byte.  (Products stay within a code's range.)
+        const uint32_t x = w ^ 0x80808080u;
+        uint32_t r[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float c = __uint_as_float(__byte_perm(x, 0x4b000000u, 0x7650 | i)) - 8388736.f;
+            r[i] = __float_as_uint(__fadd_rn(__fmul_rn(c, ratio), 12582912.f));
+        }
+        return __byte_perm(__byte_perm(r[0], r[1], 0x0040), __byte_perm(r[2], r[3], 0x0040), 0x5410);
+    }
+}
+
 // scale' = the largest scale of the pages that a new page's tokens come from, for each head; code' =
 // round(code * (scale / scale')).  The tokens of the largest scale keep their codes bit for bit, so what a further
-// eviction rounds again is what came from smaller ones.  A warp takes a part of a page's slots (whose scales it
-// looks at all the same) and a slice of their rows.
+// eviction rounds again is what came from smaller ones.  A warp takes a part of a page's slots (all of whose scales
+// it looks at) and a slice of their rows; the next unit's sources and this one's codes are on their way while the
+// scales are looked at.
 template <int CODE>
 __global__ void __launch_bounds__(kMoveThreads, kMoveCtasPerSm) move_tokens_kernel(const __grid_constant__ MoveArgs a)
 {
+    grid_dependency_wait();
     int64_t n = *a.m.n;
     if (n < 0 || n > a.max_pages) {
         if (blockIdx.x == 0 && threadIdx.x == 0) report(a.report, KVL_ERANGE, n);
@@ -340,33 +385,67 @@ __global__ void __launch_bounds__(kMoveThreads, kMoveCtasPerSm) move_tokens_kern
     const int64_t N = a.c.pool_blocks, planes = int64_t(a.c.n_layers) * 2;
     const int B = a.c.block_tokens, H = a.c.n_kv_heads, d = a.c.head_dim, row_bytes = H * d;
     const int lane = threadIdx.x & 31, per = 32 / a.lanes, rw = lane / a.lanes, ch = lane % a.lanes;
-    const int64_t per_page = planes * a.slices * a.parts, units = n * per_page;
-    const int64_t step = int64_t(gridDim.x) * (kMoveThreads / 32);
-    for (int64_t u = int64_t(blockIdx.x) * (kMoveThreads / 32) + (threadIdx.x >> 5); u < units; u += step) {
-        const int64_t k = u / per_page;
-        uint32_t rest = uint32_t(u - k * per_page);  // (at most 2^31: checked on the host)
-        const uint32_t lp = rest / uint32_t(a.slices * a.parts);
-        rest -= lp * uint32_t(a.slices * a.parts);
-        const int slice = int(rest / uint32_t(a.parts)), s_first = int(rest - uint32_t(slice) * a.parts) * a.part;
-        const int first = slice * a.lanes * 16, at = first + ch * 16;  // the slice's bytes of a row, and this lane's
+    const uint32_t per_plane = uint32_t(a.slices) * a.parts, per_page = uint32_t(planes) * per_plane;  // (the host has checked)
+    const int64_t units = n * per_page, step = int64_t(gridDim.x) * (kMoveThreads / 32);
+
+    // A unit: part of page k (its fresh page, lane l's source there), plane and slice.
+    struct Unit {
+        int64_t k;
+        uint32_t lp;
+        int slice, s_first, to;
+        int2 from;
+    };
+    auto source = [&](int64_t k, int slot) -> int2 {  // page and slot, a page of -1: none
+        const int2 x = slot < B ? reinterpret_cast<const int2 *>(a.m.from)[k * B + slot] : make_int2(-1, 0);
+        return make_int2(x.x < N && x.y >= 0 && x.y < B ? x.x : -1, x.y);
+    };
+    auto unit_at = [&](int64_t u) {
+        Unit x;
+        x.k = u / per_page;
+        uint32_t rest = uint32_t(u - x.k * per_page);
+        x.lp = rest / per_plane;
+        rest -= x.lp * per_plane;
+        x.slice = int(rest / uint32_t(a.parts));
+        x.s_first = int(rest - uint32_t(x.slice) * a.parts) * a.part;
+        x.to = a.m.to[x.k];
+        x.from = source(x.k, lane < a.part ? x.s_first + lane : B);
+        return x;
+    };
+    int64_t u = int64_t(blockIdx.x) * (kMoveThreads / 32) + (threadIdx.x >> 5);
+    if (u >= units) return;
+    Unit next = unit_at(u);
+    for (; u < units; u += step) {
+        const Unit x = next;
+        if (u + step < units) next = unit_at(u + step);
+        const int first = x.slice * a.lanes * 16, at = first + ch * 16;  // the slice's bytes of a row, and this lane's
         const bool mine = at < row_bytes;
-        const int32_t to = a.m.to[k];
-        if (to < 0 || to >= N) {
-            if (lane == 0) report(a.report, KVL_ERANGE, k);
+        if (x.to < 0 || x.to >= N) {
+            if (lane == 0) report(a.report, KVL_ERANGE, x.k);
             continue;
         }
         const int h = mine ? at / d : 0, ha = first / d, hb = (min(first + a.lanes * 16, row_bytes) - 1) / d;  // heads of the slice
-        const uint8_t *codes = static_cast<const uint8_t *>(a.c.codes) + lp * N * B * row_bytes + (mine ? at : 0);
-        const float *scales = a.c.scales + lp * N * H;
-        const int2 *from = reinterpret_cast<const int2 *>(a.m.from) + k * B;
-        auto source = [&](int slot) -> int2 {  // page and slot, a page of -1: none
-            const int2 x = slot < B ? from[slot] : make_int2(-1, 0);
-            return make_int2(x.x < N && x.y >= 0 && x.y < B ? x.x : -1, x.y);
+        const uint8_t *codes = static_cast<const uint8_t *>(a.c.codes) + x.lp * N * B * row_bytes + (mine ? at : 0);
+        uint8_t *dst = static_cast<uint8_t *>(a.c.codes) + ((int64_t(x.lp) * N + x.to) * B + x.s_first) * row_bytes + (mine ? at : 0);
+        const float *scales = a.c.scales + x.lp * N * H;
+        uint4 w[kHeld];
+        float was[kHeld];
+        auto load = [&](int s0) {  // slots s0 + rw, s0 + per + rw, ... of the part
+#pragma unroll
+            for (int y = 0; y < kHeld; ++y) {
+                const int s = s0 + y * per + rw;
+                const int32_t page = __shfl_sync(0xffffffffu, x.from.x, s & 31), slot = __shfl_sync(0xffffffffu, x.from.y, s & 31);
+                was[y] = -1.f;  // none
+                if (s < a.part && page >= 0 && mine) {
+                    w[y] = *reinterpret_cast<const uint4 *>(codes + (int64_t(page) * B + slot) * row_bytes);
+                    was[y] = scales[int64_t(page) * H + h];
+                }
+            }
         };
+        load(0);
         // lane l looks at the scales of tokens l, l + 32, ... for each head of the slice
         float now = 0.f;
         for (int s = 0; s < B; s += 32) {
-            const int32_t page = source(s + lane).x;
+            const int32_t page = a.parts == 1 ? x.from.x : source(x.k, s + lane).x;
 #pragma unroll 4
             for (int y = ha; y <= hb; ++y) {
                 const float v = page >= 0 ? scales[int64_t(page) * H + y] : 0.f;
@@ -374,40 +453,20 @@ __global__ void __launch_bounds__(kMoveThreads, kMoveCtasPerSm) move_tokens_kern
                 if (y == h) now = fmaxf(now, top);
             }
         }
-        const int s_past = min(B, s_first + a.part);
-        for (int s0 = s_first + rw; s0 - rw < s_past; s0 += per * kHeld) {
-            uint4 w[kHeld];
-            float was[kHeld];
+        for (int s0 = 0; s0 < a.part; s0 += per * kHeld) {
+            if (s0 > 0) load(s0);
 #pragma unroll
             for (int y = 0; y < kHeld; ++y) {
-                const int s = s0 + y * per;
-                const int2 x = s < s_past ? source(s) : make_int2(-1, 0);
-                was[y] = -1.f;  // none
-                if (x.x >= 0 && mine) {
-                    w[y] = *reinterpret_cast<const uint4 *>(codes + (int64_t(x.x) * B + x.y) * row_bytes);
-                    was[y] = scales[int64_t(x.x) * H + h];
-                }
-            }
-#pragma unroll
-            for (int y = 0; y < kHeld; ++y) {
-                const int s = s0 + y * per;
                 if (was[y] == -1.f) continue;
                 if (was[y] != now) {
                     const float ratio = __fdiv_rn(was[y], now);
-                    uint32_t z[4] = {w[y].x, w[y].y, w[y].z, w[y].w};
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        uint32_t l, g;
-                        codes_of<CODE>(z[i], l, g);
-                        const float2 p = __half22float2(*reinterpret_cast<const __half2 *>(&l)), q = __half22float2(*reinterpret_cast<const __half2 *>(&g));
-                        z[i] = to_codes4<CODE>(p.x * ratio, p.y * ratio, q.x * ratio, q.y * ratio);
-                    }
-                    w[y] = make_uint4(z[0], z[1], z[2], z[3]);
+                    w[y] = make_uint4(turn4<CODE>(w[y].x, ratio), turn4<CODE>(w[y].y, ratio), turn4<CODE>(w[y].z, ratio),
+                                      turn4<CODE>(w[y].w, ratio));
                 }
-                *reinterpret_cast<uint4 *>(static_cast<uint8_t *>(a.c.codes) + ((int64_t(lp) * N + to) * B + s) * row_bytes + at) = w[y];
+                *reinterpret_cast<uint4 *>(dst + int64_t(s0 + y * per + rw) * row_bytes) = w[y];
             }
         }
-        if (s_first == 0 && mine && rw == 0 && at % d == 0) a.c.scales[(int64_t(lp) * N + to) * H + h] = now;
+        if (x.s_first == 0 && mine && rw == 0 && at % d == 0) a.c.scales[(int64_t(x.lp) * N + x.to) * H + h] = now;
     }
 }
 
@@ -437,6 +496,7 @@ extern "C" kvl_status kvl_pages_evict(const kvl_pages *pages, int32_t n, const i
     a.p = *pages;
     a.e = *eviction;
     a.m = *moves;
+    a.by_block = Divider(pages->block_tokens);
     a.n = n;
     a.slots = slots;
     a.report = d_report;
@@ -451,17 +511,7 @@ extern "C" kvl_status kvl_pages_evict(const kvl_pages *pages, int32_t n, const i
     const int64_t most = std::min(pages->table_stride * int64_t(pages->block_tokens), pages->pool_blocks * int64_t(pages->block_tokens));
     unsigned ranks = 1;
     while (ranks < kMostRanks && int64_t(ranks) * kThreads * kRun < most) ranks *= 2;
-    cudaLaunchAttribute cluster;
-    cluster.id = cudaLaunchAttributeClusterDimension;
-    cluster.val.clusterDim.x = ranks;
-    cluster.val.clusterDim.y = cluster.val.clusterDim.z = 1;
-    cudaLaunchConfig_t config = {};
-    config.gridDim = dim3(unsigned(n) * ranks);
-    config.blockDim = dim3(kThreads);
-    config.stream = st;
-    config.attrs = &cluster;
-    config.numAttrs = 1;
-    return cudaLaunchKernelEx(&config, evict_select_kernel, a) == cudaSuccess ? launch_status() : (cudaGetLastError(), KVL_ECUDA);
+    return launch_behind(evict_select_kernel, unsigned(n) * ranks, kThreads, 0, stream, a, ranks);
 }
 
 extern "C" kvl_status kvl_tokens_move(const kvl_cache *cache, const kvl_moves *moves, int64_t max_pages,
@@ -482,14 +532,11 @@ extern "C" kvl_status kvl_tokens_move(const kvl_cache *cache, const kvl_moves *m
     a.lanes = 1;
     while (a.lanes < 32 && a.lanes < vectors) a.lanes *= 2;
     a.slices = (vectors + a.lanes - 1) / a.lanes;
-    a.part = 2 * kHeld * (32 / a.lanes);
+    a.part = std::min(2 * kHeld * (32 / a.lanes), 32);
     a.parts = int32_t((int64_t(cache->block_tokens) + a.part - 1) / a.part);
     if (int64_t(cache->n_layers) * 2 * a.slices * a.parts > INT32_MAX) return KVL_EINVAL;
     a.report = d_report;
     const int ctas = sms * kMoveCtasPerSm;
-    if (cache->code_type == KVL_CODE_FLOAT)
-        move_tokens_kernel<KVL_CODE_FLOAT><<<ctas, kMoveThreads, 0, static_cast<cudaStream_t>(stream)>>>(a);
-    else
-        move_tokens_kernel<KVL_CODE_INT><<<ctas, kMoveThreads, 0, static_cast<cudaStream_t>(stream)>>>(a);
-    return launch_status();
+    return launch_behind(cache->code_type == KVL_CODE_FLOAT ? move_tokens_kernel<KVL_CODE_FLOAT> : move_tokens_kernel<KVL_CODE_INT>,
+                         ctas, kMoveThreads, 0, stream, a);
 }

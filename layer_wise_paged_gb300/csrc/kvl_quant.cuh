@@ -122,6 +122,39 @@ inline bool allow_smem(K kernel, std::atomic<unsigned long long> (&ready)[kMaxDe
     return true;
 }
 
+// Launch a kernel that begins with grid_dependency_wait(): its CTAs may be on their way while the kernel before it on
+// the stream runs, if that one allows it, and wait for its end.  ranks: CTAs of a cluster.
+template <typename... P, typename A>
+inline kvl_status launch_behind(void (*kernel)(P...), unsigned grid, unsigned threads, size_t smem, void *stream, const A &args,
+                                unsigned ranks = 1)
+{
+    cudaLaunchAttribute at[2];
+    unsigned n = 0;
+    if (ranks > 1) {
+        at[n].id = cudaLaunchAttributeClusterDimension;
+        at[n].val.clusterDim.x = ranks;
+        at[n].val.clusterDim.y = at[n].val.clusterDim.z = 1;
+        ++n;
+    }
+#if KVL_PDL
+    at[n].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[n].val.programmaticStreamSerializationAllowed = 1;
+    ++n;
+#endif
+    cudaLaunchConfig_t config = {};
+    config.gridDim = dim3(grid);
+    config.blockDim = dim3(threads);
+    config.dynamicSmemBytes = smem;
+    config.stream = static_cast<cudaStream_t>(stream);
+    config.attrs = at;
+    config.numAttrs = n;
+    if (cudaLaunchKernelEx(&config, kernel, args) != cudaSuccess) {
+        cudaGetLastError();
+        return KVL_ECUDA;
+    }
+    return launch_status();
+}
+
 // ---- element types ---------------------------------------------------------------------
 
 // 8 consecutive elements of a row as floats, and back (each rounded once).

@@ -6,10 +6,11 @@
 // weights it adds up in registers; nothing goes back.  A CTA holds 256 tokens (two halves of 128) of one KV head
 // after another as halves in shared memory, and the rows stream past them 128 at a time, already scaled, converted
 // and swizzled by a first kernel, as one bulk copy a step (so a step reads 33 KB for 256 x 128 scores).
-//   warps 0-3, 4-7   weights of half 0, half 1: a thread a token
-//   warps 8-11       read the K codes of the next head from the pages, convert them to halves (exact)
-//   warp 12          issues the products: two of 128 x 128 a step, into two sets of accumulators in turn
-//   warp 13          brings the rows
+//   warps 0-15       weights: a thread a token of half 0 or 1, and every other 32 rows of a step (with 8 warps and
+//                    all rows a thread 263 us for 512 tokens of 32 heads on 31,232: they waited for tensor memory)
+//   warps 16-19      read the K codes of the next head from the pages, convert them to halves (exact)
+//   warp 20          issues the products: two of 128 x 128 a step, into two sets of accumulators in turn
+//   warp 21          brings the rows
 // Work: (entry, 256 tokens) is a job of (KV heads x row chunks that see it) steps; the steps of all jobs in a row
 // are cut into equal contiguous shares, one a CTA.  A job that crosses shares leaves its sums in the workspace, and
 // the CTA that arrives last adds them up in the order of the shares.
@@ -21,7 +22,8 @@
 namespace kvl {
 namespace {
 
-constexpr int kWarps = 14;
+constexpr int kWeighing = 16;                 // warps
+constexpr int kWarps = kWeighing + 6;
 constexpr int kThreads = kWarps * 32;
 constexpr int kTokens = 256;                  // of a job
 constexpr int kJobGroups = kTokens / kGroup;  // 16
@@ -41,7 +43,7 @@ struct Chunk {
     static constexpr int kTileBytes = kHalfBytes + kConstBytes;  // of the workspace: rows, their factors and offsets
 };
 
-enum Bar { K_FULL = 0, K_EMPTY = 2, Q_FULL = 4, Q_EMPTY = 6, S_FULL = 8, S_EMPTY = 10, JOIN = 12, LEAVE = 13, BARS = 14 };
+enum Bar { K_FULL = 0, K_EMPTY = 2, Q_FULL = 4, Q_EMPTY = 6, S_FULL = 8, S_EMPTY = 10, JOIN = 12, SUM_FULL = 13, SUM_EMPTY = 14, LEAVE = 15, BARS = 16 };
 
 // Workspace: [counters of the shares][parts: two a share, 256 sums][row tiles].  Tile of entry i's chunk c: number
 // row0 * G / 128 + i + c, of which no two entries' meet.
@@ -77,6 +79,7 @@ __global__ void __launch_bounds__(256) weigh_rows_prepare_kernel(const __grid_co
 {
     const AttendArgs &t = a.w.t;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    allow_dependents_launch();
     const int H = t.cache.n_kv_heads, G = t.attn.n_heads / H, d = t.cache.head_dim, h = blockIdx.y;
     if (blockIdx.x == 0 && h == 0)
         for (int x = threadIdx.x; x < a.sms; x += 256) a.counters[x] = 0;
@@ -256,11 +259,13 @@ __global__ void __launch_bounds__(kThreads, 1) weigh_chunk_kernel(const __grid_c
     __shared__ uint32_t s_units[kBatch];
     __shared__ __align__(16) float s_consts[kConsts][kRows * 2];
     __shared__ float s_scales[kScales][kJobGroups];
+    __shared__ float s_sum[kTokens];
     __shared__ uint32_t s_off, s_tmem;
     __shared__ int s_entry, s_gone, s_last;
     const WeighArgs &w = args.w;
     const AttendArgs &a = w.t;
     const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
+    grid_dependency_wait();
     const int H = a.cache.n_kv_heads, d = a.cache.head_dim, B = a.cache.block_tokens;
     const int G = a.attn.n_heads / H, per_block = (B + kGroup - 1) / kGroup;
     const int64_t N = a.cache.pool_blocks, plane = int64_t(a.layer) * 2 * N;
@@ -327,14 +332,16 @@ __global__ void __launch_bounds__(kThreads, 1) weigh_chunk_kernel(const __grid_c
             mbar_init(bar + 8 * (Q_EMPTY + x), 1);  // the step's products
             mbar_init(bar + 8 * (S_FULL + x), 2);   // the step's products, and the issuing thread, by which K's scales
                                                     // and the rows' factors reach the weighing warps
-            mbar_init(bar + 8 * (S_EMPTY + x), 8);  // the weighing warps
+            mbar_init(bar + 8 * (S_EMPTY + x), kWeighing);
         }
-        mbar_init(bar + 8 * JOIN, 8);
+        mbar_init(bar + 8 * JOIN, 8);       // the first side's warps
+        mbar_init(bar + 8 * SUM_FULL, 8);   // the second side's sums of a job; the first side has them
+        mbar_init(bar + 8 * SUM_EMPTY, 8);
         mbar_init(bar + 8 * LEAVE, 1);
         fence_mbar_init();
         s_gone = 0;
     }
-    if (warp == 12) {
+    if (warp == kWeighing + 4) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(&s_tmem)) : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
     }
@@ -349,11 +356,11 @@ __global__ void __launch_bounds__(kThreads, 1) weigh_chunk_kernel(const __grid_c
     Walk job;
     job.begin(w, u, cut.start(blockIdx.x + 1), s_entry, s_off, lane);
 
-    if (warp < 8) {
-        // ---- weights: half `half` of the job's tokens, a thread a token
-        const int half = warp >> 2, slot = tid & 255;
-        const uint32_t lanes = tmem + (uint32_t(warp & 3) << 21) + half * 128;
-        uint32_t s = 0, k = 0, joins = 0;  // steps, heads and joins so far
+    if (warp < kWeighing) {
+        // ---- weights: token `slot` of the job, rows 32 (side + 2 i) .. of every step
+        const int half = (warp >> 2) & 1, side = warp >> 3, slot = half * 128 + (warp & 3) * 32 + lane;
+        const uint32_t lanes = tmem + (uint32_t(warp & 3) << 21) + half * 128 + side * 32;
+        uint32_t s = 0, k = 0, joins = 0, sums = 0;  // steps, heads, joins and jobs so far
         bool ok = true;
         do {
             const int pos0 = job.s.e.len - job.s.e.fresh, rows = job.s.e.fresh * G;
@@ -365,8 +372,8 @@ __global__ void __launch_bounds__(kThreads, 1) weigh_chunk_kernel(const __grid_c
             const float *in = w.mass_in + int64_t(sq) * w.in_stride;
             float *out = w.mass_out + int64_t(sq) * w.out_stride;
             // (both on their way during the steps)
-            const float held = !there || (w.begin && j >= pos0) ? 0.f : in[j];
-            const int32_t page = there ? job.s.e.table[blk] : -1;
+            const float held = side || !there || (w.begin && j >= pos0) ? 0.f : in[j];
+            const int32_t page = there && !side ? job.s.e.table[blk] : -1;
             // rows [see_a, see_b) of the entry see the token; a lane without one may see any
             int64_t see_a = 0, see_b = INT64_MAX;
             if (there && a.attn.causal) see_a = max((int64_t(j) - pos0) * G, int64_t(0));
@@ -380,25 +387,24 @@ __global__ void __launch_bounds__(kThreads, 1) weigh_chunk_kernel(const __grid_c
                 tmem_fence_after();
                 const int row_a = (job.ca + c) * kRows, n_rows = min(kRows, rows - row_a);
                 const float ks = s_scales[k % kScales][slot / kGroup];
-                const float *consts = s_consts[s % kConsts];
-                const int from = int(max(see_a - row_a, int64_t(0))), to = int(min(see_b - row_a, int64_t(kRows)));
-                const bool whole = __all_sync(0xffffffffu, from <= 0 && to >= n_rows);
-                uint32_t v[2][32];
+                const float *consts = s_consts[s % kConsts] + side * 64;
+                const int from = int(max(see_a - row_a, int64_t(0))) - 32 * side, to = int(min(see_b - row_a, int64_t(kRows))) - 32 * side;
+                const bool whole = __all_sync(0xffffffffu, from <= -32 * side && to >= n_rows - 32 * side);
                 uint64_t s0 = 0, s1 = 0;
                 const uint64_t kk = pair_of(ks, ks);
-                auto weigh = [&](const uint32_t (&y)[32], int i) {  // columns 32 i ..
+                auto weigh = [&](const uint32_t (&y)[16], int col) {  // 16 of the side's rows, from row `col` on
 #pragma unroll
-                    for (int p = 0; p < 16; p += 2) {
+                    for (int p = 0; p < 8; p += 2) {
                         float2 q[2];
 #pragma unroll
                         for (int z = 0; z < 2; ++z) {
-                            const float4 fb = *reinterpret_cast<const float4 *>(consts + (16 * i + p + z) * 4);
+                            const float4 fb = *reinterpret_cast<const float4 *>(consts + 2 * col + (p + z) * 4);
                             const uint64_t t = mul_pair(pair_of(__uint_as_float(y[2 * (p + z)]), __uint_as_float(y[2 * (p + z) + 1])), kk);
                             q[z] = split_pair(fma_pair(t, pair_of(fb.x, fb.y), pair_of(fb.z, fb.w)));
                             q[z].x = exp2_of(q[z].x);
                             q[z].y = exp2_of(q[z].y);
                             if (!whole) {
-                                const int r = 32 * i + 2 * (p + z);
+                                const int r = col + 2 * (p + z);
                                 if (r < from || r >= to) q[z].x = 0.f;
                                 if (r + 1 < from || r + 1 >= to) q[z].y = 0.f;
                             }
@@ -407,20 +413,26 @@ __global__ void __launch_bounds__(kThreads, 1) weigh_chunk_kernel(const __grid_c
                         s1 = add_pair(s1, pair_of(q[1].x, q[1].y));
                     }
                 };
-                const int parts = (n_rows + 31) / 32;
+                const int parts = (n_rows + 31 - 32 * side) / 64 + ((n_rows + 31 - 32 * side) % 64 >= 32);  // of 32 rows, this side's
                 const uint32_t ts = lanes + set * 256;
-                tmem_ld32(ts, v[0]);
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    if (i >= parts) break;
+                uint32_t v0[16], v1[16];
+                if (parts > 0) {
+                    tmem_ld16(ts, v0);
+                    tmem_ld16(ts + 16, v1);
                     tmem_wait_ld();
-                    if (i + 1 < parts) {
-                        tmem_ld32(ts + 32 * (i + 1), v[(i + 1) & 1]);
-                    } else {
-                        tmem_fence_before();
-                        if (lane == 0) mbar_arrive(bar + 8 * (S_EMPTY + set));
+                    weigh(v0, 0);
+                    if (parts > 1) tmem_ld16(ts + 64, v0);
+                    weigh(v1, 16);
+                    if (parts > 1) {
+                        tmem_ld16(ts + 80, v1);
+                        tmem_wait_ld();
                     }
-                    weigh(v[i & 1], i);
+                }
+                tmem_fence_before();
+                if (lane == 0) mbar_arrive(bar + 8 * (S_EMPTY + set));
+                if (parts > 1) {
+                    weigh(v0, 64);
+                    weigh(v1, 80);
                 }
                 const float2 t = split_pair(add_pair(s0, s1));
                 sum += t.x + t.y;
@@ -428,6 +440,23 @@ __global__ void __launch_bounds__(kThreads, 1) weigh_chunk_kernel(const __grid_c
                 if (c == 0 || x + 1 == job.taken) ++k;
             }
             if (!ok) break;
+            if (side) {
+                if (!(ok = wait(SUM_EMPTY, (sums & 1) ^ 1))) break;
+                s_sum[slot] = sum;
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar + 8 * SUM_FULL);
+                ++sums;
+                // tokens before the first that a row sees
+                if (job.tile == 0 && job.x0 == 0 && in != out) {
+                    const int past = token_of(job.s, 0, B, per_block);
+                    for (int y = slot; y < past; y += 256) out[y] = in[y];
+                }
+                continue;
+            }
+            if (!(ok = wait(SUM_FULL, sums++ & 1))) break;
+            sum += s_sum[slot];
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar + 8 * SUM_EMPTY);
             const bool seen = page >= 0 && page < N;
             if (there && !seen && slot % kGroup == 0) report(a.report, KVL_ERANGE, job.entry);
             if (job.complete(w)) {
@@ -453,17 +482,12 @@ __global__ void __launch_bounds__(kThreads, 1) weigh_chunk_kernel(const __grid_c
                     if (there) out[j] = seen ? held + all : held;
                 }
             }
-            // tokens before the first that a row sees
-            if (job.tile == 0 && job.x0 == 0 && in != out) {
-                const int past = token_of(job.s, 0, B, per_block);
-                for (int y = slot; y < past; y += 256) out[y] = in[y];
-            }
         } while (job.next(w));
-    } else if (warp < 12) {
-        // ---- convert K: warp cw's four groups of each half tile are 64 tokens, two batches of two groups
-        const int cw = warp - 8;
+    } else if (warp < kWeighing + 4) {
+        // ---- convert K: warp cw's four groups of the tile, two on their way while another is converted
+        const int cw = warp - kWeighing;
         const uint8_t *codes = static_cast<const uint8_t *>(a.cache.codes);
-        constexpr int kPer = 512 / D, kVecs = 32 / kPer;  // rows of a warp's vector, vectors of its 32 slots
+        constexpr int kPer = 512 / D, kVecs = kGroup / kPer;  // rows of a warp's vector, vectors of a group
         // 8 lanes of a shared-memory phase write 4 chunks of an even and of an odd row: with the swizzle, 8
         // different 16-byte columns
         const int ch = (lane & 3) | (D == 128 ? (lane >> 4) << 2 : 0), rw = D == 128 ? (lane >> 2) & 3 : lane >> 2;
@@ -484,29 +508,21 @@ __global__ void __launch_bounds__(kThreads, 1) weigh_chunk_kernel(const __grid_c
             }
             const int ha = job.x0 / job.n, hb = (job.x0 + job.taken - 1) / job.n;
             uint4 reg[2][kVecs];
-            const uint8_t *src[2][2];
-            int valid[2][2];
-#pragma unroll
-            for (int b = 0; b < 2; ++b)
-#pragma unroll
-                for (int y = 0; y < 2; ++y) {
-                    const int l = 2 * b + y;
-                    const int32_t pg = __shfl_sync(0xffffffffu, page, l), tt = __shfl_sync(0xffffffffu, t0, l);
-                    valid[b][y] = ch * 16 < d ? __shfl_sync(0xffffffffu, nv, l) : (__shfl_sync(0xffffffffu, nv, l), 0);
-                    src[b][y] = codes + ((plane + max(pg, 0)) * B + tt % B) * H * d + ch * 16;
-                }
-            auto fetch = [&](int b, int h) {
+            auto fetch = [&](uint4 (&r)[kVecs], int l, int h) {  // group l of head h
+                const int32_t pg = __shfl_sync(0xffffffffu, page, l), tt = __shfl_sync(0xffffffffu, t0, l);
+                int valid = __shfl_sync(0xffffffffu, nv, l);
+                if (ch * 16 >= d) valid = 0;
+                const uint8_t *src = codes + (((plane + max(pg, 0)) * B + tt % B) * H + h) * d + ch * 16;
 #pragma unroll
                 for (int x = 0; x < kVecs; ++x) {
-                    const int r = (x % (kVecs / 2)) * kPer + rw, y = x / (kVecs / 2);
-                    reg[b][x] = make_uint4(0, 0, 0, 0);
-                    if (r < valid[b][y]) reg[b][x] = __ldg(reinterpret_cast<const uint4 *>(src[b][y] + (int64_t(r) * H + h) * d));
+                    r[x] = make_uint4(0, 0, 0, 0);
+                    if (x * kPer + rw < valid) r[x] = __ldg(reinterpret_cast<const uint4 *>(src + int64_t(x * kPer + rw) * H * d));
                 }
             };
             auto scale = [&](int h) { return page >= 0 ? __ldg(a.cache.scales + (plane + page) * H + h) : 0.f; };
             float sc = scale(ha);
-            fetch(0, ha);
-            fetch(1, ha);
+            fetch(reg[0], 0, ha);
+            fetch(reg[1], 1, ha);
             for (int h = ha; h <= hb; ++h, ++k) {
                 const uint32_t st = k & 1;
                 ok = wait(K_EMPTY + st, ((k >> 1) & 1) ^ 1);
@@ -515,29 +531,29 @@ __global__ void __launch_bounds__(kThreads, 1) weigh_chunk_kernel(const __grid_c
                 if (h < hb) sc = scale(h + 1);
                 uint8_t *dst = smem + C::kK + (st * 2 + (cw >> 1)) * C::kHalfBytes;
 #pragma unroll
-                for (int b = 0; b < 2; ++b) {
+                for (int l = 0; l < 4; ++l) {
+                    uint4 (&z)[kVecs] = reg[l & 1];
 #pragma unroll
                     for (int x = 0; x < kVecs; ++x) {
-                        const int r = (cw & 1) * 64 + b * 32 + x * kPer + rw;
-                        const uint32_t z[4] = {reg[b][x].x, reg[b][x].y, reg[b][x].z, reg[b][x].w};
+                        const int r = (cw & 1) * 64 + l * kGroup + x * kPer + rw;
                         uint4 lo, hi;
-                        codes_of<CODE>(z[0], lo.x, lo.y);
-                        codes_of<CODE>(z[1], lo.z, lo.w);
-                        codes_of<CODE>(z[2], hi.x, hi.y);
-                        codes_of<CODE>(z[3], hi.z, hi.w);
+                        codes_of<CODE>(z[x].x, lo.x, lo.y);
+                        codes_of<CODE>(z[x].y, lo.z, lo.w);
+                        codes_of<CODE>(z[x].z, hi.x, hi.y);
+                        codes_of<CODE>(z[x].w, hi.z, hi.w);
                         uint8_t *p = dst + (ch >> 2) * (128 * 128) + r * 128;
                         const int un = (ch & 3) * 2;
                         *reinterpret_cast<uint4 *>(p + ((un ^ (r & 7)) << 4)) = lo;
                         *reinterpret_cast<uint4 *>(p + (((un + 1) ^ (r & 7)) << 4)) = hi;
                     }
-                    if (h < hb) fetch(b, h + 1);
+                    if (l < 2 || h < hb) fetch(z, (l + 2) & 3, l < 2 ? h : h + 1);
                 }
                 fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(bar + 8 * (K_FULL + st));
             }
         } while (ok && job.next(w));
-    } else if (warp == 12) {
+    } else if (warp == kWeighing + 4) {
         // ---- products
         uint32_t s = 0, k = 0;
         bool ok = true;
@@ -608,7 +624,7 @@ __global__ void __launch_bounds__(kThreads, 1) weigh_chunk_kernel(const __grid_c
     }
     __syncthreads();
     if (*gone && tid == 0) report(a.report, KVL_ETIMEOUT, blockIdx.x);
-    if (warp == 12) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
+    if (warp == kWeighing + 4) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
 }
 
 template <int CODE, int TYPE, int D>
@@ -619,8 +635,7 @@ kvl_status launch_chunk(const ChunkArgs &a, int64_t tiles, void *stream)
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     weigh_rows_prepare_kernel<TYPE, D><<<dim3(unsigned(tiles), unsigned(a.w.t.cache.n_kv_heads)), 256, 0, st>>>(a);
     if (launch_status()) return KVL_ECUDA;
-    weigh_chunk_kernel<CODE, D><<<a.sms, kThreads, Chunk<D>::kSmem, st>>>(a);
-    return launch_status();
+    return launch_behind(weigh_chunk_kernel<CODE, D>, a.sms, kThreads, Chunk<D>::kSmem, stream, a);
 }
 
 template <int CODE, int TYPE>

@@ -86,10 +86,11 @@ def test_attend_shared_refusals(lib):
     assert attend_shared(lib, ws=None) == kvl.KVL_EINVAL and attend_shared(lib, ws_bytes=100) == kvl.KVL_EINVAL
     assert attend_shared(lib, parts=None) == kvl.KVL_EINVAL and attend_shared(lib, parts=FAKE + 8) == kvl.KVL_EALIGN
     assert attend_shared(lib, rep=FAKE + 8) == kvl.KVL_EALIGN
-    n = lib.kvl_attend_shared_parts_bytes(cache(), 5, 8)
+    n = lib.kvl_attend_shared_parts_bytes(cache(), 2, 1, 5, 8)
     assert n >= 5 * 8 * 130 * 4
     assert attend_shared(lib, parts_bytes=n - 1) == kvl.KVL_EINVAL
-    for bad in ((cache(head_dim=0), 5, 8), (cache(), -1, 8), (cache(), 5, 0), (cache(), 1 << 31, 8)):
+    for bad in ((cache(head_dim=0), 2, 1, 5, 8), (cache(), 2, 1, -1, 8), (cache(), 2, 1, 5, 0), (cache(), 2, 1, 1 << 31, 8),
+                (cache(), 2, -1, 5, 8), (cache(), -1, 1, 5, 8), (cache(), 2, 1, 5, 6)):
         assert lib.kvl_attend_shared_parts_bytes(*bad) == 0
     for nothing in (dict(n_rows=0), dict(n_seq=0)):
         assert attend_shared(lib, s=seqs(**nothing), parts=None, ws=None) == kvl.KVL_OK
