@@ -60,7 +60,10 @@ struct Prefix {
     static constexpr int kSmem = kRing + kUnits * kUnitBytes + 1024;
 };
 
-enum Bar { K_FULL = 0, K_EMPTY = 2, V_FULL = 4, V_EMPTY = 6, S_FULL = 8, P_FULL = 10, PV_DONE = 11, Q_FULL = 12, LEAVE = 13, BARS = 14 };
+// P_FULL and PV_DONE come in pairs, for even and odd steps, as a softmax warp may be a step ahead of the products: its
+// weights of step k + 1 may be there before the products have looked for those of step k.  Of one barrier two phases
+// would have passed then, and a wait for the first would never end (or, for PV_DONE, end too early).
+enum Bar { K_FULL = 0, K_EMPTY = 2, V_FULL = 4, V_EMPTY = 6, S_FULL = 8, P_FULL = 10, PV_DONE = 12, Q_FULL = 14, LEAVE = 15, BARS = 16 };
 
 // A group as a batch of jobs.
 struct Shared {
@@ -210,8 +213,10 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prefix_kernel(const __grid
             mbar_init(bar + 8 * (V_EMPTY + x), 1);
             mbar_init(bar + 8 * (S_FULL + x), 2);   // S^T, and the issuing thread, by which places and factors reach the softmax
         }
-        mbar_init(bar + 8 * P_FULL, kSoftmax);
-        mbar_init(bar + 8 * PV_DONE, 1);
+        for (int x = 0; x < 2; ++x) {
+            mbar_init(bar + 8 * (P_FULL + x), kSoftmax);
+            mbar_init(bar + 8 * (PV_DONE + x), 1);
+        }
         mbar_init(bar + 8 * Q_FULL, 4);
         mbar_init(bar + 8 * LEAVE, 1);
         fence_mbar_init();
@@ -316,7 +321,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prefix_kernel(const __grid
                         meet();
                         if (quarter == 0) fm[at] = -now;
                         if (s > 0) {
-                            wait(PV_DONE, (k - 1) & 1);
+                            wait(PV_DONE + (set ^ 1), ((k - 1) >> 1) & 1);
                             tmem_fence_after();
                             tmem_ld32(to, v);
                             tmem_wait_ld();
@@ -352,7 +357,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prefix_kernel(const __grid
                 fence_proxy_async_smem();
                 tmem_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(bar + 8 * P_FULL);
+                if (lane == 0) mbar_arrive(bar + 8 * (P_FULL + set));
             }
             // ---- this share's part: rows' references and sums, then O
             const int rows = min(ROWS, job.s.e.fresh * G - job.tile * ROWS);
@@ -376,7 +381,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prefix_kernel(const __grid
                 }
                 meet();
             }
-            wait(PV_DONE, (it + job.n - 1) & 1);
+            wait(PV_DONE + ((it + job.n - 1) & 1), ((it + job.n - 1) >> 1) & 1);
             tmem_fence_after();
 #pragma unroll
             for (int p = 0; p < kPasses; ++p) {
@@ -601,7 +606,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prefix_kernel(const __grid
                 const uint32_t k = it + s;
                 if (s + 1 < job.n) scores(k + 1);  // (its accumulators: the softmax has passed on the weights of k - 1)
                 wait(V_FULL + k % kVStages, (k / kVStages) & 1);
-                wait(P_FULL, k & 1);
+                wait(P_FULL + (k & 1), (k >> 1) & 1);
                 tmem_fence_after();
                 uint64_t vd = matrix_desc(sm + C::kV + (k % kVStages) * C::kVBytes, kSlots * 128, 1024);
                 uint64_t pd = matrix_desc(sm + C::kK + (k % kKStages) * C::kKBytes, kSlots * 128, 1024);
@@ -611,7 +616,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prefix_kernel(const __grid
                     vd += 2048 >> 4;
                     pd += 2048 >> 4;
                 }
-                mma_commit(one, bar + 8 * PV_DONE);
+                mma_commit(one, bar + 8 * (PV_DONE + (k & 1)));
                 mma_commit(one, bar + 8 * (V_EMPTY + k % kVStages));
                 mma_commit(one, bar + 8 * (K_EMPTY + k % kKStages));
             }

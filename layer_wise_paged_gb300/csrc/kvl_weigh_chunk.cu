@@ -6,8 +6,8 @@
 // weights it adds up in registers; nothing goes back.  A CTA holds 256 tokens (two halves of 128) of one KV head
 // after another as halves in shared memory, and the rows stream past them 128 at a time, already scaled, converted
 // and swizzled by a first kernel, as one bulk copy a step (so a step reads 33 KB for 256 x 128 scores).
-//   warps 0-15       weights: a thread a token of half 0 or 1, and every other 32 rows of a step (with 8 warps and
-//                    all rows a thread 263 us for 512 tokens of 32 heads on 31,232: they waited for tensor memory)
+//   warps 0-15       weights: a thread a token of each half and a quarter of a step's rows, so that what is read of a row
+//                    from shared memory, which the products keep busy half of the time, serves two tokens
 //   warps 16-19      read the K codes of the next head from the pages, convert them to halves (exact)
 //   warp 20          issues the products: two of 128 x 128 a step, into two sets of accumulators in turn
 //   warp 21          brings the rows
@@ -31,7 +31,7 @@ constexpr int kRows = 128;                    // of a step
 constexpr int kScales = 4;                    // heads whose scales are kept: the weights of a step may be two heads
                                               // behind the conversion, which is one ahead of its own
 constexpr int kConsts = 4;                    // steps whose rows' factors are kept, likewise
-constexpr int kConstBytes = kRows * 8;
+constexpr int kConstBytes = kRows * 4 + 16;
 constexpr int kBatch = 512;                   // entries whose steps are held at a time
 
 template <int D>
@@ -45,7 +45,8 @@ struct Chunk {
 
 enum Bar { K_FULL = 0, K_EMPTY = 2, Q_FULL = 4, Q_EMPTY = 6, S_FULL = 8, S_EMPTY = 10, JOIN = 12, SUM_FULL = 13, SUM_EMPTY = 14, LEAVE = 15, BARS = 16 };
 
-// Workspace: [counters of the shares][parts: two a share, 256 sums][row tiles].  Tile of entry i's chunk c: number
+// Workspace: [counters of the shares][parts: two a share, 256 sums][row tiles: rows, their
+// offsets, their factor].  Tile of entry i's chunk c: number
 // row0 * G / 128 + i + c, of which no two entries' meet.
 __host__ __device__ constexpr size_t counter_bytes(int sms) { return size_t(sms) * 4 + 255 & ~size_t(255); }
 __host__ __device__ constexpr size_t part_bytes(int sms) { return size_t(sms) * 2 * kTokens * 4; }
@@ -58,7 +59,8 @@ struct ChunkArgs {
     int32_t sms;
 };
 
-// ---- rows: scaled by a power of two into the range of a half, in the layout the products read -----------------
+// ---- rows: as halves, in the layout the products read.  A tile's rows are scaled by one power of two, which takes
+// their largest element into [2^14, 2^15): one factor for all.  What is lost is below 2^-39 of that element. ------------
 
 __device__ __forceinline__ int find_entry_of_tile(const kvl_sequences &s, int G, int64_t id, int lane)
 {
@@ -90,25 +92,42 @@ __global__ void __launch_bounds__(256) weigh_rows_prepare_kernel(const __grid_co
     uint8_t *tile = a.tiles + (int64_t(blockIdx.x) * H + h) * Chunk<D>::kTileBytes;
     float *consts = reinterpret_cast<float *>(tile + Chunk<D>::kHalfBytes);
     constexpr int kLanes = D / 8, kPer = 32 / kLanes;  // lanes of a row, rows of a warp's vector
+    constexpr int kTurns = kRows / (8 * kPer);
+    __shared__ float s_most[8];
     const int at = (lane % kLanes) * 8;
-#pragma unroll 4
-    for (int x = 0; x < kRows / (8 * kPer); ++x) {
+    uint4 raw[kTurns];
+    float amax = 0.f;  // of finite elements
+#pragma unroll
+    for (int x = 0; x < kTurns; ++x) {
+        const int64_t row = chunk * kRows + (warp + 8 * x) * kPer + lane / kLanes;
+        raw[x] = make_uint4(0, 0, 0, 0);
+        if (row < rows && at < d) {
+            const int tok = int(row / G), head = h * G + int(row - int64_t(tok) * G);
+            raw[x] = *reinterpret_cast<const uint4 *>(static_cast<const uint8_t *>(t.attn.q.data) +
+                                                      (int64_t(e.row0) + tok) * t.attn.q.row_stride + int64_t(head) * t.attn.q.head_stride + 2 * at);
+        }
+    }
+#pragma unroll
+    for (int x = 0; x < kTurns; ++x) {
+        float v[8];
+        load8<TYPE>(reinterpret_cast<const uint8_t *>(&raw[x]), v);
+#pragma unroll
+        for (int y = 0; y < 8; ++y) amax = fmaxf(amax, isfinite(v[y]) ? fabsf(v[y]) : 0.f);
+    }
+#pragma unroll
+    for (int o = 16; o; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+    if (lane == 0) s_most[warp] = amax;
+    __syncthreads();
+#pragma unroll
+    for (int x = 0; x < 8; ++x) amax = fmaxf(amax, s_most[x]);
+    // 2^e <= amax < 2^(e + 1), e held to what leaves both factors normal
+    const int ex = max(-100, int(__float_as_uint(amax) >> 23) - 127);
+    const float up = __uint_as_float(uint32_t(14 - ex + 127) << 23), down = __uint_as_float(uint32_t(ex - 14 + 127) << 23);
+#pragma unroll
+    for (int x = 0; x < kTurns; ++x) {
         const int r = (warp + 8 * x) * kPer + lane / kLanes;
-        const int64_t row = chunk * kRows + r;
-        const bool ok = row < rows;
-        const int tok = ok ? int(row / G) : 0, head = h * G + (ok ? int(row - int64_t(tok) * G) : 0);
-        float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-        if (ok && at < d)
-            load8<TYPE>(static_cast<const uint8_t *>(t.attn.q.data) + (int64_t(e.row0) + tok) * t.attn.q.row_stride +
-                            int64_t(head) * t.attn.q.head_stride + 2 * at, v);
-        float amax = 0.f;
-#pragma unroll
-        for (int y = 0; y < 8; ++y) amax = fmaxf(amax, fabsf(v[y]));
-#pragma unroll
-        for (int o = kLanes / 2; o; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-        const uint32_t ex = (__float_as_uint(amax) >> 23) & 0xffu;
-        const bool plain = ex < 2 || ex > 252;
-        const float up = plain ? 1.f : __uint_as_float((254u - ex) << 23), down = plain ? 1.f : __uint_as_float(ex << 23);
+        float v[8];
+        load8<TYPE>(reinterpret_cast<const uint8_t *>(&raw[x]), v);
         uint4 p;
         p.x = pack2<KVL_TYPE_HALF>(v[0] * up, v[1] * up);
         p.y = pack2<KVL_TYPE_HALF>(v[2] * up, v[3] * up);
@@ -116,13 +135,18 @@ __global__ void __launch_bounds__(256) weigh_rows_prepare_kernel(const __grid_co
         p.w = pack2<KVL_TYPE_HALF>(v[6] * up, v[7] * up);
         const int unit = at / 8;
         *reinterpret_cast<uint4 *>(tile + (unit >> 3) * (kRows * 128) + r * 128 + (((unit & 7) ^ (r & 7)) << 4)) = p;
-        if (at == 0) {
-            // pairs of rows: two factors, two offsets; a row that is not there, or whose lse is infinite, gives nothing
-            const float z = ok ? a.w.lse[(int64_t(e.row0) + tok) * t.attn.n_heads + head] : INFINITY;
-            consts[(r >> 1) * 4 + (r & 1)] = t.attn.sm_scale * kLog2e * down;
-            consts[(r >> 1) * 4 + 2 + (r & 1)] = isinf(z) ? -INFINITY : -z * kLog2e;
-        }
     }
+    if (threadIdx.x < kRows) {
+        // a row that is not there, or whose lse is infinite, gives nothing: an offset of -infinity
+        const int64_t row = chunk * kRows + threadIdx.x;
+        float z = INFINITY;
+        if (row < rows) {
+            const int tok = int(row / G), head = h * G + int(row - int64_t(tok) * G);
+            z = a.w.lse[(int64_t(e.row0) + tok) * t.attn.n_heads + head];
+        }
+        consts[threadIdx.x] = isinf(z) ? -INFINITY : -z * kLog2e;
+    }
+    if (threadIdx.x == 0) consts[kRows] = t.attn.sm_scale * kLog2e * down;
 }
 
 // ---- work ---------------------------------------------------------------------------------------------------
@@ -257,9 +281,9 @@ __global__ void __launch_bounds__(kThreads, 1) weigh_chunk_kernel(const __grid_c
     extern __shared__ uint8_t smem_raw[];
     __shared__ __align__(8) unsigned long long bars[BARS];
     __shared__ uint32_t s_units[kBatch];
-    __shared__ __align__(16) float s_consts[kConsts][kRows * 2];
+    __shared__ __align__(16) float s_consts[kConsts][kConstBytes / 4];
     __shared__ float s_scales[kScales][kJobGroups];
-    __shared__ float s_sum[kTokens];
+    __shared__ float s_sum[3][kTokens];
     __shared__ uint32_t s_off, s_tmem;
     __shared__ int s_entry, s_gone, s_last;
     const WeighArgs &w = args.w;
@@ -334,9 +358,9 @@ __global__ void __launch_bounds__(kThreads, 1) weigh_chunk_kernel(const __grid_c
                                                     // and the rows' factors reach the weighing warps
             mbar_init(bar + 8 * (S_EMPTY + x), kWeighing);
         }
-        mbar_init(bar + 8 * JOIN, 8);       // the first side's warps
-        mbar_init(bar + 8 * SUM_FULL, 8);   // the second side's sums of a job; the first side has them
-        mbar_init(bar + 8 * SUM_EMPTY, 8);
+        mbar_init(bar + 8 * JOIN, 4);        // the first side's warps
+        mbar_init(bar + 8 * SUM_FULL, 12);   // the other sides' sums of a job; the first side has them
+        mbar_init(bar + 8 * SUM_EMPTY, 4);
         mbar_init(bar + 8 * LEAVE, 1);
         fence_mbar_init();
         s_gone = 0;
@@ -357,130 +381,156 @@ __global__ void __launch_bounds__(kThreads, 1) weigh_chunk_kernel(const __grid_c
     job.begin(w, u, cut.start(blockIdx.x + 1), s_entry, s_off, lane);
 
     if (warp < kWeighing) {
-        // ---- weights: token `slot` of the job, rows 32 (side + 2 i) .. of every step
-        const int half = (warp >> 2) & 1, side = warp >> 3, slot = half * 128 + (warp & 3) * 32 + lane;
-        const uint32_t lanes = tmem + (uint32_t(warp & 3) << 21) + half * 128 + side * 32;
+        // ---- weights: tokens slot and slot + 128 of the job, rows 32 side .. of every step
+        const int side = warp >> 2, slot = (warp & 3) * 32 + lane;
+        const uint32_t lanes = tmem + (uint32_t(warp & 3) << 21) + side * 32;
         uint32_t s = 0, k = 0, joins = 0, sums = 0;  // steps, heads, joins and jobs so far
         bool ok = true;
         do {
             const int pos0 = job.s.e.len - job.s.e.fresh, rows = job.s.e.fresh * G;
-            const int g = job.tile * kJobGroups + slot / kGroup;
-            const int blk = (job.s.g0 + g) / per_block, at = (job.s.g0 + g - blk * per_block) * kGroup + slot % kGroup;
-            const int j = blk * B + at;
-            const bool there = g < job.s.groups && at < B && j < job.s.e.len;
             const int sq = a.seqs.slots ? a.seqs.slots[job.entry] : job.entry;
             const float *in = w.mass_in + int64_t(sq) * w.in_stride;
             float *out = w.mass_out + int64_t(sq) * w.out_stride;
-            // (both on their way during the steps)
-            const float held = side || !there || (w.begin && j >= pos0) ? 0.f : in[j];
-            const int32_t page = there && !side ? job.s.e.table[blk] : -1;
+            int token[2];  // -1: none
+            float held[2], sum[2] = {0.f, 0.f};
+            int32_t page[2];
             // rows [see_a, see_b) of the entry see the token; a lane without one may see any
-            int64_t see_a = 0, see_b = INT64_MAX;
-            if (there && a.attn.causal) see_a = max((int64_t(j) - pos0) * G, int64_t(0));
-            if (there && a.attn.window > 0) see_b = (int64_t(j) + a.attn.window - pos0) * G;
-            float sum = 0.f;
+            int64_t see_a[2], see_b[2];
+#pragma unroll
+            for (int y = 0; y < 2; ++y) {
+                const int g = job.tile * kJobGroups + (slot + 128 * y) / kGroup;
+                const int blk = (job.s.g0 + g) / per_block, at = (job.s.g0 + g - blk * per_block) * kGroup + slot % kGroup;
+                const int j = blk * B + at;
+                const bool there = g < job.s.groups && at < B && j < job.s.e.len;
+                token[y] = there ? j : -1;
+                // (both on their way during the steps)
+                held[y] = side || !there || (w.begin && j >= pos0) ? 0.f : in[j];
+                page[y] = there && !side ? job.s.e.table[blk] : -1;
+                see_a[y] = there && a.attn.causal ? max((int64_t(j) - pos0) * G, int64_t(0)) : 0;
+                see_b[y] = there && a.attn.window > 0 ? (int64_t(j) + a.attn.window - pos0) * G : INT64_MAX;
+            }
             int c = job.x0 % job.n;
             for (int x = 0; x < job.taken; ++x, ++s) {
                 const uint32_t set = s & 1, ph = (s >> 1) & 1;
                 ok = wait(S_FULL + set, ph);
                 if (!ok) break;
                 tmem_fence_after();
-                const int row_a = (job.ca + c) * kRows, n_rows = min(kRows, rows - row_a);
-                const float ks = s_scales[k % kScales][slot / kGroup];
-                const float *consts = s_consts[s % kConsts] + side * 64;
-                const int from = int(max(see_a - row_a, int64_t(0))) - 32 * side, to = int(min(see_b - row_a, int64_t(kRows))) - 32 * side;
-                const bool whole = __all_sync(0xffffffffu, from <= -32 * side && to >= n_rows - 32 * side);
-                uint64_t s0 = 0, s1 = 0;
-                const uint64_t kk = pair_of(ks, ks);
-                auto weigh = [&](const uint32_t (&y)[16], int col) {  // 16 of the side's rows, from row `col` on
-#pragma unroll
-                    for (int p = 0; p < 8; p += 2) {
-                        float2 q[2];
-#pragma unroll
-                        for (int z = 0; z < 2; ++z) {
-                            const float4 fb = *reinterpret_cast<const float4 *>(consts + 2 * col + (p + z) * 4);
-                            const uint64_t t = mul_pair(pair_of(__uint_as_float(y[2 * (p + z)]), __uint_as_float(y[2 * (p + z) + 1])), kk);
-                            q[z] = split_pair(fma_pair(t, pair_of(fb.x, fb.y), pair_of(fb.z, fb.w)));
-                            q[z].x = exp2_of(q[z].x);
-                            q[z].y = exp2_of(q[z].y);
-                            if (!whole) {
-                                const int r = col + 2 * (p + z);
-                                if (r < from || r >= to) q[z].x = 0.f;
-                                if (r + 1 < from || r + 1 >= to) q[z].y = 0.f;
-                            }
-                        }
-                        s0 = add_pair(s0, pair_of(q[0].x, q[0].y));
-                        s1 = add_pair(s1, pair_of(q[1].x, q[1].y));
-                    }
-                };
-                const int parts = (n_rows + 31 - 32 * side) / 64 + ((n_rows + 31 - 32 * side) % 64 >= 32);  // of 32 rows, this side's
+                const int row_a = (job.ca + c) * kRows + 32 * side, n_rows = min(32, rows - row_a);
+                const float *consts = s_consts[s % kConsts] + side * 32;
                 const uint32_t ts = lanes + set * 256;
-                uint32_t v0[16], v1[16];
-                if (parts > 0) {
-                    tmem_ld16(ts, v0);
-                    tmem_ld16(ts + 16, v1);
-                    tmem_wait_ld();
-                    weigh(v0, 0);
-                    if (parts > 1) tmem_ld16(ts + 64, v0);
-                    weigh(v1, 16);
-                    if (parts > 1) {
-                        tmem_ld16(ts + 80, v1);
-                        tmem_wait_ld();
+                if (n_rows > 0) {
+                    const float f = consts[kRows - side * 32];
+                    float kf[2];
+                    int from[2], to[2];
+                    bool whole = true;
+#pragma unroll
+                    for (int y = 0; y < 2; ++y) {
+                        kf[y] = s_scales[k % kScales][(slot + 128 * y) / kGroup] * f;
+                        from[y] = int(max(see_a[y] - row_a, int64_t(0)));
+                        to[y] = int(min(see_b[y] - row_a, int64_t(kRows)));
+                        whole = whole && from[y] == 0 && to[y] >= n_rows;
                     }
+                    whole = __all_sync(0xffffffffu, whole);
+                    uint64_t add[2][2] = {{0, 0}, {0, 0}};
+                    auto weigh = [&](const uint32_t (&v)[2][16], int col) {  // 16 rows from row `col` on
+                        const uint64_t k0 = pair_of(kf[0], kf[0]), k1 = pair_of(kf[1], kf[1]);
+#pragma unroll
+                        for (int p = 0; p < 4; ++p) {
+                            const float4 b = *reinterpret_cast<const float4 *>(consts + col + 4 * p);
+#pragma unroll
+                            for (int y = 0; y < 2; ++y)
+#pragma unroll
+                                for (int z = 0; z < 2; ++z) {
+                                    const int i = 4 * p + 2 * z;
+                                    float2 q = split_pair(fma_pair(pair_of(__uint_as_float(v[y][i]), __uint_as_float(v[y][i + 1])), y ? k1 : k0,
+                                                                   z ? pair_of(b.z, b.w) : pair_of(b.x, b.y)));
+                                    q.x = exp2_of(q.x);
+                                    q.y = exp2_of(q.y);
+                                    if (!whole) {
+                                        if (col + i < from[y] || col + i >= to[y]) q.x = 0.f;
+                                        if (col + i + 1 < from[y] || col + i + 1 >= to[y]) q.y = 0.f;
+                                    }
+                                    add[y][z] = add_pair(add[y][z], pair_of(q.x, q.y));
+                                }
+                        }
+                    };
+                    uint32_t v[2][16];
+                    tmem_ld16(ts, v[0]);
+                    tmem_ld16(ts + 128, v[1]);
+                    tmem_wait_ld();
+                    weigh(v, 0);
+                    tmem_ld16(ts + 16, v[0]);
+                    tmem_ld16(ts + 144, v[1]);
+                    tmem_wait_ld();
+                    tmem_fence_before();
+                    if (lane == 0) mbar_arrive(bar + 8 * (S_EMPTY + set));
+                    weigh(v, 16);
+#pragma unroll
+                    for (int y = 0; y < 2; ++y) {
+                        const float2 t = split_pair(add_pair(add[y][0], add[y][1]));
+                        sum[y] += t.x + t.y;
+                    }
+                } else if (lane == 0) {
+                    mbar_arrive(bar + 8 * (S_EMPTY + set));
                 }
-                tmem_fence_before();
-                if (lane == 0) mbar_arrive(bar + 8 * (S_EMPTY + set));
-                if (parts > 1) {
-                    weigh(v0, 64);
-                    weigh(v1, 80);
-                }
-                const float2 t = split_pair(add_pair(s0, s1));
-                sum += t.x + t.y;
                 if (++c == job.n) c = 0;
                 if (c == 0 || x + 1 == job.taken) ++k;
             }
             if (!ok) break;
             if (side) {
                 if (!(ok = wait(SUM_EMPTY, (sums & 1) ^ 1))) break;
-                s_sum[slot] = sum;
+                s_sum[side - 1][slot] = sum[0];
+                s_sum[side - 1][slot + 128] = sum[1];
                 __syncwarp();
                 if (lane == 0) mbar_arrive(bar + 8 * SUM_FULL);
                 ++sums;
                 // tokens before the first that a row sees
                 if (job.tile == 0 && job.x0 == 0 && in != out) {
                     const int past = token_of(job.s, 0, B, per_block);
-                    for (int y = slot; y < past; y += 256) out[y] = in[y];
+                    for (int y = slot + 128 * (side - 1); y < past; y += 384) out[y] = in[y];
                 }
                 continue;
             }
             if (!(ok = wait(SUM_FULL, sums++ & 1))) break;
-            sum += s_sum[slot];
+#pragma unroll
+            for (int y = 0; y < 2; ++y)
+#pragma unroll
+                for (int z = 0; z < 3; ++z) sum[y] += s_sum[z][slot + 128 * y];
             __syncwarp();
             if (lane == 0) mbar_arrive(bar + 8 * SUM_EMPTY);
-            const bool seen = page >= 0 && page < N;
-            if (there && !seen && slot % kGroup == 0) report(a.report, KVL_ERANGE, job.entry);
-            if (job.complete(w)) {
-                if (there) out[j] = seen ? held + sum : held;
-            } else {
-                const uint32_t first = cut.share_of(job.u0), last = cut.share_of(job.u0 + uint32_t(job.n) * H - 1);
-                args.parts[(int64_t(blockIdx.x) * 2 + (job.x0 == 0 ? 1 : 0)) * kTokens + slot] = sum;
+            bool last = true;
+            if (!job.complete(w)) {
+                const uint32_t first = cut.share_of(job.u0), end = cut.share_of(job.u0 + uint32_t(job.n) * H - 1);
+                float *part = args.parts + (int64_t(blockIdx.x) * 2 + (job.x0 == 0 ? 1 : 0)) * kTokens + slot;
+                part[0] = sum[0];
+                part[128] = sum[1];
                 __threadfence();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(bar + 8 * JOIN);
                 if (!(ok = wait(JOIN, joins++ & 1))) break;
                 if (warp == 0 && lane == 0) {
-                    s_last = atomicAdd(&args.counters[first], 1u) == last - first;
+                    s_last = atomicAdd(&args.counters[first], 1u) == end - first;
                     __threadfence();
                 }
                 __syncwarp();
                 if (lane == 0) mbar_arrive(bar + 8 * JOIN);
                 if (!(ok = wait(JOIN, joins++ & 1))) break;
-                if (s_last) {
-                    float all = 0.f;
-                    for (uint32_t b = first; b <= last; ++b)
-                        all += __ldcg(args.parts + (int64_t(b) * 2 + (b == first ? 1 : 0)) * kTokens + slot);
-                    if (there) out[j] = seen ? held + all : held;
+                last = s_last;
+                if (last) {
+                    sum[0] = sum[1] = 0.f;
+                    for (uint32_t b = first; b <= end; ++b) {
+                        const float *p = args.parts + (int64_t(b) * 2 + (b == first ? 1 : 0)) * kTokens + slot;
+                        sum[0] += __ldcg(p);
+                        sum[1] += __ldcg(p + 128);
+                    }
                 }
+            }
+#pragma unroll
+            for (int y = 0; y < 2; ++y) {
+                if (token[y] < 0) continue;
+                const bool seen = page[y] >= 0 && page[y] < N;
+                if (!seen && slot % kGroup == 0) report(a.report, KVL_ERANGE, job.entry);
+                if (last) out[token[y]] = seen ? held[y] + sum[y] : held[y];
             }
         } while (job.next(w));
     } else if (warp < kWeighing + 4) {
