@@ -42,11 +42,13 @@ struct alignas(16) Places {
     int32_t nv[kGroups];
 };
 
-template <int D, int ROWS>
+constexpr int ROWS = kPrefixTileRows;     // of a tile: 32 a softmax thread
+static_assert(ROWS == 64, "two softmax warpgroups of 32 rows each");
+
+template <int D>
 struct Prefix {
-    static constexpr int kPasses = ROWS / 64;  // of a softmax thread
     static constexpr int kVBytes = kSlots * D * 2;
-    static constexpr int kPBytes = (ROWS + 63) / 64 * (kSlots * 128);
+    static constexpr int kPBytes = kSlots * 128;
     static constexpr int kKBytes = kVBytes > kPBytes ? kVBytes : kPBytes;
     static constexpr int kQBytes = ROWS * D * 2;
     static constexpr int kV = 0;  // (at head_dim 64 the 128-high operand's second half reads on behind V: never past K)
@@ -55,7 +57,7 @@ struct Prefix {
     // K or V codes of a step, on their way: 16 KB each at head_dim 128 (with the step ahead in registers instead
     // 3.0 us a step of 128 rows, 2.4 of 64: the reads' latency)
     static constexpr int kUnitBytes = kSlots * D;
-    static constexpr int kUnits = D == 64 ? 8 : ROWS == 64 ? 4 : 3;
+    static constexpr int kUnits = D == 64 ? 8 : 4;
     static constexpr int kRing = kK + kKStages * kKBytes;
     static constexpr int kSmem = kRing + kUnits * kUnitBytes + 1024;
 };
@@ -71,7 +73,6 @@ struct Shared {
     int32_t tiles, steps;
 };
 
-template <int ROWS>
 __device__ __forceinline__ Shared shared_at(const AttendArgs &a, int g, void *rep)
 {
     const int B = a.cache.block_tokens, per_block = (B + kGroup - 1) / kGroup;
@@ -83,7 +84,6 @@ __device__ __forceinline__ Shared shared_at(const AttendArgs &a, int g, void *re
 }
 
 // A walk over the jobs of a share, each role's own.
-template <int ROWS>
 struct Walk {
     uint32_t u, u_end;
     int32_t group, job, before;  // job of the group; jobs of the groups before it
@@ -107,7 +107,7 @@ struct Walk {
         u_end = end;
         group = g;
         before = jobs;
-        s = shared_at<ROWS>(a, g, nullptr);
+        s = shared_at(a, g, nullptr);
         job = int(off / uint32_t(s.steps + kJobCost));
         here(off - job * uint32_t(s.steps + kJobCost));
     }
@@ -118,22 +118,22 @@ struct Walk {
         if (++job >= a.cache.n_kv_heads * s.tiles) {
             before += job;
             job = 0;
-            do s = shared_at<ROWS>(a, ++group, nullptr); while (s.tiles == 0);
+            do s = shared_at(a, ++group, nullptr); while (s.tiles == 0);
         }
         here(0);
         return true;
     }
 };
 
-template <int CODE, int D, int ROWS>
+template <int CODE, int D>
 __global__ void __launch_bounds__(kThreads, 1) attend_prefix_kernel(const __grid_constant__ AttendArgs a)
 {
-    using C = Prefix<D, ROWS>;
-    constexpr int kPasses = C::kPasses;
+    using C = Prefix<D>;
     extern __shared__ uint8_t smem_raw[];
     __shared__ __align__(8) unsigned long long bars[BARS];
     __shared__ Places places[kPlaces];
-    __shared__ __align__(16) float s_consts[2][ROWS * 2];  // of two jobs; for each pair of rows two factors, two references (negated)
+    __shared__ __align__(16) float s_refs[2][ROWS];  // of two jobs: the rows' references, negated
+    __shared__ float s_factor[2], s_most[4];         // the factor of their scores
     __shared__ float s_join[2][4][32];
     __shared__ uint64_t s_scan[kWarps], s_jobs[kWarps];
     __shared__ uint32_t s_off, s_tmem;
@@ -150,7 +150,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prefix_kernel(const __grid
     const int i0 = min(n_groups, tid * per_thread), i1 = min(n_groups, i0 + per_thread);
     uint64_t units = 0, jobs = 0;
     for (int i = i0; i < i1; ++i) {
-        const Shared s = shared_at<ROWS>(a, i, blockIdx.x == 0 ? a.report : nullptr);
+        const Shared s = shared_at(a, i, blockIdx.x == 0 ? a.report : nullptr);
         units += uint64_t(H) * s.tiles * (s.steps + kJobCost);
         jobs += uint64_t(H) * s.tiles;
     }
@@ -189,7 +189,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prefix_kernel(const __grid
         uint64_t at = before, j = jobs_before;
         int i = i0;
         for (;; ++i) {
-            const Shared s = shared_at<ROWS>(a, i, nullptr);
+            const Shared s = shared_at(a, i, nullptr);
             const uint64_t n = uint64_t(H) * s.tiles * (s.steps + kJobCost);
             if (first < at + n) break;
             at += n;
@@ -236,7 +236,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prefix_kernel(const __grid
         if (!mbar_try_wait(at, parity) && !*gone) wait_bar(at, parity, gone);
         __syncwarp();
     };
-    Walk<ROWS> job;
+    Walk job;
     job.begin(a, first, cut.start(blockIdx.x + 1), s_group, s_off, s_before);
     uint32_t it = 0, jobs_done = 0;  // steps and jobs of this CTA so far: the barriers' phases
 
@@ -259,12 +259,10 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prefix_kernel(const __grid
         };
         do {
             if (job.n == 0) continue;
-            float *consts = s_consts[jobs_done & 1] + 64 * w;  // (pass p: 128 p further)
-            uint64_t l[kPasses][16];
+            float *refs = s_refs[jobs_done & 1] + 32 * w;
+            uint64_t l[16];
 #pragma unroll
-            for (int p = 0; p < kPasses; ++p)
-#pragma unroll
-                for (int i = 0; i < 16; ++i) l[p][i] = 0;
+            for (int i = 0; i < 16; ++i) l[i] = 0;
             for (int s = 0; s < job.n; ++s) {
                 const uint32_t k = it + s, set = k & 1;
                 wait(S_FULL + set, (k >> 1) & 1);
@@ -272,87 +270,81 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prefix_kernel(const __grid
                 const Places &pl = places[k % kPlaces];
                 const int gi = slot / kGroup;
                 const bool there = slot % kGroup < pl.nv[gi];
-                const float ks = pl.ks[gi], lvs = there ? pl.lvs[gi] : -INFINITY, iv = there ? pl.ivs[gi] : 0.f;
-                const uint64_t kk = pair_of(ks, ks), ll = pair_of(lvs, lvs), ii = pair_of(iv, iv);
+                const float f = pl.ks[gi] * s_factor[jobs_done & 1], lvs = there ? pl.lvs[gi] : -INFINITY, iv = there ? pl.ivs[gi] : 0.f;
+                const uint64_t ff = pair_of(f, f), ll = pair_of(lvs, lvs), ii = pair_of(iv, iv);
+                const uint32_t ts = lanes + set * ROWS, to = lanes + 2 * ROWS;
+                uint32_t v[32];
+                // exponents against the rows' references, and whether one has outgrown its own
+                auto exponents = [&] {
+                    tmem_ld32(ts, v);
+                    tmem_wait_ld();
+                    float top = -INFINITY;
+#pragma unroll
+                    for (int i = 0; i < 32; i += 4) {
+                        const float4 m = *reinterpret_cast<const float4 *>(refs + i);
+                        const float2 y = split_pair(add_pair(fma_pair(pair_of(__uint_as_float(v[i]), __uint_as_float(v[i + 1])), ff, pair_of(m.x, m.y)), ll));
+                        const float2 z = split_pair(add_pair(fma_pair(pair_of(__uint_as_float(v[i + 2]), __uint_as_float(v[i + 3])), ff, pair_of(m.z, m.w)), ll));
+                        v[i] = __float_as_uint(y.x);
+                        v[i + 1] = __float_as_uint(y.y);
+                        v[i + 2] = __float_as_uint(z.x);
+                        v[i + 3] = __float_as_uint(z.y);
+                        top = max3(max3(top, y.x, y.y), z.x, z.y);
+                    }
+                    return top > kSlack;
+                };
+                uint32_t grew;
+                asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %1, 0;\n\tbar.red.or.pred q, %2, 128, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+                             : "=r"(grew)
+                             : "r"(uint32_t(exponents())), "r"(1 + w)
+                             : "memory");
+                if (grew) {
+                    // the step's largest x of each row, over all tokens; row `lane` of the 32 is this lane's
+                    float x[32];
+                    tmem_ld32(ts, v);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) x[i] = there ? fmaf(__uint_as_float(v[i]), f, lvs) : -INFINITY;
+                    s_join[w][quarter][lane] = over_lanes(x, [](float y, float z) { return fmaxf(y, z); });
+                    meet();
+                    const float big = fmaxf(fmaxf(s_join[w][0][lane], s_join[w][1][lane]), fmaxf(s_join[w][2][lane], s_join[w][3][lane]));
+                    const float was = -refs[lane];
+                    const float now = big > was + kSlack ? big + kHead : was;
+                    const float factor = exp2_of(was - now);  // 0 from before the first score
+                    meet();
+                    if (quarter == 0) refs[lane] = -now;
+                    if (s > 0) {
+                        wait(PV_DONE + (set ^ 1), ((k - 1) >> 1) & 1);
+                        tmem_fence_after();
+                        tmem_ld32(to, v);
+                        tmem_wait_ld();
+                    }
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) {
+                        const float f0 = __shfl_sync(0xffffffffu, factor, 2 * i), f1 = __shfl_sync(0xffffffffu, factor, 2 * i + 1);
+                        l[i] = mul_pair(l[i], pair_of(f0, f1));
+                        v[2 * i] = __float_as_uint(__uint_as_float(v[2 * i]) * f0);
+                        v[2 * i + 1] = __float_as_uint(__uint_as_float(v[2 * i + 1]) * f1);
+                    }
+                    if (s > 0) {
+                        tmem_st32(to, v);
+                        tmem_wait_st();
+                        tmem_fence_before();
+                    }
+                    meet();
+                    exponents();
+                }
+                // weights: into the sums, and as halves over the step's K
                 uint8_t *weights = smem + C::kK + (k % kKStages) * C::kKBytes + slot * 128;
 #pragma unroll
-                for (int p = 0; p < kPasses; ++p) {
-                    const uint32_t ts = lanes + set * ROWS + 64 * p, to = lanes + 2 * ROWS + 64 * p;
-                    float *fm = consts + 128 * p;
-                    uint32_t v[32];
-                    // exponents against the rows' references, and whether one has outgrown its own
-                    auto exponents = [&] {
-                        tmem_ld32(ts, v);
-                        tmem_wait_ld();
-                        float top = -INFINITY;
+                for (int u = 0; u < 4; ++u) {
+                    uint32_t z[4];
 #pragma unroll
-                        for (int i = 0; i < 16; ++i) {
-                            const float4 c = *reinterpret_cast<const float4 *>(fm + 4 * i);
-                            const uint64_t t = mul_pair(pair_of(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1])), kk);
-                            const float2 y = split_pair(add_pair(fma_pair(t, pair_of(c.x, c.y), pair_of(c.z, c.w)), ll));
-                            v[2 * i] = __float_as_uint(y.x);
-                            v[2 * i + 1] = __float_as_uint(y.y);
-                            top = max3(top, y.x, y.y);
-                        }
-                        return top > kSlack;
-                    };
-                    uint32_t grew;
-                    asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %1, 0;\n\tbar.red.or.pred q, %2, 128, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
-                                 : "=r"(grew)
-                                 : "r"(uint32_t(exponents())), "r"(1 + w)
-                                 : "memory");
-                    if (grew) {
-                        // the step's largest x of each row, over all tokens; row `lane` of the 32 is this lane's
-                        float x[32];
-                        tmem_ld32(ts, v);
-                        tmem_wait_ld();
-#pragma unroll
-                        for (int i = 0; i < 32; ++i) {
-                            const float f = fm[4 * (i >> 1) + (i & 1)];
-                            x[i] = there ? fmaf(__uint_as_float(v[i]) * ks, f, lvs) : -INFINITY;
-                        }
-                        s_join[w][quarter][lane] = over_lanes(x, [](float y, float z) { return fmaxf(y, z); });
-                        meet();
-                        const float big = fmaxf(fmaxf(s_join[w][0][lane], s_join[w][1][lane]), fmaxf(s_join[w][2][lane], s_join[w][3][lane]));
-                        const int at = 4 * (lane >> 1) + 2 + (lane & 1);
-                        const float was = -fm[at];
-                        const float now = big > was + kSlack ? big + kHead : was;
-                        const float factor = exp2_of(was - now);  // 0 from before the first score
-                        meet();
-                        if (quarter == 0) fm[at] = -now;
-                        if (s > 0) {
-                            wait(PV_DONE + (set ^ 1), ((k - 1) >> 1) & 1);
-                            tmem_fence_after();
-                            tmem_ld32(to, v);
-                            tmem_wait_ld();
-                        }
-#pragma unroll
-                        for (int i = 0; i < 16; ++i) {
-                            const float f0 = __shfl_sync(0xffffffffu, factor, 2 * i), f1 = __shfl_sync(0xffffffffu, factor, 2 * i + 1);
-                            l[p][i] = mul_pair(l[p][i], pair_of(f0, f1));
-                            v[2 * i] = __float_as_uint(__uint_as_float(v[2 * i]) * f0);
-                            v[2 * i + 1] = __float_as_uint(__uint_as_float(v[2 * i + 1]) * f1);
-                        }
-                        if (s > 0) {
-                            tmem_st32(to, v);
-                            tmem_wait_st();
-                            tmem_fence_before();
-                        }
-                        meet();
-                        exponents();
+                    for (int i = 0; i < 4; ++i) {
+                        const float e0 = exp2_of(__uint_as_float(v[8 * u + 2 * i])), e1 = exp2_of(__uint_as_float(v[8 * u + 2 * i + 1]));
+                        l[4 * u + i] = fma_pair(pair_of(e0, e1), ii, l[4 * u + i]);
+                        z[i] = pack2<KVL_TYPE_HALF>(e0, e1);
                     }
-                    // weights: into the sums, and as halves over the step's K
-#pragma unroll
-                    for (int u = 0; u < 4; ++u) {
-                        uint32_t z[4];
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            const float e0 = exp2_of(__uint_as_float(v[8 * u + 2 * i])), e1 = exp2_of(__uint_as_float(v[8 * u + 2 * i + 1]));
-                            l[p][4 * u + i] = fma_pair(pair_of(e0, e1), ii, l[p][4 * u + i]);
-                            z[i] = pack2<KVL_TYPE_HALF>(e0, e1);
-                        }
-                        *reinterpret_cast<uint4 *>(weights + p * (kSlots * 128) + (((4 * w + u) ^ (slot & 7)) << 4)) = make_uint4(z[0], z[1], z[2], z[3]);
-                    }
+                    *reinterpret_cast<uint4 *>(weights + (((4 * w + u) ^ (slot & 7)) << 4)) = make_uint4(z[0], z[1], z[2], z[3]);
                 }
                 fence_proxy_async_smem();
                 tmem_fence_before();
@@ -363,40 +355,35 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prefix_kernel(const __grid
             const int rows = min(ROWS, job.s.e.fresh * G - job.tile * ROWS);
             const int part_number = job.before + job.job + int(blockIdx.x);
             float *part = a.prefix_parts + int64_t(part_number) * (ROWS * (D + 2));
-#pragma unroll
-            for (int p = 0; p < kPasses; ++p) {
+            {
                 float x[32];
 #pragma unroll
                 for (int i = 0; i < 16; ++i) {
-                    const float2 t = split_pair(l[p][i]);
+                    const float2 t = split_pair(l[i]);
                     x[2 * i] = t.x;
                     x[2 * i + 1] = t.y;
                 }
                 s_join[w][quarter][lane] = over_lanes(x, [](float y, float z) { return y + z; });
                 meet();
-                const int r = 64 * p + 32 * w + lane;
+                const int r = 32 * w + lane;
                 if (quarter == 0 && r < rows && !*gone) {
-                    part[r] = -consts[128 * p + 4 * (lane >> 1) + 2 + (lane & 1)];
+                    part[r] = -refs[lane];
                     part[ROWS + r] = s_join[w][0][lane] + s_join[w][1][lane] + s_join[w][2][lane] + s_join[w][3][lane];
                 }
                 meet();
             }
             wait(PV_DONE + ((it + job.n - 1) & 1), ((it + job.n - 1) >> 1) & 1);
             tmem_fence_after();
-#pragma unroll
-            for (int p = 0; p < kPasses; ++p) {
-                uint32_t v[32];
-                tmem_ld32(lanes + 2 * ROWS + 64 * p, v);
-                tmem_wait_ld();
-                if (slot < D && !*gone) {
-                    const int r0 = 64 * p + 32 * w;
-                    float *o = part + 2 * ROWS + r0 * D + slot;
-#pragma unroll
-                    for (int i = 0; i < 32; ++i)
-                        if (r0 + i < rows) o[i * D] = __uint_as_float(v[i]);
-                }
-            }
+            uint32_t v[32];
+            tmem_ld32(lanes + 2 * ROWS, v);
+            tmem_wait_ld();
             tmem_fence_before();
+            if (slot < D && !*gone) {
+                float *o = part + 2 * ROWS + 32 * w * D + slot;
+#pragma unroll
+                for (int i = 0; i < 32; ++i)
+                    if (32 * w + i < rows) o[i * D] = __uint_as_float(v[i]);
+            }
             if (tid == 0 && job.sa == 0 && !*gone) {
                 const int64_t id = int64_t(job.s.e.row0) * G / ROWS + job.group + job.tile;
                 const int from = int(cut.share_of(job.u0)), last = int(cut.share_of(job.u0 + job.s.steps - 1));
@@ -503,32 +490,48 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prefix_kernel(const __grid
             for (int x = 0; x < C::kUnits; ++x) ask(0);
             scales(page, ks, vs);
             {
-                // ---- the job's rows, once the products of the job before are done: scaled by a power of two into the
-                // range of a half (undone in the factor), as attend_rows does
-                if (it > 0) wait(K_EMPTY + (it - 1) % kKStages, ((it - 1) / kKStages) & 1);
+                // ---- the job's rows, scaled by one power of two, which takes their largest element into [2^14, 2^15) (what
+                // is lost is below 2^-39 of it), once the products of the job before are done
                 const int rows = min(ROWS, job.s.e.fresh * G - job.tile * ROWS), set = jobs_done & 1;
-                constexpr int kLanes = D / 8, kRowsPer = 32 / kLanes;  // lanes of a row, rows of a warp's vector
+                constexpr int kLanes = D / 8, kRowsPer = 32 / kLanes, kTurns = ROWS / (4 * kRowsPer);  // lanes of a row, rows of a warp's vector
                 const int at = (lane % kLanes) * 8;
-#pragma unroll 2
-                for (int x = 0; x < ROWS / (4 * kRowsPer); ++x) {
+                uint4 raw[kTurns];
+                float amax = 0.f;  // of finite elements
+#pragma unroll
+                for (int x = 0; x < kTurns; ++x) {
                     const int r = (cw + 4 * x) * kRowsPer + lane / kLanes;
-                    const bool ok = r < rows;
-                    const uint32_t row = ok ? job.tile * ROWS + r : 0, tok = row / uint32_t(G);
-                    float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-                    if (ok && at < d) {
-                        const uint8_t *q = static_cast<const uint8_t *>(a.attn.q.data) + (int64_t(job.s.e.row0) + tok) * a.attn.q.row_stride +
-                                           int64_t(h * G + row - tok * G) * a.attn.q.head_stride + 2 * at;
-                        if (a.attn.type == KVL_TYPE_BFLOAT) load8<KVL_TYPE_BFLOAT>(q, v);
-                        else load8<KVL_TYPE_HALF>(q, v);
+                    raw[x] = make_uint4(0, 0, 0, 0);
+                    if (r < rows && at < d) {
+                        const uint32_t row = job.tile * ROWS + r, tok = row / uint32_t(G);
+                        raw[x] = *reinterpret_cast<const uint4 *>(static_cast<const uint8_t *>(a.attn.q.data) + (int64_t(job.s.e.row0) + tok) * a.attn.q.row_stride +
+                                                                  int64_t(h * G + row - tok * G) * a.attn.q.head_stride + 2 * at);
                     }
-                    float amax = 0.f;
+                }
+                auto floats = [&](const uint4 &x, float (&v)[8]) {
+                    if (a.attn.type == KVL_TYPE_BFLOAT) load8<KVL_TYPE_BFLOAT>(reinterpret_cast<const uint8_t *>(&x), v);
+                    else load8<KVL_TYPE_HALF>(reinterpret_cast<const uint8_t *>(&x), v);
+                };
 #pragma unroll
-                    for (int y = 0; y < 8; ++y) amax = fmaxf(amax, fabsf(v[y]));
+                for (int x = 0; x < kTurns; ++x) {
+                    float v[8];
+                    floats(raw[x], v);
 #pragma unroll
-                    for (int o = kLanes / 2; o; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-                    const uint32_t ex = (__float_as_uint(amax) >> 23) & 0xffu;
-                    const bool plain = ex < 2 || ex > 252;
-                    const float up = plain ? 1.f : __uint_as_float((254u - ex) << 23), down = plain ? 1.f : __uint_as_float(ex << 23);
+                    for (int y = 0; y < 8; ++y) amax = fmaxf(amax, isfinite(v[y]) ? fabsf(v[y]) : 0.f);
+                }
+#pragma unroll
+                for (int o = 16; o; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+                if (lane == 0) s_most[cw] = amax;
+                asm volatile("bar.sync 3, 128;" ::: "memory");
+                amax = fmaxf(fmaxf(s_most[0], s_most[1]), fmaxf(s_most[2], s_most[3]));
+                // 2^e <= amax < 2^(e + 1), e held to what leaves both factors normal
+                const int ex = max(-100, int(__float_as_uint(amax) >> 23) - 127);
+                const float up = __uint_as_float(uint32_t(14 - ex + 127) << 23), down = __uint_as_float(uint32_t(ex - 14 + 127) << 23);
+                if (it > 0) wait(K_EMPTY + (it - 1) % kKStages, ((it - 1) / kKStages) & 1);
+#pragma unroll
+                for (int x = 0; x < kTurns; ++x) {
+                    const int r = (cw + 4 * x) * kRowsPer + lane / kLanes;
+                    float v[8];
+                    floats(raw[x], v);
                     uint4 z;
                     z.x = pack2<KVL_TYPE_HALF>(v[0] * up, v[1] * up);
                     z.y = pack2<KVL_TYPE_HALF>(v[2] * up, v[3] * up);
@@ -536,14 +539,13 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prefix_kernel(const __grid
                     z.w = pack2<KVL_TYPE_HALF>(v[6] * up, v[7] * up);
                     const int un = at / 8;
                     *reinterpret_cast<uint4 *>(smem + C::kQ + (un >> 3) * (ROWS * 128) + r * 128 + (((un & 7) ^ (r & 7)) << 4)) = z;
-                    if (at == 0) {
-                        s_consts[set][4 * (r >> 1) + (r & 1)] = a.attn.sm_scale * kLog2e * down;
-                        s_consts[set][4 * (r >> 1) + 2 + (r & 1)] = -kNoScore;
-                    }
+                    if (at == 0) s_refs[set][r] = -kNoScore;
                 }
+                if (cw == 0 && lane == 0) s_factor[set] = a.attn.sm_scale * kLog2e * down;
                 fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(bar + 8 * Q_FULL);
+                asm volatile("bar.sync 3, 128;" ::: "memory");  // (s_most is free again)
             }
             int base = 0;
             for (int s = 0; s < n; ++s) {
@@ -632,30 +634,29 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prefix_kernel(const __grid
     if (warp == kWarps - 1) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
 }
 
-template <int CODE, int D, int ROWS>
+template <int CODE, int D>
 kvl_status launch_prefix(const AttendArgs &a, int sms, void *stream)
 {
     static std::atomic<unsigned long long> ready[kMaxDevices];
-    using C = Prefix<D, ROWS>;
-    if (!allow_smem(attend_prefix_kernel<CODE, D, ROWS>, ready, C::kSmem)) return KVL_ECUDA;
-    attend_prefix_kernel<CODE, D, ROWS><<<sms, kThreads, C::kSmem, static_cast<cudaStream_t>(stream)>>>(a);
+    using C = Prefix<D>;
+    if (!allow_smem(attend_prefix_kernel<CODE, D>, ready, C::kSmem)) return KVL_ECUDA;
+    attend_prefix_kernel<CODE, D><<<sms, kThreads, C::kSmem, static_cast<cudaStream_t>(stream)>>>(a);
     return launch_status();
 }
 
 template <int CODE>
-kvl_status launch_prefix_dim(const AttendArgs &a, int rows, int sms, void *stream)
+kvl_status launch_prefix_dim(const AttendArgs &a, int sms, void *stream)
 {
-    if (a.cache.head_dim <= 64)
-        return rows == 64 ? launch_prefix<CODE, 64, 64>(a, sms, stream) : launch_prefix<CODE, 64, 128>(a, sms, stream);
-    return rows == 64 ? launch_prefix<CODE, 128, 64>(a, sms, stream) : launch_prefix<CODE, 128, 128>(a, sms, stream);
+    return a.cache.head_dim <= 64 ? launch_prefix<CODE, 64>(a, sms, stream)
+                                  : launch_prefix<CODE, 128>(a, sms, stream);
 }
 
 }  // namespace
 
-kvl_status launch_attend_prefix(const AttendArgs &a, int rows, int sms, void *stream)
+kvl_status launch_attend_prefix(const AttendArgs &a, int sms, void *stream)
 {
-    return a.cache.code_type == KVL_CODE_FLOAT ? launch_prefix_dim<KVL_CODE_FLOAT>(a, rows, sms, stream)
-                                               : launch_prefix_dim<KVL_CODE_INT>(a, rows, sms, stream);
+    return a.cache.code_type == KVL_CODE_FLOAT ? launch_prefix_dim<KVL_CODE_FLOAT>(a, sms, stream)
+                                               : launch_prefix_dim<KVL_CODE_INT>(a, sms, stream);
 }
 
 }  // namespace kvl

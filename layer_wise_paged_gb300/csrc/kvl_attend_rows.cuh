@@ -24,7 +24,7 @@
 // The kernel serves whole sequences, and the two parts of attention over a shared prefix (Part).
 #pragma once
 
-#include "kvl_attend.cuh"
+#include "kvl_attend_prefix.cuh"
 
 namespace kvl {
 namespace {
@@ -126,6 +126,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attend_rows_kernel(const
     struct Join {
         const float *o;   // the first part's values
         int64_t step;     // to the next part's
+        int e_step;       // from four elements to the next four
         int parts;        // -1: the shared tokens' results are missing
         float own, big, sum;
     };
@@ -616,7 +617,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attend_rows_kernel(const
                 v.x *= j.own; v.y *= j.own; v.z *= j.own; v.w *= j.own;
                 sum = j.sum;
                 big = j.big;
-                const float *o = j.o + e;
+                const float *o = j.o + (e / 4) * j.e_step;
 #pragma unroll 8
                 for (int b = 0; b < j.parts; ++b) {
                     const float g = s_factor[r][b];
@@ -636,7 +637,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attend_rows_kernel(const
             const int row = tile * kRows + r, head = h * G + row % G;
             const int64_t t = int64_t(c.e.row0) + row / G;
             const float *ml = nullptr;
-            Join j = {nullptr, 0, 0, 0.f, 0.f, 0.f};
+            Join j = {nullptr, 0, 4, 0, 0.f, 0.f, 0.f};
             int64_t ml_step = 1;  // from a reference to its sum
             if (c.lo > 0 && a.prefix_rows == 0) {
                 const int64_t at = t * a.attn.n_heads + head;
@@ -652,7 +653,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attend_rows_kernel(const
                 j.step = int64_t(R) * (D + 2);
                 ml = a.prefix_parts + (j.parts ? p.x : 0) * j.step + r_g;
                 ml_step = R;
-                j.o = ml - r_g + 2 * R + int64_t(r_g) * D;
+                j.e_step = R == kChunkTileRows ? 4 * R : 4;
+                j.o = ml - r_g + 2 * R + int64_t(r_g) * (R == kChunkTileRows ? 4 : D);
             }
             float m = big;
             for (int b = lane; b < j.parts; b += 32) m = fmaxf(m, ml[b * j.step]);
@@ -687,7 +689,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attend_rows_kernel(const
             }
         }
         for (int x = tid; x < rows * (D / 4); x += kThreads) {
-            const int r = x / (D / 4), e = (x % (D / 4)) * 4;
+            // (parts of shared tokens have a row's four elements beside the next row's)
+            const int r = kOwn ? x % rows : x / (D / 4), e = (kOwn ? x / rows : x % (D / 4)) * 4;
             float big = -INFINITY;
 #pragma unroll
             for (int w = 0; w < kWarps; ++w) big = fmaxf(big, s_m[w][r]);
@@ -775,11 +778,11 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attend_rows_kernel(const
                 for (int x = 0; x < kVecs; ++x) all[(warp * kVecs + x) * 32 + lane] = v[x];
                 __syncthreads();
                 for (int x = tid; x < rows * (D / 4); x += kThreads) {
-                    const int r = x / (D / 4), e = (x % (D / 4)) * 4;
-                    float4 y = all[x];
+                    const int r = kOwn ? x % rows : x / (D / 4), e = (kOwn ? x / rows : x % (D / 4)) * 4, at = r * (D / 4) + e / 4;
+                    float4 y = all[at];
 #pragma unroll
                     for (int w = 1; w < kWarps; ++w) {
-                        const float4 z = all[w * kVecs * 32 + x];
+                        const float4 z = all[w * kVecs * 32 + at];
                         y.x += z.x; y.y += z.y; y.z += z.z; y.w += z.w;
                     }
                     finish(r, e, y, s_m[0][r], s_l[0][r]);

@@ -3,7 +3,6 @@
 //
 // A softmax over [0, len) is the join of those over [0, P) and [P, len): with references m1, m2, sums l1, l2 and
 // weighted values O1, O2, m = max(m1, m2), l = l1 2^(m1 - m) + l2 2^(m2 - m), O likewise.
-#include "kvl_attend_prefix.cuh"
 #include "kvl_attend_rows.cuh"
 
 using namespace kvl;
@@ -40,7 +39,7 @@ Layout layout_of(const kvl_cache &c, int n_seq, int n_groups, int64_t n_rows, in
         l.bytes = l.second + size_t(n_rows) * n_heads * 8;
         return l;
     }
-    l.rows = n_rows * G <= int64_t(64) * n_groups ? 64 : 128;
+    l.rows = n_rows * G <= int64_t(kPrefixTileRows) * n_groups ? kPrefixTileRows : kChunkTileRows;
     l.jobs = prefix_tiles(n_rows, G, n_groups, l.rows) * c.n_kv_heads;
     l.most = l.jobs + sms;
     l.second = (l.first + size_t(l.jobs) * 8 + 15) & ~size_t(15);
@@ -96,7 +95,7 @@ extern "C" kvl_status kvl_attend_shared(const kvl_cache *cache, int32_t layer, c
         a.prefix_most = int32_t(l.most);
         a.prefix_jobs = reinterpret_cast<int32_t *>(base + l.first);
         a.prefix_parts = reinterpret_cast<float *>(base + l.second);
-        s = launch_attend_prefix(a, l.rows, sms, stream);
+        s = l.rows == kPrefixTileRows ? launch_attend_prefix(a, sms, stream) : launch_attend_chunk_shared(a, sms, stream);
     }
     return s ? s : launch_rows_part<Part::own>(a, bound * G, sms, stream);
 }
