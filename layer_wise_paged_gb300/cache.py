@@ -199,6 +199,7 @@ class QuantCache:
         # a workspace for each stream (calls on two streams may run at the same time), and one for the newest
         # capture on it (the graph may run beside them)
         self._ws, self._ws_captured = {}, {}
+        self._held, self._held_captured, self._sizes = {}, {}, {}  # memory of single calls, likewise; its sizes
         self._capture_id = self._lib.kvl_capture_id
         self._scale = 1.0 / math.sqrt(d)
         self._args = _Args(self)
@@ -277,10 +278,13 @@ class QuantCache:
         g.n_groups, g.groups, g.tokens = n_groups, _ints(groups, "groups", n_groups + 1), _ints(shared, "shared")
         n_rows, heads, _ = q.shape
         s = self._seqs(c, starts, slots, n_rows)
-        n = self._lib.kvl_attend_shared_parts_bytes(self._cache, s.n_seq, n_groups, n_rows, heads)
-        parts = self._scratch(n, stream, st)
+        key = s.n_seq, n_groups, n_rows, heads
+        n = self._sizes.get(key)
+        if n is None:
+            n = self._size(key, self._lib.kvl_attend_shared_parts_bytes(self._cache, *key))
+        parts = self._scratch(n, st)
         r = self._lib.kvl_attend_shared(self._cache, layer, s, g, c.attn, ws,
-                                        self._ws_bytes, parts.data_ptr(), n, self._report, st)
+                                        self._ws_bytes, parts, n, self._report, st)
         if r:
             check(r, "kvl_attend_shared")
         return out
@@ -306,9 +310,11 @@ class QuantCache:
         w.causal, w.window, w.max_new, w.begin = 1 if causal else 0, window, max_new, 1 if begin else 0
         st = _stream(stream, self._index)
         s = self._seqs(c, starts, slots, n_rows)
-        n = self._lib.kvl_weigh_workspace_bytes(self._cache, s.n_seq, n_rows, heads, max(0, max_new))
-        ws = self._scratch(n, stream, st)
-        r = self._lib.kvl_weigh(self._cache, layer, s, w, ws.data_ptr(), n, self._report, st)
+        key = s.n_seq, n_rows, heads, max_new if max_new > 0 else 0, None
+        n = self._sizes.get(key)
+        if n is None:
+            n = self._size(key, self._lib.kvl_weigh_workspace_bytes(self._cache, *key[:4]))
+        r = self._lib.kvl_weigh(self._cache, layer, s, w, self._scratch(n, st), n, self._report, st)
         if r:
             check(r, "kvl_weigh")
         return mass if out is None else out
@@ -319,12 +325,23 @@ class QuantCache:
             raise ValueError(f"{name}: float32 [{self.n_slots}, tokens] in device memory, rows contiguous")
         return t.data_ptr(), max(t.stride(0), t.shape[1])
 
-    def _scratch(self, n, stream, st):
-        """Memory of one call, which is its stream's."""
-        if stream is None:
-            return torch.empty(n, dtype=torch.uint8, device=self.device)
-        with self._on(st):
-            return torch.empty(n, dtype=torch.uint8, device=self.device)
+    def _size(self, key, n):
+        if len(self._sizes) > 1000:
+            self._sizes.clear()
+        self._sizes[key] = n
+        return n
+
+    def _scratch(self, n, st):
+        """Memory (its address) that holds nothing between calls: calls of one stream share one, a graph has its own, as
+        with the workspaces."""
+        capture = self._capture_id(st)
+        held = self._held_captured if capture else self._held
+        m = held.get(st)
+        if m is None or m[0] != capture or m[1] < n:
+            with self._on(st):
+                t = torch.empty(max(n, 1 << 16), dtype=torch.uint8, device=self.device)
+            m = held[st] = capture, t.numel(), t.data_ptr(), t
+        return m[2]
 
     def _attention(self, q, out, lse, sm_scale, causal, window, max_new, stream, st):
         """Fill this thread's kvl_attention; (out, the workspace's address)."""

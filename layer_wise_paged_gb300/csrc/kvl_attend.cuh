@@ -33,14 +33,16 @@ struct AttendArgs {
     void *report;
     // attention over a shared prefix only
     kvl_shared shared;
-    int32_t *shared_done;  // 1: the shared tokens' results are there
-    int32_t *sharing;      // [n_seq] Sharing
-    float *row_o;          // [n_rows][n_heads][64, 128 or 256]: O of the rows over the shared tokens
-    float *row_ml;         // [n_rows][n_heads][2]: their references and sums
-    // where the tensor-memory kernel makes them (kvl_attend_prefix.cuh): rows of a tile (0: row_o has them)
-    int32_t prefix_rows, prefix_most;
-    int32_t *prefix_jobs;
-    float *prefix_parts;   // prefix_most of them
+    // What the join reads (see kvl_attend_shared.cu): every entry's Sharing; the rows' O and (reference, sum) over their
+    // own tokens and, where the few-rows kernel makes them, over the shared ones (`rows` further); or the
+    // tensor-memory kernel's job table and parts, parts_most of them.
+    int32_t *sharing;
+    float *row_o;          // [2][n_rows][n_heads][64, 128 or 256]
+    float *row_ml;         // [2][n_rows][n_heads][2]
+    int32_t few;           // the few-rows kernel attends the shared tokens too
+    int32_t *part_jobs, *parts_done;  // parts_done: 1 if there are results
+    float *group_parts;
+    int32_t parts_most;
 };
 
 namespace {
@@ -63,8 +65,7 @@ constexpr uint64_t kMostUnits = uint64_t(1) << 31;  // see Cut
 struct Cost {
     Entry e;
     int32_t tiles, g0, groups;
-    int32_t lo;            // the first token any row sees
-    int32_t group, row0;   // of a sequence that shares its first lo tokens: its group, and the group's first row
+    int32_t lo;  // the first token any row sees
 };
 
 // The first token a row at position `pos` sees, j > pos - window.  (A row stands before token 0 where an
@@ -112,11 +113,10 @@ struct alignas(16) Sharing {
     int32_t tokens, group, row0, reserved;
 };
 
-// An entry whose group is left out, or one of whose rows does not see all shared tokens, is left out.
-__device__ __forceinline__ Sharing sharing_of(const AttendArgs &a, int32_t i, void *rep)
+// Entry i, resolved as e; one whose group is left out, or one of whose rows does not see all shared tokens, is left out.
+__device__ __forceinline__ Sharing sharing_of(const AttendArgs &a, const Entry &e, int32_t i, void *rep)
 {
     Sharing s = {0, 0, 0, 0};
-    const Entry e = load_entry(a.seqs, a.cache.block_tokens, i, nullptr);  // (reports itself where its own tokens are attended)
     int lo = -1, hi = a.shared.n_groups;  // the last group that begins at i or before
     while (hi - lo > 1) {
         const int mid = (lo + hi) >> 1;
@@ -131,13 +131,6 @@ __device__ __forceinline__ Sharing sharing_of(const AttendArgs &a, int32_t i, vo
     if (p.len > 0) report(rep, KVL_ERANGE, i);  // (a group reports itself)
     s.tokens = -1;
     return s;
-}
-
-// Every entry's sharing, looked up once by the kernel over the shared tokens for the one over the entries' own, which
-// would go through half a dozen loads one after another for each.
-__device__ __forceinline__ void resolve_entries(const AttendArgs &a, int first, int step)
-{
-    for (int i = first; i < a.seqs.n_seq; i += step) reinterpret_cast<Sharing *>(a.sharing)[i] = sharing_of(a, i, a.report);
 }
 
 // 16 bytes into shared memory; zeros where !ok (src has to be a valid address all the same).
@@ -185,7 +178,12 @@ __device__ __forceinline__ float v_scale(float s) { return s <= kTinyScale ? 0x1
 size_t attend_rows_part_bytes(int head_dim);  // for each SM
 // most: a bound on the rows (as max_rows) of an entry, which chooses the row tile.
 kvl_status launch_attend_rows(const AttendArgs &a, int64_t most, int sms, void *stream);
+// The parts of attention over a shared prefix: every entry's own tokens, and with a.few the groups' shared ones.
+kvl_status launch_attend_row_parts(const AttendArgs &a, int64_t most, int sms, void *stream);
 size_t attend_chunk_part_bytes(int head_dim);
+constexpr int kChunkJobRows = 256;  // of the tensor-memory kernel's jobs
+// The groups' shared tokens.  Its CTAs may start beside the kernel before it on the stream, whose end they wait for.
+kvl_status launch_attend_chunk_groups(const AttendArgs &a, int sms, void *stream);
 kvl_status launch_attend_chunk(const AttendArgs &a, int sms, void *stream);
 
 // Entries with more rows than this (fresh tokens x query heads of a KV head) go to the tensor-memory kernel.

@@ -24,7 +24,9 @@
 // named barrier (kvl_attend_meet.cuh), and the tensor memory is given back.
 //
 // With SHARED the kernel attends the shared tokens of groups (one entry each, with the rows of all its sequences); every
-// share's part of a job stays in memory for the kernel over the sequences' own tokens (kvl_attend_prefix.cuh).
+// share's part of a job stays in memory for the kernel that joins them with the sequences' own (kvl_attend_shared.cu).
+// Parts are numbered job + share, so there are never more than jobs + shares; tile c of group g has the number
+// row0 * G / 256 + g + c (row0 the group's first row) in the job table, so no two meet.
 #pragma once
 
 #include <type_traits>
@@ -301,10 +303,10 @@ __global__ void __launch_bounds__(kThreads, 1) attend_chunk_kernel(const __grid_
     uint32_t u = 0;
     Cut cut;
     const int n_entries = SHARED ? a.shared.n_groups : a.seqs.n_seq;
-    if constexpr (SHARED) {
-        allow_dependents_launch();
-        resolve_entries(a, int(blockIdx.x) * kThreads + tid, int(gridDim.x) * kThreads);
-    }
+    if constexpr (SHARED) allow_dependents_launch();
+    auto leave = [&] {  // the kernel before has ended when this one has
+        if constexpr (SHARED) grid_dependency_wait();
+    };
     for (int pass = 0; pass < 2; ++pass) {
         uint32_t jobs = 0;
         for (int base = 0; base < n_entries; base += kBatch) {
@@ -359,13 +361,17 @@ __global__ void __launch_bounds__(kThreads, 1) attend_chunk_kernel(const __grid_
         }
         if (pass == 0) {
             if constexpr (SHARED)
-                if (blockIdx.x == 0 && tid == 0) *a.shared_done = before < kMostUnits;
+                if (blockIdx.x == 0 && tid == 0) a.parts_done[1] = before < kMostUnits;
             if (before == 0 || before >= kMostUnits) {
                 if (before && blockIdx.x == 0 && tid == 0) report(a.report, KVL_ERANGE, n_entries);
+                leave();
                 return;
             }
             cut = Cut(uint32_t(before), min(gridDim.x, (uint32_t(before) + kStepsPerCta - 1) / kStepsPerCta));
-            if (blockIdx.x >= cut.shares) return;
+            if (blockIdx.x >= cut.shares) {
+                leave();
+                return;
+            }
             u = cut.start(blockIdx.x);
             before = 0;
         }
@@ -402,6 +408,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_chunk_kernel(const __grid_
         if (tid == 0) report(a.report, KVL_ECUDA, blockIdx.x);
         if (warp == 8) arrive_without_result<SHARED>(a, job, lane);
         if (warp == 8) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(s_tmem) : "memory");
+        leave();
         return;
     }
     volatile int *gone = &s_gone;
@@ -867,7 +874,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_chunk_kernel(const __grid_
             const int64_t out_row = e_.row0 + tok;
             const int head = h * G + int(row - tok * G);
             const float inv = row_l == 0.f ? 0.f : 1.f / row_l;
-            float *part = SHARED ? a.prefix_parts + (int64_t(job.job) + blockIdx.x) * C::kPartFloats
+            float *part = SHARED ? a.group_parts + (int64_t(job.job) + blockIdx.x) * C::kPartFloats
                                  : a.parts + (int64_t(blockIdx.x) * 2 + (job.sa == 0 ? 1 : 0)) * C::kPartFloats;
             uint8_t *dst = static_cast<uint8_t *>(a.attn.out.data) + out_row * a.attn.out.row_stride + head * a.attn.out.head_stride;
             if (ok) {
@@ -891,9 +898,10 @@ __global__ void __launch_bounds__(kThreads, 1) attend_chunk_kernel(const __grid_
                                 if (32 * c + 8 * e < d) store8<TYPE>(dst + 2 * (32 * c + 8 * e), v);
                             }
                         } else {
+                            // (the parts of shared tokens are read a row at a time)
 #pragma unroll
                             for (int e = 0; e < 8; ++e)
-                                *reinterpret_cast<uint4 *>(part + 2 * kJobRows + (int64_t(8 * c + e) * kJobRows + r) * 4) =
+                                *reinterpret_cast<uint4 *>(part + 2 * kJobRows + (SHARED ? r * D + 32 * c + 4 * e : (int64_t(8 * c + e) * kJobRows + r) * 4)) =
                                     make_uint4(x[4 * e], x[4 * e + 1], x[4 * e + 2], x[4 * e + 3]);
                         }
                     }
@@ -912,7 +920,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_chunk_kernel(const __grid_
                 if (tid == 0 && ok && job.sa == 0) {
                     const int64_t id = int64_t(e_.row0) * G / kJobRows + job.entry + job.row_base / kJobRows;
                     const int from = int(job.cut.share_of(job.u0)), last = int(job.cut.share_of(job.u0 + job.t.steps - 1));
-                    reinterpret_cast<int2 *>(a.prefix_jobs)[id * H + h] = make_int2(job.job + int(blockIdx.x), last - from + 1);
+                    reinterpret_cast<int2 *>(a.part_jobs)[id * H + h] = make_int2(job.job + int(blockIdx.x), last - from + 1);
                 }
             tmem_fence_before();
         }
@@ -993,6 +1001,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_chunk_kernel(const __grid_
     }
     __syncthreads();
     if (warp == 8) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
+    leave();
 }
 
 template <int CODE, int TYPE, int D, bool SHARED>
@@ -1000,6 +1009,7 @@ kvl_status launch_chunk(const AttendArgs &a, int sms, void *stream)
 {
     static std::atomic<unsigned long long> ready[kMaxDevices];
     if (!allow_smem(attend_chunk_kernel<CODE, TYPE, D, SHARED>, ready, Chunk<D>::kSmem)) return KVL_ECUDA;
+    if constexpr (SHARED) return launch_behind(attend_chunk_kernel<CODE, TYPE, D, SHARED>, sms, kThreads, Chunk<D>::kSmem, stream, a);
     attend_chunk_kernel<CODE, TYPE, D, SHARED><<<sms, kThreads, Chunk<D>::kSmem, static_cast<cudaStream_t>(stream)>>>(a);
     return launch_status();
 }

@@ -11,7 +11,7 @@ size_t attend_rows_part_bytes(int head_dim)
 
 kvl_status launch_attend_rows(const AttendArgs &a, int64_t most, int sms, void *stream)
 {
-    return launch_rows_part<Part::whole>(a, most, sms, stream);
+    return launch_rows_part<false>(a, most, sms, stream);
 }
 
 }  // namespace kvl

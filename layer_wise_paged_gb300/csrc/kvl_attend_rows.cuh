@@ -21,15 +21,14 @@
 // whose results are joined in shared memory; a job that crosses shares leaves its parts in the
 // workspace and the CTA that finishes last joins them, in order of the shares.
 //
-// The kernel serves whole sequences, and the two parts of attention over a shared prefix (Part).
+// The kernel serves whole sequences, and the parts of attention over a shared prefix.
 #pragma once
 
-#include "kvl_attend_prefix.cuh"
+#include "kvl_attend.cuh"
 
 namespace kvl {
 namespace {
 
-constexpr int kMostParts = 160;  // of a row's shared tokens: no more than there are SMs
 constexpr int kWarps = 6;
 constexpr int kThreads = kWarps * 32;
 constexpr int kPair = 2;          // groups a warp takes at a time (4 at d = 64: 137 us for 256 sequences of 1,500, with 2 123)
@@ -80,38 +79,36 @@ __device__ __forceinline__ uint32_t v_at(int r, int c)
         return r * 256 + ((c ^ (((r >> 1) & 1) | (r & 4))) << 4);
 }
 
-// Whole sequences; the shared tokens of groups, whose rows' results go to a.row_o and a.row_ml; or what follows
-// the shared tokens in each sequence, joined with those.
-enum class Part { whole, shared, own };
-
-template <int NT, Part PART>
+// What a batch entry costs.  With PARTS the first n_seq are the sequences' own tokens, behind the ones they share, and
+// those after them (with a.few) the groups' shared tokens.
+template <int NT, bool PARTS>
 __device__ __forceinline__ Cost cost_of(const AttendArgs &a, int i, void *rep)
 {
     const int B = a.cache.block_tokens, per_block = (B + kGroup - 1) / kGroup;
     Cost c;
     c.lo = 0;
-    if constexpr (PART == Part::shared) {
-        c.e = load_group(a, i, rep);
-    } else {
-        c.e = load_entry(a.seqs, B, i, rep);
-        if constexpr (PART == Part::own) {
-            const Sharing s = reinterpret_cast<const Sharing *>(a.sharing)[i];
+    if constexpr (PARTS) {
+        if (i >= a.seqs.n_seq) {
+            c.e = load_group(a, i - a.seqs.n_seq, rep);
+        } else {
+            c.e = load_entry(a.seqs, B, i, rep);
+            const Sharing s = sharing_of(a, c.e, i, rep);
             c.lo = max(s.tokens, 0);
-            c.group = s.group;
-            c.row0 = s.row0;
             if (s.tokens < 0) c.e.len = c.e.fresh = 0;
         }
+    } else {
+        c.e = load_entry(a.seqs, B, i, rep);
+        c.lo = first_seen(a, c.e.len - c.e.fresh);
     }
     const int64_t rows = int64_t(c.e.fresh) * (a.attn.n_heads / a.cache.n_kv_heads);
     c.tiles = rows > a.max_rows ? 0 : int32_t((rows + 8 * NT - 1) / (8 * NT));
-    if constexpr (PART == Part::whole) c.lo = first_seen(a, c.e.len - c.e.fresh);
     c.g0 = group_of(c.lo, B, per_block);
     // a sequence of no tokens is one group of none: its rows still get their zeros
     c.groups = max(1, c.e.len > 0 ? group_of(c.e.len - 1, B, per_block) + 1 - c.g0 : 0);
     return c;
 }
 
-template <int CODE, int TYPE, int D, int NT, Part PART>
+template <int CODE, int TYPE, int D, int NT, bool PARTS>
 __global__ void __launch_bounds__(kThreads, kCtasPerSm) attend_rows_kernel(const __grid_constant__ AttendArgs a)
 {
     using S = Shape<D, NT>;
@@ -122,36 +119,29 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attend_rows_kernel(const
     __shared__ Cost s_cost;
     __shared__ int s_entry, s_last;
     __shared__ float s_m[kWarps][kRows], s_l[kWarps][kRows], s_cq[kRows];
-    // how a row's own tokens and the parts of the shared ones join
-    struct Join {
-        const float *o;   // the first part's values
-        int64_t step;     // to the next part's
-        int e_step;       // from four elements to the next four
-        int parts;        // -1: the shared tokens' results are missing
-        float own, big, sum;
-    };
-    constexpr bool kOwn = PART == Part::own;
-    __shared__ Join s_join[kOwn ? kRows : 1];
-    __shared__ float s_factor[kOwn ? kRows : 1][kOwn ? kMostParts : 1];
 
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, nn = lane >> 2, kk = lane & 3;
     const int H = a.cache.n_kv_heads, d = a.cache.head_dim, B = a.cache.block_tokens;
     const int G = a.attn.n_heads / H, per_block = (B + kGroup - 1) / kGroup;
     const int64_t N = a.cache.pool_blocks;
 
-    if constexpr (PART == Part::shared) {
+    if constexpr (PARTS) {
         allow_dependents_launch();
-        resolve_entries(a, int(blockIdx.x) * kThreads + tid, int(gridDim.x) * kThreads);
+        for (int i = int(blockIdx.x) * kThreads + int(threadIdx.x); i < a.seqs.n_seq; i += int(gridDim.x) * kThreads) {
+            const Entry e = load_entry(a.seqs, a.cache.block_tokens, i, nullptr);
+            Sharing s = sharing_of(a, e, i, nullptr);
+            if (!e.table) s.tokens = -1;
+            reinterpret_cast<Sharing *>(a.sharing)[i] = s;
+        }
     }
-    if constexpr (PART == Part::own) grid_dependency_wait();
     // ---- this CTA's share of the units ----
-    const int n_seq = PART == Part::shared ? a.shared.n_groups : a.seqs.n_seq, per_thread = (n_seq + kThreads - 1) / kThreads;
+    const int n_seq = a.seqs.n_seq + (PARTS && a.few ? a.shared.n_groups : 0), per_thread = (n_seq + kThreads - 1) / kThreads;
     const int i0 = min(n_seq, tid * per_thread), i1 = min(n_seq, i0 + per_thread);
     auto units_of = [&](const Cost &q) { return uint64_t(H * q.tiles) * uint32_t(q.groups + kJobCost); };
     Cost c;  // of the thread's last entry; kept where it is the only one
     uint64_t mine = 0;
     for (int i = i0; i < i1; ++i) {
-        c = cost_of<NT, PART>(a, i, blockIdx.x == 0 ? a.report : nullptr);
+        c = cost_of<NT, PARTS>(a, i, blockIdx.x == 0 ? a.report : nullptr);
         mine += units_of(c);
     }
     uint64_t scan = mine;
@@ -168,8 +158,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attend_rows_kernel(const
         if (w < warp) before += s_scan[w];
         total += s_scan[w];
     }
-    if constexpr (PART == Part::shared)
-        if (blockIdx.x == 0 && tid == 0) *a.shared_done = total < kMostUnits;
+    if constexpr (PARTS)
+        if (blockIdx.x == 0 && tid == 0) a.parts_done[0] = total < kMostUnits;
     if (total == 0 || total >= kMostUnits) {
         if (total && blockIdx.x == 0 && tid == 0) report(a.report, KVL_ERANGE, n_seq);
         return;
@@ -186,7 +176,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attend_rows_kernel(const
             int i = i0;
             if (per_thread > 1)
                 for (;; ++i) {
-                    c = cost_of<NT, PART>(a, i, nullptr);
+                    c = cost_of<NT, PARTS>(a, i, nullptr);
                     if (x < at + units_of(c)) break;
                     at += units_of(c);
                 }
@@ -217,7 +207,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attend_rows_kernel(const
     while (u < u_end) {
         while (off >= units_of(c)) {  // on to the entry that holds unit u
             off -= uint32_t(units_of(c));
-            c = cost_of<NT, PART>(a, ++entry, nullptr);
+            c = cost_of<NT, PARTS>(a, ++entry, nullptr);
         }
         const uint32_t per_job = c.groups + kJobCost;
         const int job = int(off / per_job), in = int(off - job * per_job);
@@ -230,6 +220,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attend_rows_kernel(const
         const int h = job / c.tiles, tile = job - h * c.tiles;
         const int rows = min(kRows, c.e.fresh * G - tile * kRows);
         const int pos0 = c.e.len - c.e.fresh;
+        const bool of_group = PARTS && entry >= a.seqs.n_seq;  // the shared tokens of a group
 
         // ---- groups of this warp: pair k holds ga + 2 (warp + kWarps k) and the next.  Lane l looks after
         // group l % 2 of pair l / 2 of a batch of 16: its page, scales and place; the next batch's are
@@ -246,7 +237,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attend_rows_kernel(const
             if (nv <= 0) return -1;
             const int32_t page = c.e.table[blk];
             if (page < 0 || page >= N) {
-                report(a.report, KVL_ERANGE, entry);
+                report(a.report, KVL_ERANGE, of_group ? a.shared.groups[entry - a.seqs.n_seq] : entry);
                 nv = 0;
                 return -1;
             }
@@ -355,8 +346,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attend_rows_kernel(const
         int lo[NT][2], hi[NT][2];
         float cq[NT][2];
         const int first_pos = pos0 + (tile * kRows) / G, last_pos = pos0 + (tile * kRows + rows - 1) / G;
-        const bool causal = PART != Part::shared && a.attn.causal;
-        auto first_token = [&](int pos) { return PART == Part::whole ? first_seen(a, pos) : c.lo; };
+        const bool causal = !of_group && a.attn.causal;
+        auto first_token = [&](int pos) { return PARTS ? c.lo : first_seen(a, pos); };
         const int all_hi = causal ? min(c.e.len, first_pos + 1) : c.e.len;
         const int all_lo = first_token(last_pos);
 #pragma unroll
@@ -604,26 +595,11 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attend_rows_kernel(const
             const int row = tile * kRows + r;
             const int64_t t = int64_t(c.e.row0) + row / G;
             const int head = h * G + row % G;
-            if constexpr (PART == Part::shared) {
-                const int64_t at = t * a.attn.n_heads + head;
+            if constexpr (PARTS) {
+                const int64_t at = (t + (of_group ? a.seqs.n_rows : 0)) * a.attn.n_heads + head;
                 *reinterpret_cast<float4 *>(a.row_o + at * D + e) = v;
                 if (e == 0) *reinterpret_cast<float2 *>(a.row_ml + at * 2) = make_float2(big, sum);
                 return;
-            }
-            if constexpr (PART == Part::own) {
-                // what the shared tokens gave: one result of the row, or parts of it, in order
-                const Join &j = s_join[r];
-                if (j.parts < 0) return;
-                v.x *= j.own; v.y *= j.own; v.z *= j.own; v.w *= j.own;
-                sum = j.sum;
-                big = j.big;
-                const float *o = j.o + (e / 4) * j.e_step;
-#pragma unroll 8
-                for (int b = 0; b < j.parts; ++b) {
-                    const float g = s_factor[r][b];
-                    const float4 y = *reinterpret_cast<const float4 *>(o + b * j.step);
-                    v.x += y.x * g; v.y += y.y * g; v.z += y.z * g; v.w += y.w * g;
-                }
             }
             const float inv = sum == 0.f ? 0.f : 1.f / sum;  // 0: the row sees nothing
             uint8_t *dst = static_cast<uint8_t *>(a.attn.out.data) + t * a.attn.out.row_stride +
@@ -632,65 +608,9 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attend_rows_kernel(const
             if (e == 0 && a.attn.lse)
                 a.attn.lse[t * a.attn.n_heads + head] = sum == 0.f ? -INFINITY : (big + __log2f(sum)) * (1.f / kLog2e);
         };
-        // By a warp a row: the factors of row r's own tokens (reference big, sum of weights sum) and of the parts.
-        auto weigh_parts = [&](int r, float big, float sum) {
-            const int row = tile * kRows + r, head = h * G + row % G;
-            const int64_t t = int64_t(c.e.row0) + row / G;
-            const float *ml = nullptr;
-            Join j = {nullptr, 0, 4, 0, 0.f, 0.f, 0.f};
-            int64_t ml_step = 1;  // from a reference to its sum
-            if (c.lo > 0 && a.prefix_rows == 0) {
-                const int64_t at = t * a.attn.n_heads + head;
-                ml = a.row_ml + at * 2;
-                j.o = a.row_o + at * D;
-                j.parts = 1;
-            } else if (c.lo > 0) {
-                const int R = a.prefix_rows, row_g = int(t - c.row0) * G + row % G, tile_g = row_g / R, r_g = row_g - tile_g * R;
-                const int64_t id = int64_t(c.row0) * G / R + c.group + tile_g;
-                const int2 p = reinterpret_cast<const int2 *>(a.prefix_jobs)[id * H + h];
-                // (not there if a wait ran out)
-                j.parts = p.x >= 0 && p.y >= 0 && p.y <= kMostParts && p.x <= a.prefix_most - p.y ? p.y : 0;
-                j.step = int64_t(R) * (D + 2);
-                ml = a.prefix_parts + (j.parts ? p.x : 0) * j.step + r_g;
-                ml_step = R;
-                j.e_step = R == kChunkTileRows ? 4 * R : 4;
-                j.o = ml - r_g + 2 * R + int64_t(r_g) * (R == kChunkTileRows ? 4 : D);
-            }
-            float m = big;
-            for (int b = lane; b < j.parts; b += 32) m = fmaxf(m, ml[b * j.step]);
-#pragma unroll
-            for (int x = 16; x; x >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, x));
-            float all = 0.f;
-            for (int b = lane; b < j.parts; b += 32) {
-                const float mb = ml[b * j.step], f = mb == -INFINITY ? 0.f : exp2_of(mb - m);
-                s_factor[r][b] = f;
-                all += ml[b * j.step + ml_step] * f;
-            }
-#pragma unroll
-            for (int x = 16; x; x >>= 1) all += __shfl_xor_sync(0xffffffffu, all, x);
-            j.own = big == -INFINITY ? 0.f : exp2_of(big - m);
-            j.big = m;
-            j.sum = sum * j.own + all;
-            if (c.lo > 0 && !*a.shared_done) j.parts = -1;
-            if (lane == 0) s_join[r] = j;
-        };
         float *part = a.parts + (int64_t(blockIdx.x) * 2 + (ga == 0 ? 1 : 0)) * S::kPartFloats;
-        if constexpr (kOwn) {
-            if (complete) {
-                for (int r = warp; r < rows; r += kWarps) {
-                    float big = -INFINITY, sum = 0.f;
-#pragma unroll
-                    for (int w = 0; w < kWarps; ++w) big = fmaxf(big, s_m[w][r]);
-#pragma unroll
-                    for (int w = 0; w < kWarps; ++w) sum += s_m[w][r] == -INFINITY ? 0.f : s_l[w][r] * exp2_of(s_m[w][r] - big);
-                    weigh_parts(r, big, sum);
-                }
-                __syncthreads();
-            }
-        }
         for (int x = tid; x < rows * (D / 4); x += kThreads) {
-            // (parts of shared tokens have a row's four elements beside the next row's)
-            const int r = kOwn ? x % rows : x / (D / 4), e = (kOwn ? x / rows : x % (D / 4)) * 4;
+            const int r = x / (D / 4), e = (x % (D / 4)) * 4;
             float big = -INFINITY;
 #pragma unroll
             for (int w = 0; w < kWarps; ++w) big = fmaxf(big, s_m[w][r]);
@@ -753,7 +673,6 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attend_rows_kernel(const
                         s_m[0][r] = big;
                         s_l[0][r] = sum;
                     }
-                    if constexpr (kOwn) weigh_parts(r, big, sum);
                 }
                 __syncthreads();
                 constexpr int kVecs = kRows * (D / 4) / 32;  // vectors of a lane
@@ -778,11 +697,11 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attend_rows_kernel(const
                 for (int x = 0; x < kVecs; ++x) all[(warp * kVecs + x) * 32 + lane] = v[x];
                 __syncthreads();
                 for (int x = tid; x < rows * (D / 4); x += kThreads) {
-                    const int r = kOwn ? x % rows : x / (D / 4), e = (kOwn ? x / rows : x % (D / 4)) * 4, at = r * (D / 4) + e / 4;
-                    float4 y = all[at];
+                    const int r = x / (D / 4), e = (x % (D / 4)) * 4;
+                    float4 y = all[x];
 #pragma unroll
                     for (int w = 1; w < kWarps; ++w) {
-                        const float4 z = all[w * kVecs * 32 + at];
+                        const float4 z = all[w * kVecs * 32 + x];
                         y.x += z.x; y.y += z.y; y.z += z.z; y.w += z.w;
                     }
                     finish(r, e, y, s_m[0][r], s_l[0][r]);
@@ -793,44 +712,42 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attend_rows_kernel(const
     }
 }
 
-template <int CODE, int TYPE, int D, int NT, Part PART>
+template <int CODE, int TYPE, int D, int NT, bool PARTS>
 kvl_status launch_rows(const AttendArgs &a, int sms, void *stream)
 {
     static std::atomic<unsigned long long> ready[kMaxDevices];
-    if (!allow_smem(attend_rows_kernel<CODE, TYPE, D, NT, PART>, ready, Shape<D, NT>::kSmem)) return KVL_ECUDA;
+    if (!allow_smem(attend_rows_kernel<CODE, TYPE, D, NT, PARTS>, ready, Shape<D, NT>::kSmem)) return KVL_ECUDA;
     // (rings of 256 elements leave room for one CTA an SM)
     const int ctas = sms * (2 * Shape<D, NT>::kSmem <= 220 * 1024 ? kCtasPerSm : 1);
-    if constexpr (PART == Part::own)
-        return launch_behind(attend_rows_kernel<CODE, TYPE, D, NT, PART>, ctas, kThreads, Shape<D, NT>::kSmem, stream, a);
-    attend_rows_kernel<CODE, TYPE, D, NT, PART><<<ctas, kThreads, Shape<D, NT>::kSmem, static_cast<cudaStream_t>(stream)>>>(a);
+    attend_rows_kernel<CODE, TYPE, D, NT, PARTS><<<ctas, kThreads, Shape<D, NT>::kSmem, static_cast<cudaStream_t>(stream)>>>(a);
     return launch_status();
 }
 
 // Row tiles of 8 or 16 by the bound on an entry's rows: a tile's tokens are read and converted once.
 // 16 rows of 256 elements would not leave a warp its registers.
-template <int CODE, int TYPE, Part PART>
+template <int CODE, int TYPE, bool PARTS>
 kvl_status launch_rows_dim(const AttendArgs &a, int64_t most, int sms, void *stream)
 {
     // Row tiles of 8 while they hold all rows, else of 16, so that the cache is read half as often (256 sequences
     // of 1,500, 4 rows, d = 128: in tiles of 8 154 us, of 16 215; 40 of 3,000, 8 rows: 57 and 75).
     if (a.cache.head_dim <= 64) {
-        if (most <= 8) return launch_rows<CODE, TYPE, 64, 1, PART>(a, sms, stream);
-        return launch_rows<CODE, TYPE, 64, 2, PART>(a, sms, stream);
+        if (most <= 8) return launch_rows<CODE, TYPE, 64, 1, PARTS>(a, sms, stream);
+        return launch_rows<CODE, TYPE, 64, 2, PARTS>(a, sms, stream);
     }
     if (a.cache.head_dim <= 128)
-        return most <= 8 ? launch_rows<CODE, TYPE, 128, 1, PART>(a, sms, stream) : launch_rows<CODE, TYPE, 128, 2, PART>(a, sms, stream);
-    return launch_rows<CODE, TYPE, 256, 1, PART>(a, sms, stream);
+        return most <= 8 ? launch_rows<CODE, TYPE, 128, 1, PARTS>(a, sms, stream) : launch_rows<CODE, TYPE, 128, 2, PARTS>(a, sms, stream);
+    return launch_rows<CODE, TYPE, 256, 1, PARTS>(a, sms, stream);
 }
 
-template <Part PART>
+template <bool PARTS>
 kvl_status launch_rows_part(const AttendArgs &a, int64_t most, int sms, void *stream)
 {
     const bool bf = a.attn.type == KVL_TYPE_BFLOAT;
     if (a.cache.code_type == KVL_CODE_FLOAT)
-        return bf ? launch_rows_dim<KVL_CODE_FLOAT, KVL_TYPE_BFLOAT, PART>(a, most, sms, stream)
-                  : launch_rows_dim<KVL_CODE_FLOAT, KVL_TYPE_HALF, PART>(a, most, sms, stream);
-    return bf ? launch_rows_dim<KVL_CODE_INT, KVL_TYPE_BFLOAT, PART>(a, most, sms, stream)
-              : launch_rows_dim<KVL_CODE_INT, KVL_TYPE_HALF, PART>(a, most, sms, stream);
+        return bf ? launch_rows_dim<KVL_CODE_FLOAT, KVL_TYPE_BFLOAT, PARTS>(a, most, sms, stream)
+                  : launch_rows_dim<KVL_CODE_FLOAT, KVL_TYPE_HALF, PARTS>(a, most, sms, stream);
+    return bf ? launch_rows_dim<KVL_CODE_INT, KVL_TYPE_BFLOAT, PARTS>(a, most, sms, stream)
+              : launch_rows_dim<KVL_CODE_INT, KVL_TYPE_HALF, PARTS>(a, most, sms, stream);
 }
 
 }  // namespace

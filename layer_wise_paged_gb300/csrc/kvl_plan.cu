@@ -633,7 +633,7 @@ extern "C" int32_t kvl_launches_per_call(int32_t which)
     case 7: case 8: case 9: return 1;   // pages extend, fork, free
     case 10: return 2;                  // compact: counts, then tables
     case 11: return 1;                  // copy
-    case 12: return 2;                  // attend_shared: shared tokens, own tokens
+    case 12: return 3;                  // attend_shared: own tokens, shared tokens, join
     case 13: return 2;                  // weigh: rows, then their weights
     case 14: return 2;                  // evict: plan, select
     case 15: return 1;                  // tokens move

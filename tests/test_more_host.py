@@ -152,4 +152,4 @@ def test_move_refusals(lib):
 
 
 def test_launch_counts(lib):
-    assert [kvl.kvl_launches_per_call(w) for w in (12, 13, 14, 15, 16)] == [2, 2, 2, 1, 0]
+    assert [kvl.kvl_launches_per_call(w) for w in (12, 13, 14, 15, 16)] == [3, 2, 2, 1, 0]
