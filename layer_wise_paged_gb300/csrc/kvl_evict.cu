@@ -190,15 +190,22 @@ __global__ void __launch_bounds__(kThreads) evict_select_kernel(const __grid_con
     const int take = q.keep - f - r;        // how many of them stay; fewer than there are
     float *mass = a.e.mass ? a.e.mass + int64_t(q.slot) * a.e.mass_stride : nullptr;
     int32_t *table = a.p.tables + int64_t(q.slot) * a.p.table_stride;
-    const int64_t round = int64_t(ranks) * kThreads * kRun;
-    const int rounds = int(ceil_div64(q.len, round));
+    // Token of a round's slot y; slots from `live` on hold none (of any thread).  (A sequence's end and a round fit 32 bits
+    // without a sign.)
+    const uint32_t round = uint32_t(ranks) * kThreads * kRun, len = uint32_t(q.len);
+    const int rounds = int((len - 1) / round) + 1;
     float x[kRun];
-    auto token = [&](int n, int y) { return n * round + (int64_t(rank) * kRun + y) * kThreads + tid; };
+    auto first_of = [&](int n) { return n * round + uint32_t(rank) * (kRun * kThreads); };
+    auto live_of = [&](int n) { return first_of(n) < len ? int((len - first_of(n) - 1) / kThreads) + 1 : 0; };
     auto load = [&](int n) {
+        const int live = live_of(n);
 #pragma unroll
         for (int y = 0; y < kRun; ++y) {
-            const int64_t j = token(n, y);
-            x[y] = mass && j < q.len ? __ldcg(mass + j) : 0.f;
+            x[y] = 0.f;
+            if (y < live) {
+                const uint32_t j = first_of(n) + y * kThreads + tid;
+                if (mass && j < len) x[y] = __ldcg(mass + j);
+            }
         }
     };
     load(0);
@@ -219,11 +226,12 @@ __global__ void __launch_bounds__(kThreads) evict_select_kernel(const __grid_con
 #pragma unroll 1
             for (int n = 0; n < rounds; ++n) {
                 if (rounds > 1) load(n);
+                const int live = live_of(n);
 #pragma unroll
                 for (int y = 0; y < kRun; ++y) {
-                    const int64_t j = token(n, y);
-                    const uint32_t k = key_of(x[y]);
-                    if (j >= lo && j < hi && (k & mask) == known) atomicAdd(&mine[(k >> shift) & (bins - 1)], 1u);
+                    if (y >= live) continue;
+                    const uint32_t j = first_of(n) + y * kThreads + tid, k = key_of(x[y]);
+                    if (j >= uint32_t(lo) && j < uint32_t(hi) && (k & mask) == known) atomicAdd(&mine[(k >> shift) & (bins - 1)], 1u);
                 }
             }
             cluster.sync();
@@ -263,13 +271,18 @@ __global__ void __launch_bounds__(kThreads) evict_select_kernel(const __grid_con
 #pragma unroll 1
     for (int n = 0; n < rounds; ++n) {
         if (rounds > 1) load(n);
+        const int live = live_of(n);
         unsigned sure[kRun], even[kRun];
 #pragma unroll
         for (int y = 0; y < kRun; ++y) {
-            const int64_t j = token(n, y);
-            const uint32_t k = key_of(x[y]);
-            const bool between = j >= lo && j < hi;
-            sure[y] = __ballot_sync(0xffffffffu, j < q.len && (!between || (take > 0 && k > least)));
+            sure[y] = even[y] = 0;
+            if (y >= live) {
+                if (lane == 0) s_count[y * 32 + warp] = 0;
+                continue;
+            }
+            const uint32_t j = first_of(n) + y * kThreads + tid, k = key_of(x[y]);
+            const bool between = j >= uint32_t(lo) && j < uint32_t(hi);
+            sure[y] = __ballot_sync(0xffffffffu, j < len && (!between || (take > 0 && k > least)));
             even[y] = __ballot_sync(0xffffffffu, between && take > 0 && k == least);
             if (lane == 0) s_count[y * 32 + warp] = __popc(sure[y]) | __popc(even[y]) << 16;
         }
@@ -289,12 +302,13 @@ __global__ void __launch_bounds__(kThreads) evict_select_kernel(const __grid_con
         kept += all;
 #pragma unroll
         for (int y = 0; y < kRun; ++y) {
+            if (y >= live) continue;
             const uint32_t w = s_before[y * 32 + warp], below = (1u << lane) - 1;
             const int s = int(ahead & 0xffffffffll) + int(w & 0xffffu) + __popc(sure[y] & below);
             const int v = int(ahead >> 32) + int(w >> 16) + __popc(even[y] & below);
             const bool stays = sure[y] >> lane & 1u, equal = even[y] >> lane & 1u;
             if (stays || (equal && v < int(equals))) {
-                const int j = int(token(n, y)), k = s + min(v, int(equals)), k_blk = a.by_block(k), at = k_blk - q.stay;
+                const int j = int(first_of(n) + y * kThreads + tid), k = s + min(v, int(equals)), k_blk = a.by_block(k), at = k_blk - q.stay;
                 if (mass) mass[k] = x[y];
                 if (at >= 0) {
                     const int j_blk = a.by_block(j);
@@ -331,7 +345,9 @@ __global__ void __launch_bounds__(kThreads) evict_select_kernel(const __grid_con
 
 // ---- codes -------------------------------------------------------------------------------------
 
-constexpr int kMoveThreads = 256, kMoveCtasPerSm = 4;
+// (8 prompts to 1,024 tokens, 32 layers: 224 us; with four CTAs an SM, which spill, 268, with six of half the tokens on
+// their way 306)
+constexpr int kMoveThreads = 256, kMoveCtasPerSm = 3;
 constexpr int kHeld = 8;  // tokens whose codes a lane has on their way
 
 struct MoveArgs {

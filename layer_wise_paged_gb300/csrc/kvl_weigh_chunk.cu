@@ -387,7 +387,7 @@ __global__ void __launch_bounds__(kThreads, 1) weigh_chunk_kernel(const __grid_c
         uint32_t s = 0, k = 0, joins = 0, sums = 0;  // steps, heads, joins and jobs so far
         bool ok = true;
         do {
-            const int pos0 = job.s.e.len - job.s.e.fresh, rows = job.s.e.fresh * G;
+            const int pos0 = job.s.e.len - job.s.e.fresh, rows = job.s.e.fresh * G;  // (at most 2^26)
             const int sq = a.seqs.slots ? a.seqs.slots[job.entry] : job.entry;
             const float *in = w.mass_in + int64_t(sq) * w.in_stride;
             float *out = w.mass_out + int64_t(sq) * w.out_stride;
@@ -395,7 +395,7 @@ __global__ void __launch_bounds__(kThreads, 1) weigh_chunk_kernel(const __grid_c
             float held[2], sum[2] = {0.f, 0.f};
             int32_t page[2];
             // rows [see_a, see_b) of the entry see the token; a lane without one may see any
-            int64_t see_a[2], see_b[2];
+            int see_a[2], see_b[2];
 #pragma unroll
             for (int y = 0; y < 2; ++y) {
                 const int g = job.tile * kJobGroups + (slot + 128 * y) / kGroup;
@@ -406,9 +406,11 @@ __global__ void __launch_bounds__(kThreads, 1) weigh_chunk_kernel(const __grid_c
                 // (both on their way during the steps)
                 held[y] = side || !there || (w.begin && j >= pos0) ? 0.f : in[j];
                 page[y] = there && !side ? job.s.e.table[blk] : -1;
-                see_a[y] = there && a.attn.causal ? max((int64_t(j) - pos0) * G, int64_t(0)) : 0;
-                see_b[y] = there && a.attn.window > 0 ? (int64_t(j) + a.attn.window - pos0) * G : INT64_MAX;
+                see_a[y] = there && a.attn.causal ? int(max((int64_t(j) - pos0) * G, int64_t(0))) : 0;  // (past the rows, if none)
+                see_b[y] = there && a.attn.window > 0 ? int(max(min((int64_t(j) + a.attn.window - pos0) * G, int64_t(rows)), int64_t(0))) : rows;
             }
+            // (of most tiles every row sees every token)
+            const bool always = __all_sync(0xffffffffu, see_a[0] == 0 && see_a[1] == 0 && see_b[0] >= rows && see_b[1] >= rows);
             int c = job.x0 % job.n;
             for (int x = 0; x < job.taken; ++x, ++s) {
                 const uint32_t set = s & 1, ph = (s >> 1) & 1;
@@ -421,50 +423,62 @@ __global__ void __launch_bounds__(kThreads, 1) weigh_chunk_kernel(const __grid_c
                 if (n_rows > 0) {
                     const float f = consts[kRows - side * 32];
                     float kf[2];
-                    int from[2], to[2];
-                    bool whole = true;
 #pragma unroll
-                    for (int y = 0; y < 2; ++y) {
-                        kf[y] = s_scales[k % kScales][(slot + 128 * y) / kGroup] * f;
-                        from[y] = int(max(see_a[y] - row_a, int64_t(0)));
-                        to[y] = int(min(see_b[y] - row_a, int64_t(kRows)));
-                        whole = whole && from[y] == 0 && to[y] >= n_rows;
-                    }
-                    whole = __all_sync(0xffffffffu, whole);
-                    uint64_t add[2][2] = {{0, 0}, {0, 0}};
-                    auto weigh = [&](const uint32_t (&v)[2][16], int col) {  // 16 rows from row `col` on
-                        const uint64_t k0 = pair_of(kf[0], kf[0]), k1 = pair_of(kf[1], kf[1]);
+                    for (int y = 0; y < 2; ++y) kf[y] = s_scales[k % kScales][(slot + 128 * y) / kGroup] * f;
+                    int from[2] = {0, 0}, to[2] = {kRows, kRows};
+                    bool seen[2] = {true, true}, whole = true;  // by some lane's row; by all
+                    if (!always) {
 #pragma unroll
-                        for (int p = 0; p < 4; ++p) {
-                            const float4 b = *reinterpret_cast<const float4 *>(consts + col + 4 * p);
-#pragma unroll
-                            for (int y = 0; y < 2; ++y)
-#pragma unroll
-                                for (int z = 0; z < 2; ++z) {
-                                    const int i = 4 * p + 2 * z;
-                                    float2 q = split_pair(fma_pair(pair_of(__uint_as_float(v[y][i]), __uint_as_float(v[y][i + 1])), y ? k1 : k0,
-                                                                   z ? pair_of(b.z, b.w) : pair_of(b.x, b.y)));
-                                    q.x = exp2_of(q.x);
-                                    q.y = exp2_of(q.y);
-                                    if (!whole) {
-                                        if (col + i < from[y] || col + i >= to[y]) q.x = 0.f;
-                                        if (col + i + 1 < from[y] || col + i + 1 >= to[y]) q.y = 0.f;
-                                    }
-                                    add[y][z] = add_pair(add[y][z], pair_of(q.x, q.y));
-                                }
+                        for (int y = 0; y < 2; ++y) {
+                            from[y] = see_a[y] - row_a;
+                            to[y] = see_b[y] - row_a;
+                            seen[y] = __any_sync(0xffffffffu, from[y] < n_rows && to[y] > 0);
+                            whole = whole && from[y] <= 0 && to[y] >= n_rows;
                         }
-                    };
+                        whole = __all_sync(0xffffffffu, whole);
+                    }
+                    const uint64_t kk[2] = {pair_of(kf[0], kf[0]), pair_of(kf[1], kf[1])};
+                    uint64_t add[2][2] = {{0, 0}, {0, 0}};
                     uint32_t v[2][16];
-                    tmem_ld16(ts, v[0]);
-                    tmem_ld16(ts + 128, v[1]);
-                    tmem_wait_ld();
-                    weigh(v, 0);
-                    tmem_ld16(ts + 16, v[0]);
-                    tmem_ld16(ts + 144, v[1]);
-                    tmem_wait_ld();
-                    tmem_fence_before();
-                    if (lane == 0) mbar_arrive(bar + 8 * (S_EMPTY + set));
-                    weigh(v, 16);
+#pragma unroll
+                    for (int col = 0; col < 32; col += 16) {
+                        tmem_ld16(ts + col, v[0]);
+                        tmem_ld16(ts + col + 128, v[1]);
+                        tmem_wait_ld();
+                        if (col == 16) {
+                            tmem_fence_before();
+                            if (lane == 0) mbar_arrive(bar + 8 * (S_EMPTY + set));
+                        }
+                        auto weights = [&](int y, int i, uint64_t b) {  // of rows col + i, col + i + 1
+                            float2 q = split_pair(fma_pair(pair_of(__uint_as_float(v[y][i]), __uint_as_float(v[y][i + 1])), kk[y], b));
+                            return make_float2(exp2_of(q.x), exp2_of(q.y));
+                        };
+                        if (whole) {
+#pragma unroll
+                            for (int p = 0; p < 4; ++p) {
+                                const float4 b = *reinterpret_cast<const float4 *>(consts + col + 4 * p);
+#pragma unroll
+                                for (int y = 0; y < 2; ++y) {
+                                    const float2 q = weights(y, 4 * p, pair_of(b.x, b.y)), z = weights(y, 4 * p + 2, pair_of(b.z, b.w));
+                                    add[y][0] = add_pair(add[y][0], pair_of(q.x, q.y));
+                                    add[y][1] = add_pair(add[y][1], pair_of(z.x, z.y));
+                                }
+                            }
+                        } else {
+#pragma unroll
+                            for (int y = 0; y < 2; ++y) {
+                                if (!seen[y]) continue;
+#pragma unroll
+                                for (int i = 0; i < 16; i += 2) {
+                                    const float2 b = *reinterpret_cast<const float2 *>(consts + col + i);
+                                    float2 q = weights(y, i, pair_of(b.x, b.y));
+                                    if (col + i < from[y] || col + i >= to[y]) q.x = 0.f;
+                                    if (col + i + 1 < from[y] || col + i + 1 >= to[y]) q.y = 0.f;
+                                    add[y][0] = add_pair(add[y][0], pair_of(q.x, q.y));
+                                }
+                            }
+                        }
+                    }
 #pragma unroll
                     for (int y = 0; y < 2; ++y) {
                         const float2 t = split_pair(add_pair(add[y][0], add[y][1]));
