@@ -846,6 +846,8 @@ __global__ void __launch_bounds__(kThreads, 1) attend_chunk_kernel(const __grid_
             }
             // ---- the row's result, or its part
             const bool complete = !SHARED && job.complete;
+            // (groups that are not in ascending order may be more jobs than there is room for)
+            if constexpr (SHARED) ok = ok && job.job < a.parts_most - int(blockIdx.x);
             const int rows = job.t.rows, h = job.h;
             const Entry e_ = job.e;
             uint32_t nan_at[D / 32];

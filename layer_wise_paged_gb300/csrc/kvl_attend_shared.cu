@@ -145,12 +145,17 @@ __global__ void __launch_bounds__(kThreads) join_kernel(const __grid_constant__ 
     if (a.attn.lse && lane == 0) a.attn.lse[row] = sum == 0.f ? -INFINITY : (m + __log2f(sum)) * (1.f / kLog2e);
 }
 
+int64_t join_ctas(const kvl_cache &c, int64_t n_rows, int n_heads)
+{
+    const int D = padded_dim(c.head_dim);
+    return ceil_div64(n_rows * n_heads * (D / 4 < 32 ? D / 4 : 32), kThreads);
+}
+
 template <int TYPE>
 kvl_status launch_join(const AttendArgs &a, void *stream)
 {
-    const int D = padded_dim(a.cache.head_dim), lanes = D / 4 < 32 ? D / 4 : 32;
-    const int64_t ctas = ceil_div64(a.seqs.n_rows * a.attn.n_heads * lanes, kThreads);
-    if (ctas > INT32_MAX) return KVL_EINVAL;
+    const int D = padded_dim(a.cache.head_dim);
+    const int64_t ctas = join_ctas(a.cache, a.seqs.n_rows, a.attn.n_heads);
     return launch_behind(D == 64 ? join_kernel<TYPE, 64> : D == 128 ? join_kernel<TYPE, 128> : join_kernel<TYPE, 256>,
                          unsigned(ctas), kThreads, 0, stream, a);
 }
@@ -166,7 +171,8 @@ extern "C" size_t kvl_attend_shared_parts_bytes(const kvl_cache *cache, int32_t 
     if (check_cache(cache) != KVL_OK || n_seq < 0 || n_seq > (1 << 20) || n_groups < 0 || n_groups > (1 << 20) || n_rows < 0 ||
         n_rows > INT32_MAX || n_heads <= 0 || n_heads > 65535 || n_heads % cache->n_kv_heads)
         return 0;
-    return layout_of(*cache, n_seq, n_groups, n_rows, n_heads).bytes;
+    const Layout l = layout_of(*cache, n_seq, n_groups, n_rows, n_heads);
+    return l.most > INT32_MAX ? 0 : l.bytes;
 }
 
 extern "C" kvl_status kvl_attend_shared(const kvl_cache *cache, int32_t layer, const kvl_sequences *seqs,
@@ -192,7 +198,9 @@ extern "C" kvl_status kvl_attend_shared(const kvl_cache *cache, int32_t layer, c
         return kvl_attend(cache, layer, seqs, attn, d_workspace, workspace_bytes, d_report, stream);
     const int sms = sm_count();
     if (sms <= 0) return KVL_ECUDA;
+    if (join_ctas(*cache, seqs->n_rows, attn->n_heads) > INT32_MAX) return KVL_EINVAL;
     const Layout l = layout_of(*cache, seqs->n_seq, shared->n_groups, seqs->n_rows, attn->n_heads);
+    if (l.most > INT32_MAX) return KVL_EINVAL;
     uint8_t *base = static_cast<uint8_t *>(d_parts);
     AttendArgs a = attend_args(cache, layer, seqs, attn, d_workspace, d_report);
     a.shared = *shared;

@@ -4,7 +4,7 @@
 // through all KV heads, so that a group's sum stays in its registers and has one writer: S^T [16 tokens x 8 rows]
 // = K [16 x d] Q^T with 16 x 8 x 16 tensor instructions, codes converted in registers (as attention of few rows
 // does), weights by one exponential each, summed over the columns.  K comes through the warp's own ring of tiles
-// (16 tokens of a head) by 16-byte asynchronous copies.  The rows' Q of all heads is held in shared memory; more
+// (16 tokens of two heads, whose products are independent chains) by 16-byte asynchronous copies.  The rows' Q of all heads is held in shared memory; more
 // rows than a tile, or more heads than fit, take further passes over the groups.
 //
 // Work: the groups of all entries in a row are cut into equal contiguous shares, one a CTA.
@@ -15,14 +15,16 @@ namespace {
 
 constexpr int kWarps = 8;
 constexpr int kThreads = kWarps * 32;
-constexpr int kStages = 4;       // tiles of a warp's ring
+constexpr int kPair = 2;         // heads of a tile (one: 256 ragged sequences 147 us, two 136)
+constexpr int kStages = 2;       // tiles of a warp's ring (3 at d = 64: the same; of one head 3: the same, 6: 198 us)
 constexpr int kCtasPerSm = 2;
 constexpr int kQBytes = 40 * 1024;
 
 template <int D, int NT>
 struct Shape {
     static constexpr int kRows = 8 * NT;
-    static constexpr int kTile = kGroup * D;
+    static constexpr int kHead = kGroup * D;
+    static constexpr int kTile = kPair * kHead;
     static constexpr int kHeadBytes = kRows * (D * 2 + 8);  // Q of a head, and (factor, offset) of its rows
     static constexpr int kSmem = kQBytes + kWarps * kStages * kTile;
 };
@@ -58,7 +60,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) weigh_rows_kernel(const 
     __shared__ uint64_t s_scan[kWarps];
     __shared__ uint32_t s_off;
     __shared__ int s_entry;
-    __shared__ float s_scale[kWarps][kStages];
+    __shared__ float s_scale[kWarps][kStages * kPair];
     const AttendArgs &a = w.t;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, nn = lane >> 2, kk = lane & 3;
     const int H = a.cache.n_kv_heads, d = a.cache.head_dim, B = a.cache.block_tokens;
@@ -218,16 +220,22 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) weigh_rows_kernel(const 
                         const int nv = page < 0 || t0 >= any_hi || t0 + kGroup <= any_lo ? 0 : __shfl_sync(0xffffffffu, ahead ? nv_n : nv_l, load_k & 31);
                         const int h = ha + load_h;
                         const uint8_t *src = codes + (((plane + max(page, 0)) * B + t0 % B) * H + h) * d;
-                        const uint32_t dst = ring + at_stage * S::kTile;
 #pragma unroll
-                        for (int x = 0; x < D / 32; ++x) {
-                            const int r = x * (32 / kChunks) + row_l;
-                            const bool ok = r < nv && ch_l * 16 < d;
-                            copy_async16(dst + k_at<D>(r, ch_l), src + (ok ? r * row_bytes + ch_l * 16 : 0), ok);
+                        for (int y = 0; y < kPair; ++y) {
+                            const uint32_t dst = ring + at_stage * S::kTile + y * S::kHead;
+                            const bool there = load_h + y < heads;
+#pragma unroll
+                            for (int x = 0; x < D / 32; ++x) {
+                                const int r = x * (32 / kChunks) + row_l;
+                                const bool ok = there && r < nv && ch_l * 16 < d;
+                                copy_async16(dst + k_at<D>(r, ch_l), src + (ok ? r * row_bytes + y * d + ch_l * 16 : 0), ok);
+                            }
                         }
-                        if (lane == 0 && nv > 0) copy_async4(scale_at + 4 * at_stage, a.cache.scales + (plane + page) * H + h);
+                        if (lane < kPair && load_h + lane < heads && nv > 0)
+                            copy_async4(scale_at + 4 * (at_stage * kPair + lane), a.cache.scales + (plane + page) * H + h + lane);
                         at_stage = at_stage + 1 == kStages ? 0 : at_stage + 1;
-                        if (++load_h == heads) {
+                        load_h += kPair;
+                        if (load_h >= heads) {
                             load_h = 0;
                             ++load_k;
                         }
@@ -256,49 +264,60 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) weigh_rows_kernel(const 
                         if (kk == 0 && nn + 8 * y < nv)
                             held[y] = again ? out[j] : w.begin && j >= pos0 ? 0.f : in[j];
                     }
-                    for (int h = 0; h < heads; ++h) {
+                    for (int h = 0; h < heads; h += kPair) {
                         load_tile();
                         copy_async_wait<kStages - 1>();
                         __syncwarp();
                         if (seen) {
                             const uint8_t *kt = smem + (ring - smem_u32(smem)) + stage * S::kTile;
-                            const float ks = s_scale[warp][stage];
-                            float s[NT][4];
+                            float s[kPair][NT][4];
 #pragma unroll
-                            for (int t = 0; t < NT; ++t) s[t][0] = s[t][1] = s[t][2] = s[t][3] = 0.f;
+                            for (int y = 0; y < kPair; ++y)
+#pragma unroll
+                                for (int t = 0; t < NT; ++t) s[y][t][0] = s[y][t][1] = s[y][t][2] = s[y][t][3] = 0.f;
+                            // (of an odd number of heads the last tile's second half is zeros: its Q is not looked at)
 #pragma unroll
                             for (int i = 0; i < D / 64; ++i) {
                                 const int ch = kk + 4 * i;
-                                const uint4 ka = *reinterpret_cast<const uint4 *>(kt + k_at<D>(nn, ch));
-                                const uint4 kb = *reinterpret_cast<const uint4 *>(kt + k_at<D>(nn + 8, ch));
-                                uint32_t q[NT][8];
 #pragma unroll
-                                for (int t = 0; t < NT; ++t) {
-                                    const uint4 *p = reinterpret_cast<const uint4 *>(sq + (h * kRows + 8 * t + nn) * D + ch * 16);
-                                    const uint4 x = p[0], y = p[1];
-                                    q[t][0] = x.x; q[t][1] = x.y; q[t][2] = x.z; q[t][3] = x.w;
-                                    q[t][4] = y.x; q[t][5] = y.y; q[t][6] = y.z; q[t][7] = y.w;
-                                }
-                                const uint32_t wa[4] = {ka.x, ka.y, ka.z, ka.w}, wb[4] = {kb.x, kb.y, kb.z, kb.w};
+                                for (int y = 0; y < kPair; ++y) {
+                                    if (y > 0 && h + y >= heads) continue;
+                                    const uint4 ka = *reinterpret_cast<const uint4 *>(kt + y * S::kHead + k_at<D>(nn, ch));
+                                    const uint4 kb = *reinterpret_cast<const uint4 *>(kt + y * S::kHead + k_at<D>(nn + 8, ch));
+                                    uint32_t q[NT][8];
 #pragma unroll
-                                for (int z = 0; z < 4; ++z) {
-                                    uint32_t a0, a1, a2, a3;
-                                    codes_of<CODE>(wa[z], a0, a2);
-                                    codes_of<CODE>(wb[z], a1, a3);
+                                    for (int t = 0; t < NT; ++t) {
+                                        const uint4 *p = reinterpret_cast<const uint4 *>(sq + ((h + y) * kRows + 8 * t + nn) * D + ch * 16);
+                                        const uint4 x = p[0], z = p[1];
+                                        q[t][0] = x.x; q[t][1] = x.y; q[t][2] = x.z; q[t][3] = x.w;
+                                        q[t][4] = z.x; q[t][5] = z.y; q[t][6] = z.z; q[t][7] = z.w;
+                                    }
+                                    const uint32_t wa[4] = {ka.x, ka.y, ka.z, ka.w}, wb[4] = {kb.x, kb.y, kb.z, kb.w};
 #pragma unroll
-                                    for (int t = 0; t < NT; ++t) mma16816(s[t], a0, a1, a2, a3, q[t][2 * z], q[t][2 * z + 1]);
+                                    for (int z = 0; z < 4; ++z) {
+                                        uint32_t a0, a1, a2, a3;
+                                        codes_of<CODE>(wa[z], a0, a2);
+                                        codes_of<CODE>(wb[z], a1, a3);
+#pragma unroll
+                                        for (int t = 0; t < NT; ++t) mma16816(s[y][t], a0, a1, a2, a3, q[t][2 * z], q[t][2 * z + 1]);
+                                    }
                                 }
                             }
 #pragma unroll
-                            for (int t = 0; t < NT; ++t) {
-                                const float4 fb = *reinterpret_cast<const float4 *>(s_fb + h * kRows + 8 * t + 2 * kk);
+                            for (int y = 0; y < kPair; ++y) {
+                                if (y > 0 && h + y >= heads) continue;
+                                const float ks = s_scale[warp][stage * kPair + y];
 #pragma unroll
-                                for (int x = 0; x < 4; ++x) {
-                                    const float f = x & 1 ? fb.z : fb.x, b = x & 1 ? fb.w : fb.y;
-                                    const int j = t0 + nn + 8 * (x >> 1);
-                                    const bool hide = b == -INFINITY || (!whole && (nn + 8 * (x >> 1) >= nv || j < lo[t][x & 1] || j >= hi[t][x & 1]));
-                                    const float p = exp2_of(fmaf(s[t][x], ks * f, b));
-                                    sum[x >> 1] += hide ? 0.f : p;
+                                for (int t = 0; t < NT; ++t) {
+                                    const float4 fb = *reinterpret_cast<const float4 *>(s_fb + (h + y) * kRows + 8 * t + 2 * kk);
+#pragma unroll
+                                    for (int x = 0; x < 4; ++x) {
+                                        const float f = x & 1 ? fb.z : fb.x, b = x & 1 ? fb.w : fb.y;
+                                        const int j = t0 + nn + 8 * (x >> 1);
+                                        const bool hide = b == -INFINITY || (!whole && (nn + 8 * (x >> 1) >= nv || j < lo[t][x & 1] || j >= hi[t][x & 1]));
+                                        const float p = exp2_of(fmaf(s[y][t][x], ks * f, b));
+                                        sum[x >> 1] += hide ? 0.f : p;
+                                    }
                                 }
                             }
                         }
