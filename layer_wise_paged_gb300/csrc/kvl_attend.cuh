@@ -113,17 +113,51 @@ struct alignas(16) Sharing {
     int32_t tokens, group, row0, reserved;
 };
 
+// Up to kHeldGroups groups as a CTA holds them in shared memory: looked up there, an entry's sharing is a few dozen
+// cycles, in memory half a dozen loads one after another.
+constexpr int kHeldGroups = 128;
+struct HeldGroup {
+    int32_t tokens;            // as given
+    int32_t len, row0, fresh;  // of load_group
+};
+struct HeldGroups {
+    int32_t first[kHeldGroups + 1];
+    HeldGroup group[kHeldGroups];
+};
+
+// By a whole CTA, before a barrier.
+__device__ __forceinline__ void hold_groups(const AttendArgs &a, HeldGroups &held)
+{
+    const int n = a.shared.n_groups;
+    if (n > kHeldGroups) return;
+    for (int g = threadIdx.x; g <= n; g += blockDim.x) {
+        held.first[g] = a.shared.groups[g];
+        if (g == n) continue;
+        const Entry p = load_group(a, g, nullptr);
+        held.group[g] = HeldGroup{a.shared.tokens[g], p.len, p.row0, p.fresh};
+    }
+}
+
 // Entry i, resolved as e; one whose group is left out, or one of whose rows does not see all shared tokens, is left out.
-__device__ __forceinline__ Sharing sharing_of(const AttendArgs &a, const Entry &e, int32_t i, void *rep)
+__device__ __forceinline__ Sharing sharing_of(const AttendArgs &a, const HeldGroups &held, const Entry &e, int32_t i, void *rep)
 {
     Sharing s = {0, 0, 0, 0};
+    const bool here = a.shared.n_groups <= kHeldGroups;
+    const int32_t *first = here ? held.first : a.shared.groups;
     int lo = -1, hi = a.shared.n_groups;  // the last group that begins at i or before
     while (hi - lo > 1) {
         const int mid = (lo + hi) >> 1;
-        if (a.shared.groups[mid] <= i) lo = mid; else hi = mid;
+        if (first[mid] <= i) lo = mid; else hi = mid;
     }
-    if (e.fresh <= 0 || lo < 0 || i >= a.shared.groups[lo + 1] || a.shared.tokens[lo] == 0) return s;
-    const Entry p = load_group(a, lo, nullptr);
+    if (e.fresh <= 0 || lo < 0 || i >= first[lo + 1]) return s;
+    HeldGroup p;
+    if (here) {
+        p = held.group[lo];
+    } else {
+        const Entry g = load_group(a, lo, nullptr);
+        p = HeldGroup{a.shared.tokens[lo], g.len, g.row0, g.fresh};
+    }
+    if (p.tokens == 0) return s;
     s.group = lo;
     s.row0 = p.row0;
     s.tokens = p.len;

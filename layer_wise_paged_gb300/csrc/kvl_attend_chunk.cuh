@@ -899,11 +899,18 @@ __global__ void __launch_bounds__(kThreads, 1) attend_chunk_kernel(const __grid_
                                 for (int y = 0; y < 8; ++y) v[y] = __uint_as_float(x[8 * e + y]) * inv;
                                 if (32 * c + 8 * e < d) store8<TYPE>(dst + 2 * (32 * c + 8 * e), v);
                             }
+                        } else if constexpr (SHARED) {
+                            // (the parts of shared tokens are read a row at a time: 32 bytes a store, whole sectors)
+#pragma unroll
+                            for (int e = 0; e < 4; ++e)
+                                asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(part + 2 * kJobRows + r * D + 32 * c + 8 * e),
+                                             "r"(x[8 * e]), "r"(x[8 * e + 1]), "r"(x[8 * e + 2]), "r"(x[8 * e + 3]), "r"(x[8 * e + 4]),
+                                             "r"(x[8 * e + 5]), "r"(x[8 * e + 6]), "r"(x[8 * e + 7])
+                                             : "memory");
                         } else {
-                            // (the parts of shared tokens are read a row at a time)
 #pragma unroll
                             for (int e = 0; e < 8; ++e)
-                                *reinterpret_cast<uint4 *>(part + 2 * kJobRows + (SHARED ? r * D + 32 * c + 4 * e : (int64_t(8 * c + e) * kJobRows + r) * 4)) =
+                                *reinterpret_cast<uint4 *>(part + 2 * kJobRows + (int64_t(8 * c + e) * kJobRows + r) * 4) =
                                     make_uint4(x[4 * e], x[4 * e + 1], x[4 * e + 2], x[4 * e + 3]);
                         }
                     }

@@ -82,7 +82,7 @@ __device__ __forceinline__ uint32_t v_at(int r, int c)
 // What a batch entry costs.  With PARTS the first n_seq are the sequences' own tokens, behind the ones they share, and
 // those after them (with a.few) the groups' shared tokens.
 template <int NT, bool PARTS>
-__device__ __forceinline__ Cost cost_of(const AttendArgs &a, int i, void *rep)
+__device__ __forceinline__ Cost cost_of(const AttendArgs &a, const HeldGroups *held, int i, void *rep)
 {
     const int B = a.cache.block_tokens, per_block = (B + kGroup - 1) / kGroup;
     Cost c;
@@ -92,7 +92,7 @@ __device__ __forceinline__ Cost cost_of(const AttendArgs &a, int i, void *rep)
             c.e = load_group(a, i - a.seqs.n_seq, rep);
         } else {
             c.e = load_entry(a.seqs, B, i, rep);
-            const Sharing s = sharing_of(a, c.e, i, rep);
+            const Sharing s = sharing_of(a, *held, c.e, i, rep);
             c.lo = max(s.tokens, 0);
             if (s.tokens < 0) c.e.len = c.e.fresh = 0;
         }
@@ -125,11 +125,16 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attend_rows_kernel(const
     const int G = a.attn.n_heads / H, per_block = (B + kGroup - 1) / kGroup;
     const int64_t N = a.cache.pool_blocks;
 
+    const HeldGroups *held = nullptr;
     if constexpr (PARTS) {
+        __shared__ HeldGroups s_groups;
+        held = &s_groups;
         allow_dependents_launch();
+        hold_groups(a, s_groups);
+        __syncthreads();
         for (int i = int(blockIdx.x) * kThreads + int(threadIdx.x); i < a.seqs.n_seq; i += int(gridDim.x) * kThreads) {
             const Entry e = load_entry(a.seqs, a.cache.block_tokens, i, nullptr);
-            Sharing s = sharing_of(a, e, i, nullptr);
+            Sharing s = sharing_of(a, s_groups, e, i, nullptr);
             if (!e.table) s.tokens = -1;
             reinterpret_cast<Sharing *>(a.sharing)[i] = s;
         }
@@ -141,7 +146,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attend_rows_kernel(const
     Cost c;  // of the thread's last entry; kept where it is the only one
     uint64_t mine = 0;
     for (int i = i0; i < i1; ++i) {
-        c = cost_of<NT, PARTS>(a, i, blockIdx.x == 0 ? a.report : nullptr);
+        c = cost_of<NT, PARTS>(a, held, i, blockIdx.x == 0 ? a.report : nullptr);
         mine += units_of(c);
     }
     uint64_t scan = mine;
@@ -176,7 +181,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attend_rows_kernel(const
             int i = i0;
             if (per_thread > 1)
                 for (;; ++i) {
-                    c = cost_of<NT, PARTS>(a, i, nullptr);
+                    c = cost_of<NT, PARTS>(a, held, i, nullptr);
                     if (x < at + units_of(c)) break;
                     at += units_of(c);
                 }
@@ -207,7 +212,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attend_rows_kernel(const
     while (u < u_end) {
         while (off >= units_of(c)) {  // on to the entry that holds unit u
             off -= uint32_t(units_of(c));
-            c = cost_of<NT, PARTS>(a, ++entry, nullptr);
+            c = cost_of<NT, PARTS>(a, held, ++entry, nullptr);
         }
         const uint32_t per_job = c.groups + kJobCost;
         const int job = int(off / per_job), in = int(off - job * per_job);

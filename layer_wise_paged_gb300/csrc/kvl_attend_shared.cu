@@ -46,7 +46,7 @@ Layout layout_of(const kvl_cache &c, int n_seq, int n_groups, int64_t n_rows, in
         l.most = l.jobs + workspace_sms();
         l.part_jobs = (l.bytes + 15) & ~size_t(15);
         l.parts = (l.part_jobs + size_t(l.jobs) * 8 + 15) & ~size_t(15);
-        l.bytes = l.parts + size_t(l.most) * kChunkJobRows * (D + 2) * 4;
+        l.bytes = l.parts + size_t(l.most) * kChunkJobRows * (D + 2) * 4 + 16;  // (to begin on 32 bytes)
     }
     return l;
 }
@@ -65,9 +65,7 @@ __global__ void __launch_bounds__(kThreads) join_kernel(const __grid_constant__ 
     const int heads = a.attn.n_heads, n_seq = a.seqs.n_seq;
     const int64_t t = unit / heads;
     const int head = int(unit - t * heads);
-    grid_dependency_wait();
-    if (t >= a.seqs.n_rows || a.parts_done[0] == 0 || (!a.few && a.parts_done[1] == 0)) return;
-    // the row's entry: the last that starts at t or before
+    // the row's entry: the last that starts at t or before (looked for while the kernels before run)
     int lo = 0, hi = n_seq;
     while (hi - lo > 1) {
         const int step = (hi - lo + kLanes - 1) / kLanes, i = lo + lane * step;
@@ -76,8 +74,11 @@ __global__ void __launch_bounds__(kThreads) join_kernel(const __grid_constant__ 
         lo += last * step;
         hi = min(hi, lo + step);
     }
+    const bool there = t < a.seqs.n_rows && t >= a.seqs.starts[lo] && t < a.seqs.starts[lo + 1];
+    grid_dependency_wait();
     const Sharing s = reinterpret_cast<const Sharing *>(a.sharing)[lo];
-    if (t < a.seqs.starts[lo] || t >= a.seqs.starts[lo + 1] || s.tokens < 0) return;
+    const bool done = a.parts_done[0] != 0 && (a.few || a.parts_done[1] != 0);
+    if (!there || !done || s.tokens < 0) return;
     const int64_t row = t * heads + head;
     const float2 own = *reinterpret_cast<const float2 *>(a.row_ml + row * 2);
     float4 v[kVecs];
@@ -212,7 +213,7 @@ extern "C" kvl_status kvl_attend_shared(const kvl_cache *cache, int32_t layer, c
     s = launch_attend_row_parts(a, l.few ? seqs->n_rows * G : bound * G, sms, stream);
     if (!s && !l.few) {
         a.part_jobs = reinterpret_cast<int32_t *>(base + l.part_jobs);
-        a.group_parts = reinterpret_cast<float *>(base + l.parts);
+        a.group_parts = reinterpret_cast<float *>((reinterpret_cast<uintptr_t>(base + l.parts) + 31) & ~uintptr_t(31));
         a.parts_most = int32_t(l.most);
         s = launch_attend_chunk_groups(a, sms, stream);
     }

@@ -178,6 +178,16 @@ def test_bad_groups(groups, shared, code):
     assert (wout[:, :2] == 77.0).all()
 
 
+def test_groups_out_of_order_stay_within_their_memory():
+    """The same sequences named by two groups: more work than there is room for; it is reported and the call ends."""
+    c = CASES["seventy sequences, int8"]
+    cache, wide, starts = make(c)
+    dev = Q.on_gpu(cache)
+    wout, _ = call(dev, c, wide.cuda(), starts.cuda(), groups=[0, 70, 0, 70, 0, 70], shared=[512] * 5)
+    assert dev.status()[0] == kvl.KVL_EINVAL
+    assert (wout[:, :2] == 77.0).all()
+
+
 def test_pages_out_of_range_are_reported():
     c = CASES["two of one prompt"]
     cache, wide, starts = make(c)
