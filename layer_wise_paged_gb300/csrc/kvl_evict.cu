@@ -179,11 +179,13 @@ __global__ void __launch_bounds__(kThreads) evict_select_kernel(const __grid_con
     const cooperative_groups::cluster_group cluster = cooperative_groups::this_cluster();
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int ranks = int(cluster.num_blocks()), rank = int(cluster.block_rank()), i = blockIdx.x / ranks;
-    grid_dependency_wait();
     allow_dependents_launch();
-    if (a.m.at[a.n] < 0) return;
+    // (the choice needs nothing of the plan, which runs meanwhile; an entry that the plan refuses is not acted on)
     const Ask q = ask_of(a, i);
-    if (!q.cut) return;
+    if (q.error || !q.cut) {
+        grid_dependency_wait();  // the plan has ended when this kernel has
+        return;
+    }
     const int32_t B = a.p.block_tokens;
     const int f = min(a.e.first, q.keep), r = min(a.e.recent, q.keep - f);
     const int lo = f, hi = q.len - r;       // the tokens to choose from
@@ -266,6 +268,8 @@ __global__ void __launch_bounds__(kThreads) evict_select_kernel(const __grid_con
 
     // ---- places, masses, sources.  A round's masses are in registers before any is written, and a token moves down,
     // never past tokens that a later round still reads.
+    grid_dependency_wait();
+    if (a.m.at[a.n] < 0) return;
     const int64_t first_page = a.m.at[i];
     long long kept = 0;  // tokens that stay before this round; those that equal `least` in the high half
 #pragma unroll 1

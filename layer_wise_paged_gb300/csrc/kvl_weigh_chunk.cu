@@ -289,7 +289,6 @@ __global__ void __launch_bounds__(kThreads, 1) weigh_chunk_kernel(const __grid_c
     const WeighArgs &w = args.w;
     const AttendArgs &a = w.t;
     const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
-    grid_dependency_wait();
     const int H = a.cache.n_kv_heads, d = a.cache.head_dim, B = a.cache.block_tokens;
     const int G = a.attn.n_heads / H, per_block = (B + kGroup - 1) / kGroup;
     const int64_t N = a.cache.pool_blocks, plane = int64_t(a.layer) * 2 * N;
@@ -336,10 +335,14 @@ __global__ void __launch_bounds__(kThreads, 1) weigh_chunk_kernel(const __grid_c
         if (pass == 0) {
             if (before == 0 || before >= kMostUnits) {
                 if (before && blockIdx.x == 0 && tid == 0) report(a.report, KVL_ERANGE, a.seqs.n_seq);
+                grid_dependency_wait();  // the rows' kernel has ended when this one has
                 return;
             }
             cut = Cut(uint32_t(before), min(gridDim.x, uint32_t(before)));
-            if (blockIdx.x >= cut.shares) return;
+            if (blockIdx.x >= cut.shares) {
+                grid_dependency_wait();
+                return;
+            }
             u = cut.start(blockIdx.x);
             before = 0;
         }
@@ -661,7 +664,8 @@ __global__ void __launch_bounds__(kThreads, 1) weigh_chunk_kernel(const __grid_c
             mbar_wait_bounded(bar + 8 * LEAVE, 0);
         }
     } else {
-        // ---- rows
+        // ---- rows.  (Only these, and the counters of joins, which come after them, are the first kernel's.)
+        grid_dependency_wait();
         uint32_t s = 0;
         bool ok = true;
         do {
@@ -688,6 +692,7 @@ __global__ void __launch_bounds__(kThreads, 1) weigh_chunk_kernel(const __grid_c
     }
     __syncthreads();
     if (*gone && tid == 0) report(a.report, KVL_ETIMEOUT, blockIdx.x);
+    grid_dependency_wait();
     if (warp == kWeighing + 4) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
 }
 
