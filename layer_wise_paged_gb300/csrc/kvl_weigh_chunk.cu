@@ -96,13 +96,15 @@ __global__ void __launch_bounds__(256) weigh_rows_prepare_kernel(const __grid_co
     __shared__ float s_most[8];
     const int at = (lane % kLanes) * 8;
     uint4 raw[kTurns];
-    float amax = 0.f;  // of finite elements
+    float z_of[kTurns], amax = 0.f;  // of finite elements
 #pragma unroll
     for (int x = 0; x < kTurns; ++x) {
         const int64_t row = chunk * kRows + (warp + 8 * x) * kPer + lane / kLanes;
         raw[x] = make_uint4(0, 0, 0, 0);
+        z_of[x] = 0.f;
         if (row < rows && at < d) {
             const int tok = int(row / G), head = h * G + int(row - int64_t(tok) * G);
+            z_of[x] = a.w.lse[(int64_t(e.row0) + tok) * t.attn.n_heads + head];
             raw[x] = *reinterpret_cast<const uint4 *>(static_cast<const uint8_t *>(t.attn.q.data) +
                                                       (int64_t(e.row0) + tok) * t.attn.q.row_stride + int64_t(head) * t.attn.q.head_stride + 2 * at);
         }
@@ -110,6 +112,7 @@ __global__ void __launch_bounds__(256) weigh_rows_prepare_kernel(const __grid_co
 #pragma unroll
     for (int x = 0; x < kTurns; ++x) {
         float v[8];
+        if (isinf(z_of[x])) raw[x] = make_uint4(0, 0, 0, 0);  // (gives nothing, whatever it holds)
         load8<TYPE>(reinterpret_cast<const uint8_t *>(&raw[x]), v);
 #pragma unroll
         for (int y = 0; y < 8; ++y) amax = fmaxf(amax, isfinite(v[y]) ? fabsf(v[y]) : 0.f);

@@ -163,6 +163,19 @@ def test_infinite_and_nan_lse(new):
     assert torch.isnan(got[:past]).all() and torch.isfinite(got[past:]).all()
 
 
+@pytest.mark.parametrize("garbage", [math.inf, -math.inf, math.nan, 3e38])
+@pytest.mark.parametrize("new", [3, 60])
+def test_rows_of_an_infinite_lse_may_hold_anything(new, garbage):
+    """What pads a batch: rows that give nothing, and that the rows beside them do not feel."""
+    c = case([100], [new], heads=4, kv_heads=1)
+    cache, wide, starts, lse, mass = make(c)
+    lse[1, 1:3], lse[2] = -math.inf, math.inf
+    want, tol = K.weigh(cache, 1, wide[:, 1:5], starts, [0], lse, mass, False, 1 / math.sqrt(128), True, 0)
+    wide[1, 2:4], wide[2] = garbage, garbage
+    dev = Q.on_gpu(cache)
+    held_to(dev.weigh(1, wide.cuda()[:, 1:5], starts.cuda(), lse.cuda(), mass.cuda()), want, tol, c, mass)
+
+
 @pytest.mark.parametrize("new", [3, 60])
 def test_nan_codes_stay_with_their_token(new):
     """A NaN in a token that rows 0 and 1 do not see: with finite lse it reaches that token's mass alone."""
