@@ -38,6 +38,7 @@ _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
 
 _current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 _MOST = 2 ** 31 - 1
+_SHARED_ROWS = 40  # rows of a KV head that an entry may have for kvl_attend_shared to read shared tokens once
 _several = None  # whether there is another device than the current one (asked at the first call)
 
 
@@ -203,7 +204,13 @@ class QuantCache:
         self._capture_id = self._lib.kvl_capture_id
         self._scale = 1.0 / math.sqrt(d)
         self._args = _Args(self)
-        self._moved = None
+        # what an eviction asks to be moved: 8 bytes a token of the pool
+        words = torch.empty(2 * N * B + N + self.n_slots + 2, dtype=torch.int32, device=self.device)
+        words[-1:].zero_()  # nothing yet
+        at = words.data_ptr()
+        to = at + 8 * N * B
+        self._moves = kvl_moves(at, to, to + 4 * N, to + 4 * (N + self.n_slots + 1))
+        self._moves_words = words
         self._report = self.report.data_ptr()
         self.reset_status()
 
@@ -278,13 +285,16 @@ class QuantCache:
         g.n_groups, g.groups, g.tokens = n_groups, _ints(groups, "groups", n_groups + 1), _ints(shared, "shared")
         n_rows, heads, _ = q.shape
         s = self._seqs(c, starts, slots, n_rows)
-        key = s.n_seq, n_groups, n_rows, heads
-        n = self._sizes.get(key)
-        if n is None:
-            n = self._size(key, self._lib.kvl_attend_shared_parts_bytes(self._cache, *key))
-        parts = self._scratch(n, st)
+        n, parts = 0, (None, None)
+        # (what is computed as by attend needs no memory for parts)
+        if window == 0 and (max_new if 0 < max_new < n_rows else n_rows) * heads <= _SHARED_ROWS * self.n_kv_heads:
+            key = s.n_seq, n_groups, n_rows, heads
+            n = self._sizes.get(key)
+            if n is None:
+                n = self._size(key, self._lib.kvl_attend_shared_parts_bytes(self._cache, *key))
+            parts = self._scratch(n, st)
         r = self._lib.kvl_attend_shared(self._cache, layer, s, g, c.attn, ws,
-                                        self._ws_bytes, parts, n, self._report, st)
+                                        self._ws_bytes, parts[0], n, self._report, st)
         if r:
             check(r, "kvl_attend_shared")
         return out
@@ -314,7 +324,8 @@ class QuantCache:
         n = self._sizes.get(key)
         if n is None:
             n = self._size(key, self._lib.kvl_weigh_workspace_bytes(self._cache, *key[:4]))
-        r = self._lib.kvl_weigh(self._cache, layer, s, w, self._scratch(n, st), n, self._report, st)
+        scratch = self._scratch(n, st)
+        r = self._lib.kvl_weigh(self._cache, layer, s, w, scratch[0], n, self._report, st)
         if r:
             check(r, "kvl_weigh")
         return mass if out is None else out
@@ -332,15 +343,16 @@ class QuantCache:
         return n
 
     def _scratch(self, n, st):
-        """Memory (its address) that holds nothing between calls: calls of one stream share one, a graph has its own, as
-        with the workspaces."""
+        """(address, memory) of n bytes or more that hold nothing between calls: calls of one stream share one, a graph has
+        its own, as with the workspaces.  The caller keeps the memory until its launch is made: another thread's
+        call on the stream may put a larger one in its place."""
         capture = self._capture_id(st)
         held = self._held_captured if capture else self._held
         m = held.get(st)
         if m is None or m[0] != capture or m[1] < n:
             with self._on(st):
                 t = torch.empty(max(n, 1 << 16), dtype=torch.uint8, device=self.device)
-            m = held[st] = capture, t.numel(), t.data_ptr(), t
+            m = held[st] = capture, t.numel(), (t.data_ptr(), t)
         return m[2]
 
     def _attention(self, q, out, lse, sm_scale, causal, window, max_new, stream, st):
@@ -432,24 +444,13 @@ class QuantCache:
         e.mass, e.mass_stride = (None, 0) if mass is None else self._mass(mass, "mass")
         e.tokens = 0 if mass is None else mass.shape[1]
         st = _stream(stream, self._index)
-        check(self._lib.kvl_pages_evict(self._pages, n, _ints(slots, "slots"), e, self._moves(st), self._report, st),
+        check(self._lib.kvl_pages_evict(self._pages, n, _ints(slots, "slots"), e, self._moves, self._report, st),
               "kvl_pages_evict")
 
     def move_tokens(self, stream=None):
         """Move the tokens that the last evict kept into their fresh pages (every layer)."""
         st = _stream(stream, self._index)
-        check(self._lib.kvl_tokens_move(self._cache, self._moves(st), self.pool_blocks, self._report, st), "kvl_tokens_move")
-
-    def _moves(self, st):
-        if self._moved is None:  # 8 bytes a token of the pool, at the first eviction
-            with self._on(st):
-                N = self.pool_blocks
-                words = torch.empty(2 * N * self.block_tokens + N + self.n_slots + 2, dtype=torch.int32, device=self.device)
-                words[-1:].zero_()  # nothing to move
-            at = words.data_ptr()
-            to = at + 8 * N * self.block_tokens
-            self._moved = kvl_moves(at, to, to + 4 * N, to + 4 * (N + self.n_slots + 1)), words
-        return self._moved[0]
+        check(self._lib.kvl_tokens_move(self._cache, self._moves, self.pool_blocks, self._report, st), "kvl_tokens_move")
 
     # -- status ---------------------------------------------------------------
     def status(self, stream=None):

@@ -205,6 +205,19 @@ def test_nothing_to_move_before_an_eviction_and_no_entries():
     same(dev, cache, mass.cuda(), mass)
 
 
+def test_nothing_to_move_before_a_captured_eviction_runs():
+    cache, mass = make(case([100], [50]))
+    dev = Q.on_gpu(cache)
+    m, slots, keep = mass.cuda(), ints([0]), ints([50])
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        dev.evict(slots, keep, m)
+    dev.move_tokens()
+    assert dev.status() == (0, 0)
+    same(dev, cache, m, mass)
+
+
 def test_again_and_again():
     """Evictions one after another, beside the pages that the ones before gave up."""
     cache, mass = make(case([200, 150], [120, 100]))
