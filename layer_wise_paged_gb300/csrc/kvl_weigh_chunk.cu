@@ -30,7 +30,9 @@ constexpr int kJobGroups = kTokens / kGroup;  // 16
 constexpr int kRows = 128;                    // of a step
 constexpr int kScales = 4;                    // heads whose scales are kept: the weights of a step may be two heads
                                               // behind the conversion, which is one ahead of its own
-constexpr int kConsts = 4;                    // steps whose rows' factors are kept, likewise
+constexpr int kConsts = 8;                    // steps whose rows' factors are kept: two ahead of the products, and two
+                                              // behind whose weights may still read theirs (they give a step's
+                                              // accumulators back before they have used all of it)
 constexpr int kConstBytes = kRows * 4 + 16;
 constexpr int kBatch = 512;                   // entries whose steps are held at a time
 
