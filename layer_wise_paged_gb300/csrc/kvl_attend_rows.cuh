@@ -44,6 +44,11 @@ constexpr int kCtasPerSm = 2;     // 12 warps an SM: 168 registers a thread, 192
 // 256 sequences of 1,500 122.5 with any; one token of 1,500 10.5, with shares of 40 13.0, with jobs of up to
 // 96 groups whole 14.6, with none whole 10.5.
 constexpr int kJobCost = 48;
+// (A job of the parts of a shared prefix costs less, as the join is another kernel's: 48 prompts of 18 rows on 2,200
+// and their own tokens 62 us with 28, 66 with 22, 63 with 34, 67 with 48; 100 groups of 2 on 1,000 135, 138, 137, 139;
+// 18 for own tokens and 40 for groups 72, 28 and 48 67.  CTAs of 4 warps, 3 an SM: 59.5, but 3 branches of 2,000
+// 15.9 for 14.8.)
+constexpr int kPartJobCost = 28;
 constexpr int kUnitsPerCta = 12;
 constexpr int kSmallJob = 48;
 
@@ -112,7 +117,7 @@ template <int CODE, int TYPE, int D, int NT, bool PARTS>
 __global__ void __launch_bounds__(kThreads, kCtasPerSm) attend_rows_kernel(const __grid_constant__ AttendArgs a)
 {
     using S = Shape<D, NT>;
-    constexpr int kRows = S::kRows, kChunks = D / 16, kLaneBytes = D / 8;
+    constexpr int kRows = S::kRows, kChunks = D / 16, kLaneBytes = D / 8, kCost = PARTS ? kPartJobCost : kJobCost;
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ uint64_t s_scan[kWarps];
     __shared__ uint32_t s_off, s_u[2];
@@ -142,7 +147,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attend_rows_kernel(const
     // ---- this CTA's share of the units ----
     const int n_seq = a.seqs.n_seq + (PARTS && a.few ? a.shared.n_groups : 0), per_thread = (n_seq + kThreads - 1) / kThreads;
     const int i0 = min(n_seq, tid * per_thread), i1 = min(n_seq, i0 + per_thread);
-    auto units_of = [&](const Cost &q) { return uint64_t(H * q.tiles) * uint32_t(q.groups + kJobCost); };
+    auto units_of = [&](const Cost &q) { return uint64_t(H * q.tiles) * uint32_t(q.groups + kCost); };
     Cost c;  // of the thread's last entry; kept where it is the only one
     uint64_t mine = 0;
     for (int i = i0; i < i1; ++i) {
@@ -186,7 +191,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attend_rows_kernel(const
                     at += units_of(c);
                 }
             uint32_t in = uint32_t(x - at);
-            if (c.groups <= kSmallJob) in -= in % (c.groups + kJobCost);
+            if (c.groups <= kSmallJob) in -= in % (c.groups + kCost);
             if (k == 0) {
                 s_entry = i;
                 s_off = in;
@@ -214,11 +219,11 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attend_rows_kernel(const
             off -= uint32_t(units_of(c));
             c = cost_of<NT, PARTS>(a, held, ++entry, nullptr);
         }
-        const uint32_t per_job = c.groups + kJobCost;
+        const uint32_t per_job = c.groups + kCost;
         const int job = int(off / per_job), in = int(off - job * per_job);
         const int taken = int(min(per_job - in, u_end - u));
-        const int ga = max(0, in - kJobCost), gb = max(0, in + taken - kJobCost);
-        const uint32_t group0 = u - in + kJobCost;  // the unit of the job's first group
+        const int ga = max(0, in - kCost), gb = max(0, in + taken - kCost);
+        const uint32_t group0 = u - in + kCost;  // the unit of the job's first group
         off += taken;
         u += taken;
         if (ga == gb) continue;  // its groups are the next share's

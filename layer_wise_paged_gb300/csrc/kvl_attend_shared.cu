@@ -33,8 +33,8 @@ Layout layout_of(const kvl_cache &c, int n_seq, int n_groups, int64_t n_rows, in
     Layout l = {};
     const int D = padded_dim(c.head_dim), G = n_heads / c.n_kv_heads;
     // Rows of a group (fresh tokens x query heads of a KV head) on average.  Both kernels (us, few rows / tensor memory;
-    // 8 KV heads of 128, prefix of 30,000): 16 rows 33 / 53, 32 44 / 53, 64 67 / 56, 128 112 / 59; 16 groups of 32
-    // rows on 2,000 77 / 84; 48 of 18 on 2,600 (4 heads of 64) 73 / 101.
+    // 8 KV heads of 128, prefix of 30,000): 16 rows 34 / 54, 32 43 / 54, 48 53 / 55, 64 64 / 55, 128 109 / 58; 16 groups
+    // on 2,000 32 rows 72 / 85, 48 108 / 98, 64 135 / 110; 48 of 18 on 2,600 (4 heads of 64) 67 / 102.
     l.few = c.head_dim > 128 || n_rows * G <= int64_t(kChunkRows) * n_groups;
     const size_t rows = size_t(n_rows) * n_heads * (l.few ? 2 : 1);
     l.sharing = 16;

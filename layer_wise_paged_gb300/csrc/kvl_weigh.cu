@@ -9,8 +9,8 @@ namespace {
 
 // Entries of more rows than this (fresh tokens x query heads of a KV head; of those the call's bound allows, without one
 // the average) go to the tensor-memory kernel, which takes its time for 128 of them, the few-rows kernel for each 16.
-// Measured (us, few rows / tensor memory, 8 KV heads of 128): 32 sequences of 2,000 8 rows 31 / 68, 16 45 / 69, 32
-// 84 / 70; one of 30,000 16 rows 24 / 36, 32 42 / 35.
+// Measured (us, few rows / tensor memory, 8 KV heads of 128): 32 sequences of 2,000 8 rows 30 / 65, 16 43 / 67, 32
+// 82 / 66; one of 30,000 16 rows 23 / 31, 32 41 / 31.
 constexpr int kChunkRowsOfWeigh = 16;
 // (Past this many rows a KV head's steps would outlast the kernel's bounded waits.)
 constexpr int64_t kMostChunkRows = int64_t(1) << 26;
