@@ -21,7 +21,9 @@ namespace kvl {
 namespace {
 
 constexpr int kDigits = 2048;  // 11 bits
-constexpr int kRun = 16;       // tokens of a thread in a round
+// Tokens of a thread in a round (one sequence of 777, 8 of up to 4,096, one of 30,000, one of 128,000: us with 4 20.4, 208,
+// 40.8, 173; with 8 21.8, 209, 38.0, 168; with 16 27.1, 213, 45.4, 169).
+constexpr int kRun = 8;
 constexpr int kMostRanks = 8;  // CTAs of a sequence
 
 // n / d for 0 <= n < 2^31 by one product: the quotient of n and 2^(31 + s) / d rounded up, s = ceil(log2(d)).
@@ -294,7 +296,7 @@ __global__ void __launch_bounds__(kThreads) evict_select_kernel(const __grid_con
         const uint32_t c = tid < kRun * 32 ? s_count[tid] : 0;
         long long total;
         const long long b = block_scan<long long>((c & 0xffffu) | (long long)(c >> 16) << 32, scan, total);
-        if (tid < kRun * 32) s_before[tid] = uint32_t(b & 0xffff) | uint32_t(b >> 32) << 16;  // (each at most 16,384)
+        if (tid < kRun * 32) s_before[tid] = uint32_t(b & 0xffff) | uint32_t(b >> 32) << 16;  // (each at most kRun * 1,024)
         if (tid == 0) s_total = total;
         cluster.sync();
         long long all = 0, ahead = kept;
