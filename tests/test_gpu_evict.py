@@ -50,6 +50,8 @@ CASES = {
     "wide rows": case([60], [37], H=8, d=256, L=1, code="int8"),
     "rows of 720 bytes": case([60], [37], H=9, d=80, L=1),
     "long": case([5000, 4097], [3000, 17], first=4, recent=64, H=1, d=16, L=1),
+    "longer than a cluster's registers": case([140000, 70001], [9000, 40], first=4, recent=1000, H=1, d=16, L=1, B=64),
+    "longer than a cluster's registers, few masses": case([70001], [20000], first=4, recent=70, H=1, d=16, L=1, B=40, mass="few"),
     "many sequences": case([20 + 7 * i for i in range(60)], [10 + 5 * (i % 30) for i in range(60)], first=2, recent=3, H=1,
                            d=16, L=1),
     "more sequences than a CTA's threads": case([5 + i % 29 for i in range(1100)], [3 + i % 17 for i in range(1100)], first=1,
