@@ -271,7 +271,10 @@ __global__ void __launch_bounds__(kThreads) evict_select_kernel(const __grid_con
     // ---- places, masses, sources.  A round's masses are in registers before any is written, and a token moves down,
     // never past tokens that a later round still reads.
     grid_dependency_wait();
-    if (a.m.at[a.n] < 0) return;
+    if (a.m.at[a.n] < 0) {  // refused
+        cluster.sync();     // (the others may still be reading this CTA's histogram)
+        return;
+    }
     const int64_t first_page = a.m.at[i];
     long long kept = 0;  // tokens that stay before this round; those that equal `least` in the high half
 #pragma unroll 1
