@@ -40,7 +40,10 @@ struct AttendArgs {
     float *row_o;          // [2][n_rows][n_heads][64, 128 or 256]
     float *row_ml;         // [2][n_rows][n_heads][2]
     int32_t few;           // the few-rows kernel attends the shared tokens too
-    int32_t *part_jobs, *parts_done;  // parts_done: 1 if there are results
+    int32_t *part_jobs;
+    // [0], [1]: 1 if there are results of the first kernel (of the second); [2]: 1 if those of shared tokens are not all
+    // there, so that no entry that shares tokens is written
+    int32_t *parts_done;
     float *group_parts;
     int32_t parts_most;
 };

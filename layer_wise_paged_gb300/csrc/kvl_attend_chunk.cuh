@@ -304,9 +304,14 @@ __global__ void __launch_bounds__(kThreads, 1) attend_chunk_kernel(const __grid_
     Cut cut;
     const int n_entries = SHARED ? a.shared.n_groups : a.seqs.n_seq;
     if constexpr (SHARED) allow_dependents_launch();
-    auto leave = [&] {  // the kernel before has ended when this one has
-        if constexpr (SHARED) grid_dependency_wait();
+    // The kernel before has ended when this one has.  failed: parts of this CTA's are missing.
+    auto leave = [&](bool failed) {
+        if constexpr (SHARED) {
+            grid_dependency_wait();
+            if (failed) a.parts_done[2] = 1;
+        }
     };
+    bool no_room = false;
     for (int pass = 0; pass < 2; ++pass) {
         uint32_t jobs = 0;
         for (int base = 0; base < n_entries; base += kBatch) {
@@ -364,12 +369,12 @@ __global__ void __launch_bounds__(kThreads, 1) attend_chunk_kernel(const __grid_
                 if (blockIdx.x == 0 && tid == 0) a.parts_done[1] = before < kMostUnits;
             if (before == 0 || before >= kMostUnits) {
                 if (before && blockIdx.x == 0 && tid == 0) report(a.report, KVL_ERANGE, n_entries);
-                leave();
+                leave(false);
                 return;
             }
             cut = Cut(uint32_t(before), min(gridDim.x, (uint32_t(before) + kStepsPerCta - 1) / kStepsPerCta));
             if (blockIdx.x >= cut.shares) {
-                leave();
+                leave(false);
                 return;
             }
             u = cut.start(blockIdx.x);
@@ -408,7 +413,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_chunk_kernel(const __grid_
         if (tid == 0) report(a.report, KVL_ECUDA, blockIdx.x);
         if (warp == 8) arrive_without_result<SHARED>(a, job, lane);
         if (warp == 8) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(s_tmem) : "memory");
-        leave();
+        leave(tid == 0);
         return;
     }
     volatile int *gone = &s_gone;
@@ -847,7 +852,10 @@ __global__ void __launch_bounds__(kThreads, 1) attend_chunk_kernel(const __grid_
             // ---- the row's result, or its part
             const bool complete = !SHARED && job.complete;
             // (groups that are not in ascending order may be more jobs than there is room for)
-            if constexpr (SHARED) ok = ok && job.job < a.parts_most - int(blockIdx.x);
+            if constexpr (SHARED) {
+                no_room = no_room || job.job >= a.parts_most - int(blockIdx.x);
+                ok = ok && !no_room;
+            }
             const int rows = job.t.rows, h = job.h;
             const Entry e_ = job.e;
             uint32_t nan_at[D / 32];
@@ -1010,7 +1018,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_chunk_kernel(const __grid_
     }
     __syncthreads();
     if (warp == 8) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
-    leave();
+    leave(tid == 0 && (*gone || no_room));
 }
 
 template <int CODE, int TYPE, int D, bool SHARED>

@@ -135,6 +135,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attend_rows_kernel(const
         __shared__ HeldGroups s_groups;
         held = &s_groups;
         allow_dependents_launch();
+        if (blockIdx.x == 0 && tid == 0) a.parts_done[2] = 0;
         hold_groups(a, s_groups);
         __syncthreads();
         for (int i = int(blockIdx.x) * kThreads + int(threadIdx.x); i < a.seqs.n_seq; i += int(gridDim.x) * kThreads) {

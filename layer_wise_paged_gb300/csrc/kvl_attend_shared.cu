@@ -78,7 +78,7 @@ __global__ void __launch_bounds__(kThreads) join_kernel(const __grid_constant__ 
     grid_dependency_wait();
     const Sharing s = reinterpret_cast<const Sharing *>(a.sharing)[lo];
     const bool done = a.parts_done[0] != 0 && (a.few || a.parts_done[1] != 0);
-    if (!there || !done || s.tokens < 0) return;
+    if (!there || !done || s.tokens < 0 || (s.tokens > 0 && a.parts_done[2] != 0)) return;
     const int64_t row = t * heads + head;
     const float2 own = *reinterpret_cast<const float2 *>(a.row_ml + row * 2);
     float4 v[kVecs];
@@ -97,7 +97,7 @@ __global__ void __launch_bounds__(kThreads) join_kernel(const __grid_constant__ 
         const int H = a.cache.n_kv_heads, G = heads / H, h = head / G;
         const int64_t in = (t - s.row0) * G + head % G, tile = in / kChunkJobRows, r = in - tile * kChunkJobRows;
         const int2 j = reinterpret_cast<const int2 *>(a.part_jobs)[(int64_t(s.row0) * G / kChunkJobRows + s.group + tile) * H + h];
-        if (j.x < 0 || j.y < 0 || j.x > a.parts_most - j.y) return;  // (not there: a wait ran out, and is reported)
+        if (j.x < 0 || j.y < 0 || j.x > a.parts_most - j.y) return;  // (no read past the parts, whatever the table holds)
         parts = j.y;
         step = int64_t(kChunkJobRows) * (D + 2);
         ml = a.group_parts + j.x * step + r;

@@ -149,3 +149,37 @@ def test_nan_in_tokens_behind_the_shared_ones():
     assert dev.status() == (0, 0)
     assert torch.isnan(lse[0]).all() and torch.isfinite(lse[1:]).all() and torch.isfinite(wout[1:, 2:].float()).all()
 
+
+# ---- what is left out ----------------------------------------------------------------------------------------------
+
+def left_or_right(c, cache, wide, starts, entries, wout, lse):
+    """Every row of `entries` was written as the definition has it or not at all; all others not at all."""
+    zero = torch.zeros(2, dtype=torch.int32)
+    rows = torch.zeros(wide.shape[0], dtype=torch.bool)
+    out, z = wout.cpu(), lse.cpu()
+    for i in entries:
+        a, b = int(starts[i]), int(starts[i + 1])
+        rows[a:b] = True
+        if (out[a:b, 2:] == 77.0).all() and (z[a:b] == 77.0).all():
+            continue
+        zero[1] = b - a
+        o, y, to, ty = Q.attend(cache, 1, wide[a:b, 1:1 + c["heads"]], zero, [i], 1 / math.sqrt(c["d"]), c["causal"], 0)
+        near(out[a:b, 2:].double(), o, to, f"out of entry {i}")
+        near(z[a:b].double(), y, ty, f"lse of entry {i}")
+    assert (out[~rows] == 77.0).all() and (z[~rows] == 77.0).all() and (out[:, :2] == 77.0).all()
+
+
+def test_more_jobs_than_there_is_room_for_give_nothing_stale():
+    """The same sequences named by several groups are more jobs than parts have room for: no row gets what a call before
+    left there."""
+    n, times = 1200, 20
+    c = of_groups([n], [48], heads=4, kv_heads=1, d=16)
+    cache, wide, starts = make(c)
+    dev = Q.on_gpu(cache)
+    for k in range(2):
+        call(dev, c, wide.roll(k + 1, 0).cuda(), starts.cuda(), groups=[0] + [n] * (2 * times - 1), shared=[48] * (2 * times - 1))
+        assert dev.status() == (0, 0)
+        wout, lse = call(dev, c, wide.cuda(), starts.cuda(), groups=[0, n] * times, shared=[48] * (2 * times - 1))
+        assert dev.status() == (kvl.KVL_EINVAL, 1)
+        assert (wout == 77.0).all() and (lse == 77.0).all()
+        dev.reset_status()
