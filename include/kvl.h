@@ -519,8 +519,9 @@ kvl_status kvl_attend(const kvl_cache *cache, int32_t layer, const kvl_sequences
  * Every row sees all shared tokens: tokens[g] is at most lens - (fresh rows) of each entry with rows.  An entry for
  * which it is more is left out, its rows not written, and reported (KVL_ERANGE with its number); so are the
  * entries of a group that is bad: reported with the group's number, KVL_EINVAL for its range, KVL_ERANGE for
- * more shared tokens than its first sequence holds.  Where the kernel of the shared tokens gives up (KVL_ETIMEOUT), no
- * entry that shares tokens is written.
+ * more shared tokens than its first sequence holds.  Where groups or starts descend (reported, KVL_EINVAL), or the
+ * kernel of the shared tokens gives up (KVL_ETIMEOUT), no entry that shares tokens is written; where starts
+ * descend, others may be left out too.
  * A call with a window, without groups, or whose entries may have more than 40 rows (bound by max_new, times
  * n_heads / H), reads every entry's own table, as kvl_attend does.
  * d_workspace is kvl_attend's; d_parts (16-byte aligned; not looked at by such a call) needs no preparation and

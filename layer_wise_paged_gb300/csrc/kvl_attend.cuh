@@ -42,7 +42,7 @@ struct AttendArgs {
     int32_t few;           // the few-rows kernel attends the shared tokens too
     int32_t *part_jobs;
     // [0], [1]: 1 if there are results of the first kernel (of the second); [2]: 1 if those of shared tokens are not all
-    // there, so that no entry that shares tokens is written
+    // there or not where the join looks, so that no entry that shares tokens is written
     int32_t *parts_done;
     float *group_parts;
     int32_t parts_most;
@@ -128,17 +128,23 @@ struct HeldGroups {
     HeldGroup group[kHeldGroups];
 };
 
-// By a whole CTA, before a barrier.
-__device__ __forceinline__ void hold_groups(const AttendArgs &a, HeldGroups &held)
+// By a whole CTA, before a barrier.  Whether a group of this thread's ends before it begins.
+__device__ __forceinline__ bool hold_groups(const AttendArgs &a, HeldGroups &held)
 {
     const int n = a.shared.n_groups;
-    if (n > kHeldGroups) return;
+    const bool here = n <= kHeldGroups;
+    bool falls = false;
+    if (!here && blockIdx.x > 0) return false;  // (nothing to hold; one CTA looks at the order)
     for (int g = threadIdx.x; g <= n; g += blockDim.x) {
-        held.first[g] = a.shared.groups[g];
+        const int32_t first = a.shared.groups[g];
+        if (here) held.first[g] = first;
         if (g == n) continue;
+        falls = falls || a.shared.groups[g + 1] < first;
+        if (!here) continue;
         const Entry p = load_group(a, g, nullptr);
         held.group[g] = HeldGroup{a.shared.tokens[g], p.len, p.row0, p.fresh};
     }
+    return falls;
 }
 
 // Entry i, resolved as e; one whose group is left out, or one of whose rows does not see all shared tokens, is left out.

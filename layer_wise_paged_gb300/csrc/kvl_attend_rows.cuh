@@ -136,8 +136,10 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attend_rows_kernel(const
         held = &s_groups;
         allow_dependents_launch();
         if (blockIdx.x == 0 && tid == 0) a.parts_done[2] = 0;
-        hold_groups(a, s_groups);
+        const bool falls = hold_groups(a, s_groups);
         __syncthreads();
+        // Of groups, or starts (below), that descend the rows of two may have one place among the parts.
+        if (blockIdx.x == 0 && falls) a.parts_done[2] = 1;
         for (int i = int(blockIdx.x) * kThreads + int(threadIdx.x); i < a.seqs.n_seq; i += int(gridDim.x) * kThreads) {
             const Entry e = load_entry(a.seqs, a.cache.block_tokens, i, nullptr);
             Sharing s = sharing_of(a, s_groups, e, i, nullptr);
@@ -154,6 +156,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attend_rows_kernel(const
     for (int i = i0; i < i1; ++i) {
         c = cost_of<NT, PARTS>(a, held, i, blockIdx.x == 0 ? a.report : nullptr);
         mine += units_of(c);
+        if constexpr (PARTS)
+            if (blockIdx.x == 0 && i < a.seqs.n_seq && a.seqs.starts[i + 1] < a.seqs.starts[i]) a.parts_done[2] = 1;
     }
     uint64_t scan = mine;
 #pragma unroll

@@ -183,3 +183,38 @@ def test_more_jobs_than_there_is_room_for_give_nothing_stale():
         assert dev.status() == (kvl.KVL_EINVAL, 1)
         assert (wout == 77.0).all() and (lse == 77.0).all()
         dev.reset_status()
+
+
+@pytest.mark.parametrize("n,times", [(130, 2), (200, 3), (8, 2)])
+def test_groups_out_of_order_give_nothing_wrong(n, times):
+    """The same sequences named by several groups: a descending range is reported, and no row gets another's result, nor
+    one of a call before."""
+    c = of_groups([n], [48], heads=4, kv_heads=1)
+    cache, wide, starts = make(c)
+    dev = Q.on_gpu(cache)
+    groups, shared = [0, n] * times, [48] * (2 * times - 1)
+    for k in range(3):  # (the calls before leave their parts in the scratch memory)
+        call(dev, c, wide.roll(k + 1, 0).cuda(), starts.cuda(), groups=groups_of([n] + [0] * (2 * times - 2)), shared=shared)
+        assert dev.status() == (0, 0)
+        wout, lse = call(dev, c, wide.cuda(), starts.cuda(), groups=groups, shared=shared)
+        code, detail = dev.status()
+        assert code == kvl.KVL_EINVAL and detail == 1
+        left_or_right(c, cache, wide, starts, range(n), wout, lse)
+        dev.reset_status()
+
+
+@pytest.mark.parametrize("heads", [4, 1])
+def test_rows_out_of_order_give_nothing_wrong(heads):
+    """Two groups whose rows lie the other way round, with a bad entry between: it is reported, and no row gets another's
+    result."""
+    new, a, b = 10, 12, 13
+    c = of_groups([a, 1, b], [48, 16, 64], own=5, new=new, heads=heads, kv_heads=1)
+    cache, wide, _ = make(c)
+    wide = wide[:(a + b) * new]
+    starts = torch.tensor([b * new + new * i for i in range(a + 1)] + [new * i for i in range(b + 1)], dtype=torch.int32)
+    dev = Q.on_gpu(cache)
+    for _ in range(3):
+        wout, lse = call(dev, c, wide.cuda(), starts.cuda())
+        code, detail = dev.status()
+        assert code == kvl.KVL_EINVAL
+        left_or_right(c, cache, wide, starts, [i for i in range(a + 1 + b) if i != a], wout, lse)
