@@ -48,7 +48,7 @@ struct Chunk {
 enum Bar { K_FULL = 0, K_EMPTY = 2, Q_FULL = 4, Q_EMPTY = 6, S_FULL = 8, S_EMPTY = 10, JOIN = 12, SUM_FULL = 13, SUM_EMPTY = 14, LEAVE = 15, BARS = 16 };
 
 // Workspace: [counters of the shares][parts: two a share, 256 sums][row tiles: rows, their
-// offsets, their factor].  Tile of entry i's chunk c: number
+// offsets, their factor, a byte for each 32: whether a row among them gives nothing].  Tile of entry i's chunk c: number
 // row0 * G / 128 + i + c, of which no two entries' meet.
 __host__ __device__ constexpr size_t counter_bytes(int sms) { return size_t(sms) * 4 + 255 & ~size_t(255); }
 __host__ __device__ constexpr size_t part_bytes(int sms) { return size_t(sms) * 2 * kTokens * 4; }
@@ -150,6 +150,9 @@ __global__ void __launch_bounds__(256) weigh_rows_prepare_kernel(const __grid_co
             z = a.w.lse[(int64_t(e.row0) + tok) * t.attn.n_heads + head];
         }
         consts[threadIdx.x] = isinf(z) ? -INFINITY : -z * kLog2e;
+        // (rows that are not there need no mark: where all that are see a NaN key, it counts or all of them are marked)
+        const bool nothing = __any_sync(0xffffffffu, row < rows && isinf(z));
+        if (lane == 0) reinterpret_cast<uint8_t *>(consts + kRows + 1)[warp] = nothing;
     }
     if (threadIdx.x == 0) consts[kRows] = t.attn.sm_scale * kLog2e * down;
 }
@@ -430,11 +433,13 @@ __global__ void __launch_bounds__(kThreads, 1) weigh_chunk_kernel(const __grid_c
                 const uint32_t ts = lanes + set * 256;
                 if (n_rows > 0) {
                     const float f = consts[kRows - side * 32];
+                    // a row of an infinite lse gives nothing even of a NaN key, whose product is a NaN whatever the row
+                    const bool count = reinterpret_cast<const uint8_t *>(consts + kRows + 1 - side * 32)[side] == 0;
                     float kf[2];
 #pragma unroll
                     for (int y = 0; y < 2; ++y) kf[y] = s_scales[k % kScales][(slot + 128 * y) / kGroup] * f;
                     int from[2] = {0, 0}, to[2] = {kRows, kRows};
-                    bool seen[2] = {true, true}, whole = true;  // by some lane's row; by all
+                    bool seen[2] = {true, true}, whole = count;  // by some lane's row; by all
                     if (!always) {
 #pragma unroll
                         for (int y = 0; y < 2; ++y) {
@@ -480,8 +485,8 @@ __global__ void __launch_bounds__(kThreads, 1) weigh_chunk_kernel(const __grid_c
                                 for (int i = 0; i < 16; i += 2) {
                                     const float2 b = *reinterpret_cast<const float2 *>(consts + col + i);
                                     float2 q = weights(y, i, pair_of(b.x, b.y));
-                                    if (col + i < from[y] || col + i >= to[y]) q.x = 0.f;
-                                    if (col + i + 1 < from[y] || col + i + 1 >= to[y]) q.y = 0.f;
+                                    if (col + i < from[y] || col + i >= to[y] || b.x == -INFINITY) q.x = 0.f;
+                                    if (col + i + 1 < from[y] || col + i + 1 >= to[y] || b.y == -INFINITY) q.y = 0.f;
                                     add[y][0] = add_pair(add[y][0], pair_of(q.x, q.y));
                                 }
                             }

@@ -1,11 +1,15 @@
-"""kvl_weigh over many entries."""
+"""kvl_weigh over many entries, and what gives nothing: rows of an infinite lse beside NaN codes."""
 from __future__ import annotations
+
+import math
 
 import pytest
 import torch
 
 import layer_wise_paged_gb300 as kvl
-from tests.test_gpu_weigh import case, run
+from tests import _kept as K
+from tests import _quant as Q
+from tests.test_gpu_weigh import case, held_to, make, run
 
 pytestmark = pytest.mark.gpu
 
@@ -28,3 +32,31 @@ CASES = {
 @pytest.mark.parametrize("name", CASES)
 def test_many_entries(name):
     run(CASES[name])
+
+
+@pytest.mark.parametrize("new,dead", [(3, [2]), (60, [59]), (60, [57, 58, 59]), (64, [63]), (200, [199])])
+def test_a_nan_key_that_only_rows_of_an_infinite_lse_see(new, dead):
+    """It gives nothing, as such rows do: the token's mass stays, and so does everyone else's."""
+    c = case([300], [new], heads=4, kv_heads=1)
+    cache, wide, starts, lse, mass = make(c)
+    for i, r in enumerate(dead):
+        lse[r] = (math.inf, -math.inf)[i % 2]
+    want, tol = K.weigh(cache, 1, wide[:, 1:5], starts, [0], lse, mass, False, 1 / math.sqrt(128), True, 0)
+    first = 300 - new + min(dead)  # the first token that only they see
+    for j in range(first, 300):
+        cache["codes"][1, 0, int(cache["tables"][0, j // 16]), j % 16, 0, 5] = 0x7F
+    got = Q.on_gpu(cache).weigh(1, wide.cuda()[:, 1:5], starts.cuda(), lse.cuda(), mass.cuda())
+    held_to(got, want, tol, c, mass)
+    assert torch.equal(got[0, first:].cpu(), mass[0, first:])
+
+
+@pytest.mark.parametrize("new", [3, 60, 64, 200])
+@pytest.mark.parametrize("causal", [True, False])
+def test_nan_keys_and_no_row_that_counts(new, causal):
+    c = case([300], [new], heads=4, kv_heads=1)
+    cache, wide, starts, lse, mass = make(c)
+    for j in (0, 17, 250, 299):
+        cache["codes"][1, 0, int(cache["tables"][0, j // 16]), j % 16, 0, 5] = 0xFF
+    lse[:] = math.inf
+    got = Q.on_gpu(cache).weigh(1, wide.cuda()[:, 1:5], starts.cuda(), lse.cuda(), mass.cuda(), causal=causal)
+    assert torch.equal(got.cpu(), mass)
