@@ -548,6 +548,7 @@ kvl_status kvl_attend_shared(const kvl_cache *cache, int32_t layer, const kvl_se
  * the layers after it add).  A row whose lse is infinite gives nothing.  mass_out may be mass_in; entries without
  * fresh rows, and what lies past a sequence's tokens, are not written.  Slots of a call must differ.  Sums are in
  * 32 bits and come out the same every time.  A sequence longer than a row of masses is left out (KVL_ERANGE).
+ * Where starts descend (reported, KVL_EINVAL), entries beside the bad one may be left out too.
  * Scales are taken to be finite.  d_workspace (16-byte aligned) needs no preparation and holds nothing between
  * calls; kvl_weigh_workspace_bytes is 0 for bad arguments. */
 typedef struct kvl_weighing {

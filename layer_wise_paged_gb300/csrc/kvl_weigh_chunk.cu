@@ -302,8 +302,10 @@ __global__ void __launch_bounds__(kThreads, 1) weigh_chunk_kernel(const __grid_c
     const int64_t N = a.cache.pool_blocks, plane = int64_t(a.layer) * 2 * N;
 
     // ---- this CTA's share: the entries' steps a batch at a time, their sum, then the entry that holds the first
+    // (where starts descend two entries' row tiles may have one number: nothing is weighed)
     uint64_t before = 0;
     uint32_t u = 0;
+    bool falls = false;
     Cut cut;
     for (int pass = 0; pass < 2; ++pass) {
         for (int base = 0; base < a.seqs.n_seq; base += kBatch) {
@@ -313,6 +315,7 @@ __global__ void __launch_bounds__(kThreads, 1) weigh_chunk_kernel(const __grid_c
                 for (int i = warp; i < n; i += kWarps) {
                     const Span s = span_of(w, base + i, pass == 0 && blockIdx.x == 0 && lane == 0 ? a.report : nullptr);
                     const uint64_t steps = warp_steps(w, s, lane);
+                    falls = falls || a.seqs.starts[base + i + 1] < a.seqs.starts[base + i];
                     if (lane == 0) s_units[i] = uint32_t(min(steps, kMostUnits));
                 }
                 __syncthreads();
@@ -341,8 +344,9 @@ __global__ void __launch_bounds__(kThreads, 1) weigh_chunk_kernel(const __grid_c
             }
         }
         if (pass == 0) {
-            if (before == 0 || before >= kMostUnits) {
-                if (before && blockIdx.x == 0 && tid == 0) report(a.report, KVL_ERANGE, a.seqs.n_seq);
+            falls = __syncthreads_or(falls);
+            if (before == 0 || before >= kMostUnits || falls) {
+                if (before >= kMostUnits && blockIdx.x == 0 && tid == 0) report(a.report, KVL_ERANGE, a.seqs.n_seq);
                 grid_dependency_wait();  // the rows' kernel has ended when this one has
                 return;
             }

@@ -1,4 +1,4 @@
-"""kvl_weigh over many entries, and what gives nothing: rows of an infinite lse beside NaN codes."""
+"""kvl_weigh over many entries, and what gives nothing: rows of an infinite lse beside NaN codes, entries out of order."""
 from __future__ import annotations
 
 import math
@@ -60,3 +60,25 @@ def test_nan_keys_and_no_row_that_counts(new, causal):
     lse[:] = math.inf
     got = Q.on_gpu(cache).weigh(1, wide.cuda()[:, 1:5], starts.cuda(), lse.cuda(), mass.cuda(), causal=causal)
     assert torch.equal(got.cpu(), mass)
+
+
+@pytest.mark.parametrize("new", [10, 60])
+def test_entries_out_of_order_give_nothing_wrong(new):
+    """Entries whose rows lie the other way round, with a bad one between: it is reported, and every other's masses are as
+    the definition has them or as they were."""
+    c = case([200, 50, 180], [new, 1, new + 40], heads=8, kv_heads=2)
+    cache, wide, _, _, mass = make(c)
+    wide = wide[:2 * new + 40]
+    starts = torch.tensor([new + 40, 2 * new + 40, 0, new + 40], dtype=torch.int32)
+    lse = torch.zeros((2 * new + 40, 8))
+    for a, b, s in ((0, new + 40, 2), (new + 40, 2 * new + 40, 0)):
+        lse[a:b] = Q.attend(cache, 1, wide[a:b, 1:9], torch.tensor([0, b - a]), [s], 1 / math.sqrt(128), True, 0)[1].float()
+    dev = Q.on_gpu(cache)
+    got = dev.weigh(1, wide.cuda()[:, 1:9], starts.cuda(), lse.cuda(), mass.cuda(), begin=True).cpu()
+    assert dev.status() == (kvl.KVL_EINVAL, 1)
+    assert torch.equal(got[1], mass[1])
+    for a, b, s, n in ((0, new + 40, 2, 180), (new + 40, 2 * new + 40, 0, 200)):
+        if torch.equal(got[s], mass[s]):
+            continue
+        want, tol = K.weigh(cache, 1, wide[a:b, 1:9], torch.tensor([0, b - a]), [s], lse[a:b], mass, True, 1 / math.sqrt(128), True, 0)
+        assert float(((got[s].double() - want[s]).abs() - tol[s]).max()) <= 0
