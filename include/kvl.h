@@ -525,7 +525,8 @@ kvl_status kvl_attend(const kvl_cache *cache, int32_t layer, const kvl_sequences
  * A call with a window, without groups, or whose entries may have more than 40 rows (bound by max_new, times
  * n_heads / H), reads every entry's own table, as kvl_attend does.
  * d_workspace is kvl_attend's; d_parts (16-byte aligned; not looked at by such a call) needs no preparation and
- * holds nothing between calls. */
+ * holds nothing between calls.  A call's launches pass data through it, so calls that may run at the same time, or are
+ * made by host threads at the same time on one stream, need one each. */
 typedef struct kvl_shared {
     int32_t n_groups; /* at most 1048576 */
     int32_t reserved; /* 0 */
@@ -550,7 +551,7 @@ kvl_status kvl_attend_shared(const kvl_cache *cache, int32_t layer, const kvl_se
  * 32 bits and come out the same every time.  A sequence longer than a row of masses is left out (KVL_ERANGE).
  * Where starts descend (reported, KVL_EINVAL), entries beside the bad one may be left out too.
  * Scales are taken to be finite.  d_workspace (16-byte aligned) needs no preparation and holds nothing between
- * calls; kvl_weigh_workspace_bytes is 0 for bad arguments. */
+ * calls; calls need one each as with d_parts above.  kvl_weigh_workspace_bytes is 0 for bad arguments. */
 typedef struct kvl_weighing {
     kvl_rows q;             /* n_rows rows of n_heads heads */
     const float *lse;       /* [n_rows][n_heads] */
@@ -632,6 +633,8 @@ kvl_status kvl_pages_copy(const kvl_cache *cache, const int32_t *pairs, const in
  * else is done to the pages, and the pages they were in lose a reference.
  * If a slot is bad (KVL_EINVAL), named twice (KVL_EDUP) or too long for its table or masses, or there are too few
  * free pages (pages freed by this call do not count; KVL_ERANGE with detail n), nothing is changed.
+ * Its launches pass data through `moves` to each other and to kvl_tokens_move: no other eviction into the same
+ * `moves` comes between, from another host thread or stream.
  * A key keeps the rotary position it was turned by, while attention counts positions from the
  * sequence's shortened start: later keys are turned by their own positions before they are appended. */
 typedef struct kvl_eviction {

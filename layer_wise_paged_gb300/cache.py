@@ -166,7 +166,11 @@ class QuantCache:
     [slots, pages per sequence]; lens: int32 [slots] tokens held; refs: int32 [N] references
     of each page (0: free).  pairs / n_pairs (made here when not given) receive the page copies
     that ``extend`` and ``compact`` ask for; ``copy_pages`` makes them.  ``empty`` allocates
-    all of it.
+    all of it.  What ``evict`` asks to be moved takes 8 bytes a token of the pool, which the cache
+    holds from the start.  Memory that single calls need grows to the largest of each stream's and stays.
+
+    Several host threads may attend and weigh at the same time, on one stream too.  What changes pages
+    (extend, fork, free, compact, evict, with the copies or moves that follow) is for one thread at a time.
     """
 
     def __init__(self, codes, scales, tables, lens, refs, code="e4m3", pairs=None, n_pairs=None):
@@ -201,6 +205,7 @@ class QuantCache:
         # capture on it (the graph may run beside them)
         self._ws, self._ws_captured = {}, {}
         self._held, self._held_captured, self._sizes = {}, {}, {}  # memory of single calls, likewise; its sizes
+        self._order = threading.Lock()  # its launches of one call are not mixed with another thread's on the stream
         self._capture_id = self._lib.kvl_capture_id
         self._scale = 1.0 / math.sqrt(d)
         self._args = _Args(self)
@@ -292,9 +297,11 @@ class QuantCache:
             n = self._sizes.get(key)
             if n is None:
                 n = self._size(key, self._lib.kvl_attend_shared_parts_bytes(self._cache, *key))
-            parts = self._scratch(n, st)
-        r = self._lib.kvl_attend_shared(self._cache, layer, s, g, c.attn, ws,
-                                        self._ws_bytes, parts[0], n, self._report, st)
+        with self._order:
+            if n:
+                parts = self._scratch(n, st)
+            r = self._lib.kvl_attend_shared(self._cache, layer, s, g, c.attn, ws,
+                                            self._ws_bytes, parts[0], n, self._report, st)
         if r:
             check(r, "kvl_attend_shared")
         return out
@@ -324,8 +331,9 @@ class QuantCache:
         n = self._sizes.get(key)
         if n is None:
             n = self._size(key, self._lib.kvl_weigh_workspace_bytes(self._cache, *key[:4]))
-        scratch = self._scratch(n, st)
-        r = self._lib.kvl_weigh(self._cache, layer, s, w, scratch[0], n, self._report, st)
+        with self._order:
+            scratch = self._scratch(n, st)
+            r = self._lib.kvl_weigh(self._cache, layer, s, w, scratch[0], n, self._report, st)
         if r:
             check(r, "kvl_weigh")
         return mass if out is None else out
@@ -344,8 +352,8 @@ class QuantCache:
 
     def _scratch(self, n, st):
         """(address, memory) of n bytes or more that hold nothing between calls: calls of one stream share one, a graph has
-        its own, as with the workspaces.  The caller keeps the memory until its launch is made: another thread's
-        call on the stream may put a larger one in its place."""
+        its own, as with the workspaces.  The launches of a call pass data through it, so the caller holds _order from
+        here until they are made."""
         capture = self._capture_id(st)
         held = self._held_captured if capture else self._held
         m = held.get(st)
