@@ -404,11 +404,15 @@ class QuantCache:
     def _workspace(self, held, st, capture):
         # In a capture the zeroing is a part of the graph, and the memory its pool's, as the graph's
         # temporaries are.
-        with self._on(st):
-            ws = torch.empty(self._ws_bytes, dtype=torch.uint8, device=self.device)
-            ws[:KVL_ATTEND_ZERO_BYTES].zero_()
-        held[st] = capture, ws.data_ptr(), ws
-        return held[st]
+        with self._order:
+            made = held.get(st)  # by another thread's call meanwhile: its launch may be on the way
+            if made is not None and made[0] == capture:
+                return made
+            with self._on(st):
+                ws = torch.empty(self._ws_bytes, dtype=torch.uint8, device=self.device)
+                ws[:KVL_ATTEND_ZERO_BYTES].zero_()
+            held[st] = made = capture, ws.data_ptr(), ws
+            return made
 
     # -- pages ----------------------------------------------------------------
     def extend(self, slots, counts, stream=None):

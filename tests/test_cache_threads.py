@@ -77,3 +77,25 @@ def test_calls_of_two_threads_are_made_one_after_the_other(monkeypatch, name):
     for x in threads:
         x.join()
     assert not errors and launches.mixed == 0
+
+
+def test_two_first_calls_on_a_stream_share_one_workspace(monkeypatch):
+    """The first thread's would be freed, and given to other tensors, before its launch is made."""
+    class Slow:
+        def __enter__(self):
+            time.sleep(0.02)
+
+        def __exit__(self, *args):
+            return False
+
+    cache = Memory(SimpleNamespace())
+    cache.device, cache._ws_bytes, cache._ws = "cpu", 1 << 15, {}
+    monkeypatch.setattr(cache, "_on", lambda st: Slow(), raising=False)
+    got = []
+    threads = [threading.Thread(target=lambda: got.append(cache._workspace(cache._ws, 7, 0))) for _ in range(4)]
+    for x in threads:
+        x.start()
+    for x in threads:
+        x.join()
+    assert len(got) == 4 and len({ws[1] for ws in got}) == 1 and cache._ws[7] is got[0]
+    assert cache._workspace(cache._ws, 7, 5)[0] == 5 and cache._workspace(cache._ws, 8, 0) is not got[0]
