@@ -522,11 +522,12 @@ kvl_status kvl_attend(const kvl_cache *cache, int32_t layer, const kvl_sequences
  * more shared tokens than its first sequence holds.  Where groups or starts descend (reported, KVL_EINVAL), or the
  * kernel of the shared tokens gives up (KVL_ETIMEOUT), no entry that shares tokens is written; where starts
  * descend, others may be left out too.
- * A call with a window, without groups, or whose entries may have more than 40 rows (bound by max_new, times
- * n_heads / H), reads every entry's own table, as kvl_attend does.
+ * A call with a window, without groups, or whose entries may have more than KVL_SHARED_ROWS rows (max_new, without
+ * one n_rows, times n_heads / H), reads every entry's own table, as kvl_attend does.
  * d_workspace is kvl_attend's; d_parts (16-byte aligned; not looked at by such a call) needs no preparation and
  * holds nothing between calls.  A call's launches pass data through it, so calls that may run at the same time, or are
  * made by host threads at the same time on one stream, need one each. */
+#define KVL_SHARED_ROWS 40
 typedef struct kvl_shared {
     int32_t n_groups; /* at most 1048576 */
     int32_t reserved; /* 0 */

@@ -43,6 +43,7 @@ KVL_CODE_FLOAT, KVL_CODE_INT = 0, 1
 KVL_TYPE_BFLOAT, KVL_TYPE_HALF, KVL_TYPE_FLOAT = 0, 1, 2
 KVL_ROPE_PLAIN, KVL_ROPE_LINEAR, KVL_ROPE_BASE, KVL_ROPE_WAVELENGTH = 0, 1, 2, 3
 KVL_ATTEND_ZERO_BYTES = 16384
+KVL_SHARED_ROWS = 40
 
 
 class kvl_geom(ctypes.Structure):

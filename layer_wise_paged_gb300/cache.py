@@ -21,7 +21,7 @@ import torch
 
 from . import lib as _lib
 from . import (KVL_ATTEND_ZERO_BYTES, KVL_CODE_FLOAT, KVL_CODE_INT, KVL_REPORT_BYTES, KVL_ROPE_BASE,
-               KVL_ROPE_LINEAR, KVL_ROPE_PLAIN, KVL_ROPE_WAVELENGTH, KVL_TYPE_BFLOAT, KVL_TYPE_FLOAT,
+               KVL_ROPE_LINEAR, KVL_ROPE_PLAIN, KVL_ROPE_WAVELENGTH, KVL_SHARED_ROWS, KVL_TYPE_BFLOAT, KVL_TYPE_FLOAT,
                KVL_TYPE_HALF, check, kvl_attention, kvl_cache, kvl_eviction, kvl_moves, kvl_pages, kvl_read_status,
                kvl_rope, kvl_rows, kvl_sequences, kvl_shared, kvl_weighing)
 
@@ -38,7 +38,6 @@ _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
 
 _current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 _MOST = 2 ** 31 - 1
-_SHARED_ROWS = 40  # rows of a KV head that an entry may have for kvl_attend_shared to read shared tokens once
 _several = None  # whether there is another device than the current one (asked at the first call)
 
 
@@ -280,8 +279,10 @@ class QuantCache:
         """``attend`` of a batch whose sequences share prefixes (forks of one prompt): entries groups[g] ..
         groups[g + 1] (int32, n_groups + 1) have their first shared[g] tokens (int32, n_groups) in the same
         pages, which are read once for the rows of all of them.  After ``fork`` and ``extend`` that holds of
-        the parent's whole pages: shared = length // block_tokens * block_tokens.  Give max_new: entries
-        that may have more than 40 rows (times heads of a KV head), or a window, are computed as by ``attend``."""
+        the parent's whole pages: shared = length // block_tokens * block_tokens.  A batch that may have entries
+        of more than 40 rows (KVL_SHARED_ROWS: fresh tokens times query heads of a KV head), or a window, is computed as
+        by ``attend``, every sequence by its own table.  So give max_new: without it every entry may have all rows
+        of the batch."""
         n_groups = shared.shape[0]
         st = _stream(stream, self._index)
         out, ws = self._attention(q, out, lse, sm_scale, causal, window, max_new, stream, st)
@@ -292,7 +293,7 @@ class QuantCache:
         s = self._seqs(c, starts, slots, n_rows)
         n, parts = 0, (None, None)
         # (what is computed as by attend needs no memory for parts)
-        if window == 0 and (max_new if 0 < max_new < n_rows else n_rows) * heads <= _SHARED_ROWS * self.n_kv_heads:
+        if window == 0 and (max_new if 0 < max_new < n_rows else n_rows) * heads <= KVL_SHARED_ROWS * self.n_kv_heads:
             key = s.n_seq, n_groups, n_rows, heads
             n = self._sizes.get(key)
             if n is None:

@@ -189,11 +189,12 @@ extern "C" kvl_status kvl_attend_shared(const kvl_cache *cache, int32_t layer, c
         return KVL_EINVAL;
     if (misaligned4(shared->groups) || misaligned4(shared->tokens) || !aligned16(d_parts)) return KVL_EALIGN;
     if (nothing) return KVL_OK;
-    // With a window most rows see little of a long prefix, and entries of many rows are bound by the products, which
-    // sharing does not spare: both read their own tables.
+    // What this does not serve reads its own tables: entries of more rows, whose own tokens would want the tensor-memory
+    // kernel, and windows, whose rows do not all see all shared tokens (those longer than the sequences too).  From 256
+    // rows an entry on nothing would be gained, as one fills a job of that kernel; below, a prefix is walked once an entry.
     const int G = attn->n_heads / cache->n_kv_heads;
     const int64_t bound = attn->max_new > 0 && attn->max_new < seqs->n_rows ? attn->max_new : seqs->n_rows;
-    if (shared->n_groups == 0 || attn->window > 0 || bound * G > kChunkRows)
+    if (shared->n_groups == 0 || attn->window > 0 || bound * G > KVL_SHARED_ROWS)
         return kvl_attend(cache, layer, seqs, attn, d_workspace, workspace_bytes, d_report, stream);
     if (!d_parts || parts_bytes < kvl_attend_shared_parts_bytes(cache, seqs->n_seq, shared->n_groups, seqs->n_rows, attn->n_heads))
         return KVL_EINVAL;

@@ -83,6 +83,12 @@ def test_groups_of_few_rows(name):
     check(FEW[name])
 
 
+@pytest.mark.parametrize("new", [kvl.KVL_SHARED_ROWS, kvl.KVL_SHARED_ROWS + 1])
+def test_as_many_rows_as_share_and_one_more(new):
+    """The binding brings memory for parts exactly where the library wants it."""
+    check(of_groups([3, 2], [64, 37], own=4, new=new, heads=2, kv_heads=2, d=64))
+
+
 @pytest.mark.parametrize("groups", [130, 520])
 def test_more_groups_of_many_rows_than_are_held(groups):
     """Past 128 groups an entry's group is looked for in memory, past 512 jobs are numbered over several batches."""
