@@ -289,7 +289,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_chunk_kernel(const __grid_
     __shared__ float s_cq[2][kJobRows];
     __shared__ uint32_t s_units[kBatch], s_tiles[SHARED ? kBatch : 1];
     __shared__ Job job, next;
-    __shared__ int s_last, s_gone, s_nan;
+    __shared__ int s_last, s_gone, s_nan, s_no_room;
     __shared__ uint32_t s_tmem;
 
     const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
@@ -311,7 +311,6 @@ __global__ void __launch_bounds__(kThreads, 1) attend_chunk_kernel(const __grid_
             if (failed) a.parts_done[2] = 1;
         }
     };
-    bool no_room = false;
     for (int pass = 0; pass < 2; ++pass) {
         uint32_t jobs = 0;
         for (int base = 0; base < n_entries; base += kBatch) {
@@ -399,7 +398,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_chunk_kernel(const __grid_
         }
         mbar_init(bar + 8 * LEAVE, 1);
         fence_mbar_init();
-        s_gone = 0;
+        s_gone = s_no_room = 0;
     }
     if (warp == 8) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(&s_tmem)) : "memory");
@@ -853,8 +852,9 @@ __global__ void __launch_bounds__(kThreads, 1) attend_chunk_kernel(const __grid_
             const bool complete = !SHARED && job.complete;
             // (groups that are not in ascending order may be more jobs than there is room for)
             if constexpr (SHARED) {
-                no_room = no_room || job.job >= a.parts_most - int(blockIdx.x);
-                ok = ok && !no_room;
+                const bool room = job.job < a.parts_most - int(blockIdx.x);
+                if (!room) s_no_room = 1;
+                ok = ok && room;
             }
             const int rows = job.t.rows, h = job.h;
             const Entry e_ = job.e;
@@ -1018,7 +1018,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_chunk_kernel(const __grid_
     }
     __syncthreads();
     if (warp == 8) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
-    leave(tid == 0 && (*gone || no_room));
+    leave(tid == 0 && (*gone || (SHARED && s_no_room)));
 }
 
 template <int CODE, int TYPE, int D, bool SHARED>
