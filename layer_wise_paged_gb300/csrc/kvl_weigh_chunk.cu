@@ -48,7 +48,7 @@ struct Chunk {
 enum Bar { K_FULL = 0, K_EMPTY = 2, Q_FULL = 4, Q_EMPTY = 6, S_FULL = 8, S_EMPTY = 10, JOIN = 12, SUM_FULL = 13, SUM_EMPTY = 14, LEAVE = 15, BARS = 16 };
 
 // Workspace: [counters of the shares][parts: two a share, 256 sums][row tiles: rows, their
-// offsets, their factor, a byte for each 32: whether a row among them gives nothing].  Tile of entry i's chunk c: number
+// offsets, their factor, negative where a row among them gives nothing].  Tile of entry i's chunk c: number
 // row0 * G / 128 + i + c, of which no two entries' meet.
 __host__ __device__ constexpr size_t counter_bytes(int sms) { return size_t(sms) * 4 + 255 & ~size_t(255); }
 __host__ __device__ constexpr size_t part_bytes(int sms) { return size_t(sms) * 2 * kTokens * 4; }
@@ -98,6 +98,7 @@ __global__ void __launch_bounds__(256) weigh_rows_prepare_kernel(const __grid_co
     __shared__ float s_most[8];
     const int at = (lane % kLanes) * 8;
     uint4 raw[kTurns];
+    bool infinite = false;
     float z_of[kTurns], amax = 0.f;  // of finite elements
 #pragma unroll
     for (int x = 0; x < kTurns; ++x) {
@@ -114,7 +115,10 @@ __global__ void __launch_bounds__(256) weigh_rows_prepare_kernel(const __grid_co
 #pragma unroll
     for (int x = 0; x < kTurns; ++x) {
         float v[8];
-        if (isinf(z_of[x])) raw[x] = make_uint4(0, 0, 0, 0);  // (gives nothing, whatever it holds)
+        if (isinf(z_of[x])) {  // gives nothing, whatever it holds
+            raw[x] = make_uint4(0, 0, 0, 0);
+            infinite = true;
+        }
         load8<TYPE>(reinterpret_cast<const uint8_t *>(&raw[x]), v);
 #pragma unroll
         for (int y = 0; y < 8; ++y) amax = fmaxf(amax, isfinite(v[y]) ? fabsf(v[y]) : 0.f);
@@ -122,7 +126,8 @@ __global__ void __launch_bounds__(256) weigh_rows_prepare_kernel(const __grid_co
 #pragma unroll
     for (int o = 16; o; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
     if (lane == 0) s_most[warp] = amax;
-    __syncthreads();
+    // (rows that are not there need no mark: a NaN key that all others see counts, or all of them are marked)
+    const bool nothing = __syncthreads_or(infinite);
 #pragma unroll
     for (int x = 0; x < 8; ++x) amax = fmaxf(amax, s_most[x]);
     // 2^e <= amax < 2^(e + 1), e held to what leaves both factors normal
@@ -150,11 +155,8 @@ __global__ void __launch_bounds__(256) weigh_rows_prepare_kernel(const __grid_co
             z = a.w.lse[(int64_t(e.row0) + tok) * t.attn.n_heads + head];
         }
         consts[threadIdx.x] = isinf(z) ? -INFINITY : -z * kLog2e;
-        // (rows that are not there need no mark: where all that are see a NaN key, it counts or all of them are marked)
-        const bool nothing = __any_sync(0xffffffffu, row < rows && isinf(z));
-        if (lane == 0) reinterpret_cast<uint8_t *>(consts + kRows + 1)[warp] = nothing;
     }
-    if (threadIdx.x == 0) consts[kRows] = t.attn.sm_scale * kLog2e * down;
+    if (threadIdx.x == 0) consts[kRows] = t.attn.sm_scale * kLog2e * (nothing ? -down : down);
 }
 
 // ---- work ---------------------------------------------------------------------------------------------------
@@ -318,7 +320,7 @@ __global__ void __launch_bounds__(kThreads, 1) weigh_chunk_kernel(const __grid_c
                     falls = falls || a.seqs.starts[base + i + 1] < a.seqs.starts[base + i];
                     if (lane == 0) s_units[i] = uint32_t(min(steps, kMostUnits));
                 }
-                __syncthreads();
+                falls = __syncthreads_or(falls);
             }
             for (int i = 0; i < n; i += 32) {
                 uint64_t x = i + lane < n ? s_units[i + lane] : 0, sum = x;
@@ -344,7 +346,6 @@ __global__ void __launch_bounds__(kThreads, 1) weigh_chunk_kernel(const __grid_c
             }
         }
         if (pass == 0) {
-            falls = __syncthreads_or(falls);
             if (before == 0 || before >= kMostUnits || falls) {
                 if (before >= kMostUnits && blockIdx.x == 0 && tid == 0) report(a.report, KVL_ERANGE, a.seqs.n_seq);
                 grid_dependency_wait();  // the rows' kernel has ended when this one has
@@ -437,13 +438,13 @@ __global__ void __launch_bounds__(kThreads, 1) weigh_chunk_kernel(const __grid_c
                 const uint32_t ts = lanes + set * 256;
                 if (n_rows > 0) {
                     const float f = consts[kRows - side * 32];
-                    // a row of an infinite lse gives nothing even of a NaN key, whose product is a NaN whatever the row
-                    const bool count = reinterpret_cast<const uint8_t *>(consts + kRows + 1 - side * 32)[side] == 0;
                     float kf[2];
 #pragma unroll
-                    for (int y = 0; y < 2; ++y) kf[y] = s_scales[k % kScales][(slot + 128 * y) / kGroup] * f;
+                    for (int y = 0; y < 2; ++y) kf[y] = s_scales[k % kScales][(slot + 128 * y) / kGroup] * fabsf(f);
                     int from[2] = {0, 0}, to[2] = {kRows, kRows};
-                    bool seen[2] = {true, true}, whole = count;  // by some lane's row; by all
+                    // by some lane's row; by all, all of which count: one of an infinite lse gives nothing even of a NaN
+                    // key, whose product is a NaN whatever the row
+                    bool seen[2] = {true, true}, whole = f > 0.f;
                     if (!always) {
 #pragma unroll
                         for (int y = 0; y < 2; ++y) {
