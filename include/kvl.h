@@ -521,7 +521,8 @@ kvl_status kvl_attend(const kvl_cache *cache, int32_t layer, const kvl_sequences
  * entries of a group that is bad: reported with the group's number, KVL_EINVAL for its range, KVL_ERANGE for
  * more shared tokens than its first sequence holds.  Where groups or starts descend (reported, KVL_EINVAL), or the
  * kernel of the shared tokens gives up (KVL_ETIMEOUT), no entry that shares tokens is written; where starts
- * descend, others may be left out too.
+ * descend, others may be left out too.  A group whose first sequence is bad, or whose first or last start is out of
+ * range, is left out with it.
  * A call with a window, without groups, or whose entries may have more than KVL_SHARED_ROWS rows (max_new, without
  * one n_rows, times n_heads / H), reads every entry's own table, as kvl_attend does.
  * d_workspace is kvl_attend's; d_parts (16-byte aligned; not looked at by such a call) needs no preparation and
@@ -546,7 +547,9 @@ kvl_status kvl_attend_shared(const kvl_cache *cache, int32_t layer, const kvl_se
  *   mass_out[slot][j] = mass_in[slot][j] + sum over fresh rows t and query heads h that see j of
  *                       exp(sm_scale * (q_th . K_j) - lse_th)
  * with rows, visibility and sm_scale as kvl_attend's and lse as it returned them, so each term is the probability
- * that row t's head h gave token j.  With begin != 0 the fresh tokens' mass_in counts as 0 (a step's first call;
+ * that row t's head h gave token j.  q enters the products as halves under a power of two, one for each row or, where
+ * entries have more than 16 rows, one for 128 rows beside each other, of whose largest finite element what is below 2^-39
+ * is lost.  With begin != 0 the fresh tokens' mass_in counts as 0 (a step's first call;
  * the layers after it add).  A row whose lse is infinite gives nothing.  mass_out may be mass_in; entries without
  * fresh rows, and what lies past a sequence's tokens, are not written.  Slots of a call must differ.  Sums are in
  * 32 bits and come out the same every time.  A sequence longer than a row of masses is left out (KVL_ERANGE).

@@ -22,7 +22,8 @@ namespace {
 
 constexpr int kDigits = 2048;  // 11 bits
 // Tokens of a thread in a round (one sequence of 777, 8 of up to 4,096, one of 30,000, one of 128,000: us with 4 20.4, 208,
-// 40.8, 173; with 8 21.8, 209, 38.0, 168; with 16 27.1, 213, 45.4, 169).
+// 40.8, 173; with 8 21.8, 209, 38.0, 168; with 16 27.1, 213, 45.4, 169).  A table with room for up to
+// 8,192 tokens a sequence has one CTA for each.
 constexpr int kRun = 8;
 constexpr int kMostRanks = 8;  // CTAs of a sequence
 
@@ -354,8 +355,9 @@ __global__ void __launch_bounds__(kThreads) evict_select_kernel(const __grid_con
 
 // ---- codes -------------------------------------------------------------------------------------
 
-// (8 prompts to 1,024 tokens, 32 layers, plan and selection with it: 209 us; measured beside each other three CTAs an SM
-// 224, four, which spill, 268, six of half the tokens on their way 306)
+// (8 prompts to 1,024 tokens, 32 layers, plan and selection with it: 210 us; measured beside each other three CTAs an SM
+// 224, four, which spill, 268, six of half the tokens on their way 306.  The moves alone, pages of 16 / 64: e4m3 190 / 208,
+// int8 215 / 236: a page of 64 has four parts of two slices, each of which looks at all its scales)
 constexpr int kMoveThreads = 256, kMoveCtasPerSm = 3;
 constexpr int kHeld = 8;  // tokens whose codes a lane has on their way
 

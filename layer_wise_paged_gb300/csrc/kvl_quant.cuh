@@ -122,8 +122,11 @@ inline bool allow_smem(K kernel, std::atomic<unsigned long long> (&ready)[kMaxDe
     return true;
 }
 
-// Launch a kernel that begins with grid_dependency_wait(): its CTAs may be on their way while the kernel before it on
-// the stream runs, if that one allows it, and wait for its end.  ranks: CTAs of a cluster.
+// Launch a kernel whose CTAs may start while the kernel before it on the stream runs, if that one allows it.  Each CTA
+// calls grid_dependency_wait() before it reads what that kernel writes or writes what it reads, and in any case before it
+// ends, so that whatever follows finds both done.  What it does ahead of the wait rests on kernels further back: they have
+// ended, as the first of such a chain is launched plainly, and the second of two behind it touches only what none writes
+// before its own wait.  ranks: CTAs of a cluster.
 template <typename... P, typename A>
 inline kvl_status launch_behind(void (*kernel)(P...), unsigned grid, unsigned threads, size_t smem, void *stream, const A &args,
                                 unsigned ranks = 1)
